@@ -1,0 +1,709 @@
+"""The cache operators of a verify step: what is measured, and their plain forms.
+
+Five operators around one paged KV cache held in 4 bits: append (head norms,
+rotation, quantisation), attention of the k+1 verify rows over the cache,
+reserve / release of pages around a verify, fork of sequences, and compaction
+of the page pool.
+
+Layout of one page of one layer, per KV head (P tokens, head dimension D; all
+parts follow each other, page = kv_heads of these units):
+  K codes   [P][D/2]             byte c of a token: dims 2c (low nibble), 2c+1
+  V codes   [P/8][16][8][D/32]   token t, dims n*D/16 ..: group t/8, n, t%8
+  K scales  [P/8][D/32][8]       one byte (2^(byte-127)) per token and 32 dims
+  V scales  [P/8][D/32][8]
+Codes are e2m1 (sign, then 0 .5 1 1.5 2 3 4 6).
+"""
+
+import math
+import random
+
+import torch
+
+own = False
+
+DEV = "cuda"
+LEVELS = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ---------------------------------------------------------------- the cases
+
+def listed():
+    return [
+        # the rows of the benchmark's verify batch (B=64, k=6): one layer's call per step
+        dict(name="append_verify_b64_k6", op="append", batch=64, kmin=6, kmax=6, dtype="bf16",
+             heads=32, kv_heads=8, dim=128, page=16, ctx_lo=128, ctx_hi=8192, norm=True, rot=128,
+             interleaved=False),
+        # prompts entering the cache in one call: the largest append
+        dict(name="append_prompt_b4", op="append", batch=4, kmin=1500, kmax=4000, dtype="bf16",
+             heads=32, kv_heads=8, dim=128, page=64, ctx_lo=0, ctx_hi=1000, norm=True, rot=64,
+             interleaved=True),
+        # one user, one token, a long context: latency and the split over the context
+        dict(name="attn_decode_b1_32k", op="attention", batch=1, kmin=0, kmax=0, dtype="bf16",
+             heads=32, kv_heads=8, dim=128, page=16, ctx_lo=32771, ctx_hi=32771, window=0,
+             sinks=0),
+        # the benchmark's verify batch over ragged contexts: the ordinary call
+        dict(name="attn_verify_b64_k6", op="attention", batch=64, kmin=6, kmax=6, dtype="bf16",
+             heads=32, kv_heads=8, dim=128, page=16, ctx_lo=512, ctx_hi=16384, window=0, sinks=0),
+        # the varlen batch (B=256, k in 1..8) with a window and visible first tokens
+        dict(name="attn_window_b256_varlen", op="attention", batch=256, kmin=1, kmax=8,
+             dtype="bf16", heads=64, kv_heads=8, dim=64, page=64, ctx_lo=64, ctx_hi=16384,
+             window=1024, sinks=4),
+        # the fp32 batch (B=32, k=5) over short contexts
+        dict(name="attn_f32_b32_k5", op="attention", batch=32, kmin=5, kmax=5, dtype="f32",
+             heads=16, kv_heads=4, dim=128, page=32, ctx_lo=1, ctx_hi=2000, window=0, sinks=0),
+        # pages around one verify step of the large batch (B=512, k=5): latency
+        dict(name="pages_step_b512_k5", op="reserve", batch=512, kmin=5, kmax=5, page=16,
+             kv_heads=2, dim=64, layers=1, ctx_lo=16, ctx_hi=8192, pool=65536, shared=0.1,
+             drop=0.05),
+        # prompts admitted and sequences that end, shared tails copied in every layer
+        dict(name="pages_admit_b64", op="reserve", batch=64, kmin=200, kmax=8000, page=16,
+             kv_heads=8, dim=64, layers=2, ctx_lo=1, ctx_hi=4096, pool=40000, shared=0.8,
+             drop=0.5),
+        # parallel samples of a few prompts
+        dict(name="fork_b64", op="fork", sources=8, copies=7, page=16, ctx_lo=512, ctx_hi=4096),
+        # a full batch of forks of long prompts
+        dict(name="fork_b1024", op="fork", sources=128, copies=7, page=16, ctx_lo=1024,
+             ctx_hi=16384),
+        # a small half-empty pool
+        dict(name="compact_b64", op="compact", batch=64, page=16, kv_heads=8, dim=128, layers=1,
+             ctx_lo=16, ctx_hi=2048, pool=8192, shared=0.2),
+        # a pool of many layers
+        dict(name="compact_b256_layers", op="compact", batch=256, page=16, kv_heads=4, dim=128,
+             layers=4, ctx_lo=16, ctx_hi=4096, pool=32768, shared=0.2),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng: random.Random):
+    """One more case of the ranges the listed ones stand for."""
+    op = rng.choice(["append", "attention", "attention", "reserve", "fork", "compact"])
+    dim = rng.choice([64, 128, 128, 256])
+    page = rng.choice([16, 16, 32, 64, 128])
+    if op == "append":
+        prompt = rng.random() < 0.4
+        batch = _log(rng, 1, 16 if prompt else 512)
+        kmax = _log(rng, 16, 8000 // batch) if prompt else rng.randint(0, 8)
+        kv = rng.choice([1, 2, 4, 8])
+        rot = rng.choice([0, dim // 2, dim, dim])
+        return dict(op=op, batch=batch, kmin=0 if not prompt else kmax // 3, kmax=kmax,
+                    dtype=rng.choice(["bf16", "bf16", "f32"]), heads=kv * rng.choice([1, 3, 4]),
+                    kv_heads=kv, dim=dim, page=page, ctx_lo=0, ctx_hi=_log(rng, 1, 16384),
+                    norm=rng.random() < 0.7, rot=rot, interleaved=rng.random() < 0.5)
+    if op == "attention":
+        dtype = rng.choice(["bf16", "bf16", "f32"])
+        batch = _log(rng, 1, 256)
+        kv = rng.choice([1, 2, 4, 8])
+        # tokens of the batch so that the cache stays within the listed cases' sizes
+        tokens = 1.2e8 / (kv * dim * (2 if dtype == "f32" else 1))
+        hi = max(2, min(100000, int(tokens / batch)))
+        windowed = rng.random() < 0.4
+        ctx_hi = _log(rng, 2, hi)
+        return dict(op=op, batch=batch, kmin=0, kmax=rng.choice([0, 3, 5, 6, 8]), dtype=dtype,
+                    heads=kv * rng.choice([1, 2, 4, 5, 8]), kv_heads=kv, dim=dim, page=page,
+                    ctx_lo=rng.choice([0, ctx_hi // 3]), ctx_hi=ctx_hi,
+                    window=_log(rng, 1, 4096) if windowed else 0,
+                    sinks=rng.choice([0, 1, 4, 37]) if windowed else 0)
+    if op == "reserve":
+        batch = _log(rng, 1, 1024)
+        kmax = rng.choice([0, 5, 8, 300 if batch <= 64 else 8])
+        ctx_hi = _log(rng, 16, 4096)
+        pool = batch * 2 * (-(-(ctx_hi + kmax + 1) // page)) + rng.randint(64, 4096)
+        layers = 1 if pool > 30000 else rng.randint(1, 3)
+        return dict(op=op, batch=batch, kmin=0, kmax=kmax, page=page, kv_heads=1, dim=64,
+                    layers=layers, ctx_lo=1, ctx_hi=ctx_hi, pool=pool,
+                    shared=rng.choice([0.0, 0.3, 0.9]), drop=rng.choice([0.0, 0.1, 0.6]))
+    if op == "fork":
+        return dict(op=op, sources=_log(rng, 1, 128), copies=rng.randint(1, 7), page=page,
+                    ctx_lo=1, ctx_hi=_log(rng, 2, 16384))
+    batch = _log(rng, 1, 512)
+    ctx_hi = _log(rng, 16, 2048)
+    pool = 2 * batch * (-(-ctx_hi // page)) + rng.randint(1, 999)
+    return dict(op=op, batch=batch, page=page, kv_heads=rng.choice([1, 2]), dim=64,
+                layers=rng.randint(1, 3), ctx_lo=1, ctx_hi=ctx_hi, pool=pool,
+                shared=rng.choice([0.0, 0.5]))
+
+
+# ---------------------------------------------------------------- host plans
+
+def _lens(rng, n, lo, hi):
+    """n context lengths, logarithmic between lo and hi."""
+    a, b = math.log(lo + 1), math.log(hi + 1)
+    return [min(hi, max(lo, int(round(math.exp(rng.uniform(a, b)) - 1)))) for _ in range(n)]
+
+
+def _plan(case, seed):
+    """What the host knows of a call: row counts, context lengths, offsets.  The lengths of a
+    case are fixed, which sequence has which goes by the seed (outputs keep their shapes)."""
+    sizes = random.Random(str(sorted(case.items())))
+    rng = random.Random(f"{seed} {case['op']}")
+    n = case["sources"] if case["op"] == "fork" else case["batch"]
+    ctx = _lens(sizes, n, case["ctx_lo"], case["ctx_hi"])
+    rng.shuffle(ctx)
+    plan = dict(ctx=ctx, rng=rng)
+    if "kmax" in case:
+        plan["rows"] = [sizes.randint(case["kmin"], case["kmax"]) + 1 for _ in ctx]
+        rng.shuffle(plan["rows"])
+        plan["cu"] = [0]
+        for r in plan["rows"]:
+            plan["cu"].append(plan["cu"][-1] + r)
+    return plan
+
+
+def _pages_for(n, page):
+    return -(-n // page)
+
+
+def _page_bytes(case):
+    return case["page"] * case["kv_heads"] * case["dim"] * 17 // 16
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def _generator(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed * 7919 + 17)
+    return g
+
+
+# ---------------------------------------------------------------- the 4-bit format
+
+def _quantise(x):
+    """x [..., D] (fp64 or fp32) -> codes [..., D] uint8 and scale bytes [..., D/32] uint8."""
+    b = x.unflatten(-1, (-1, 32))
+    amax = b.abs().amax(-1)
+    m, e = torch.frexp(amax)                       # amax = m 2^e, m in [0.5, 1)
+    e = torch.where(m > 0.75, e - 2, e - 3)        # smallest e with amax <= 6 * 2^e
+    byte = (e + 127).clamp(1, 254)
+    byte = torch.where(amax > 0, byte, torch.ones_like(byte))
+    y = torch.ldexp(b, (127 - byte).unsqueeze(-1).to(torch.int32))
+    a = y.abs()
+    code = torch.zeros_like(a, dtype=torch.uint8)
+    # between two levels the middle goes to the even code
+    for i, mid in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)):
+        code += (a > mid) if i % 2 == 0 else (a >= mid)
+    code |= (y < 0).to(torch.uint8) << 3
+    bad = ~torch.isfinite(amax)
+    byte = torch.where(bad, torch.full_like(byte, 255), byte)
+    code = torch.where(bad.unsqueeze(-1), torch.zeros_like(code), code)
+    return code.flatten(-2), byte.to(torch.uint8)
+
+
+def _values(code, byte, dtype=torch.float32):
+    """Codes and scale bytes -> values; a scale byte 255 stands for NaN."""
+    lut = torch.tensor(LEVELS + tuple(-v for v in LEVELS), dtype=dtype, device=code.device)
+    v = lut[code.int()].unflatten(-1, (-1, 32))
+    s = torch.ldexp(torch.ones((), dtype=dtype, device=code.device), byte.to(torch.int32) - 127)
+    s = torch.where(byte == 255, torch.full_like(s, math.nan), s)
+    return (v * s.unsqueeze(-1)).flatten(-2)
+
+
+def _split(pages, page, kv_heads, dim):
+    """Views of a page pool [n, page_bytes]: K codes, V codes, K scales, V scales."""
+    n = pages.shape[0]
+    u = pages.view(n, kv_heads, -1)
+    a, s = page * dim // 2, page * dim // 32
+    return (u[:, :, :a].unflatten(-1, (page, dim // 2)),
+            u[:, :, a:2 * a].unflatten(-1, (page // 8, 16, 8, dim // 32)),
+            u[:, :, 2 * a:2 * a + s].unflatten(-1, (page // 8, dim // 32, 8)),
+            u[:, :, 2 * a + s:].unflatten(-1, (page // 8, dim // 32, 8)))
+
+
+def _nibbles(b):
+    return torch.stack((b & 15, b >> 4), -1).flatten(-2)
+
+
+def _read_pages(pages, page, kv_heads, dim, dtype=torch.float32):
+    """Values of whole pages: K, V [n, page, kv_heads, dim]."""
+    kc, vc, ks, vs = _split(pages, page, kv_heads, dim)
+    n = pages.shape[0]
+    k_code = _nibbles(kc)                                                  # n h P D
+    v_code = _nibbles(vc).permute(0, 1, 2, 4, 3, 5).reshape(n, kv_heads, page, dim)
+    scale = [s.permute(0, 1, 2, 4, 3).reshape(n, kv_heads, page, dim // 32) for s in (ks, vs)]
+    return (_values(k_code, scale[0], dtype).transpose(1, 2),
+            _values(v_code, scale[1], dtype).transpose(1, 2))
+
+
+def _fill_pages(pages, page, kv_heads, dim, g):
+    """Random K and V (normal, a few loud channels in K) in every page, in the format."""
+    loud = 1 + 3 * (torch.rand(dim, generator=g, device=DEV) < 0.05)
+    step = max(1, (1 << 25) // (page * kv_heads * dim))
+    for i in range(0, pages.shape[0], step):
+        part = pages[i:i + step]
+        kc, vc, ks, vs = _split(part, page, kv_heads, dim)
+        shape = (part.shape[0], kv_heads, page, dim)
+        for codes, scales, mul in ((kc, ks, loud), (vc, vs, 1)):
+            c, s = _quantise(torch.randn(shape, generator=g, device=DEV) * mul)
+            b = c[..., 0::2] | (c[..., 1::2] << 4)
+            if codes is vc:
+                b = b.unflatten(2, (-1, 8)).unflatten(-1, (16, -1)).transpose(3, 4)
+            codes.copy_(b.reshape(codes.shape))
+            scales.copy_(s.unflatten(2, (-1, 8)).transpose(-1, -2))
+
+
+# ---------------------------------------------------------------- state
+
+def _bookkeeping(case, plan, seqs, ld, pool, shared=0.0):
+    """Tables of sequences over a shuffled pool, a share of the sequences holding the pages of
+    the one before them (as a fork leaves them): (table, lens, refs) as lists."""
+    rng, page = plan["rng"], case["page"]
+    ids = list(range(pool))
+    rng.shuffle(ids)
+    table = [[-1] * ld for _ in range(seqs)]
+    lens = [0] * seqs
+    refs = [0] * pool
+    for b, n in enumerate(plan["ctx"]):
+        if b and rng.random() < shared:
+            n = lens[b - 1]
+            own_ids = table[b - 1][:_pages_for(n, page)]
+        else:
+            own_ids = [ids.pop() for _ in range(_pages_for(n, page))]
+        lens[b] = n
+        for i, p in enumerate(own_ids):
+            table[b][i] = p
+            refs[p] += 1
+    return table, lens, refs
+
+
+def _cache(st, case, flat, seqs, ld, pool, pages):
+    """The state's tensors: one int32 buffer (table, lengths, reference counts) and the pages."""
+    st["flat"] = flat
+    st["table"] = flat[:seqs * ld].view(seqs, ld)
+    st["lens"] = flat[seqs * ld:seqs * ld + seqs]
+    st["refs"] = flat[seqs * ld + seqs:seqs * ld + seqs + pool]
+    st["pages"] = pages
+    if own:
+        from lossless_rejection_sampling_spec_amd import binding
+        st["cache"] = binding.KVCache(pages=pages, page_table=st["table"], seq_lens=st["lens"],
+                                      ref_counts=st["refs"], page_size=case["page"],
+                                      kv_heads=case.get("kv_heads", 1),
+                                      head_dim=case.get("dim", 64))
+    return st
+
+
+def _rotation_table(positions, rot):
+    """cos and sin of position * 10000^(-2i/rot): [positions, rot], cos first."""
+    inv = 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=DEV) / rot)
+    ang = torch.arange(positions, dtype=torch.float64, device=DEV)[:, None] * inv
+    return torch.cat((ang.cos(), ang.sin()), -1).float()
+
+
+def prepare(case, seed):
+    plan = _plan(case, seed)
+    g = _generator(seed)
+    op, page = case["op"], case["page"]
+    st = dict(case=case, plan=plan)
+    if op in ("append", "attention"):
+        batch, dtype = case["batch"], TYPES[case["dtype"]]
+        full = [c + r for c, r in zip(plan["ctx"], plan["rows"])]
+        ld = _pages_for(max(plan["ctx"]) + max(plan["rows"]), page)
+        pool = sum(_pages_for(c, page) + _pages_for(r, page) + 1
+                   for c, r in zip(plan["ctx"], plan["rows"]))
+        table, lens, refs = _bookkeeping(case, dict(plan, ctx=full), batch, ld, pool)
+        flat = _i32([x for r in table for x in r] + lens + refs)
+        pages = torch.zeros(1, pool, _page_bytes(case), dtype=torch.uint8, device=DEV)
+        _fill_pages(pages[0], page, case["kv_heads"], case["dim"], g)
+        _cache(st, case, flat, batch, ld, pool, pages)
+        rows = plan["cu"][-1]
+        st["cu"], st["ctx"] = _i32(plan["cu"]), _i32(plan["ctx"])
+        h, hk, d = case["heads"], case["kv_heads"], case["dim"]
+        if op == "append":
+            # one fused projection's output: q, k and v are views of it
+            qkv = torch.randn(rows, h + 2 * hk, d, generator=g, device=DEV)
+            qkv[:, h:h + hk] *= 1 + 3 * (torch.rand(d, generator=g, device=DEV) < 0.05)
+            qkv = qkv.to(dtype)
+            st["q"], st["k"], st["v"] = qkv[:, :h], qkv[:, h:h + hk], qkv[:, h + hk:]
+            if case["norm"]:
+                st["qw"] = 1 + 0.1 * torch.randn(d, generator=g, device=DEV)
+                st["kw"] = 1 + 0.1 * torch.randn(d, generator=g, device=DEV)
+            if case["rot"]:
+                st["cos_sin"] = _rotation_table(ld * page, case["rot"])
+        else:
+            st["q"] = torch.randn(rows, h, d, generator=g, device=DEV).to(dtype)
+            st["groups"] = _groups(case, plan)
+        return st
+    if op == "fork":
+        n, copies = case["sources"], case["copies"]
+        ld = _pages_for(max(plan["ctx"]) + 64, page)
+        pool = sum(_pages_for(c, page) for c in plan["ctx"]) + 9
+        seqs = n * (copies + 1)
+        table, lens, refs = _bookkeeping(case, plan, seqs, ld, pool)
+        flat = _i32([x for r in table for x in r] + lens + refs)
+        pages = torch.zeros(1, pool, page * 68, dtype=torch.uint8, device=DEV)
+        _cache(st, case, flat, seqs, ld, pool, pages)
+        st["src"] = _i32([i for i in range(n) for _ in range(copies)])
+        st["dst"] = _i32(list(range(n, seqs)))
+    else:
+        batch, pool = case["batch"], case["pool"]
+        full = [c + case.get("kmax", 0) + 1 for c in plan["ctx"]]
+        ld = _pages_for(max(full), page) + 1
+        table, lens, refs = _bookkeeping(case, plan, batch, ld, pool, case["shared"])
+        flat = _i32([x for r in table for x in r] + lens + refs)
+        pages = torch.randint(0, 256, (case["layers"], pool, _page_bytes(case)), generator=g,
+                              dtype=torch.uint8, device=DEV)
+        _cache(st, case, flat, batch, ld, pool, pages)
+        if op == "reserve":
+            rng = plan["rng"]
+            after = [n + r for n, r in zip(lens, plan["rows"])]
+            # most give back the drafts that were rejected, some sequences end
+            give = [a if rng.random() < case["drop"] else rng.randint(0, r - 1)
+                    for a, r in zip(after, plan["rows"])]
+            st["cu"], st["give"] = _i32(plan["cu"]), _i32(give)
+            st["max_new"] = max(plan["rows"]) // page + 2
+            st["max_drop"] = max(_pages_for(x, page) for x in after)
+    st["flat0"] = st["flat"].clone()
+    return st
+
+
+# ---------------------------------------------------------------- one pass
+
+def run(st):
+    case = st["case"]
+    if own:
+        from lossless_rejection_sampling_spec_amd import binding
+    op = case["op"]
+    if op == "append":
+        rot = dict(cos_sin=st.get("cos_sin"), interleaved=case["interleaved"])
+        if own:
+            q, status, kv, vv = binding.kv_append(
+                st["cache"], st["q"], st["k"], st["v"], st["cu"], st["ctx"], q_weight=st.get("qw"),
+                k_weight=st.get("kw"), eps=1e-6, want_values=True, **rot)
+        else:
+            q, status, kv, vv = _plain_append(st, **rot)
+        return dict(q=q, k=kv, v=vv, pages=st["pages"], status=status)
+    if op == "attention":
+        sizes = dict(max_k=case["kmax"], max_context=case["ctx_hi"] + case["kmax"] + 1)
+        if own:
+            out, status = binding.kv_attention(
+                st["cache"], st["q"], st["cu"], st["ctx"], scale=case["dim"] ** -0.5,
+                window=case["window"], sinks=case["sinks"], **sizes)
+        else:
+            out, status = _plain_attention(st)
+        return dict(out=out, status=status)
+    # the pass changes the tables: it starts from the same ones every time (one copy)
+    st["flat"].copy_(st["flat0"])
+    if op == "reserve":
+        if own:
+            ctx, s0 = binding.kv_reserve(st["cache"], st["cu"])
+            s1 = binding.kv_release(st["cache"], st["give"], ctx)
+        else:
+            ctx, s0 = _plain_reserve(st)
+            s1 = _plain_release(st, ctx)
+        return dict(ctx=ctx, status=s0, released=s1, tables=st["flat"], pages=st["pages"])
+    if op == "fork":
+        status = (binding.kv_fork(st["cache"], st["src"], st["dst"]) if own else _plain_fork(st))
+        return dict(status=status, tables=st["flat"])
+    live = binding.kv_compact(st["cache"]) if own else _plain_compact(st)
+    return dict(live=live, tables=st["flat"], pages=st["pages"])
+
+
+# ---------------------------------------------------------------- plain forms
+
+def _rotate(x, cos_sin, pos, interleaved):
+    """x [rows, heads, dim]; the first `rot` dims turn by the table's angles."""
+    rot = cos_sin.shape[1]
+    cs = cos_sin[pos].to(x.dtype).unsqueeze(1)
+    c, s = cs[..., :rot // 2], cs[..., rot // 2:]
+    if interleaved:
+        a, b = x[..., 0:rot:2], x[..., 1:rot:2]
+        y = torch.stack((a * c - b * s, b * c + a * s), -1).flatten(-2)
+    else:
+        a, b = x[..., :rot // 2], x[..., rot // 2:rot]
+        y = torch.cat((a * c - b * s, b * c + a * s), -1)
+    return torch.cat((y, x[..., rot:]), -1)
+
+
+def _plain_append(st, cos_sin, interleaved):
+    case = st["case"]
+    page, hk, d = case["page"], case["kv_heads"], case["dim"]
+    cu, ctx = st["cu"].long(), st["ctx"].long()
+    row = torch.arange(st["q"].shape[0], device=DEV)
+    b = torch.searchsorted(cu, row, right=True) - 1
+    pos = ctx[b] + row - cu[b]
+
+    def turned(x, w):
+        x = x.double()                    # 64 bits: codes next to a border
+        if w is not None:
+            x = x * torch.rsqrt((x * x).mean(-1, keepdim=True) + 1e-6) * w.double()
+        return x if cos_sin is None else _rotate(x, cos_sin, pos, interleaved)
+
+    q = turned(st["q"], st.get("qw"))
+    slot = st["table"].long()[b, pos // page]
+    t = pos % page
+    kc, vc, ks, vs = _split(st["pages"][0], page, hk, d)
+    out = []
+    for x, codes, scales in ((turned(st["k"], st.get("kw")), kc, ks), (st["v"].double(), vc, vs)):
+        c, s = _quantise(x)
+        byte = c[..., 0::2] | (c[..., 1::2] << 4)
+        if codes is kc:
+            codes[slot, :, t] = byte
+        else:
+            codes[slot, :, t // 8, :, t % 8] = byte.unflatten(-1, (16, -1))
+        scales[slot, :, t // 8, :, t % 8] = s
+        out.append(_values(c, s).to(st["q"].dtype))
+    return q.to(st["q"].dtype), torch.zeros_like(st["ctx"]), out[0], out[1]
+
+
+def _visible(pos, t, case):
+    m = t <= pos
+    if case["window"]:
+        m = m & ((t > pos - case["window"]) | (t < case["sinks"]))
+    return m
+
+
+def _plain_attention(st):
+    case = st["case"]
+    page, hk, d, h = case["page"], case["kv_heads"], case["dim"], case["heads"]
+    kc, vc, ks, vs = _split(st["pages"][0], page, hk, d)
+    out = torch.empty_like(st["q"])
+    for g in st["groups"]:                # requests of similar lengths, padded to one
+        slot, t = st["table"].long()[g["seq"][:, None], g["t"] // page], g["t"] % page
+        k = _values(_nibbles(kc[slot, :, t]), ks[slot, :, t // 8, :, t % 8])
+        v = _values(_nibbles(vc[slot, :, t // 8, :, t % 8]).flatten(-2),
+                    vs[slot, :, t // 8, :, t % 8])
+        n, r = g["row"].shape
+        q = st["q"][g["row"]].float().view(n, r, hk, h // hk, d).transpose(1, 2).flatten(2, 3)
+        s = torch.matmul(q, k.permute(0, 2, 3, 1).contiguous()) * d ** -0.5
+        keep = _visible(g["pos"][:, :, None], g["t"][:, None], case) & g["real"][:, None]
+        keep = keep[:, None, :, None].expand(n, 1, r, h // hk, -1).flatten(2, 3)
+        p = torch.softmax(s.masked_fill(~keep, -math.inf), -1)
+        y = torch.matmul(p, v.transpose(1, 2).contiguous())
+        y = y.view(n, hk, r, h // hk, d).transpose(1, 2).reshape(n, r, h, d)
+        out[g["rows"]] = y[g["of"], g["at"]].to(out.dtype)
+    return out, torch.zeros_like(st["ctx"])
+
+
+def _groups(case, plan):
+    """Requests grouped by length: what the plain attention pads to one shape."""
+    spans = []
+    for c, r in zip(plan["ctx"], plan["rows"]):
+        first = max(0, c - case["window"] + 1) if case["window"] else 0
+        spans.append(list(range(min(case["sinks"], first))) + list(range(first, c + r)))
+    order = sorted(range(len(spans)), key=lambda b: len(spans[b]))
+    per_token = case["kv_heads"] * case["dim"]
+    groups, part = [], []
+    for b in order:
+        n = len(spans[b])
+        if part and (n > 1.5 * len(spans[part[0]]) + 64 or n * (len(part) + 1) * per_token > 2 ** 27):
+            groups.append(part)
+            part = []
+        part.append(b)
+    groups.append(part)
+    made = []
+    for part in groups:
+        width = max(len(spans[b]) for b in part)
+        high = max(plan["rows"][b] for b in part)
+        at = [(i, j, plan["cu"][b] + j) for i, b in enumerate(part) for j in range(plan["rows"][b])]
+        row = [[plan["cu"][b] + min(j, plan["rows"][b] - 1) for j in range(high)] for b in part]
+        pos = [[plan["ctx"][b] + min(j, plan["rows"][b] - 1) for j in range(high)] for b in part]
+        made.append(dict(
+            seq=_i32(part).long(), row=_i32(row).long(), pos=_i32(pos),
+            t=_i32([spans[b] + [0] * (width - len(spans[b])) for b in part]).long(),
+            real=torch.arange(width, device=DEV) < _i32([len(spans[b]) for b in part])[:, None],
+            of=_i32([x[0] for x in at]).long(), at=_i32([x[1] for x in at]).long(),
+            rows=_i32([x[2] for x in at]).long()))
+    return made
+
+
+def _plain_reserve(st):
+    page, table, lens, refs = st["case"]["page"], st["table"], st["lens"], st["refs"]
+    ld, pool = table.shape[1], refs.shape[0]
+    old = lens.long()
+    rows = (st["cu"][1:] - st["cu"][:-1]).long()
+    have, want = (old + page - 1) // page, (old + rows + page - 1) // page
+    tail = table.gather(1, (old // page).clamp(max=ld - 1)[:, None])[:, 0].long().clamp(min=0)
+    cow = ((old % page != 0) & (refs[tail] > 1)).long()
+    fits = want <= ld
+    need = torch.where(fits, want - have + cow, 0)
+    end = need.cumsum(0)
+    kept = (refs > 0).int().argmax()          # a page in use: what does not copy stays there
+    ok = fits & (end <= (refs == 0).sum())
+    free = torch.argsort((refs > 0).to(torch.int8), stable=True)
+    j = torch.arange(st["max_new"], device=DEV)
+    rank = (end - need)[:, None] + j
+    page_id = free[rank.clamp(max=pool - 1)]
+    use = (j < need[:, None]) & ok[:, None]
+    slot = (have - cow)[:, None] + j
+    wide = torch.cat((table, table.new_zeros(table.shape[0], 1)), 1)     # a spare column
+    wide.scatter_(1, torch.where(use, slot, ld), page_id.int())
+    table.copy_(wide[:, :ld])
+    refs.index_add_(0, tail, -(cow * ok).int())
+    refs.index_add_(0, page_id.flatten(), use.flatten().int())
+    copy = (cow * ok).bool()
+    dst, src = torch.where(copy, page_id[:, 0], kept), torch.where(copy, tail, kept)
+    st["pages"][:, dst] = st["pages"][:, src]
+    lens.add_((rows * ok).int())
+    return torch.where(ok, old, -1).int(), torch.where(ok, 0, 7).int()
+
+
+def _plain_release(st, ctx):
+    page, table, lens, refs = st["case"]["page"], st["table"], st["lens"], st["refs"]
+    old = lens.long()
+    give = torch.where(ctx >= 0, st["give"].long(), 0)
+    new = old - give
+    keep, have = (new + page - 1) // page, (old + page - 1) // page
+    ld = table.shape[1]
+    slot = keep[:, None] + torch.arange(min(st["max_drop"], ld), device=DEV)
+    drop = slot < have[:, None]
+    slot = slot.clamp(max=ld - 1)
+    ids = table.gather(1, slot).long().clamp(min=0)
+    refs.index_add_(0, ids.flatten(), -drop.flatten().int())
+    col = torch.arange(ld, device=DEV)
+    table.masked_fill_((col >= keep[:, None]) & (col < have[:, None]), -1)
+    lens.copy_(new.int())
+    return torch.zeros_like(st["give"])
+
+
+def _plain_fork(st):
+    page, table, lens, refs = st["case"]["page"], st["table"], st["lens"], st["refs"]
+    src, dst = st["src"].long(), st["dst"].long()
+    n = lens[src]
+    held = torch.arange(table.shape[1], device=DEV) < ((n + page - 1) // page)[:, None]
+    ids = table[src]
+    table[dst] = torch.where(held, ids, table[dst])
+    lens[dst] = n
+    refs.index_add_(0, ids.long().clamp(min=0).flatten(), held.flatten().int())
+    return torch.zeros_like(st["src"])
+
+
+def _plain_compact(st):
+    page, table, lens, refs = st["case"]["page"], st["table"], st["lens"], st["refs"]
+    pool = refs.shape[0]
+    at = torch.arange(pool, device=DEV)
+    live = refs > 0
+    count = live.sum()
+    holes = ((at < count) & ~live).sum()
+    free = torch.argsort(live.to(torch.int8), stable=True)
+    rank = live.long().cumsum(0) - 1 - (count - holes)          # of a mover among the movers
+    moves = live & (at >= count)
+    to = torch.where(moves, free[rank.clamp(0, pool - 1)], at)   # new id of each live page
+    come = at.clone()                                            # page that ends up in each place
+    come.scatter_(0, torch.where(moves, to, pool - 1), torch.where(moves, at, pool - 1))
+    # (pages that stay write the pool's last place, which never is a hole below a mover)
+    come = torch.where((at < count) & ~live, come, at)
+    for layer in st["pages"]:
+        layer.copy_(layer[come])
+    held = torch.arange(table.shape[1], device=DEV) < ((lens + page - 1) // page)[:, None]
+    table.copy_(torch.where(held, to[table.long().clamp(min=0)].int(), table))
+    refs.copy_(torch.where(at < count, refs[come], torch.zeros_like(refs)))
+    return count.int().view(1)
+
+
+# ---------------------------------------------------------------- the definition in 64 bits
+
+def exact(case, seed):
+    """Outputs that are computed numbers, from the definitions, in float64."""
+    op = case["op"]
+    if op not in ("append", "attention"):
+        return None
+    st = prepare(case, seed)
+    plan, page, d = st["plan"], case["page"], case["dim"]
+    if op == "append":
+        where = torch.cat([torch.arange(c, c + r, device=DEV)
+                           for c, r in zip(plan["ctx"], plan["rows"])]).double()
+
+        def spun(x, w):
+            x = x.double()
+            if w is not None:
+                x = x / ((x ** 2).sum(-1, keepdim=True) / d + 1e-6).sqrt() * w.double()
+            if not case["rot"]:
+                return x
+            half = case["rot"] // 2
+            tab = st["cos_sin"].double()[where.long()][:, None]
+            i = torch.arange(half, device=DEV)
+            lo, hi = (2 * i, 2 * i + 1) if case["interleaved"] else (i, i + half)
+            z = torch.complex(x[..., lo], x[..., hi]) * torch.complex(tab[..., :half],
+                                                                      tab[..., half:])
+            y = x.clone()
+            y[..., lo], y[..., hi] = z.real, z.imag
+            return y
+
+        def nearest(x):
+            blocks = x.reshape(*x.shape[:-1], d // 32, 32)
+            top = blocks.abs().amax(-1, keepdim=True)
+            s = 2.0 ** torch.ceil(torch.log2(top / 6).clamp(min=-126))
+            s = torch.where(top > 6 * s, 2 * s, torch.where(top <= 3 * s, s / 2, s))
+            s = s.clamp(min=2.0 ** -126)
+            y = blocks / s
+            lv = torch.tensor(LEVELS, dtype=torch.float64, device=DEV)
+            best = torch.zeros_like(y)
+            gap = torch.full_like(y, math.inf)
+            for code in (0, 2, 4, 6, 1, 3, 5, 7):       # even codes first: they keep a tie
+                delta = (y.abs() - lv[code]).abs()
+                best = torch.where(delta < gap, lv[code], best)
+                gap = torch.minimum(gap, delta)
+            return (best * torch.where(y < 0, -1.0, 1.0) * s).reshape(x.shape)
+
+        return dict(q=spun(st["q"], st.get("qw")), k=nearest(spun(st["k"], st.get("kw"))),
+                    v=nearest(st["v"].double()), pages=None, status=None)
+    group = case["heads"] // case["kv_heads"]
+    out = torch.empty(st["q"].shape, dtype=torch.float64, device=DEV)
+    pool = st["pages"][0]
+    for b, (c, r) in enumerate(zip(plan["ctx"], plan["rows"])):
+        n, o = c + r, plan["cu"][b]
+        ids = st["table"][b, :_pages_for(n, page)].long()
+        k, v = _read_pages(pool[ids], page, case["kv_heads"], d, torch.float64)
+        k, v = k.reshape(-1, case["kv_heads"], d)[:n], v.reshape(-1, case["kv_heads"], d)[:n]
+        t = torch.arange(n, device=DEV)
+        pos = t[c:, None]
+        hide = t > pos
+        if case["window"]:
+            hide |= (t <= pos - case["window"]) & (t >= case["sinks"])
+        for head in range(case["heads"]):
+            z = st["q"][o:o + r, head].double() @ k[:, head // group].T.contiguous()
+            z = (z / math.sqrt(d)).masked_fill(hide, -math.inf)
+            w = torch.exp(z - z.amax(-1, keepdim=True))
+            out[o:o + r, head] = (w @ v[:, head // group].contiguous()) / w.sum(-1, keepdim=True)
+    return dict(out=out, status=None)
+
+
+# ---------------------------------------------------------------- what a pass cannot do without
+
+def _seen(c, r, case):
+    """Cache positions a request's rows see together, and (row, position) pairs."""
+    n, w, s = c + r, case["window"], case["sinks"]
+    if not w:
+        return n, sum(c + j + 1 for j in range(r))
+    first = max(0, c - w + 1)
+    pairs = 0
+    for j in range(r):
+        lo = max(0, c + j - w + 1)
+        pairs += c + j + 1 - lo + min(s, lo)
+    return n - first + min(s, first), pairs
+
+
+def work(case):
+    plan = _plan(case, 0)
+    op, page = case["op"], case["page"]
+    if op in ("append", "attention"):
+        size = 2 if case["dtype"] == "bf16" else 4
+        rows, h, hk, d = plan["cu"][-1], case["heads"], case["kv_heads"], case["dim"]
+        if op == "append":
+            moved = rows * ((2 * h + 4 * hk) * d * size + hk * d * 17 // 16 + case["rot"] * 4)
+            return dict(bytes=moved, flops=rows * (h + hk) * d * 8)
+        seen = [_seen(c, r, case) for c, r in zip(plan["ctx"], plan["rows"])]
+        return dict(bytes=sum(n for n, _ in seen) * hk * d * 17 // 16 + 2 * rows * h * d * size,
+                    flops=4 * sum(p for _, p in seen) * h * d)
+    if op == "fork":
+        held = sum(_pages_for(c, page) for c in plan["ctx"])
+        # the table rows are read once and written for each copy; counts are read and written
+        return dict(bytes=4 * (held * (1 + case["copies"]) + 2 * held), flops=0)
+    full = [c + case.get("kmax", 0) + 1 for c in plan["ctx"]]
+    ld = _pages_for(max(full), page) + 1
+    table, lens, refs = _bookkeeping(case, plan, case["batch"], ld, case["pool"], case["shared"])
+    if op == "reserve":
+        rows = plan["rows"]
+        fresh = sum(_pages_for(n + r, page) - _pages_for(n, page) for n, r in zip(lens, rows))
+        cow = sum(1 for b, n in enumerate(lens) if n % page and refs[table[b][n // page]] > 1)
+        return dict(bytes=4 * case["pool"] + 8 * (fresh + cow) * 2 + 16 * case["batch"]
+                    + 2 * cow * _page_bytes(case) * case["layers"], flops=0)
+    live = sum(1 for x in refs if x)
+    moves = sum(1 for x in refs[live:] if x)
+    held = sum(_pages_for(n, page) for n in lens)
+    return dict(bytes=8 * case["pool"] + 8 * held + 2 * moves * _page_bytes(case) * case["layers"],
+                flops=0)
