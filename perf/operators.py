@@ -179,7 +179,7 @@ def _quantise(x):
     amax = b.abs().amax(-1)
     m, e = torch.frexp(amax)                       # amax = m 2^e, m in [0.5, 1)
     e = torch.where(m > 0.75, e - 2, e - 3)        # smallest e with amax <= 6 * 2^e
-    byte = (e + 127).clamp(1, 254)
+    byte = (e + 127).clamp(1, 252)
     byte = torch.where(amax > 0, byte, torch.ones_like(byte))
     y = torch.ldexp(b, (127 - byte).unsqueeze(-1).to(torch.int32))
     a = y.abs()
@@ -522,7 +522,7 @@ def _plain_reserve(st):
     need = torch.where(fits, want - have + cow, 0)
     end = need.cumsum(0)
     kept = (refs > 0).int().argmax()          # a page in use: what does not copy stays there
-    ok = fits & (end <= (refs == 0).sum())
+    ok = fits & ((end <= (refs == 0).sum()) | (need == 0))
     free = torch.argsort((refs > 0).to(torch.int8), stable=True)
     j = torch.arange(st["max_new"], device=DEV)
     rank = (end - need)[:, None] + j
