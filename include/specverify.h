@@ -124,11 +124,14 @@ enum {
   SV_ROW_BAD_K = 3,
   SV_ROW_BAD_TOKEN = 4,
   SV_ROW_BAD_PARAM = 5,
-  SV_ROW_INTERNAL = 6   /* a wait between workgroups ran out (another kernel kept the
+  SV_ROW_INTERNAL = 6,  /* a wait between workgroups ran out (another kernel kept the
                            GPU's compute units busy for a long time), or the workspace
                            was poisoned by such a call: accepted is -1, the request's
                            other outputs are undefined, and the workspace must be
                            re-initialised (spec_verify_workspace_init) */
+  SV_ROW_NO_PAGES = 7,  /* spec_kv_reserve: the pool or the request's table row is full */
+  SV_ROW_BAD_PAGE = 8   /* cache calls: a page id the request needs is outside the pool, or
+                           its position lies past its table row */
 };
 
 /* ABI version of the loaded library (SPECVERIFY_ABI_VERSION). */
@@ -318,6 +321,178 @@ int spec_verify_sampled_noalloc(const void* target_logits, int target_dtype, int
                                 int vocab, int32_t* accepted, int32_t* out_tokens,
                                 float* p_at_draft, float* q_at_draft, int32_t* status,
                                 void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The KV cache around a verify: paged, held in 4 bits
+ * ---------------------------------------------------------------------------
+ * A step of a serving loop is reserve -> (per layer: append, attention) ->
+ * verify -> drain -> release: "The four high-risk coupling points" item 1 of
+ * "Adding Speculative Decoding" (slots reserved for the k+1 rows, given back
+ * after the drain), the chain mask of its "Verification and sampling" item 1,
+ * and the page-wise free of the Rust page's "Production Pitfalls" item 2.
+ *
+ * Values: blocks of 32 dims share a scale 2^(byte - 127); an element is a
+ *   4-bit code, sign bit then {0, .5, 1, 1.5, 2, 3, 4, 6}.  A block's scale is
+ *   the smallest power of two s with amax <= 6 s (byte held to [1, 252]; larger
+ *   magnitudes saturate), codes round to nearest, ties to the even code.  A
+ *   block with a NaN or an infinity is stored with byte 255 and reads as NaN.
+ * Pages: one layer's pool is [num_pages][kv_heads] units; a unit holds
+ *   page_size tokens (16, 32, 64, 128 or 256) of one KV head of dimension
+ *   D = head_dim (64, 128 or 256), P = page_size, without gaps:
+ *     K codes  [P][D/2]             byte c of a token: dims 2c (low half), 2c+1
+ *     V codes  [P/8][16][8][D/32]   token t, dims n*D/16 ...: [t/8][n][t%8]
+ *     K scales [P/8][D/32][8]       token t, dims 32 i ...:   [t/8][i][t%8]
+ *     V scales [P/8][D/32][8]
+ *   A pool starts 16-byte aligned.  All layers share the tables.
+ * Tables: page_table int32 [batch, ld_table]: page of positions
+ *   [i P, (i+1) P) of request b at [b][i]; ld_table * P <= 2^30.
+ *   seq_lens int32 [batch]: positions a request holds.  ref_counts int32
+ *   [num_pages]: table entries that name the page; 0 = free.  Entries past
+ *   ceil(seq_len / P) mean nothing.  A request (slot) without rows in a call
+ *   is SV_ROW_BAD_K there and left alone.
+ * Offsets: the first request whose offsets are negative, go back or pass
+ *   total_rows, and every later one, is SV_ROW_BAD_K.
+ * Calls that change the same tables, counts or pages are ordered by the
+ *   caller (one stream).  Batches hold at most 1,024 requests, pools at most
+ *   2^24 pages.  Return values as elsewhere (SV_ERR_NULL also for a workspace
+ *   that is needed and NULL or not 16-byte aligned).
+ */
+
+/* Bytes of a page of one layer (0 on invalid sizes). */
+size_t spec_kv_page_bytes(int kv_heads, int head_dim, int page_size);
+
+/*
+ * Head norms, rotation and the cache write of the call's rows in one pass.
+ * Row cu[b] + j sits at position p = context_lens[b] + j.  Per head of q and k:
+ *   y = x / sqrt(mean(x^2) + eps) * weight   (weight NULL: y = x)
+ *   the first rot_dim dims turn by the angles of row p of cos_sin:
+ *   (u, w) -> (u cos - w sin, w cos + u sin), pair i being dims (i, i + rot/2),
+ *   or (2i, 2i+1) if interleaved != 0
+ * v goes in as it is.  Evaluated in fp64 and rounded once: q_out to `dtype`,
+ * k and v to the cache's values.
+ *   q, k, v        [total_rows][heads or kv_heads][head_dim] of dtype, rows
+ *                  ld_q, ld_k, ld_v elements apart (views of one fused
+ *                  projection are fine); any alignment of dtype's elements
+ *   q_weight, k_weight  float [head_dim] or NULL; eps in [0, 1]
+ *   cos_sin        float [max_position][rot_dim], cos first, or NULL with
+ *                  rot_dim = 0; rot_dim a multiple of 16, at most head_dim
+ *   pages          the layer's pool (written: the rows' tokens only)
+ *   q_out          [total_rows][heads][head_dim], rows ld_qout apart; may be q
+ *                  itself with the same ld
+ *   k_values, v_values  [total_rows][kv_heads][head_dim] of dtype, or both
+ *                  NULL: the values the cache now stands for
+ *   status         int32 [batch]: SV_ROW_OK, SV_ROW_BAD_K, SV_ROW_BAD_PARAM
+ *                  (context_lens[b] < 0 or rows past max_position; rows within
+ *                  it are still processed), SV_ROW_BAD_PAGE (rows whose page is
+ *                  missing are not stored; q_out and the others are)
+ * Rows of no request are left as they were.
+ * Returns SV_ERR_SHAPE for heads not a multiple of kv_heads, heads > 1024, an
+ * ld shorter than its row, and sizes outside the limits above.
+ */
+int spec_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                   int64_t ld_v, int dtype, const float* q_weight, const float* k_weight, float eps,
+                   const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                   const int32_t* cu_seqlens, const int32_t* context_lens, int batch,
+                   int total_rows, int heads, int kv_heads, int head_dim, void* pages,
+                   int64_t num_pages, int page_size, const int32_t* page_table, int64_t ld_table,
+                   void* q_out, int64_t ld_qout, void* k_values, void* v_values, int32_t* status,
+                   void* stream);
+
+/* Bytes of workspace spec_kv_attention needs with these sizes (0 on invalid sizes). */
+size_t spec_kv_attention_workspace_bytes(int dtype, int batch, int max_k, int heads, int kv_heads,
+                                         int head_dim, int max_context, int window, int sinks);
+
+/*
+ * Attention of the verify rows over the cache (decode: k = 0).  Row j of
+ * request b, at position p = context_lens[b] + j, sees the positions
+ *   t <= p, and with window > 0 only t > p - window or t < sinks
+ * and gets out = sum_t softmax_t(scale q.k_t) v_t per head; query head h reads
+ * KV head h / (heads / kv_heads).  Statistics and sums in fp32, K and V exact
+ * as stored, weights rounded to bf16 for bf16 rows (not for fp32 rows), the
+ * result rounded once.  What a row does not see never reaches it, NaN included.
+ *   q, out         [total_rows][heads][head_dim] of dtype, rows ld_q / ld_out apart
+ *   max_k          at most 63; requests with more drafts are SV_ROW_BAD_K
+ *   max_context    bound of context_lens[b] + rows; requests past it are
+ *                  SV_ROW_BAD_PARAM, like context_lens[b] < 0
+ *   scale > 0, window >= 0 (0: off), sinks >= 0 (used with a window)
+ *   status         int32 [batch]: as above, SV_ROW_BAD_PAGE for a page id outside
+ *                  the pool (or past the table row) at a position some row sees
+ *   workspace      spec_kv_attention_workspace_bytes(), any contents; calls that
+ *                  may run at once (two captured graphs among them) need their own
+ * Rows of BAD_PARAM and BAD_PAGE requests are NaN; rows of BAD_K requests and of
+ * no request are left as they were.  Identical inputs give identical bits, and a
+ * request's rows depend on the call's sizes but not on the other requests.
+ */
+int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_seqlens,
+                      const int32_t* context_lens, int batch, int total_rows, int max_k, int heads,
+                      int kv_heads, int head_dim, const void* pages, int64_t num_pages,
+                      int page_size, const int32_t* page_table, int64_t ld_table, int max_context,
+                      float scale, int window, int sinks, void* out, int64_t ld_out,
+                      int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace spec_kv_reserve and spec_kv_compact need (0 on invalid sizes). */
+size_t spec_kv_pages_workspace_bytes(int seqs, int64_t num_pages);
+
+/*
+ * Pages for the rows of a call.  Per request with r = cu[b+1] - cu[b] rows:
+ *   context_lens[b] = seq_lens[b]; seq_lens[b] += r; the table row gets pages
+ *   for the new positions; a last page that is partly filled and shared
+ *   (ref_count > 1) is replaced by a copy of its own, in every layer.
+ * Free pages go out lowest id first, in request order.  A request fails whole
+ * with SV_ROW_NO_PAGES if it needs pages and the needs of requests 0..b (those
+ * that fit their table row) pass what is free, or if its table row is too
+ * short; with SV_ROW_BAD_PAGE if its last page's id is outside the pool; with
+ * SV_ROW_BAD_PARAM for a negative length.  Then context_lens[b] = -1 and
+ * nothing of it changes.
+ *   pages          pool of layer 0, layer l at + l * layer_bytes; page_bytes
+ *                  a page's (multiples of 16)
+ *   workspace      spec_kv_pages_workspace_bytes(), any contents
+ */
+int spec_kv_reserve(const int32_t* cu_seqlens, int batch, int page_size, int32_t* seq_lens,
+                    int32_t* page_table, int64_t ld_table, int32_t* ref_counts, int64_t num_pages,
+                    void* pages, int64_t page_bytes, int layers, int64_t layer_bytes,
+                    int32_t* context_lens, int32_t* status, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * Gives positions back: seq_lens[b] -= rollback[b] (what spec_verify_drain
+ * writes, or a whole sequence's length), and the pages past the new length
+ * leave the table (-1) with their counts down by one.  Requests with
+ * context_lens[b] < 0 are skipped (context_lens may be NULL).  status:
+ * SV_ROW_BAD_PARAM for rollback[b] outside [0, seq_lens[b]] or a length past
+ * the table row (nothing changes), SV_ROW_BAD_PAGE if a page id was outside
+ * the pool (that entry is dropped, the rest is done).
+ */
+int spec_kv_release(const int32_t* rollback, const int32_t* context_lens, int batch, int page_size,
+                    int32_t* seq_lens, int32_t* page_table, int64_t ld_table, int32_t* ref_counts,
+                    int64_t num_pages, int32_t* status, void* stream);
+
+/*
+ * Sequences that start as another one: for each pair, row dst[i] gets the
+ * pages of the first lens[i] positions (lens NULL: all) of row src[i], whose
+ * counts go up; nothing is copied until spec_kv_reserve has to write a shared
+ * page.  Row dst[i] must be empty (seq_lens 0).  status int32 [pairs]:
+ * SV_ROW_BAD_PARAM for a row outside [0, seqs), a dst that is not empty or
+ * that an earlier pair names, a src that is some pair's dst, lens[i] outside
+ * [0, seq_lens[src]]; SV_ROW_BAD_PAGE for a page id outside the pool; the pair
+ * then changes nothing.  pairs in [1, 1024].
+ */
+int spec_kv_fork(const int32_t* src, const int32_t* dst, const int32_t* lens, int pairs, int seqs,
+                 int page_size, int32_t* seq_lens, int32_t* page_table, int64_t ld_table,
+                 int32_t* ref_counts, int64_t num_pages, int32_t* status, void* stream);
+
+/*
+ * Moves the pages in use to the front of the pool: with L pages in use, the
+ * i-th lowest used id >= L moves to the i-th lowest free id < L, in every
+ * layer, and tables and counts follow.  live[0] = L: afterwards pages
+ * L .. num_pages-1 are free (their bytes are left as they were).  Table rows
+ * 0 .. seqs-1 must be all that name pages.
+ */
+int spec_kv_compact(int seqs, int page_size, const int32_t* seq_lens, int32_t* page_table,
+                    int64_t ld_table, int32_t* ref_counts, int64_t num_pages, void* pages,
+                    int64_t page_bytes, int layers, int64_t layer_bytes, int32_t* live,
+                    void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

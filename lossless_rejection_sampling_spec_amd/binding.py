@@ -9,6 +9,7 @@ raises when the library is missing: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import os
 import threading
 
@@ -20,11 +21,13 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 SV_F32, SV_BF16 = 0, 1
 ONEHOT, LOGITS, PROBS, MATCH = 0, 1, 2, 3
 ROW_OK, ROW_NONFINITE, ROW_EMPTY, ROW_BAD_K, ROW_BAD_TOKEN, ROW_BAD_PARAM, ROW_INTERNAL = range(7)
+ROW_NO_PAGES, ROW_BAD_PAGE = 7, 8
 MAX_K = 63
 
 _lib = None
 _lock = threading.Lock()
 _ws_cache: dict = {}
+_kv_ws_cache: dict = {}
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int
@@ -72,6 +75,32 @@ def load_library(path: str) -> ctypes.CDLL:
     L.spec_verify_sampled_noalloc.argtypes = [
         _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
         _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.spec_kv_page_bytes.restype = _sz
+    L.spec_kv_page_bytes.argtypes = [_i32, _i32, _i32]
+    L.spec_kv_append.restype = _i32
+    L.spec_kv_append.argtypes = [
+        _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _i32,
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp,
+        _vp, _vp]
+    L.spec_kv_attention_workspace_bytes.restype = _sz
+    L.spec_kv_attention_workspace_bytes.argtypes = [_i32] * 9
+    L.spec_kv_attention.restype = _i32
+    L.spec_kv_attention.argtypes = [
+        _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i64,
+        _i32, ctypes.c_float, _i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp]
+    L.spec_kv_pages_workspace_bytes.restype = _sz
+    L.spec_kv_pages_workspace_bytes.argtypes = [_i32, _i64]
+    L.spec_kv_reserve.restype = _i32
+    L.spec_kv_reserve.argtypes = [_vp, _i32, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
+                                  _i64, _vp, _vp, _vp, _sz, _vp]
+    L.spec_kv_release.restype = _i32
+    L.spec_kv_release.argtypes = [_vp, _vp, _i32, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _vp]
+    L.spec_kv_fork.restype = _i32
+    L.spec_kv_fork.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _i64, _vp,
+                               _vp]
+    L.spec_kv_compact.restype = _i32
+    L.spec_kv_compact.argtypes = [_i32, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64,
+                                  _vp, _vp, _sz, _vp]
     return L
 
 
@@ -345,6 +374,266 @@ def accounting(cu_seqlens: torch.Tensor, accepted: torch.Tensor, status: torch.T
                                         int(k_low), int(k_high), _ptr(k_next), _ptr(counters),
                                         _stream(dev)))
     return k_next
+
+
+def kv_page_bytes(kv_heads: int, head_dim: int, page_size: int) -> int:
+    """Bytes of one page of one layer (0 on invalid sizes)."""
+    return int(lib().spec_kv_page_bytes(kv_heads, head_dim, page_size))
+
+
+@dataclasses.dataclass
+class KVCache:
+    """The device state of a 4-bit paged KV cache (see include/specverify.h).
+
+    pages       uint8 [layers, num_pages, kv_page_bytes]
+    page_table  int32 [requests, pages per request], shared by all layers
+    seq_lens    int32 [requests]
+    ref_counts  int32 [num_pages], 0 = free
+    """
+    pages: torch.Tensor
+    page_table: torch.Tensor
+    seq_lens: torch.Tensor
+    ref_counts: torch.Tensor
+    page_size: int
+    kv_heads: int
+    head_dim: int
+
+    def __post_init__(self):
+        n = kv_page_bytes(self.kv_heads, self.head_dim, self.page_size)
+        if n == 0:
+            raise ValueError("KVCache: head_dim is 64, 128 or 256, page_size 16, 32, 64, 128 or 256")
+        p = self.pages
+        if (p.dtype != torch.uint8 or not p.is_cuda or p.dim() != 3 or p.shape[2] != n
+                or p.shape[0] < 1 or p.shape[1] < 1 or p.stride()[1:] != (n, 1)
+                or p.stride(0) < p.shape[1] * n and p.shape[0] > 1 or p.data_ptr() % 16
+                or p.stride(0) % 16 and p.shape[0] > 1):
+            raise ValueError(f"pages must be a 16-byte aligned uint8 device tensor "
+                             f"[layers, num_pages, {n}]")
+        t = self.page_table
+        if (t.dtype != torch.int32 or t.device != p.device or t.dim() != 2 or t.shape[0] < 1
+                or t.shape[1] < 1 or t.stride(1) != 1 or t.stride(0) < t.shape[1]):
+            raise ValueError("page_table must be an int32 device tensor [requests, pages], "
+                             "unit stride along a row")
+        _check_vec(self.seq_lens, "seq_lens", torch.int32, t.shape[0])
+        _check_vec(self.ref_counts, "ref_counts", torch.int32, p.shape[1])
+        if self.seq_lens.device != p.device or self.ref_counts.device != p.device:
+            raise ValueError("seq_lens and ref_counts must be on the pages' device")
+
+    @classmethod
+    def create(cls, *, layers: int, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
+               requests: int, max_context: int, device) -> "KVCache":
+        """An empty cache: every page free, every request of length 0."""
+        n = kv_page_bytes(kv_heads, head_dim, page_size)
+        if n == 0:
+            raise ValueError("KVCache: head_dim is 64, 128 or 256, page_size 16, 32, 64, 128 or 256")
+        width = -(-int(max_context) // page_size)
+        return cls(pages=torch.zeros(layers, num_pages, n, dtype=torch.uint8, device=device),
+                   page_table=torch.full((requests, width), -1, dtype=torch.int32, device=device),
+                   seq_lens=torch.zeros(requests, dtype=torch.int32, device=device),
+                   ref_counts=torch.zeros(num_pages, dtype=torch.int32, device=device),
+                   page_size=page_size, kv_heads=kv_heads, head_dim=head_dim)
+
+
+def _kv_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
+    """Scratch of the cache calls, kept per (device, current stream): calls on
+    one stream are ordered, so they share one.  While a graph is captured the
+    call gets memory of the graph's own, so two graphs never share any.  An
+    outgrown buffer goes back to torch's allocator, which reuses it on its own
+    stream only, behind the work that still reads it."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    ws = _kv_ws_cache.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        _kv_ws_cache[key] = ws
+    return ws
+
+
+def _kv_batch(cache: KVCache, cu_seqlens: torch.Tensor) -> int:
+    batch = cu_seqlens.numel() - 1
+    _check_vec(cu_seqlens, "cu_seqlens", torch.int32, 2)
+    if batch > cache.page_table.shape[0]:
+        raise ValueError(f"{batch} requests, but the page table has {cache.page_table.shape[0]}")
+    return batch
+
+
+def _check_heads(t: torch.Tensor, name: str, cache: KVCache, heads: int | None = None) -> None:
+    if (t.dim() != 3 or t.shape[2] != cache.head_dim or t.stride(2) != 1
+            or t.shape[1] > 1 and t.stride(1) != cache.head_dim or t.device != cache.pages.device):
+        raise ValueError(f"{name} must be [rows, heads, {cache.head_dim}] on the cache's device, "
+                         "heads side by side")
+    if heads is not None and t.shape[1] != heads:
+        raise ValueError(f"{name} must have {heads} heads")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Elements from row to row of [rows, heads, dim] (a single row has no stride of its own)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def kv_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+              cu_seqlens: torch.Tensor, context_lens: torch.Tensor, *, layer: int = 0,
+              q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+              eps: float = 1e-6, cos_sin: torch.Tensor | None = None, interleaved: bool = False,
+              out: torch.Tensor | None = None, want_values: bool = False):
+    """spec_kv_append: head norms, rotation and the 4-bit cache write of the
+    call's rows in one pass.
+
+    q [rows, heads, D], k and v [rows, kv_heads, D] (float32 or bfloat16, views
+    of one fused projection are fine); q_weight, k_weight float32 [D] or None;
+    cos_sin float32 [positions, rot_dim], cos first, or None; `out` may be q.
+
+    Returns (q_out, status[B]), and with want_values (q_out, status, k_values,
+    v_values): the values the cache now stands for."""
+    dev = cache.pages.device
+    batch = _kv_batch(cache, cu_seqlens)
+    _check_heads(q, "q", cache)
+    for t, name in ((k, "k"), (v, "v")):
+        _check_heads(t, name, cache, cache.kv_heads)
+        if t.dtype != q.dtype or t.shape[0] != q.shape[0]:
+            raise ValueError(f"{name} must have q's dtype and rows")
+    _check_vec(context_lens, "context_lens", torch.int32, batch)
+    _check_vec(q_weight, "q_weight", torch.float32, cache.head_dim)
+    _check_vec(k_weight, "k_weight", torch.float32, cache.head_dim)
+    rot = positions = 0
+    if cos_sin is not None:
+        _check_vec(cos_sin, "cos_sin", torch.float32)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [positions, rot_dim]")
+        positions, rot = cos_sin.shape
+    if not 0 <= layer < cache.pages.shape[0]:
+        raise ValueError(f"layer {layer} of {cache.pages.shape[0]}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _check_heads(out, "out", cache, q.shape[1])
+    if out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must match q's shape and dtype")
+    status = torch.empty(batch, dtype=torch.int32, device=dev)
+    kv = [torch.empty(k.shape, dtype=k.dtype, device=dev) if want_values else None
+          for _ in range(2)]
+    with torch.cuda.device(dev):
+        _raise(lib().spec_kv_append(
+            _ptr(q), _ld(q), _ptr(k), _ld(k), _ptr(v), _ld(v), _dtype_code(q), _ptr(q_weight),
+            _ptr(k_weight), float(eps), _ptr(cos_sin), positions, rot, int(interleaved),
+            _ptr(cu_seqlens), _ptr(context_lens), batch, q.shape[0], q.shape[1], cache.kv_heads,
+            cache.head_dim, _ptr(cache.pages[layer]), cache.pages.shape[1], cache.page_size,
+            _ptr(cache.page_table), cache.page_table.stride(0), _ptr(out), _ld(out), _ptr(kv[0]),
+            _ptr(kv[1]), _ptr(status), _stream(dev)))
+    return (out, status, *kv) if want_values else (out, status)
+
+
+def kv_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor,
+                 context_lens: torch.Tensor, *, max_k: int, max_context: int, layer: int = 0,
+                 scale: float | None = None, window: int = 0, sinks: int = 0,
+                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """spec_kv_attention: attention of the k+1 verify rows of each request over
+    the cache (k = 0: decode).  scale defaults to head_dim ** -0.5.  Returns
+    (out [rows, heads, D], status[B])."""
+    dev = cache.pages.device
+    batch = _kv_batch(cache, cu_seqlens)
+    _check_heads(q, "q", cache)
+    _check_vec(context_lens, "context_lens", torch.int32, batch)
+    if not 0 <= layer < cache.pages.shape[0]:
+        raise ValueError(f"layer {layer} of {cache.pages.shape[0]}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _check_heads(out, "out", cache, q.shape[1])
+    if out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must match q's shape and dtype")
+    status = torch.empty(batch, dtype=torch.int32, device=dev)
+    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+    need = int(lib().spec_kv_attention_workspace_bytes(
+        _dtype_code(q), batch, max_k, q.shape[1], cache.kv_heads, cache.head_dim, max_context,
+        window, sinks))
+    if need == 0:
+        raise ValueError("invalid sizes for spec_kv_attention")
+    with torch.cuda.device(dev):
+        ws = _kv_workspace(dev, need) if workspace is None else workspace
+        _raise(lib().spec_kv_attention(
+            _ptr(q), _ld(q), _dtype_code(q), _ptr(cu_seqlens), _ptr(context_lens), batch,
+            q.shape[0], max_k, q.shape[1], cache.kv_heads, cache.head_dim,
+            _ptr(cache.pages[layer]), cache.pages.shape[1], cache.page_size,
+            _ptr(cache.page_table), cache.page_table.stride(0), max_context, scale, window, sinks,
+            _ptr(out), _ld(out), _ptr(status), _ptr(ws), ws.numel(), _stream(dev)))
+    return out, status
+
+
+def _pages_workspace(cache: KVCache, seqs: int, workspace):
+    need = int(lib().spec_kv_pages_workspace_bytes(seqs, cache.pages.shape[1]))
+    if need == 0:
+        raise ValueError("invalid sizes: at most 1024 requests and 2^24 pages")
+    return _kv_workspace(cache.pages.device, need) if workspace is None else workspace
+
+
+def kv_reserve(cache: KVCache, cu_seqlens: torch.Tensor, *, workspace: torch.Tensor | None = None):
+    """spec_kv_reserve: pages for the rows of a call (shared last pages are
+    copied).  Returns (context_lens[B], status[B])."""
+    dev = cache.pages.device
+    batch = _kv_batch(cache, cu_seqlens)
+    context = torch.empty(batch, dtype=torch.int32, device=dev)
+    status = torch.empty(batch, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        ws = _pages_workspace(cache, batch, workspace)
+        _raise(lib().spec_kv_reserve(
+            _ptr(cu_seqlens), batch, cache.page_size, _ptr(cache.seq_lens),
+            _ptr(cache.page_table), cache.page_table.stride(0), _ptr(cache.ref_counts),
+            cache.pages.shape[1], _ptr(cache.pages), cache.pages.shape[2], cache.pages.shape[0],
+            cache.pages.stride(0), _ptr(context), _ptr(status), _ptr(ws), ws.numel(),
+            _stream(dev)))
+    return context, status
+
+
+def kv_release(cache: KVCache, rollback: torch.Tensor, context_lens: torch.Tensor | None = None):
+    """spec_kv_release: gives positions back (rollback as drain returns it, with
+    the context_lens of the reserve before it).  Returns status[B]."""
+    dev = cache.pages.device
+    batch = rollback.numel()
+    _check_vec(rollback, "rollback", torch.int32, 1)
+    _check_vec(context_lens, "context_lens", torch.int32, batch)
+    if batch > cache.page_table.shape[0]:
+        raise ValueError(f"{batch} requests, but the page table has {cache.page_table.shape[0]}")
+    status = torch.empty(batch, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _raise(lib().spec_kv_release(
+            _ptr(rollback), _ptr(context_lens), batch, cache.page_size, _ptr(cache.seq_lens),
+            _ptr(cache.page_table), cache.page_table.stride(0), _ptr(cache.ref_counts),
+            cache.pages.shape[1], _ptr(status), _stream(dev)))
+    return status
+
+
+def kv_fork(cache: KVCache, src: torch.Tensor, dst: torch.Tensor,
+            lens: torch.Tensor | None = None):
+    """spec_kv_fork: row dst[i] starts as the first lens[i] positions (None: all)
+    of row src[i], sharing its pages.  Returns status[pairs]."""
+    dev = cache.pages.device
+    pairs = src.numel()
+    _check_vec(src, "src", torch.int32, 1)
+    _check_vec(dst, "dst", torch.int32, pairs)
+    _check_vec(lens, "lens", torch.int32, pairs)
+    status = torch.empty(pairs, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _raise(lib().spec_kv_fork(
+            _ptr(src), _ptr(dst), _ptr(lens), pairs, cache.page_table.shape[0], cache.page_size,
+            _ptr(cache.seq_lens), _ptr(cache.page_table), cache.page_table.stride(0),
+            _ptr(cache.ref_counts), cache.pages.shape[1], _ptr(status), _stream(dev)))
+    return status
+
+
+def kv_compact(cache: KVCache, *, workspace: torch.Tensor | None = None):
+    """spec_kv_compact: moves the pages in use to the front of the pool.
+    Returns live (int32 [1]): pages live .. num_pages-1 are free afterwards."""
+    dev = cache.pages.device
+    live = torch.empty(1, dtype=torch.int32, device=dev)
+    seqs = cache.page_table.shape[0]
+    with torch.cuda.device(dev):
+        ws = _pages_workspace(cache, seqs, workspace)
+        _raise(lib().spec_kv_compact(
+            seqs, cache.page_size, _ptr(cache.seq_lens), _ptr(cache.page_table),
+            cache.page_table.stride(0), _ptr(cache.ref_counts), cache.pages.shape[1],
+            _ptr(cache.pages), cache.pages.shape[2], cache.pages.shape[0], cache.pages.stride(0),
+            _ptr(live), _ptr(ws), ws.numel(), _stream(dev)))
+    return live
 
 
 def workload_tensors(w, device) -> dict:

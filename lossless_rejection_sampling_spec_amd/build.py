@@ -10,7 +10,8 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = [os.path.join(PKG, "csrc", "specverify.hip"), os.path.join(PKG, "csrc", "drain.hip")]
+SRC = [os.path.join(PKG, "csrc", name)
+       for name in ("specverify.hip", "drain.hip", "kvcache.hip", "kvattn.hip")]
 INC = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecverify.so")
 # Test-only build: every wait between workgroups gives up after one poll, so

@@ -1,0 +1,733 @@
+// kvattn.hip -- spec_kv_attention: the k+1 verify rows of each request over
+// the 4-bit paged cache (include/specverify.h states the operator).
+//
+// For request b, row j (position c+j) and query head h over KV head h/G:
+//   out = sum_t exp(scale q.k_t - m) v_t / sum_t exp(scale q.k_t - m)
+// over the visible t, in one pass with a running maximum m and sum.
+//
+// One workgroup (4 waves) takes one KV head, up to 16*MT of the R = (k+1)*G
+// rows that share it, and one chunk of the context; its waves take every
+// fourth tile of 32 tokens and work alone until the end, where their partial
+// results are joined through LDS.  A wave computes
+//   S^T[token][row] = K Q^T   then   O^T[dim][row] += V^T P^T
+// with v_mfma_f32_16x16x32_bf16.  With tokens as the rows of S^T, a lane holds
+// the scores of ONE query row (its column), for 8 tokens that are exactly the
+// 8 contraction entries of its P^T operand: softmax statistics are per lane
+// and the probabilities go from accumulator to operand without LDS or
+// shuffles.  K and V come as e2m1 codes and are widened to bf16 by the
+// hardware conversion, which applies the power-of-two block scale (exact).
+//
+// What bounds it: HBM reads of the cache (D*17/16 bytes per token and KV head)
+// as long as R <= 32; per 32-token tile a wave issues D*2/32*MT MFMAs and about
+// 120 + 110*MT vector instructions (D=128).
+
+#include "kv_common.h"
+
+namespace svk {
+
+constexpr int TILE = 32;          // tokens per wave step
+constexpr int WAVES = 4;
+constexpr float LOG2E = 1.44269504088896340736f;
+// the running maximum is raised only when a score passes it by this much (in
+// powers of two): until then weights stay below 2^8, which fp32 sums and bf16
+// weights hold with the same relative precision
+constexpr float RAISE = 8.0f;
+
+struct AttnArgs {
+  const void* q;
+  int64_t ld_q;
+  const int32_t* cu;
+  const int32_t* ctx;
+  int batch, total_rows, max_k, heads, kv_heads;
+  const uint8_t* pages;
+  int64_t num_pages;
+  int page, page_log2;
+  const int32_t* table;
+  int64_t ld_table;
+  int max_context;
+  float scale;
+  int window, sinks;
+  void* out;
+  int64_t ld_out;
+  int32_t* status;
+  float* part;          // chunk partials: [item][rows][D], then [item][rows][2] (max, sum)
+  int chunks, chunk_tiles, row_blocks;
+};
+
+// The tiles a request reads: tokens that some row sees, in steps of 32.
+struct Span {
+  int n;            // positions up to the last row's, exclusive
+  int first;        // first position row 0's window shows
+  int sink_tiles, tile0, tiles;
+};
+
+__device__ __forceinline__ Span span_of(int ctx, int rows, int window, int sinks) {
+  Span s;
+  s.n = ctx + rows;
+  s.first = window > 0 ? max(0, ctx - window + 1) : 0;
+  s.tile0 = s.first / TILE;
+  s.sink_tiles = min((sinks + TILE - 1) / TILE, s.tile0);
+  s.tiles = s.sink_tiles + (s.n - 1) / TILE - s.tile0 + 1;
+  return s;
+}
+
+// SV_ROW_* of a request by its numbers alone (pages are checked where read).
+__device__ __forceinline__ int request_status(const AttnArgs& a, int b, int broken, int& row0,
+                                              int& rows, int& ctx) {
+  row0 = rows = ctx = 0;
+  if (b >= broken) return SV_ROW_BAD_K;
+  row0 = a.cu[b];
+  rows = a.cu[b + 1] - row0;
+  if (rows < 1 || rows > a.max_k + 1) return SV_ROW_BAD_K;
+  ctx = a.ctx[b];
+  if (ctx < 0 || (int64_t)ctx + rows > a.max_context) return SV_ROW_BAD_PARAM;
+  return SV_ROW_OK;
+}
+
+__device__ __forceinline__ bool page_needed(const Span& s, int slot, int page_log2, int sinks) {
+  const int t0 = slot << page_log2, t1 = t0 + (1 << page_log2);
+  return t0 < s.n && (t1 > s.first || t0 < sinks);
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f32<__bf16>(__bf16 x) { return (float)x; }
+
+// Combine over the four lanes that hold one query row (lanes l, l^16, l^32, l^48).
+__device__ __forceinline__ float row_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float row_sum(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+// A scale byte as the float 2^(byte-127).
+__device__ __forceinline__ float scale_of(uint32_t word, int byte) {
+  return __builtin_bit_cast(float, ((word >> (8 * byte)) & 255u) << 23);
+}
+// Bit 7 of every byte that is 0xFF.
+__device__ __forceinline__ uint32_t ff_bytes(uint32_t x) {
+  return (~x - 0x01010101u) & x & 0x80808080u;
+}
+
+template <int BYTE>
+__device__ __forceinline__ uint32_t widen(uint32_t word, float scale) {
+  return __builtin_bit_cast(uint32_t,
+                            __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, BYTE));
+}
+
+// One wave's operands of a tile.
+template <int D>
+struct Tile {
+  uint32_t k[2][D / 32];       // two tokens' D/4 dims
+  uint32_t ks[(D + 127) / 128][2];   // K scales of 8 tokens, per block of the lane's dims
+  uint32_t v[D / 16];          // 8 tokens' D/16 dims
+  uint32_t vs[2];              // V scales of the 8 tokens
+};
+
+template <int D, int MT, typename T>
+struct Attn {
+  static constexpr int STEPS = D / 32;           // contraction steps of K Q^T
+  static constexpr int FR = D / 16;              // output fragments of 16 dims
+  // fp32 queries and weights are split into three bf16 terms (3 x 8 bits hold
+  // fp32's 24): products with the exact bf16 K and V then lose nothing
+  static constexpr int NT = sizeof(T) == 4 ? 3 : 1;
+
+  bf16x8 q[MT][STEPS][NT];
+  f32x4 o[MT][FR];
+  float m[MT], l[MT];     // running max of raw scores; this lane's part of the sum
+
+  static __device__ __forceinline__ void split(float x, __bf16* t) {
+    float r = x;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      t[i] = (__bf16)r;
+      r -= (float)t[i];
+    }
+  }
+
+  __device__ __forceinline__ void init(const AttnArgs& a, int row0, int R, int G, int h, int rb) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt] = -INFINITY;
+      l[mt] = 0.f;
+#pragma unroll
+      for (int f = 0; f < FR; ++f) o[mt][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int r = (rb * MT + mt) * 16 + n;
+      const int j = r / G, hq = h * G + r - j * G;
+      const T* src = (const T*)a.q + (int64_t)(row0 + j) * a.ld_q + (int64_t)hq * D + g * (D / 4);
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        T x[8];
+        if (r < R) __builtin_memcpy(x, src + 8 * s, sizeof(x));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          __bf16 t[NT];
+          if constexpr (NT == 1) t[0] = r < R ? x[i] : (__bf16)0.f;
+          else split(r < R ? to_f32<T>(x[i]) : 0.f, t);
+#pragma unroll
+          for (int k = 0; k < NT; ++k) q[mt][s][k][i] = t[k];
+        }
+      }
+    }
+  }
+
+  // p0, p1: units of the tile's first and second 16 tokens.
+  static __device__ __forceinline__ void load(const AttnArgs& a, Tile<D>& t, const uint8_t* p0,
+                                              const uint8_t* p1, int base) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int P = a.page;
+    const uint8_t* pk = (n & 8) ? p1 : p0;
+    const uint8_t* pv = (g & 2) ? p1 : p0;
+    const int gk = ((base + 8 * (n >> 2)) & (P - 1)) >> 3;    // group of 8 tokens in its page
+    const int gv = ((base + 8 * g) & (P - 1)) >> 3;
+    const uint8_t* k0 = pk + (8 * gk + (n & 3)) * (D / 2) + g * (D / 8);
+    constexpr int KA = D == 64 ? 8 : 16;
+    __builtin_memcpy(t.k[0], __builtin_assume_aligned(k0, KA), D / 8);
+    __builtin_memcpy(t.k[1], __builtin_assume_aligned(k0 + 4 * (D / 2), KA), D / 8);
+    __builtin_memcpy(t.ks, __builtin_assume_aligned(
+        pk + off_ks(P, D) + gk * (D / 4) + (g * (D / 4) / 32) * 8, 8), sizeof(t.ks));
+    __builtin_memcpy(t.v, __builtin_assume_aligned(
+        pv + off_v(P, D) + gv * (4 * D) + n * (D / 4), 16), D / 4);
+    __builtin_memcpy(t.vs, __builtin_assume_aligned(
+        pv + off_vs(P, D) + gv * (D / 4) + (n * D / 512) * 8, 8), 8);
+  }
+
+  // masked: some row does not see some token of the tile.
+  template <bool MASKED>
+  __device__ __forceinline__ void step(const AttnArgs& a, Tile<D>& t, int base, int ctx, int R,
+                                       int G, int rb, const Span& sp, float c) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    auto sees = [&](int tok, int pos) {
+      return tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
+    };
+    if constexpr (MASKED) {
+      // tokens that no row sees (past the end, or between sinks and window) may
+      // hold anything: their V becomes finite, so that a weight of 0 keeps it out
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int tok = base + 8 * g + i;
+        if (tok >= sp.n || (tok < sp.first && tok >= a.sinks)) {
+          const int sh = 8 * (i & 3);
+          t.vs[i >> 2] = (t.vs[i >> 2] & ~(255u << sh)) | (127u << sh);
+        }
+      }
+    }
+    // scores: s[tile half][mt], lane: row n, tokens base + 8g + 4*half + r
+    f32x4 s[2][MT];
+    uint32_t kbad = 0;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[hf][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        const uint32_t sb = (t.ks[st / 4][hf] >> (8 * (n & 3))) & 255u;
+        if (st % 4 == 0 && sb == 255u) kbad |= 1u << hf;
+        const float sc = __builtin_bit_cast(float, sb << 23);
+        const uint32_t w = t.k[hf][st];
+        u32x4 kb;
+        kb[0] = widen<0>(w, sc);
+        kb[1] = widen<1>(w, sc);
+        kb[2] = widen<2>(w, sc);
+        kb[3] = widen<3>(w, sc);
+        const bf16x8 ka = __builtin_bit_cast(bf16x8, kb);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int k = NT - 1; k >= 0; --k)
+            s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, q[mt][st][k], s[hf][mt], 0, 0, 0);
+      }
+    }
+    if (__any(kbad != 0)) {
+      // a K block stored as NaN (scale 255): the token's scores are NaN
+      uint32_t any = kbad | (uint32_t)__shfl_xor((int)kbad, 16);
+      any |= (uint32_t)__shfl_xor((int)any, 32);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t f = (uint32_t)__shfl((int)any, 4 * g + r);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          if (f >> hf & 1)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) s[hf][mt][r] = __builtin_nanf("");
+      }
+    }
+    bf16x8 p[MT][NT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int pos = ctx + ((rb * MT + mt) * 16 + n) / G;
+      if constexpr (MASKED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!sees(base + 8 * g + i, pos)) s[i >> 2][mt][i & 3] = -INFINITY;
+      }
+      float mx = fmaxf(fmaxf(s[0][mt][0], s[0][mt][1]), fmaxf(s[0][mt][2], s[0][mt][3]));
+      mx = fmaxf(mx, fmaxf(fmaxf(s[1][mt][0], s[1][mt][1]), fmaxf(s[1][mt][2], s[1][mt][3])));
+      // (a first visible score raises -inf; a row that has seen nothing stays there)
+      if (__any((mx - m[mt]) * c > RAISE)) {
+        const float nm = fmaxf(m[mt], row_max(mx));
+        const float w = nm == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[mt] - nm) * c);
+        l[mt] *= w;
+#pragma unroll
+        for (int f = 0; f < FR; ++f) o[mt][f] *= w;
+        m[mt] = nm;
+      }
+      const float mc = m[mt] == -INFINITY ? 0.f : m[mt] * c;
+      float e[8], sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc));
+        sum += e[i];
+      }
+      l[mt] += sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        __bf16 w[NT];
+        split(e[i], w);
+#pragma unroll
+        for (int k = 0; k < NT; ++k) p[mt][k][i] = w[k];
+      }
+    }
+    const uint32_t vbad = ff_bytes(t.vs[0]) | ff_bytes(t.vs[1]);
+    if (__any(vbad != 0)) nan_values(a, t, base, ctx, G, rb);
+    float vsc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) vsc[i] = scale_of(t.vs[i >> 2], i & 3);
+    // fragment pair c2: dims 2*c2 and 2*c2+1 of every lane's D/16
+#pragma unroll
+    for (int c2 = 0; c2 < FR / 2; ++c2) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int byte = i * (D / 32) + c2;
+        const uint32_t x = t.v[byte / 4];
+        w[i] = byte % 4 == 0 ? widen<0>(x, vsc[i]) : byte % 4 == 1 ? widen<1>(x, vsc[i])
+             : byte % 4 == 2 ? widen<2>(x, vsc[i]) : widen<3>(x, vsc[i]);
+      }
+      u32x4 lo, hi;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x05040100u);
+        hi[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x07060302u);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = NT - 1; k >= 0; --k) {
+          o[mt][2 * c2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, lo), p[mt][k], o[mt][2 * c2], 0, 0, 0);
+          o[mt][2 * c2 + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, hi), p[mt][k], o[mt][2 * c2 + 1], 0, 0, 0);
+        }
+    }
+  }
+
+  // V blocks stored as NaN: rows that see the token get NaN in those dims, the
+  // others must not (0 * NaN), so the block is made finite for the product.
+  __device__ __forceinline__ void nan_values(const AttnArgs& a, Tile<D>& t, int base, int ctx, int G,
+                                          int rb) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+#pragma nounroll
+    for (int src = 0; src < 64; ++src) {
+      if (src & 15 & (16 / STEPS - 1)) continue;        // one lane per block of 32 dims
+      const int block = (src & 15) / (16 / STEPS);
+#pragma nounroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w = (uint32_t)__builtin_amdgcn_readlane((int)(i < 4 ? t.vs[0] : t.vs[1]), src);
+        if (((w >> (8 * (i & 3))) & 255u) != 255u) continue;
+        const int tok = base + 8 * (src >> 4) + i;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int pos = ctx + ((rb * MT + mt) * 16 + n) / G;
+          const bool sees =
+              tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int mine = (g * (D / 4) + r * (D / 16)) / 32;
+            if (sees && mine == block)
+#pragma unroll
+              for (int f = 0; f < FR; ++f) o[mt][f][r] = __builtin_nanf("");
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t f = ff_bytes(t.vs[k]);               // 0x80 in the bytes that are 255
+      t.vs[k] &= ~f;                                      // 255 -> 127
+    }
+  }
+
+  static constexpr int WORDS = MT * (FR * 4 + 2);
+
+  __device__ __forceinline__ void put(float* lds) const {
+    const int lane = threadIdx.x & 63;
+    int w = 0;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      lds[64 * w++ + lane] = m[mt];
+      lds[64 * w++ + lane] = l[mt];
+#pragma unroll
+      for (int f = 0; f < FR; ++f)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) lds[64 * w++ + lane] = o[mt][f][r];
+    }
+  }
+  __device__ __forceinline__ void join(const float* lds, float c) {
+    const int lane = threadIdx.x & 63;
+    int w = 0;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const float m2 = lds[64 * w++ + lane], l2 = lds[64 * w++ + lane];
+      const float nm = fmaxf(m[mt], m2);
+      const float w1 = m[mt] == nm ? 1.f : __builtin_amdgcn_exp2f((m[mt] - nm) * c);
+      const float w2 = m2 == nm ? 1.f : __builtin_amdgcn_exp2f((m2 - nm) * c);
+      m[mt] = nm;
+      l[mt] = l[mt] * w1 + l2 * w2;
+#pragma unroll
+      for (int f = 0; f < FR; ++f)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[mt][f][r] = o[mt][f][r] * w1 + lds[64 * w++ + lane] * w2;
+    }
+  }
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* dst, const float* x) {
+  T y[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) y[i] = (T)x[i];
+  __builtin_memcpy(dst, y, sizeof(y));
+}
+
+template <int D, int MT, typename T>
+__global__ __launch_bounds__(256, (MT * D >= 512 ? 1 : 2)) void k_attn(AttnArgs a) {
+  using A = Attn<D, MT, T>;
+  __shared__ float lds[2][A::WORDS * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int broken = first_broken(a.cu, a.batch, a.total_rows);
+  const int G = a.heads / a.kv_heads;
+  const int items = a.batch * a.kv_heads * a.row_blocks * a.chunks;
+  int row0, rows, ctx;
+
+  if ((int)blockIdx.x >= items) {       // the last workgroups write the statuses, a wave each
+    const int b = ((int)blockIdx.x - items) * WAVES + wave;
+    if (b >= a.batch) return;
+    int st = request_status(a, b, broken, row0, rows, ctx);
+    if (st == SV_ROW_OK) {
+      const Span sp = span_of(ctx, rows, a.window, a.sinks);
+      const int32_t* tab = a.table + (int64_t)b * a.ld_table;
+      bool bad = false;
+      for (int s = lane; s <= (sp.n - 1) >> a.page_log2; s += 64)
+        if (page_needed(sp, s, a.page_log2, a.sinks))
+          bad |= s >= a.ld_table || (uint32_t)tab[s] >= (uint64_t)a.num_pages;
+      if (__any(bad)) st = SV_ROW_BAD_PAGE;
+    }
+    if (lane == 0) a.status[b] = st;
+    return;
+  }
+
+  // chunk is the slowest index: first chunks, which every request has, start first
+  int it = blockIdx.x;
+  const int rb = it % a.row_blocks;
+  it /= a.row_blocks;
+  const int h = it % a.kv_heads;
+  it /= a.kv_heads;
+  const int b = it % a.batch, chunk = it / a.batch;
+  const int st = request_status(a, b, broken, row0, rows, ctx);
+  if (st == SV_ROW_BAD_K) return;
+  const int R = rows * G;
+  if (rb * MT * 16 >= R) return;
+  const Span sp = span_of(ctx, rows, a.window, a.sinks);
+  const int tbegin = chunk * a.chunk_tiles;
+  if (st == SV_ROW_OK ? tbegin >= sp.tiles : chunk > 0) return;
+  const int tend = min(tbegin + a.chunk_tiles, sp.tiles);
+  const float c = a.scale * LOG2E;
+
+  A x;
+  x.init(a, row0, R, G, h, rb);
+  bool bad = st != SV_ROW_OK;
+  if (!bad) {
+    const int32_t* tab = a.table + (int64_t)b * a.ld_table;
+    const int64_t unit = unit_bytes(a.page, D), page_bytes = unit * a.kv_heads;
+    const uint8_t* pool = a.pages + h * unit;
+    auto base_of = [&](int i) {
+      return (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.tile0) * TILE;
+    };
+    auto unit_at = [&](int tok) -> const uint8_t* {
+      const int slot = tok >> a.page_log2;
+      int64_t id = 0;
+      if (page_needed(sp, slot, a.page_log2, a.sinks)) {
+        if (slot < a.ld_table) id = (uint32_t)tab[slot];
+        if (slot >= a.ld_table || id >= a.num_pages) {
+          bad = true;
+          id = 0;
+        }
+      }
+      return pool + id * page_bytes;
+    };
+    auto fetch = [&](Tile<D>& t, int i) {
+      const int base = base_of(i);
+      A::load(a, t, unit_at(base), unit_at(base + 16), base);
+    };
+    auto work = [&](Tile<D>& t, int i) {
+      const int base = base_of(i);
+      const bool masked = base + TILE - 1 > ctx ||
+                          (a.window > 0 && base <= ctx + rows - 1 - a.window && base + TILE > a.sinks);
+      if (masked) x.template step<true>(a, t, base, ctx, R, G, rb, sp, c);
+      else x.template step<false>(a, t, base, ctx, R, G, rb, sp, c);
+    };
+    Tile<D> t0, t1;
+    int i = tbegin + wave;
+    if (i < tend) fetch(t0, i);
+    while (i < tend) {
+      if (i + WAVES < tend) fetch(t1, i + WAVES);
+      work(t0, i);
+      i += WAVES;
+      if (i >= tend) break;
+      if (i + WAVES < tend) fetch(t0, i + WAVES);
+      work(t1, i);
+      i += WAVES;
+    }
+  }
+  // a page id out of range: the request's rows are NaN
+  if (bad)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) x.l[mt] = __builtin_nanf("");
+
+  // join the four waves: 2, 3 into 0, 1, then 1 into 0
+  if (wave >= 2) x.put(lds[wave - 2]);
+  __syncthreads();
+  if (wave < 2) x.join(lds[wave], c);
+  __syncthreads();
+  if (wave == 1) x.put(lds[0]);
+  __syncthreads();
+  if (wave != 0) return;
+  x.join(lds[0], c);
+
+  const int n = lane & 15, g = lane >> 4;
+  const bool whole = st != SV_ROW_OK || sp.tiles <= a.chunk_tiles;
+  // this item's place among the partials
+  const int64_t item = (((int64_t)chunk * a.batch + b) * a.kv_heads + h) * a.row_blocks + rb;
+  float* part = a.part + item * (MT * 16) * D;
+  float* stat = a.part + (int64_t)items * (MT * 16) * D + item * (MT * 16) * 2;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const float sum = row_sum(x.l[mt]);
+    const int r = (rb * MT + mt) * 16 + n;
+    if (r >= R) continue;
+    float y[D / 4];
+    const float inv = whole ? 1.f / sum : 1.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int f = 0; f < A::FR; ++f) y[k * A::FR + f] = x.o[mt][f][k] * inv;
+    if (whole) {
+      const int j = r / G, hq = h * G + r - j * G;
+      store_row<T, D / 4>((T*)a.out + (int64_t)(row0 + j) * a.ld_out + (int64_t)hq * D + g * (D / 4), y);
+    } else {
+      store_row<float, D / 4>(part + (mt * 16 + n) * D + g * (D / 4), y);
+      if (g == 0) {
+        stat[(mt * 16 + n) * 2] = x.m[mt];
+        stat[(mt * 16 + n) * 2 + 1] = sum;
+      }
+    }
+  }
+}
+
+// Joins the chunks of requests longer than one: a wave per row.
+template <int D, int MT, typename T>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int broken = first_broken(a.cu, a.batch, a.total_rows);
+  const int G = a.heads / a.kv_heads;
+  constexpr int PER = MT * 16 / WAVES;      // workgroups of one item
+  int it = blockIdx.x;
+  const int local = (it % PER) * WAVES + (threadIdx.x >> 6);
+  it /= PER;
+  const int first = it;                      // its item of chunk 0
+  const int rb = it % a.row_blocks;
+  it /= a.row_blocks;
+  const int h = it % a.kv_heads, b = it / a.kv_heads;
+  int row0, rows, ctx;
+  if (request_status(a, b, broken, row0, rows, ctx) != SV_ROW_OK) return;
+  const Span sp = span_of(ctx, rows, a.window, a.sinks);
+  const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+  const int r = rb * MT * 16 + local;
+  if (n < 2 || r >= rows * G) return;
+  const int64_t per_chunk = (int64_t)a.batch * a.kv_heads * a.row_blocks;
+  const float* part = a.part + ((int64_t)first * (MT * 16) + local) * D;
+  const float* stat = a.part + per_chunk * a.chunks * (MT * 16) * D + ((int64_t)first * (MT * 16) + local) * 2;
+  const float c = a.scale * LOG2E;
+  float m = -INFINITY;
+  for (int k = lane; k < n; k += 64) m = fmaxf(m, stat[k * per_chunk * (MT * 16) * 2]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  constexpr int E = D / 64;                  // dims per lane
+  float acc[E] = {}, sum = 0.f;
+  for (int k = 0; k < n; ++k) {
+    const float mk = stat[k * per_chunk * (MT * 16) * 2], lk = stat[k * per_chunk * (MT * 16) * 2 + 1];
+    const float w = mk == m ? 1.f : __builtin_amdgcn_exp2f((mk - m) * c);
+    sum += lk * w;
+    float y[E];
+    __builtin_memcpy(y, part + k * per_chunk * (MT * 16) * D + lane * E, sizeof(y));
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += y[e] * w;
+  }
+  const int j = r / G, hq = h * G + r - j * G;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] /= sum;
+  store_row<T, E>((T*)a.out + (int64_t)(row0 + j) * a.ld_out + (int64_t)hq * D + lane * E, acc);
+}
+
+// ---- host side
+
+struct Plan {
+  int mt, row_blocks, chunks, chunk_tiles;
+  size_t bytes;
+};
+
+// Rows per workgroup and the split over the context, by the call's sizes alone.
+static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, int d,
+                    int max_context, int window, int sinks, Plan& p) {
+  const int64_t R = (int64_t)(max_k + 1) * (heads / kv_heads);
+  const int most = dtype == SV_F32 ? (d == 256 ? 1 : 2) : (d == 256 ? 2 : 4);
+  p.mt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+  if (p.mt > most) p.mt = most;
+  p.row_blocks = (int)((R + p.mt * 16 - 1) / (p.mt * 16));
+  // tiles a request can have: two borders more than its tokens fill
+  int64_t tokens = max_context;
+  if (window > 0) {
+    const int64_t seen = (int64_t)window + max_k + 1 + sinks + 3 * TILE;
+    if (seen < tokens) tokens = seen;
+  }
+  const int64_t tiles = (tokens + TILE - 1) / TILE;
+  const int64_t wide = (int64_t)batch * kv_heads * p.row_blocks;
+  // chunks of 2048 tokens, halved down to 256 while the grid stays under two
+  // workgroups per compute unit
+  int64_t ct = 64;
+  while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 512) ct /= 2;
+  if (wide >= 4096) ct = 256;
+  p.chunk_tiles = (int)ct;
+  p.chunks = (int)((tiles + ct - 1) / ct);
+  const int64_t items = wide * p.chunks;
+  if (items * (p.mt * 4) >= (1ll << 31) - 4096) return false;
+  p.bytes = p.chunks > 1 ? (size_t)items * (p.mt * 16) * (d + 2) * sizeof(float) : 0;
+  return true;
+}
+
+static bool sizes_ok(int dtype, int batch, int max_k, int heads, int kv_heads, int d,
+                     int max_context, int window, int sinks) {
+  return (dtype == SV_F32 || dtype == SV_BF16) && batch >= 1 && batch <= MAX_BATCH && max_k >= 0 &&
+         max_k <= 63 && kv_heads >= 1 && heads >= kv_heads && heads % kv_heads == 0 &&
+         heads <= 1024 && dim_ok(d) && max_context >= 1 && max_context <= (1 << 30) &&
+         window >= 0 && window <= (1 << 30) && sinks >= 0 && sinks <= (1 << 30);
+}
+
+template <int D, int MT, typename T>
+static int launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
+  const int items = a.batch * a.kv_heads * p.row_blocks * p.chunks;
+  hipLaunchKernelGGL((k_attn<D, MT, T>), dim3(items + (a.batch + WAVES - 1) / WAVES),
+                     dim3(64 * WAVES), 0, s, a);
+  if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
+  if (p.chunks > 1) {
+    const int wide = a.batch * a.kv_heads * p.row_blocks;
+    hipLaunchKernelGGL((k_attn_join<D, MT, T>), dim3(wide * (MT * 16 / WAVES)), dim3(64 * WAVES), 0,
+                       s, a);
+    if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
+  }
+  return SV_OK;
+}
+
+}  // namespace svk
+
+using namespace svk;
+
+extern "C" {
+
+size_t spec_kv_attention_workspace_bytes(int dtype, int batch, int max_k, int heads, int kv_heads,
+                                         int head_dim, int max_context, int window, int sinks) {
+  Plan p;
+  if (!sizes_ok(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks) ||
+      !plan_of(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks, p))
+    return 0;
+  return p.bytes > 16 ? p.bytes : 16;
+}
+
+int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_seqlens,
+                      const int32_t* context_lens, int batch, int total_rows, int max_k, int heads,
+                      int kv_heads, int head_dim, const void* pages, int64_t num_pages,
+                      int page_size, const int32_t* page_table, int64_t ld_table, int max_context,
+                      float scale, int window, int sinks, void* out, int64_t ld_out,
+                      int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !cu_seqlens || !context_lens || !pages || !page_table || !out || !status)
+    return SV_ERR_NULL;
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  Plan p;
+  if (!sizes_ok(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks) ||
+      total_rows < 1 || !page_ok(page_size) || num_pages < 1 || num_pages > 0x7fffffff ||
+      ld_table < 1 || ld_table > (1 << 30) / page_size || ld_q < (int64_t)heads * head_dim ||
+      ld_out < (int64_t)heads * head_dim || !(scale > 0.f) || !(scale <= 3.0e38f) ||
+      !aligned16(pages) ||
+      !plan_of(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks, p))
+    return SV_ERR_SHAPE;
+  if (p.bytes && (!workspace || !aligned16(workspace))) return SV_ERR_NULL;
+  if (p.bytes > workspace_bytes) return SV_ERR_WORKSPACE;
+  AttnArgs a;
+  a.q = q;
+  a.ld_q = ld_q;
+  a.cu = cu_seqlens;
+  a.ctx = context_lens;
+  a.batch = batch;
+  a.total_rows = total_rows;
+  a.max_k = max_k;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.pages = (const uint8_t*)pages;
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.page_log2 = __builtin_ctz((unsigned)page_size);
+  a.table = page_table;
+  a.ld_table = ld_table;
+  a.max_context = max_context;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.status = status;
+  a.part = (float*)workspace;
+  a.chunks = p.chunks;
+  a.chunk_tiles = p.chunk_tiles;
+  a.row_blocks = p.row_blocks;
+  hipStream_t s = (hipStream_t)stream;
+#define SVK_CASE(DD, MM, TT) \
+  if (head_dim == DD && p.mt == MM) return launch<DD, MM, TT>(a, p, s)
+  if (dtype == SV_BF16) {
+    SVK_CASE(64, 1, __bf16);
+    SVK_CASE(64, 2, __bf16);
+    SVK_CASE(64, 4, __bf16);
+    SVK_CASE(128, 1, __bf16);
+    SVK_CASE(128, 2, __bf16);
+    SVK_CASE(128, 4, __bf16);
+    SVK_CASE(256, 1, __bf16);
+    SVK_CASE(256, 2, __bf16);
+  } else {
+    SVK_CASE(64, 1, float);
+    SVK_CASE(64, 2, float);
+    SVK_CASE(128, 1, float);
+    SVK_CASE(128, 2, float);
+    SVK_CASE(256, 1, float);
+  }
+#undef SVK_CASE
+  return SV_ERR_SHAPE;
+}
+
+}  // extern "C"

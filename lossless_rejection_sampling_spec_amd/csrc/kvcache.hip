@@ -1,0 +1,837 @@
+// kvcache.hip -- the 4-bit paged KV cache around the verify
+// (include/specverify.h states each operator):
+//   spec_kv_append    head norms, rotation and quantisation of the call's rows
+//   spec_kv_reserve   pages for the rows of a call, copy-on-write of shared tails
+//   spec_kv_release   positions given back after the drain
+//   spec_kv_fork      sequences that share another one's pages
+//   spec_kv_compact   live pages moved to the front of the pool
+//
+// Page state is the reference count alone: a page is free when its count is 0.
+// Counts change by integer atomics only, so their values do not depend on the
+// order; pages are handed out lowest id first.  Every result is deterministic.
+
+#include "kv_common.h"
+
+namespace svk {
+
+// ------------------------------------------------------------------- append
+//
+// One head of one row is D/8 lanes, 8 dims each, so its sum of squares and the
+// rotation's partner dims come by shuffles inside the head and a block of 32
+// dims is four neighbouring lanes.  All arithmetic is fp64 and rounds once at
+// the end: a code next to a border, or a bf16 query, then never depends on how
+// the sum was ordered, and the same row gives the same bytes whichever call
+// wrote it.  The pass is bound by its launch for a verify batch and by HBM for
+// prompts; fp64 adds about 100 instructions per lane.
+
+struct AppendArgs {
+  const void *q, *k, *v;
+  int64_t ld_q, ld_k, ld_v;
+  const float *qw, *kw;
+  float eps;
+  const float* cos_sin;
+  int max_position, rot, interleaved;
+  const int32_t *cu, *ctx;
+  int batch, total_rows, heads, kv_heads;
+  uint8_t* pages;
+  int64_t num_pages;
+  int page, page_log2;
+  const int32_t* table;
+  int64_t ld_table;
+  void* q_out;
+  int64_t ld_qout;
+  void *k_val, *v_val;
+  int32_t* status;
+  int data_blocks;
+};
+
+__device__ __forceinline__ double shfl_xor_f64(double x, int m) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)u, m);
+  const uint32_t hi = (uint32_t)__shfl_xor((int)(uint32_t)(u >> 32), m);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double shfl_f64(double x, int src) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)u, src);
+  const uint32_t hi = (uint32_t)__shfl((int)(uint32_t)(u >> 32), src);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// x as a float that a further rounding to fewer bits treats as x itself: where
+// the conversion was inexact and the float sits on one of its 13 or more coarse
+// positions, it moves one step back towards x (so no tie that x is not).
+__device__ __forceinline__ float sticky_f32(double x) {
+  const float f = (float)x;
+  uint32_t u = __builtin_bit_cast(uint32_t, f);
+  const double ax = __builtin_fabs(x), af = __builtin_fabs((double)f);
+  if ((u & 0xfffu) == 0 && ax != af && af < __builtin_inf()) u += ax > af ? 1u : ~0u;
+  return __builtin_bit_cast(float, u);
+}
+
+template <typename T>
+__device__ __forceinline__ T round_to(double x);
+template <>
+__device__ __forceinline__ float round_to<float>(double x) { return (float)x; }
+template <>
+__device__ __forceinline__ __bf16 round_to<__bf16>(double x) { return (__bf16)sticky_f32(x); }
+
+template <int D, typename T>
+__global__ __launch_bounds__(256) void k_append(AppendArgs a) {
+  constexpr int LPH = D / 8;                  // lanes per head
+  constexpr int TASKS = 256 / LPH;
+  __shared__ int32_t scu[MAX_BATCH + 1];
+  __shared__ int sbroken;
+  const int tid = threadIdx.x, lane = tid & 63;
+
+  if ((int)blockIdx.x >= a.data_blocks) {     // statuses: a wave per request
+    const int broken = first_broken(a.cu, a.batch, a.total_rows);
+    const int b = ((int)blockIdx.x - a.data_blocks) * 4 + (tid >> 6);
+    if (b >= a.batch) return;
+    int st = SV_ROW_BAD_K;
+    if (b < broken && a.cu[b + 1] > a.cu[b]) {
+      const int rows = a.cu[b + 1] - a.cu[b], ctx = a.ctx[b];
+      st = SV_ROW_OK;
+      if (ctx < 0 || (int64_t)ctx + rows > a.max_position) st = SV_ROW_BAD_PARAM;
+      else {
+        bool bad = false;
+        const int s1 = (ctx + rows - 1) >> a.page_log2;
+        for (int s = (ctx >> a.page_log2) + lane; s <= s1; s += 64)
+          bad |= s >= a.ld_table ||
+                 (uint32_t)a.table[(int64_t)b * a.ld_table + s] >= (uint64_t)a.num_pages;
+        if (__any(bad)) st = SV_ROW_BAD_PAGE;
+      }
+    }
+    if (lane == 0) a.status[b] = st;
+    return;
+  }
+
+  for (int i = tid; i <= a.batch; i += 256) scu[i] = a.cu[i];
+  if (tid < 64) {
+    const int broken = first_broken(a.cu, a.batch, a.total_rows);
+    if (tid == 0) sbroken = broken;
+  }
+  __syncthreads();
+  const int broken = sbroken;
+  const int per_row = a.heads + 2 * a.kv_heads;
+  const int64_t tasks = (int64_t)a.total_rows * per_row;
+  const int c = tid % LPH;                    // dims 8c .. 8c+7
+
+  // the lanes of a head go through the loop together; a head never crosses a wave
+  for (int64_t t0 = (int64_t)blockIdx.x * TASKS; t0 < tasks; t0 += (int64_t)a.data_blocks * TASKS) {
+    const int64_t task = t0 + tid / LPH;
+    bool live = task < tasks;
+    const int row = live ? (int)(task / per_row) : 0;
+    const int hh = live ? (int)(task - (int64_t)row * per_row) : 0;
+    // its request: the last with cu[b] <= row (good up to `broken`)
+    int lo = 0, hi = broken;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (scu[mid + 1] <= row) lo = mid + 1;
+      else hi = mid;
+    }
+    const int b = lo;
+    live = live && b < broken && row >= scu[b];
+    int64_t pos = 0;
+    if (live) {
+      const int ctx = a.ctx[b];
+      pos = (int64_t)ctx + (row - scu[b]);
+      live = ctx >= 0 && pos < a.max_position;
+    }
+    const bool is_q = hh < a.heads;
+    const bool is_k = !is_q && hh < a.heads + a.kv_heads;
+    const int kh = is_q ? 0 : is_k ? hh - a.heads : hh - a.heads - a.kv_heads;
+    const T* src = is_q   ? (const T*)a.q + (int64_t)row * a.ld_q + (int64_t)hh * D
+                   : is_k ? (const T*)a.k + (int64_t)row * a.ld_k + (int64_t)kh * D
+                          : (const T*)a.v + (int64_t)row * a.ld_v + (int64_t)kh * D;
+    double x[8];
+    {
+      T raw[8];
+      if (live) __builtin_memcpy(raw, src + 8 * c, sizeof(raw));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = live ? (double)(float)raw[i] : 0.0;
+    }
+    const float* w = is_q ? a.qw : is_k ? a.kw : nullptr;
+    double ss = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = __builtin_fma(x[i], x[i], ss);
+#pragma unroll
+    for (int d = 1; d < LPH; d <<= 1) ss += shfl_xor_f64(ss, d);
+    if (w) {
+      const double inv = 1.0 / __builtin_sqrt(ss / D + (double)a.eps);
+      float wf[8];
+      __builtin_memcpy(wf, w + 8 * c, sizeof(wf));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * (double)wf[i];
+    }
+    if (a.rot) {
+      const int half = a.rot / 2;
+      const bool turn = live && (is_q || is_k) && 8 * c < a.rot;
+      const float* cs = a.cos_sin + (turn ? pos : 0) * a.rot;
+      if (a.interleaved) {
+        if (turn) {
+          float co[4], si[4];
+          __builtin_memcpy(co, cs + 4 * c, sizeof(co));
+          __builtin_memcpy(si, cs + half + 4 * c, sizeof(si));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const double u = x[2 * i], v = x[2 * i + 1];
+            x[2 * i] = u * co[i] - v * si[i];
+            x[2 * i + 1] = v * co[i] + u * si[i];
+          }
+        }
+      } else {
+        // dim i of the first half turns with dim i + half: half/8 lanes away
+        const bool second = 8 * c >= half;
+        const int partner = lane + (turn ? (second ? -half / 8 : half / 8) : 0);
+        double y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = shfl_f64(x[i], partner);
+        if (turn) {
+          float co[8], si[8];
+          const int at = 8 * c - (second ? half : 0);
+          __builtin_memcpy(co, cs + at, sizeof(co));
+          __builtin_memcpy(si, cs + half + at, sizeof(si));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[i] = second ? x[i] * co[i] + y[i] * si[i] : x[i] * co[i] - y[i] * si[i];
+        }
+      }
+    }
+    if (is_q && live) {
+      T y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = round_to<T>(x[i]);
+      __builtin_memcpy((T*)a.q_out + (int64_t)row * a.ld_qout + (int64_t)hh * D + 8 * c, y, sizeof(y));
+    }
+
+    // the block of 32 dims: smallest power of two that holds its largest
+    // magnitude as 6 (codes end at 6), within [2^-126, 2^125]
+    double amax = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      amax = __builtin_fmax(amax, __builtin_fabs(x[i]));
+      bad |= !(__builtin_fabs(x[i]) < __builtin_inf());
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      amax = __builtin_fmax(amax, shfl_xor_f64(amax, d));
+      bad |= __shfl_xor((int)bad, d) != 0;
+    }
+    int byte = 1;
+    if (amax > 0 && !bad) {
+      // amax = f 2^e, f in [1, 2): f <= 1.5 fits 6 * 2^(e-2), else 6 * 2^(e-1)
+      const int e = __builtin_amdgcn_frexp_exp(amax) - 1;
+      const double f = __builtin_amdgcn_ldexp(amax, -e);
+      byte = e + 127 - (f > 1.5 ? 1 : 2);
+      byte = byte < 1 ? 1 : byte > 252 ? 252 : byte;
+    }
+    uint32_t word = 0;
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // |x| may pass the largest code where the scale stopped at 2^125
+      const double y = __builtin_amdgcn_ldexp(x[i], 127 - byte);
+      z[i] = bad ? 0.f : sticky_f32(__builtin_fmin(__builtin_fmax(y, -8.0), 8.0)) + 0.f;
+    }
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, z[0], z[1], 1.f, 0);
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, z[2], z[3], 1.f, 1);
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, z[4], z[5], 1.f, 2);
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, z[6], z[7], 1.f, 3);
+    if (is_q || !live) continue;
+    if (bad) byte = 255;
+
+    if (a.k_val) {                            // the values the cache now stands for
+      const float sc = bad ? __builtin_nanf("") : __builtin_bit_cast(float, (uint32_t)byte << 23);
+      const f32x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.f, 0);
+      const f32x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.f, 1);
+      const f32x2 y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.f, 2);
+      const f32x2 y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.f, 3);
+      const T y[8] = {(T)(y0[0] * sc), (T)(y0[1] * sc), (T)(y1[0] * sc), (T)(y1[1] * sc),
+                      (T)(y2[0] * sc), (T)(y2[1] * sc), (T)(y3[0] * sc), (T)(y3[1] * sc)};
+      T* dst = (T*)(is_k ? a.k_val : a.v_val) + ((int64_t)row * a.kv_heads + kh) * D + 8 * c;
+      __builtin_memcpy(dst, y, sizeof(y));
+    }
+    const int64_t slot = pos >> a.page_log2;
+    if (slot >= a.ld_table) continue;
+    const uint32_t id = (uint32_t)a.table[(int64_t)b * a.ld_table + slot];
+    if (id >= (uint64_t)a.num_pages) continue;
+    const int P = a.page, t = (int)pos & (P - 1);
+    uint8_t* u = a.pages + ((int64_t)id * a.kv_heads + kh) * unit_bytes(P, D);
+    uint8_t* sc = u + (is_k ? off_ks(P, D) : off_vs(P, D)) + (t >> 3) * (D / 4) + (t & 7);
+    if ((c & 3) == 0) sc[(c >> 2) * 8] = (uint8_t)byte;
+    if (is_k) {
+      *(uint32_t*)(u + t * (D / 2) + 4 * c) = word;
+    } else {
+      uint8_t* d = u + off_v(P, D) + (t >> 3) * (4 * D) + (t & 7) * (D / 32);
+      if constexpr (D == 64) {                // two 16ths of the dims per lane
+        *(uint16_t*)(d + (2 * c) * 16) = (uint16_t)word;
+        *(uint16_t*)(d + (2 * c + 1) * 16) = (uint16_t)(word >> 16);
+      } else if constexpr (D == 128) {
+        *(uint32_t*)(d + c * 32) = word;
+      } else {                                // half a 16th per lane
+        *(uint32_t*)(d + (c >> 1) * 64 + (c & 1) * 4) = word;
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------------- pages
+
+constexpr int CHUNK = 4096;                   // counts a workgroup looks at
+constexpr int PER_THREAD = CHUNK / 256;
+
+// Sums over a workgroup of NT threads: inclusive in thread order, and the total.
+template <int NT, typename I>
+__device__ __forceinline__ I block_scan(I x, I* wsum, I& total) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const I y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  if (lane == 63) wsum[w] = x;
+  __syncthreads();
+  I carry = 0;
+  total = 0;
+  for (int i = 0; i < NT / 64; ++i) {
+    if (i < w) carry += wsum[i];
+    total += wsum[i];
+  }
+  __syncthreads();
+  return x + carry;
+}
+
+// Pages in use in each chunk of the pool.
+__global__ __launch_bounds__(256) void k_count(const int32_t* __restrict__ refs, int num_pages,
+                                               int32_t* __restrict__ used) {
+  __shared__ int wsum[4];
+  const int p0 = blockIdx.x * CHUNK + threadIdx.x * PER_THREAD;
+  int n = 0;
+  for (int i = 0; i < PER_THREAD; ++i)
+    if (p0 + i < num_pages) n += refs[p0 + i] != 0;
+  int total;
+  block_scan<256, int>(n, wsum, total);
+  if (threadIdx.x == 0) used[blockIdx.x] = total;
+}
+
+// Sum of used[0 .. upto) by a workgroup of 256, and of all of it.
+__device__ __forceinline__ void used_before(const int32_t* used, int chunks, int upto, int* wsum,
+                                            int& before, int& all) {
+  int x = 0, y = 0;
+  for (int i = threadIdx.x; i < chunks; i += 256) {
+    const int u = used[i];
+    y += u;
+    if (i < upto) x += u;
+  }
+  block_scan<256, int>(x, wsum, before);
+  block_scan<256, int>(y, wsum, all);
+}
+
+struct PageArgs {
+  const int32_t* cu;
+  int batch, page_log2;
+  int32_t *seq_lens, *table;
+  int64_t ld_table;
+  int32_t* refs;
+  int num_pages, chunks;
+  uint8_t* pages;
+  int64_t page_bytes, layer_bytes;
+  int layers;
+  int32_t *ctx, *status;
+  // workspace
+  int32_t* used;          // [chunks]
+  int64_t* first;         // [batch + 1] rank of a request's first new page among the free ones
+  int32_t* copy;          // [batch] page to copy into the request's first new page, or -1
+};
+
+__device__ __forceinline__ int pages_of(int64_t n, int page_log2) {
+  return (int)((n + (1 << page_log2) - 1) >> page_log2);
+}
+
+// One workgroup, a thread per request: what each needs, in request order.
+__global__ __launch_bounds__(1024) void k_reserve_plan(PageArgs a) {
+  __shared__ int64_t wsum[16];
+  const int b = threadIdx.x;
+  int64_t free_pages = 0;
+  for (int i = b; i < a.chunks; i += 1024) free_pages -= a.used[i];
+  int64_t all;
+  block_scan<1024, int64_t>(free_pages, wsum, all);
+  all += a.num_pages;
+  const int broken = first_broken(a.cu, a.batch, 0x7fffffff);
+  int st = SV_ROW_BAD_K, len = 0, rows = 0, tail = -1;
+  int64_t need = 0;
+  if (b < broken) {
+    rows = a.cu[b + 1] - a.cu[b];
+    len = a.seq_lens[b];
+    if (rows > 0) {
+      const int64_t want = ((int64_t)len + rows + (1 << a.page_log2) - 1) >> a.page_log2;
+      const int have = len < 0 ? 0 : pages_of(len, a.page_log2);
+      if (len < 0) st = SV_ROW_BAD_PARAM;
+      else if (want > a.ld_table) st = SV_ROW_NO_PAGES;
+      else {
+        st = SV_ROW_OK;
+        need = want - have;
+        if (len & ((1 << a.page_log2) - 1)) {
+          const int32_t id = a.table[(int64_t)b * a.ld_table + have - 1];
+          if ((uint32_t)id >= (uint32_t)a.num_pages) {
+            st = SV_ROW_BAD_PAGE;
+            need = 0;
+          } else if (a.refs[id] > 1) {
+            tail = id;
+            need += 1;
+          }
+        }
+      }
+    }
+  }
+  int64_t total;
+  const int64_t end = block_scan<1024, int64_t>(need, wsum, total);
+  if (b < a.batch) {
+    if (st == SV_ROW_OK && need > 0 && end > all) st = SV_ROW_NO_PAGES;
+    a.first[b] = end - need;
+    if (b == a.batch - 1) a.first[a.batch] = end;
+    a.copy[b] = st == SV_ROW_OK ? tail : -1;
+    a.status[b] = st;
+    a.ctx[b] = st == SV_ROW_OK ? len : -1;
+    if (st == SV_ROW_OK) a.seq_lens[b] = len + rows;
+  }
+}
+
+// Hands out the free pages of a chunk by their rank.
+__global__ __launch_bounds__(256) void k_reserve_assign(PageArgs a) {
+  __shared__ int wsum[4];
+  int before, all;
+  used_before(a.used, a.chunks, blockIdx.x, wsum, before, all);
+  const int64_t rank0 = (int64_t)blockIdx.x * CHUNK - before;
+  const int64_t want = a.first[a.batch];
+  if (rank0 >= want) return;
+  const int p0 = blockIdx.x * CHUNK + threadIdx.x * PER_THREAD;
+  int n = 0;
+  uint32_t free_bits = 0;
+  for (int i = 0; i < PER_THREAD; ++i)
+    if (p0 + i < a.num_pages && a.refs[p0 + i] == 0) {
+      ++n;
+      free_bits |= 1u << i;
+    }
+  int total;
+  int64_t rank = rank0 + block_scan<256, int>(n, wsum, total) - n;
+  for (int i = 0; i < PER_THREAD; ++i) {
+    if (!(free_bits >> i & 1)) continue;
+    if (rank >= want) break;
+    int lo = 0, hi = a.batch;                 // the request whose range holds this rank
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.first[mid] <= rank) lo = mid;
+      else hi = mid;
+    }
+    // (ranges of requests that need nothing are empty: the last start <= rank has the rank)
+    const int j = (int)(rank - a.first[lo]);
+    ++rank;
+    const int ctx = a.ctx[lo];
+    if (ctx < 0) continue;                    // it failed: the page stays free
+    const int have = pages_of(ctx, a.page_log2), cow = a.copy[lo] >= 0;
+    a.table[(int64_t)lo * a.ld_table + have - cow + j] = p0 + i;
+    a.refs[p0 + i] = 1;
+  }
+}
+
+// Copies the shared tails (all layers) and gives their old pages' counts back.
+__global__ __launch_bounds__(256) void k_copy_tails(PageArgs a) {
+  const int b = blockIdx.x, layer = blockIdx.y;
+  const int src = a.copy[b];
+  if (src < 0) return;
+  const int dst = a.table[(int64_t)b * a.ld_table + pages_of(a.ctx[b], a.page_log2) - 1];
+  const u32x4* s = (const u32x4*)(a.pages + layer * a.layer_bytes + src * a.page_bytes);
+  u32x4* d = (u32x4*)(a.pages + layer * a.layer_bytes + dst * a.page_bytes);
+  for (int64_t i = threadIdx.x; i < a.page_bytes / 16; i += 256) d[i] = s[i];
+  if (layer == 0 && threadIdx.x == 0) atomicSub(&a.refs[src], 1);
+}
+
+__global__ __launch_bounds__(256) void k_release(const int32_t* __restrict__ give,
+                                                 const int32_t* __restrict__ ctx, int page_log2,
+                                                 int32_t* __restrict__ seq_lens,
+                                                 int32_t* __restrict__ table, int64_t ld_table,
+                                                 int32_t* __restrict__ refs, int num_pages,
+                                                 int32_t* __restrict__ status) {
+  const int b = blockIdx.x;
+  const int len = seq_lens[b], g = give[b];
+  const bool skip = ctx && ctx[b] < 0;
+  __syncthreads();
+  const int have = len < 0 ? 0 : pages_of(len, page_log2);
+  int st = SV_ROW_OK;
+  if (!skip && (len < 0 || g < 0 || g > len || have > ld_table)) st = SV_ROW_BAD_PARAM;
+  bool bad = false;
+  if (!skip && st == SV_ROW_OK) {
+    int32_t* row = table + (int64_t)b * ld_table;
+    for (int s = pages_of(len - g, page_log2) + threadIdx.x; s < have; s += 256) {
+      const int32_t id = row[s];
+      if ((uint32_t)id < (uint32_t)num_pages) atomicSub(&refs[id], 1);
+      else bad = true;
+      row[s] = -1;
+    }
+  }
+  const bool any_bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    status[b] = any_bad ? SV_ROW_BAD_PAGE : st;
+    if (!skip && st == SV_ROW_OK) seq_lens[b] = len - g;
+  }
+}
+
+// One workgroup per pair.  Each looks at all pairs, so that what it decides does
+// not depend on what another has already written.
+__global__ __launch_bounds__(256) void k_fork(const int32_t* __restrict__ src,
+                                              const int32_t* __restrict__ dst,
+                                              const int32_t* __restrict__ lens, int pairs, int seqs,
+                                              int page_log2, int32_t* seq_lens, int32_t* table,
+                                              int64_t ld_table, int32_t* refs, int num_pages,
+                                              int32_t* __restrict__ status) {
+  const int i = blockIdx.x, s = src[i], d = dst[i];
+  bool clash = false;       // an earlier pair writes d, or some pair writes s
+  for (int k = threadIdx.x; k < pairs; k += 256) {
+    const int t = dst[k];
+    clash |= (k < i && t == d) || t == s;
+  }
+  int st = SV_ROW_OK;
+  if (__syncthreads_or(clash) || (uint32_t)s >= (uint32_t)seqs || (uint32_t)d >= (uint32_t)seqs)
+    st = SV_ROW_BAD_PARAM;
+  int n = 0, held = 0;
+  const int32_t* from = table;
+  int32_t* to = table;
+  if (st == SV_ROW_OK) {
+    const int have = seq_lens[s];
+    n = lens ? lens[i] : have;
+    if (seq_lens[d] != 0 || n < 0 || n > have) st = SV_ROW_BAD_PARAM;
+    else {
+      held = pages_of(n, page_log2);
+      from = table + (int64_t)s * ld_table;
+      to = table + (int64_t)d * ld_table;
+      bool bad = held > ld_table;
+      if (!bad)
+        for (int k = threadIdx.x; k < held; k += 256)
+          bad |= (uint32_t)from[k] >= (uint32_t)num_pages;
+      if (__syncthreads_or(bad)) st = SV_ROW_BAD_PAGE;
+    }
+  }
+  if (st == SV_ROW_OK)
+    for (int k = threadIdx.x; k < held; k += 256) {
+      const int32_t id = from[k];
+      to[k] = id;
+      atomicAdd(&refs[id], 1);
+    }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    status[i] = st;
+    if (st == SV_ROW_OK) seq_lens[d] = n;
+  }
+}
+
+struct CompactArgs {
+  int seqs, page_log2;
+  const int32_t* seq_lens;
+  int32_t* table;
+  int64_t ld_table;
+  int32_t* refs;
+  int num_pages, chunks;
+  uint8_t* pages;
+  int64_t page_bytes, layer_bytes;
+  int layers;
+  int32_t* live;
+  int32_t* used;          // [chunks]
+  int32_t* counts;        // [1] pages to move
+  int32_t* hole;          // free pages below `live`, ascending
+  int32_t* mover;         // pages in use from `live` on, descending
+  int32_t* place;         // a mover's index in that order, by page
+  int copy_blocks;
+};
+
+// With L pages in use: the free ids below L (holes) and the used ids from L on
+// (movers) are equally many; the i-th mover from below goes to the i-th hole.
+__global__ __launch_bounds__(256) void k_compact_rank(CompactArgs a) {
+  __shared__ int wsum[4];
+  int before, live;
+  used_before(a.used, a.chunks, blockIdx.x, wsum, before, live);
+  const int p0 = blockIdx.x * CHUNK + threadIdx.x * PER_THREAD;
+  int n = 0;
+  uint32_t bits = 0;
+  for (int i = 0; i < PER_THREAD; ++i)
+    if (p0 + i < a.num_pages && a.refs[p0 + i] != 0) {
+      ++n;
+      bits |= 1u << i;
+    }
+  int total;
+  int rank = before + block_scan<256, int>(n, wsum, total) - n;   // used pages before p
+  for (int i = 0; i < PER_THREAD; ++i) {
+    const int p = p0 + i;
+    if (p >= a.num_pages) break;
+    const bool used = bits >> i & 1;
+    if (p == live) a.counts[0] = live - rank;
+    if (p < live && !used) a.hole[p - rank] = p;
+    if (p >= live && used) {
+      a.mover[live - 1 - rank] = p;
+      a.place[p] = live - 1 - rank;
+    }
+    rank += used;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.live[0] = live;
+    if (live == a.num_pages) a.counts[0] = 0;
+  }
+}
+
+__global__ __launch_bounds__(256) void k_compact_move(CompactArgs a) {
+  const int moves = a.counts[0], live = a.live[0];
+  if ((int)blockIdx.x >= a.copy_blocks) {     // a sequence's table
+    const int b = (int)blockIdx.x - a.copy_blocks;
+    const int len = a.seq_lens[b];
+    const int64_t held = len < 0 ? 0 : pages_of(len, a.page_log2);
+    int32_t* row = a.table + (int64_t)b * a.ld_table;
+    for (int64_t s = threadIdx.x; s < held && s < a.ld_table; s += 256) {
+      const int32_t id = row[s];
+      if (id >= live && id < a.num_pages) {
+        // a page the counts call free (a table at odds with them) keeps its id
+        const uint32_t at = (uint32_t)a.place[id];
+        if (at < (uint32_t)moves && a.mover[at] == id) row[s] = a.hole[moves - 1 - at];
+      }
+    }
+    return;
+  }
+  const int64_t vecs = a.page_bytes / 16;
+  const int64_t segs = (vecs + 1023) / 1024;
+  const int64_t units = (int64_t)moves * a.layers * segs;
+  for (int64_t u = blockIdx.x; u < units; u += a.copy_blocks) {
+    const int64_t seg = u % segs, rest = u / segs;
+    const int layer = (int)(rest % a.layers), i = (int)(rest / a.layers);
+    const int64_t from = a.mover[moves - 1 - i], to = a.hole[i];
+    const u32x4* s = (const u32x4*)(a.pages + layer * a.layer_bytes + from * a.page_bytes);
+    u32x4* d = (u32x4*)(a.pages + layer * a.layer_bytes + to * a.page_bytes);
+    u32x4 x[4];
+    const int64_t v0 = seg * 1024 + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (v0 + 256 * k < vecs) x[k] = s[v0 + 256 * k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (v0 + 256 * k < vecs) d[v0 + 256 * k] = x[k];
+    if (layer == 0 && seg == 0 && threadIdx.x == 0) {
+      a.refs[to] = a.refs[from];
+      a.refs[from] = 0;
+    }
+  }
+}
+
+// ---- host side
+
+constexpr int MAX_PAGES = 1 << 24;
+
+static size_t round16(size_t x) { return (x + 15) / 16 * 16; }
+static int chunks_of(int64_t num_pages) { return (int)((num_pages + CHUNK - 1) / CHUNK); }
+
+static bool pool_ok(int seqs, int page, int64_t ld_table, int64_t num_pages) {
+  return seqs >= 1 && seqs <= MAX_BATCH && page_ok(page) && ld_table >= 1 &&
+         ld_table <= (1 << 30) / page && num_pages >= 1 && num_pages <= MAX_PAGES;
+}
+
+template <int D, typename T>
+static int launch_append(AppendArgs a, hipStream_t s) {
+  constexpr int TASKS = 256 / (D / 8);
+  const int64_t tasks = (int64_t)a.total_rows * (a.heads + 2 * a.kv_heads);
+  int64_t blocks = (tasks + TASKS - 1) / TASKS;
+  if (blocks > 4096) blocks = 4096;
+  a.data_blocks = (int)blocks;
+  hipLaunchKernelGGL((k_append<D, T>), dim3((unsigned)blocks + (a.batch + 3) / 4), dim3(256), 0, s, a);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
+}
+
+}  // namespace svk
+
+using namespace svk;
+
+extern "C" {
+
+size_t spec_kv_page_bytes(int kv_heads, int head_dim, int page_size) {
+  if (kv_heads < 1 || kv_heads > 1024 || !dim_ok(head_dim) || !page_ok(page_size)) return 0;
+  return (size_t)(kv_heads * unit_bytes(page_size, head_dim));
+}
+
+int spec_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                   int64_t ld_v, int dtype, const float* q_weight, const float* k_weight, float eps,
+                   const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                   const int32_t* cu_seqlens, const int32_t* context_lens, int batch,
+                   int total_rows, int heads, int kv_heads, int head_dim, void* pages,
+                   int64_t num_pages, int page_size, const int32_t* page_table, int64_t ld_table,
+                   void* q_out, int64_t ld_qout, void* k_values, void* v_values, int32_t* status,
+                   void* stream) {
+  if (!q || !k || !v || !cu_seqlens || !context_lens || !pages || !page_table || !q_out || !status ||
+      (rot_dim != 0 && !cos_sin) || (!k_values) != (!v_values))
+    return SV_ERR_NULL;
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  const int64_t d = head_dim;
+  if (!pool_ok(batch, page_size, ld_table, num_pages) || !dim_ok(head_dim) || total_rows < 1 ||
+      kv_heads < 1 || heads < kv_heads || heads > 1024 || heads % kv_heads != 0 ||
+      ld_q < heads * d || ld_k < kv_heads * d || ld_v < kv_heads * d || ld_qout < heads * d ||
+      rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0 || (rot_dim && max_position < 1) ||
+      !(eps >= 0.f) || !(eps <= 1.f) || !aligned16(pages))
+    return SV_ERR_SHAPE;
+  AppendArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.ld_q = ld_q;
+  a.ld_k = ld_k;
+  a.ld_v = ld_v;
+  a.qw = q_weight;
+  a.kw = k_weight;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_position = rot_dim ? max_position : 0x7fffffff;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  a.cu = cu_seqlens;
+  a.ctx = context_lens;
+  a.batch = batch;
+  a.total_rows = total_rows;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.pages = (uint8_t*)pages;
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.page_log2 = __builtin_ctz((unsigned)page_size);
+  a.table = page_table;
+  a.ld_table = ld_table;
+  a.q_out = q_out;
+  a.ld_qout = ld_qout;
+  a.k_val = k_values;
+  a.v_val = v_values;
+  a.status = status;
+  a.data_blocks = 0;
+  hipStream_t s = (hipStream_t)stream;
+  if (dtype == SV_BF16)
+    return head_dim == 64    ? launch_append<64, __bf16>(a, s)
+           : head_dim == 128 ? launch_append<128, __bf16>(a, s)
+                             : launch_append<256, __bf16>(a, s);
+  return head_dim == 64    ? launch_append<64, float>(a, s)
+         : head_dim == 128 ? launch_append<128, float>(a, s)
+                           : launch_append<256, float>(a, s);
+}
+
+size_t spec_kv_pages_workspace_bytes(int seqs, int64_t num_pages) {
+  if (!pool_ok(seqs, 16, 1, num_pages)) return 0;
+  // reserve: used, first, copy; compact: used, one count, three words per page
+  const size_t used = round16(4 * (size_t)chunks_of(num_pages));
+  const size_t reserve = used + round16(8 * ((size_t)seqs + 1)) + round16(4 * (size_t)seqs);
+  const size_t compact = used + 16 + 3 * round16(4 * (size_t)num_pages);
+  return reserve > compact ? reserve : compact;
+}
+
+int spec_kv_reserve(const int32_t* cu_seqlens, int batch, int page_size, int32_t* seq_lens,
+                    int32_t* page_table, int64_t ld_table, int32_t* ref_counts, int64_t num_pages,
+                    void* pages, int64_t page_bytes, int layers, int64_t layer_bytes,
+                    int32_t* context_lens, int32_t* status, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!cu_seqlens || !seq_lens || !page_table || !ref_counts || !pages || !context_lens || !status ||
+      !workspace)
+    return SV_ERR_NULL;
+  if (!pool_ok(batch, page_size, ld_table, num_pages) || page_bytes < 16 || page_bytes % 16 != 0 ||
+      layers < 1 || layers > 65535 ||
+      (layers > 1 && (layer_bytes % 16 != 0 || layer_bytes < num_pages * page_bytes)) || !aligned16(pages) ||
+      !aligned16(workspace))
+    return SV_ERR_SHAPE;
+  if (workspace_bytes < spec_kv_pages_workspace_bytes(batch, num_pages)) return SV_ERR_WORKSPACE;
+  PageArgs a;
+  a.cu = cu_seqlens;
+  a.batch = batch;
+  a.page_log2 = __builtin_ctz((unsigned)page_size);
+  a.seq_lens = seq_lens;
+  a.table = page_table;
+  a.ld_table = ld_table;
+  a.refs = ref_counts;
+  a.num_pages = (int)num_pages;
+  a.chunks = chunks_of(num_pages);
+  a.pages = (uint8_t*)pages;
+  a.page_bytes = page_bytes;
+  a.layer_bytes = layer_bytes;
+  a.layers = layers;
+  a.ctx = context_lens;
+  a.status = status;
+  uint8_t* w = (uint8_t*)workspace;
+  a.used = (int32_t*)w;
+  w += round16(4 * (size_t)a.chunks);
+  a.first = (int64_t*)w;
+  w += round16(8 * ((size_t)batch + 1));
+  a.copy = (int32_t*)w;
+  hipStream_t s = (hipStream_t)stream;
+  hipLaunchKernelGGL(k_count, dim3(a.chunks), dim3(256), 0, s, a.refs, a.num_pages, a.used);
+  hipLaunchKernelGGL(k_reserve_plan, dim3(1), dim3(1024), 0, s, a);
+  hipLaunchKernelGGL(k_reserve_assign, dim3(a.chunks), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_copy_tails, dim3(batch, layers), dim3(256), 0, s, a);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
+}
+
+int spec_kv_release(const int32_t* rollback, const int32_t* context_lens, int batch, int page_size,
+                    int32_t* seq_lens, int32_t* page_table, int64_t ld_table, int32_t* ref_counts,
+                    int64_t num_pages, int32_t* status, void* stream) {
+  if (!rollback || !seq_lens || !page_table || !ref_counts || !status) return SV_ERR_NULL;
+  if (!pool_ok(batch, page_size, ld_table, num_pages)) return SV_ERR_SHAPE;
+  hipLaunchKernelGGL(k_release, dim3(batch), dim3(256), 0, (hipStream_t)stream, rollback,
+                     context_lens, __builtin_ctz((unsigned)page_size), seq_lens, page_table,
+                     ld_table, ref_counts, (int)num_pages, status);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
+}
+
+int spec_kv_fork(const int32_t* src, const int32_t* dst, const int32_t* lens, int pairs, int seqs,
+                 int page_size, int32_t* seq_lens, int32_t* page_table, int64_t ld_table,
+                 int32_t* ref_counts, int64_t num_pages, int32_t* status, void* stream) {
+  if (!src || !dst || !seq_lens || !page_table || !ref_counts || !status) return SV_ERR_NULL;
+  if (!pool_ok(seqs, page_size, ld_table, num_pages) || pairs < 1 || pairs > MAX_BATCH)
+    return SV_ERR_SHAPE;
+  hipLaunchKernelGGL(k_fork, dim3(pairs), dim3(256), 0, (hipStream_t)stream, src, dst, lens, pairs,
+                     seqs, __builtin_ctz((unsigned)page_size), seq_lens, page_table, ld_table,
+                     ref_counts, (int)num_pages, status);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
+}
+
+int spec_kv_compact(int seqs, int page_size, const int32_t* seq_lens, int32_t* page_table,
+                    int64_t ld_table, int32_t* ref_counts, int64_t num_pages, void* pages,
+                    int64_t page_bytes, int layers, int64_t layer_bytes, int32_t* live,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (!seq_lens || !page_table || !ref_counts || !pages || !live || !workspace) return SV_ERR_NULL;
+  if (!pool_ok(seqs, page_size, ld_table, num_pages) || page_bytes < 16 || page_bytes % 16 != 0 ||
+      layers < 1 || layers > 65535 ||
+      (layers > 1 && (layer_bytes % 16 != 0 || layer_bytes < num_pages * page_bytes)) || !aligned16(pages) ||
+      !aligned16(workspace))
+    return SV_ERR_SHAPE;
+  if (workspace_bytes < spec_kv_pages_workspace_bytes(seqs, num_pages)) return SV_ERR_WORKSPACE;
+  CompactArgs a;
+  a.seqs = seqs;
+  a.page_log2 = __builtin_ctz((unsigned)page_size);
+  a.seq_lens = seq_lens;
+  a.table = page_table;
+  a.ld_table = ld_table;
+  a.refs = ref_counts;
+  a.num_pages = (int)num_pages;
+  a.chunks = chunks_of(num_pages);
+  a.pages = (uint8_t*)pages;
+  a.page_bytes = page_bytes;
+  a.layer_bytes = layer_bytes;
+  a.layers = layers;
+  a.live = live;
+  uint8_t* w = (uint8_t*)workspace;
+  a.used = (int32_t*)w;
+  w += round16(4 * (size_t)a.chunks);
+  a.counts = (int32_t*)w;
+  w += 16;
+  const size_t per = round16(4 * (size_t)num_pages);
+  a.hole = (int32_t*)w;
+  a.mover = (int32_t*)(w + per);
+  a.place = (int32_t*)(w + 2 * per);
+  a.copy_blocks = 2048;
+  hipStream_t s = (hipStream_t)stream;
+  hipLaunchKernelGGL(k_count, dim3(a.chunks), dim3(256), 0, s, a.refs, a.num_pages, a.used);
+  hipLaunchKernelGGL(k_compact_rank, dim3(a.chunks), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_compact_move, dim3(a.copy_blocks + seqs), dim3(256), 0, s, a);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
+}
+
+}  // extern "C"

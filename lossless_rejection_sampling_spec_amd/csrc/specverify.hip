@@ -3389,6 +3389,8 @@ const char* spec_verify_status_string(int code) {
     case 100 + SV_ROW_BAD_TOKEN: return "row: draft id outside [0, vocab)";
     case 100 + SV_ROW_BAD_PARAM: return "row: bad draft kind or temperature";
     case 100 + SV_ROW_INTERNAL: return "row: internal wait ran out (re-initialise the workspace)";
+    case 100 + SV_ROW_NO_PAGES: return "row: the page pool or the request's table row is full";
+    case 100 + SV_ROW_BAD_PAGE: return "row: a needed page id is outside the pool";
     default: return "unknown code";
   }
 }
