@@ -11,8 +11,8 @@
 // results are joined through LDS.  A wave computes
 //   S^T[token][row] = K Q^T   then   O^T[dim][row] += V^T P^T
 // with v_mfma_f32_16x16x32_bf16.  With tokens as the rows of S^T, a lane holds
-// the scores of ONE query row (its column), for 8 tokens that are exactly the
-// 8 contraction entries of its P^T operand: softmax statistics are per lane
+// the scores of ONE query row (its column), for 8 tokens (4 of each half of the
+// tile) that are exactly the 8 contraction entries of its P^T operand: softmax statistics are per lane
 // and the probabilities go from accumulator to operand without LDS or
 // shuffles.  K and V come as e2m1 codes and are widened to bf16 by the
 // hardware conversion, which applies the power-of-two block scale (exact).
@@ -101,33 +101,23 @@ __device__ __forceinline__ float row_max(float x) {
   x = fmaxf(x, __shfl_xor(x, 16));
   return fmaxf(x, __shfl_xor(x, 32));
 }
-__device__ __forceinline__ float row_sum(float x) {
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
-}
-
 // A scale byte as the float 2^(byte-127).
 __device__ __forceinline__ float scale_of(uint32_t word, int byte) {
   return __builtin_bit_cast(float, ((word >> (8 * byte)) & 255u) << 23);
 }
-// Bit 7 of every byte that is 0xFF.
-__device__ __forceinline__ uint32_t ff_bytes(uint32_t x) {
-  return (~x - 0x01010101u) & x & 0x80808080u;
-}
-
 template <int BYTE>
 __device__ __forceinline__ uint32_t widen(uint32_t word, float scale) {
   return __builtin_bit_cast(uint32_t,
                             __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, BYTE));
 }
 
-// One wave's operands of a tile.
+// A lane's operands of a tile, for each half of 16 tokens.
 template <int D>
 struct Tile {
-  uint32_t k[2][D / 32];       // two tokens' D/4 dims
-  uint32_t ks[(D + 127) / 128][2];   // K scales of 8 tokens, per block of the lane's dims
-  uint32_t v[D / 16];          // 8 tokens' D/16 dims
-  uint32_t vs[2];              // V scales of the 8 tokens
+  uint32_t k[2][D / 32];              // token n, D/4 dims
+  uint32_t ks[2][(D + 127) / 128];    // its scale bytes, per block of the lane's dims
+  uint32_t v[D / 16];                 // tokens 4g .. 4g+3 of each half, D/16 dims
+  uint32_t vs[2];                     // their scale bytes
 };
 
 template <int D, int MT, typename T>
@@ -140,7 +130,9 @@ struct Attn {
 
   bf16x8 q[MT][STEPS][NT];
   f32x4 o[MT][FR];
-  float m[MT], l[MT];     // running max of raw scores; this lane's part of the sum
+  f32x4 l[MT];            // sums of the weights: a row of ones among the products (4 equal)
+  float m[MT], mc[MT];    // running max of the raw scores; times scale log2 e, or 0
+  uint32_t poison = 0;    // outputs that saw a V block stored as NaN
 
   static __device__ __forceinline__ void split(float x, __bf16* t) {
     float r = x;
@@ -156,7 +148,8 @@ struct Attn {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       m[mt] = -INFINITY;
-      l[mt] = 0.f;
+      mc[mt] = 0.f;
+      l[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int f = 0; f < FR; ++f) o[mt][f] = f32x4{0.f, 0.f, 0.f, 0.f};
       const int r = (rb * MT + mt) * 16 + n;
@@ -178,59 +171,76 @@ struct Attn {
     }
   }
 
-  // p0, p1: units of the tile's first and second 16 tokens.
-  static __device__ __forceinline__ void load(const AttnArgs& a, Tile<D>& t, const uint8_t* p0,
-                                              const uint8_t* p1, int base) {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    const int P = a.page;
-    const uint8_t* pk = (n & 8) ? p1 : p0;
-    const uint8_t* pv = (g & 2) ? p1 : p0;
-    const int gk = ((base + 8 * (n >> 2)) & (P - 1)) >> 3;    // group of 8 tokens in its page
-    const int gv = ((base + 8 * g) & (P - 1)) >> 3;
-    const uint8_t* k0 = pk + (8 * gk + (n & 3)) * (D / 2) + g * (D / 8);
+  // Half hf of a tile: 16 tokens at token `tb` of unit p.  The unit's address is
+  // scalar and the lane's offsets are the same in every tile, so the loads need
+  // no vector arithmetic.
+  static __device__ __forceinline__ void load(Tile<D>& t, int hf, const uint8_t* p, int P, int tb) {
+    const uint32_t lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     constexpr int KA = D == 64 ? 8 : 16;
-    __builtin_memcpy(t.k[0], __builtin_assume_aligned(k0, KA), D / 8);
-    __builtin_memcpy(t.k[1], __builtin_assume_aligned(k0 + 4 * (D / 2), KA), D / 8);
-    __builtin_memcpy(t.ks, __builtin_assume_aligned(
-        pk + off_ks(P, D) + gk * (D / 4) + (g * (D / 4) / 32) * 8, 8), sizeof(t.ks));
-    __builtin_memcpy(t.v, __builtin_assume_aligned(
-        pv + off_v(P, D) + gv * (4 * D) + n * (D / 4), 16), D / 4);
-    __builtin_memcpy(t.vs, __builtin_assume_aligned(
-        pv + off_vs(P, D) + gv * (D / 4) + (n * D / 512) * 8, 8), 8);
+    const uint8_t* k = p + tb * (D / 2);
+    __builtin_memcpy(t.k[hf], __builtin_assume_aligned(k + (n * (D / 2) + g * (D / 8)), KA), D / 8);
+    const uint8_t* ks = p + off_ks(P, D) + tb * (D / 32);
+#pragma unroll
+    for (uint32_t i = 0; i < (D + 127) / 128; ++i)
+      t.ks[hf][i] = ks[(n >> 3) * (D / 4) + (g * (D / 4) / 32 + i) * 8 + (n & 7)];
+    const uint8_t* v = p + off_v(P, D) + tb * (D / 2);
+    __builtin_memcpy(t.v + hf * (D / 32),
+                     __builtin_assume_aligned(
+                         v + ((g >> 1) * (4 * D) + n * (D / 4) + (g & 1) * (D / 8)), KA), D / 8);
+    const uint8_t* vs = p + off_vs(P, D) + tb * (D / 32);
+    __builtin_memcpy(&t.vs[hf], __builtin_assume_aligned(
+        vs + ((g >> 1) * (D / 4) + (n * D / 512) * 8 + (g & 1) * 4), 4), 4);
+  }
+  // Entry i of a lane's 8 tokens, relative to the tile.
+  static __device__ __forceinline__ int token(int g, int i) {
+    return 16 * (i >> 2) + 4 * g + (i & 3);
   }
 
   // masked: some row does not see some token of the tile.
-  template <bool MASKED>
-  __device__ __forceinline__ void step(const AttnArgs& a, Tile<D>& t, int base, int ctx, int R,
-                                       int G, int rb, const Span& sp, float c) {
+  __device__ __forceinline__ void step(const AttnArgs& a, Tile<D>& t, bool masked, int base,
+                                       int ctx, int R, int G, int rb, const Span& sp, float c) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     auto sees = [&](int tok, int pos) {
       return tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
     };
-    if constexpr (MASKED) {
+    if (masked) {
       // tokens that no row sees (past the end, or between sinks and window) may
       // hold anything: their V becomes finite, so that a weight of 0 keeps it out
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int tok = base + 8 * g + i;
+        const int tok = base + token(g, i);
         if (tok >= sp.n || (tok < sp.first && tok >= a.sinks)) {
           const int sh = 8 * (i & 3);
           t.vs[i >> 2] = (t.vs[i >> 2] & ~(255u << sh)) | (127u << sh);
         }
       }
     }
-    // scores: s[tile half][mt], lane: row n, tokens base + 8g + 4*half + r
+    constexpr int KB = (D + 127) / 128;
+    float ksc[2][KB], vsc[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        ksc[hf][i] = __builtin_bit_cast(float, t.ks[hf][i] << 23);
+        top = max(top, t.ks[hf][i] << 23);
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      vsc[i] = scale_of(t.vs[i >> 2], i & 3);
+      top = max(top, __builtin_bit_cast(uint32_t, vsc[i]));
+    }
+    // a scale of 255: some block of the tile is stored as NaN
+    const bool odd = __any(top == 0x7f800000u);
+    // scores: s[half][mt], lane: row n, tokens base + 16*half + 4g + r
     f32x4 s[2][MT];
-    uint32_t kbad = 0;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) s[hf][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
-        const uint32_t sb = (t.ks[st / 4][hf] >> (8 * (n & 3))) & 255u;
-        if (st % 4 == 0 && sb == 255u) kbad |= 1u << hf;
-        const float sc = __builtin_bit_cast(float, sb << 23);
+        const float sc = ksc[hf][st / 4];
         const uint32_t w = t.k[hf][st];
         u32x4 kb;
         kb[0] = widen<0>(w, sc);
@@ -245,9 +255,14 @@ struct Attn {
             s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, q[mt][st][k], s[hf][mt], 0, 0, 0);
       }
     }
-    if (__any(kbad != 0)) {
-      // a K block stored as NaN (scale 255): the token's scores are NaN
-      uint32_t any = kbad | (uint32_t)__shfl_xor((int)kbad, 16);
+    if (odd) {
+      // a K block stored as NaN: the token's scores are NaN
+      uint32_t any = 0;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int i = 0; i < KB; ++i) any |= (t.ks[hf][i] == 255u ? 1u : 0u) << hf;
+      any |= (uint32_t)__shfl_xor((int)any, 16);
       any |= (uint32_t)__shfl_xor((int)any, 32);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -258,18 +273,26 @@ struct Attn {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) s[hf][mt][r] = __builtin_nanf("");
       }
+      nan_values(a, t, base, ctx, G, rb);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vsc[i] = scale_of(t.vs[i >> 2], i & 3);
+    }
+    if (masked) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int pos = ctx + ((rb * MT + mt) * 16 + n) / G;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!sees(base + token(g, i), pos)) s[i >> 2][mt][i & 3] = -INFINITY;
+      }
     }
     bf16x8 p[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int pos = ctx + ((rb * MT + mt) * 16 + n) / G;
-      if constexpr (MASKED) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (!sees(base + 8 * g + i, pos)) s[i >> 2][mt][i & 3] = -INFINITY;
-      }
-      float mx = fmaxf(fmaxf(s[0][mt][0], s[0][mt][1]), fmaxf(s[0][mt][2], s[0][mt][3]));
-      mx = fmaxf(mx, fmaxf(fmaxf(s[1][mt][0], s[1][mt][1]), fmaxf(s[1][mt][2], s[1][mt][3])));
+      float mx = fmaxf(fmaxf(s[0][mt][0], s[0][mt][1]), s[0][mt][2]);
+      mx = fmaxf(fmaxf(mx, s[0][mt][3]), s[1][mt][0]);
+      mx = fmaxf(fmaxf(mx, s[1][mt][1]), s[1][mt][2]);
+      mx = fmaxf(mx, s[1][mt][3]);
       // (a first visible score raises -inf; a row that has seen nothing stays there)
       if (__any((mx - m[mt]) * c > RAISE)) {
         const float nm = fmaxf(m[mt], row_max(mx));
@@ -278,28 +301,27 @@ struct Attn {
 #pragma unroll
         for (int f = 0; f < FR; ++f) o[mt][f] *= w;
         m[mt] = nm;
+        mc[mt] = nm == -INFINITY ? 0.f : nm * c;
       }
-      const float mc = m[mt] == -INFINITY ? 0.f : m[mt] * c;
-      float e[8], sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc));
-        sum += e[i];
-      }
-      l[mt] += sum;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc[mt]));
         __bf16 w[NT];
-        split(e[i], w);
+        split(e, w);
 #pragma unroll
         for (int k = 0; k < NT; ++k) p[mt][k][i] = w[k];
       }
     }
-    const uint32_t vbad = ff_bytes(t.vs[0]) | ff_bytes(t.vs[1]);
-    if (__any(vbad != 0)) nan_values(a, t, base, ctx, G, rb);
-    float vsc[8];
+    {
+      bf16x8 one;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) vsc[i] = scale_of(t.vs[i >> 2], i & 3);
+      for (int i = 0; i < 8; ++i) one[i] = (__bf16)1.f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = NT - 1; k >= 0; --k)
+          l[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, p[mt][k], l[mt], 0, 0, 0);
+    }
     // fragment pair c2: dims 2*c2 and 2*c2+1 of every lane's D/16
 #pragma unroll
     for (int c2 = 0; c2 < FR / 2; ++c2) {
@@ -330,9 +352,10 @@ struct Attn {
   }
 
   // V blocks stored as NaN: rows that see the token get NaN in those dims, the
-  // others must not (0 * NaN), so the block is made finite for the product.
+  // others must not (0 * NaN), so the block is made finite for the product and
+  // `poison` keeps who saw it: bit 4 mt + r, dims g*D/4 + r*D/16 ...
   __device__ __forceinline__ void nan_values(const AttnArgs& a, Tile<D>& t, int base, int ctx, int G,
-                                          int rb) {
+                                             int rb) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
 #pragma nounroll
     for (int src = 0; src < 64; ++src) {
@@ -342,27 +365,27 @@ struct Attn {
       for (int i = 0; i < 8; ++i) {
         const uint32_t w = (uint32_t)__builtin_amdgcn_readlane((int)(i < 4 ? t.vs[0] : t.vs[1]), src);
         if (((w >> (8 * (i & 3))) & 255u) != 255u) continue;
-        const int tok = base + 8 * (src >> 4) + i;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int pos = ctx + ((rb * MT + mt) * 16 + n) / G;
+        const int tok = base + token(src >> 4, i);
+#pragma nounroll
+        for (int bit = 0; bit < 4 * MT; ++bit) {
+          const int pos = ctx + ((rb * MT + (bit >> 2)) * 16 + n) / G;
           const bool sees =
               tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int mine = (g * (D / 4) + r * (D / 16)) / 32;
-            if (sees && mine == block)
-#pragma unroll
-              for (int f = 0; f < FR; ++f) o[mt][f][r] = __builtin_nanf("");
-          }
+          const int mine = (g * (D / 4) + (bit & 3) * (D / 16)) / 32;
+          if (sees && mine == block) poison |= 1u << bit;
         }
       }
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t f = ff_bytes(t.vs[k]);               // 0x80 in the bytes that are 255
-      t.vs[k] &= ~f;                                      // 255 -> 127
-    }
+    for (int k = 0; k < 8; ++k)
+      if (((t.vs[k >> 2] >> (8 * (k & 3))) & 255u) == 255u) t.vs[k >> 2] ^= 128u << (8 * (k & 3));
+  }
+  __device__ __forceinline__ void apply_poison() {
+#pragma unroll
+    for (int bit = 0; bit < 4 * MT; ++bit)
+      if (poison >> bit & 1)
+#pragma unroll
+        for (int f = 0; f < FR; ++f) o[bit >> 2][f][bit & 3] = __builtin_nanf("");
   }
 
   static constexpr int WORDS = MT * (FR * 4 + 2);
@@ -373,7 +396,7 @@ struct Attn {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       lds[64 * w++ + lane] = m[mt];
-      lds[64 * w++ + lane] = l[mt];
+      lds[64 * w++ + lane] = l[mt][0];
 #pragma unroll
       for (int f = 0; f < FR; ++f)
 #pragma unroll
@@ -390,7 +413,7 @@ struct Attn {
       const float w1 = m[mt] == nm ? 1.f : __builtin_amdgcn_exp2f((m[mt] - nm) * c);
       const float w2 = m2 == nm ? 1.f : __builtin_amdgcn_exp2f((m2 - nm) * c);
       m[mt] = nm;
-      l[mt] = l[mt] * w1 + l2 * w2;
+      l[mt][0] = l[mt][0] * w1 + l2 * w2;
 #pragma unroll
       for (int f = 0; f < FR; ++f)
 #pragma unroll
@@ -407,8 +430,8 @@ __device__ __forceinline__ void store_row(T* dst, const float* x) {
   __builtin_memcpy(dst, y, sizeof(y));
 }
 
-template <int D, int MT, typename T>
-__global__ __launch_bounds__(256, (MT * D >= 512 ? 1 : 2)) void k_attn(AttnArgs a) {
+template <int D, int MT, int DEPTH, typename T>
+__global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) void k_attn(AttnArgs a) {
   using A = Attn<D, MT, T>;
   __shared__ float lds[2][A::WORDS * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -434,21 +457,22 @@ __global__ __launch_bounds__(256, (MT * D >= 512 ? 1 : 2)) void k_attn(AttnArgs 
     return;
   }
 
-  // chunk is the slowest index: first chunks, which every request has, start first
+  // chunk is the slowest index, the last ones first: a request's chunk 0 holds what
+  // is left over of full ones, so the shortest items start last
   int it = blockIdx.x;
   const int rb = it % a.row_blocks;
   it /= a.row_blocks;
   const int h = it % a.kv_heads;
   it /= a.kv_heads;
-  const int b = it % a.batch, chunk = it / a.batch;
+  const int b = it % a.batch, chunk = a.chunks - 1 - it / a.batch;
   const int st = request_status(a, b, broken, row0, rows, ctx);
   if (st == SV_ROW_BAD_K) return;
   const int R = rows * G;
   if (rb * MT * 16 >= R) return;
   const Span sp = span_of(ctx, rows, a.window, a.sinks);
-  const int tbegin = chunk * a.chunk_tiles;
-  if (st == SV_ROW_OK ? tbegin >= sp.tiles : chunk > 0) return;
-  const int tend = min(tbegin + a.chunk_tiles, sp.tiles);
+  const int over = (sp.tiles - 1) % a.chunk_tiles + 1;
+  const int tend = over + chunk * a.chunk_tiles, tbegin = max(0, tend - a.chunk_tiles);
+  if (st == SV_ROW_OK ? tend > sp.tiles : chunk > 0) return;
   const float c = a.scale * LOG2E;
 
   A x;
@@ -461,47 +485,60 @@ __global__ __launch_bounds__(256, (MT * D >= 512 ? 1 : 2)) void k_attn(AttnArgs 
     auto base_of = [&](int i) {
       return (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.tile0) * TILE;
     };
-    auto unit_at = [&](int tok) -> const uint8_t* {
-      const int slot = tok >> a.page_log2;
-      int64_t id = 0;
-      if (page_needed(sp, slot, a.page_log2, a.sinks)) {
-        if (slot < a.ld_table) id = (uint32_t)tab[slot];
-        if (slot >= a.ld_table || id >= a.num_pages) {
+    // lane i: the pages of the chunk's tile i (its first and second 16 tokens)
+    int id[2];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      id[hf] = 0;
+      const int slot = (base_of(tbegin + lane) + 16 * hf) >> a.page_log2;
+      if (tbegin + lane < tend && page_needed(sp, slot, a.page_log2, a.sinks)) {
+        bool out = slot >= a.ld_table;
+        if (!out) {
+          id[hf] = tab[slot];
+          out = (uint32_t)id[hf] >= (uint64_t)a.num_pages;
+        }
+        if (out) {
+          id[hf] = 0;
           bad = true;
-          id = 0;
         }
       }
-      return pool + id * page_bytes;
-    };
+    }
+    bad = __any(bad);
     auto fetch = [&](Tile<D>& t, int i) {
-      const int base = base_of(i);
-      A::load(a, t, unit_at(base), unit_at(base + 16), base);
+      const int64_t i0 = __builtin_amdgcn_readlane(id[0], i - tbegin);
+      const int64_t i1 = __builtin_amdgcn_readlane(id[1], i - tbegin);
+      const int tb = base_of(i) & (a.page - 1);
+      A::load(t, 0, pool + i0 * page_bytes, a.page, tb);
+      A::load(t, 1, pool + i1 * page_bytes, a.page, (tb + 16) & (a.page - 1));
     };
     auto work = [&](Tile<D>& t, int i) {
       const int base = base_of(i);
       const bool masked = base + TILE - 1 > ctx ||
                           (a.window > 0 && base <= ctx + rows - 1 - a.window && base + TILE > a.sinks);
-      if (masked) x.template step<true>(a, t, base, ctx, R, G, rb, sp, c);
-      else x.template step<false>(a, t, base, ctx, R, G, rb, sp, c);
+      x.step(a, t, masked, base, ctx, R, G, rb, sp, c);
     };
-    Tile<D> t0, t1;
-    int i = tbegin + wave;
-    if (i < tend) fetch(t0, i);
-    while (i < tend) {
-      if (i + WAVES < tend) fetch(t1, i + WAVES);
-      work(t0, i);
-      i += WAVES;
-      if (i >= tend) break;
-      if (i + WAVES < tend) fetch(t0, i + WAVES);
-      work(t1, i);
-      i += WAVES;
+    // DEPTH tiles are on their way at any time: a buffer is filled again as soon
+    // as its tile is done.  Past the end the last tile is loaded once more: with a
+    // branch around the loads the compiler could not count those in flight and
+    // would wait for all of them at every tile.
+    Tile<D> t[DEPTH];
+    const int last = tend - 1;
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k) fetch(t[k], min(tbegin + wave + k * WAVES, last));
+    for (int i = tbegin + wave; i < tend; i += DEPTH * WAVES) {
+#pragma unroll
+      for (int k = 0; k < DEPTH; ++k) {
+        if (i + k * WAVES < tend) work(t[k], i + k * WAVES);
+        fetch(t[k], min(i + (k + DEPTH) * WAVES, last));
+      }
     }
   }
   // a page id out of range: the request's rows are NaN
   if (bad)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) x.l[mt] = __builtin_nanf("");
+    for (int mt = 0; mt < MT; ++mt) x.l[mt][0] = __builtin_nanf("");
 
+  if (__any(x.poison != 0)) x.apply_poison();
   // join the four waves: 2, 3 into 0, 1, then 1 into 0
   if (wave >= 2) x.put(lds[wave - 2]);
   __syncthreads();
@@ -520,7 +557,7 @@ __global__ __launch_bounds__(256, (MT * D >= 512 ? 1 : 2)) void k_attn(AttnArgs 
   float* stat = a.part + (int64_t)items * (MT * 16) * D + item * (MT * 16) * 2;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const float sum = row_sum(x.l[mt]);
+    const float sum = x.l[mt][0];
     const int r = (rb * MT + mt) * 16 + n;
     if (r >= R) continue;
     float y[D / 4];
@@ -542,15 +579,17 @@ __global__ __launch_bounds__(256, (MT * D >= 512 ? 1 : 2)) void k_attn(AttnArgs 
   }
 }
 
-// Joins the chunks of requests longer than one: a wave per row.
-template <int D, int MT, typename T>
+// Joins the chunks of requests longer than one: WR waves per row.
+template <int D, int MT, int WR, typename T>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  const int lane = threadIdx.x & 63;
+  constexpr int E = D / 64;                  // dims per lane
+  __shared__ float red[WAVES][D + 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int broken = first_broken(a.cu, a.batch, a.total_rows);
   const int G = a.heads / a.kv_heads;
-  constexpr int PER = MT * 16 / WAVES;      // workgroups of one item
+  constexpr int PER = MT * 16 / (WAVES / WR);      // workgroups of one item
   int it = blockIdx.x;
-  const int local = (it % PER) * WAVES + (threadIdx.x >> 6);
+  const int local = (it % PER) * (WAVES / WR) + wave / WR;
   it /= PER;
   const int first = it;                      // its item of chunk 0
   const int rb = it % a.row_blocks;
@@ -561,26 +600,57 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   const Span sp = span_of(ctx, rows, a.window, a.sinks);
   const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
   const int r = rb * MT * 16 + local;
-  if (n < 2 || r >= rows * G) return;
+  if (n < 2) return;
+  const bool live = r < rows * G;
   const int64_t per_chunk = (int64_t)a.batch * a.kv_heads * a.row_blocks;
-  const float* part = a.part + ((int64_t)first * (MT * 16) + local) * D;
+  const float* part = a.part + ((int64_t)first * (MT * 16) + local) * D + lane * E;
   const float* stat = a.part + per_chunk * a.chunks * (MT * 16) * D + ((int64_t)first * (MT * 16) + local) * 2;
+  const int64_t step = per_chunk * (MT * 16);
   const float c = a.scale * LOG2E;
   float m = -INFINITY;
-  for (int k = lane; k < n; k += 64) m = fmaxf(m, stat[k * per_chunk * (MT * 16) * 2]);
+  if (live)
+    for (int k = lane; k < n; k += 64) m = fmaxf(m, stat[k * step * 2]);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  constexpr int E = D / 64;                  // dims per lane
+  // every wave of the row weighs the chunks the same; it adds up every WR-th
   float acc[E] = {}, sum = 0.f;
-  for (int k = 0; k < n; ++k) {
-    const float mk = stat[k * per_chunk * (MT * 16) * 2], lk = stat[k * per_chunk * (MT * 16) * 2 + 1];
-    const float w = mk == m ? 1.f : __builtin_amdgcn_exp2f((mk - m) * c);
-    sum += lk * w;
-    float y[E];
-    __builtin_memcpy(y, part + k * per_chunk * (MT * 16) * D + lane * E, sizeof(y));
+  for (int k0 = 0; k0 < n && live; k0 += 64) {
+    float w = 0.f;
+    if (k0 + lane < n) {
+      const float mk = stat[(k0 + lane) * step * 2];
+      w = mk == m ? 1.f : __builtin_amdgcn_exp2f((mk - m) * c);
+      sum += w * stat[(k0 + lane) * step * 2 + 1];
+    }
+    const int most = min(64, n - k0);
+    for (int k1 = wave % WR; k1 < most; k1 += 8 * WR) {
+      float y[8][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += y[e] * w;
+      for (int u = 0; u < 8; ++u)             // (past the end: the last chunk once more, weight 0)
+        __builtin_memcpy(y[u], part + (k0 + min(k1 + u * WR, most - 1)) * step * D, sizeof(y[u]));
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int k = k1 + u * WR;
+        const float wk = __builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), min(k, most - 1)));
+        if (k < most)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(y[u][e], wk, acc[e]);
+      }
+    }
   }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+  if constexpr (WR > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) red[wave][lane * E + e] = acc[e];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < WR; ++w)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += red[w][lane * E + e];
+  }
+  if (!live) return;
   const int j = r / G, hq = h * G + r - j * G;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] /= sum;
@@ -610,15 +680,14 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
   }
   const int64_t tiles = (tokens + TILE - 1) / TILE;
   const int64_t wide = (int64_t)batch * kv_heads * p.row_blocks;
-  // chunks of 2048 tokens, halved down to 256 while the grid stays under two
+  // chunks of 64 tiles (a lane of a wave each), halved down to 256 tokens while the grid stays under two
   // workgroups per compute unit
   int64_t ct = 64;
   while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 512) ct /= 2;
-  if (wide >= 4096) ct = 256;
   p.chunk_tiles = (int)ct;
   p.chunks = (int)((tiles + ct - 1) / ct);
   const int64_t items = wide * p.chunks;
-  if (items * (p.mt * 4) >= (1ll << 31) - 4096) return false;
+  if (items * (p.mt * 16) >= (1ll << 31) - 4096) return false;
   p.bytes = p.chunks > 1 ? (size_t)items * (p.mt * 16) * (d + 2) * sizeof(float) : 0;
   return true;
 }
@@ -631,16 +700,20 @@ static bool sizes_ok(int dtype, int batch, int max_k, int heads, int kv_heads, i
          window >= 0 && window <= (1 << 30) && sinks >= 0 && sinks <= (1 << 30);
 }
 
-template <int D, int MT, typename T>
+template <int D, int MT, int DEPTH, typename T>
 static int launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
   const int items = a.batch * a.kv_heads * p.row_blocks * p.chunks;
-  hipLaunchKernelGGL((k_attn<D, MT, T>), dim3(items + (a.batch + WAVES - 1) / WAVES),
+  hipLaunchKernelGGL((k_attn<D, MT, DEPTH, T>), dim3(items + (a.batch + WAVES - 1) / WAVES),
                      dim3(64 * WAVES), 0, s, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   if (p.chunks > 1) {
     const int wide = a.batch * a.kv_heads * p.row_blocks;
-    hipLaunchKernelGGL((k_attn_join<D, MT, T>), dim3(wide * (MT * 16 / WAVES)), dim3(64 * WAVES), 0,
-                       s, a);
+    // one row per workgroup where few rows have many chunks, else one per wave
+    if (p.chunks > 8 && wide * MT * 16 <= 2048)
+      hipLaunchKernelGGL((k_attn_join<D, MT, 4, T>), dim3(wide * (MT * 16)), dim3(64 * WAVES), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_attn_join<D, MT, 1, T>), dim3(wide * (MT * 16 / WAVES)), dim3(64 * WAVES),
+                         0, s, a);
     if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   }
   return SV_OK;
@@ -708,23 +781,23 @@ int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_
   a.chunk_tiles = p.chunk_tiles;
   a.row_blocks = p.row_blocks;
   hipStream_t s = (hipStream_t)stream;
-#define SVK_CASE(DD, MM, TT) \
-  if (head_dim == DD && p.mt == MM) return launch<DD, MM, TT>(a, p, s)
+#define SVK_CASE(DD, MM, KK, TT) \
+  if (head_dim == DD && p.mt == MM) return launch<DD, MM, KK, TT>(a, p, s)
   if (dtype == SV_BF16) {
-    SVK_CASE(64, 1, __bf16);
-    SVK_CASE(64, 2, __bf16);
-    SVK_CASE(64, 4, __bf16);
-    SVK_CASE(128, 1, __bf16);
-    SVK_CASE(128, 2, __bf16);
-    SVK_CASE(128, 4, __bf16);
-    SVK_CASE(256, 1, __bf16);
-    SVK_CASE(256, 2, __bf16);
+    SVK_CASE(64, 1, 3, __bf16);
+    SVK_CASE(64, 2, 2, __bf16);
+    SVK_CASE(64, 4, 2, __bf16);
+    SVK_CASE(128, 1, 3, __bf16);
+    SVK_CASE(128, 2, 2, __bf16);
+    SVK_CASE(128, 4, 2, __bf16);
+    SVK_CASE(256, 1, 2, __bf16);
+    SVK_CASE(256, 2, 2, __bf16);
   } else {
-    SVK_CASE(64, 1, float);
-    SVK_CASE(64, 2, float);
-    SVK_CASE(128, 1, float);
-    SVK_CASE(128, 2, float);
-    SVK_CASE(256, 1, float);
+    SVK_CASE(64, 1, 2, float);
+    SVK_CASE(64, 2, 2, float);
+    SVK_CASE(128, 1, 2, float);
+    SVK_CASE(128, 2, 2, float);
+    SVK_CASE(256, 1, 2, float);
   }
 #undef SVK_CASE
   return SV_ERR_SHAPE;
