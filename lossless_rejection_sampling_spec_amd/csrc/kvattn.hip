@@ -143,8 +143,23 @@ struct Attn {
     }
   }
 
-  __device__ __forceinline__ void init(const AttnArgs& a, int row0, int R, int G, int h, int rb) {
+  // The query rows' operands: requested first, taken over once they are there.
+  struct Raw {
+    T x[MT][STEPS][8];
+  };
+  static __device__ __forceinline__ void ask(const AttnArgs& a, Raw& raw, int row0, int R, int G,
+                                             int h, int rb) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = min((rb * MT + mt) * 16 + n, R - 1);
+      const int j = r / G, hq = h * G + r - j * G;
+      const T* src = (const T*)a.q + (int64_t)(row0 + j) * a.ld_q + (int64_t)hq * D + g * (D / 4);
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) __builtin_memcpy(raw.x[mt][s], src + 8 * s, sizeof(raw.x[mt][s]));
+    }
+  }
+  __device__ __forceinline__ void init(const Raw& raw) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       m[mt] = -INFINITY;
@@ -152,22 +167,16 @@ struct Attn {
       l[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int f = 0; f < FR; ++f) o[mt][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int r = (rb * MT + mt) * 16 + n;
-      const int j = r / G, hq = h * G + r - j * G;
-      const T* src = (const T*)a.q + (int64_t)(row0 + j) * a.ld_q + (int64_t)hq * D + g * (D / 4);
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        T x[8];
-        if (r < R) __builtin_memcpy(x, src + 8 * s, sizeof(x));
+      for (int s = 0; s < STEPS; ++s)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           __bf16 t[NT];
-          if constexpr (NT == 1) t[0] = r < R ? x[i] : (__bf16)0.f;
-          else split(r < R ? to_f32<T>(x[i]) : 0.f, t);
+          if constexpr (NT == 1) t[0] = raw.x[mt][s][i];
+          else split(to_f32<T>(raw.x[mt][s][i]), t);
 #pragma unroll
           for (int k = 0; k < NT; ++k) q[mt][s][k][i] = t[k];
         }
-      }
     }
   }
 
@@ -388,38 +397,6 @@ struct Attn {
         for (int f = 0; f < FR; ++f) o[bit >> 2][f][bit & 3] = __builtin_nanf("");
   }
 
-  static constexpr int WORDS = MT * (FR * 4 + 2);
-
-  __device__ __forceinline__ void put(float* lds) const {
-    const int lane = threadIdx.x & 63;
-    int w = 0;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      lds[64 * w++ + lane] = m[mt];
-      lds[64 * w++ + lane] = l[mt][0];
-#pragma unroll
-      for (int f = 0; f < FR; ++f)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) lds[64 * w++ + lane] = o[mt][f][r];
-    }
-  }
-  __device__ __forceinline__ void join(const float* lds, float c) {
-    const int lane = threadIdx.x & 63;
-    int w = 0;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const float m2 = lds[64 * w++ + lane], l2 = lds[64 * w++ + lane];
-      const float nm = fmaxf(m[mt], m2);
-      const float w1 = m[mt] == nm ? 1.f : __builtin_amdgcn_exp2f((m[mt] - nm) * c);
-      const float w2 = m2 == nm ? 1.f : __builtin_amdgcn_exp2f((m2 - nm) * c);
-      m[mt] = nm;
-      l[mt][0] = l[mt][0] * w1 + l2 * w2;
-#pragma unroll
-      for (int f = 0; f < FR; ++f)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[mt][f][r] = o[mt][f][r] * w1 + lds[64 * w++ + lane] * w2;
-    }
-  }
 };
 
 template <typename T, int N>
@@ -433,14 +410,16 @@ __device__ __forceinline__ void store_row(T* dst, const float* x) {
 template <int D, int MT, int DEPTH, typename T>
 __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) void k_attn(AttnArgs a) {
   using A = Attn<D, MT, T>;
-  __shared__ float lds[2][A::WORDS * 64];
+  constexpr int FR = A::FR;
+  __shared__ float part_o[WAVES][MT * FR * 4][64];
+  __shared__ float part_m[WAVES][MT][16], part_l[WAVES][MT][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int broken = first_broken(a.cu, a.batch, a.total_rows);
   const int G = a.heads / a.kv_heads;
   const int items = a.batch * a.kv_heads * a.row_blocks * a.chunks;
   int row0, rows, ctx;
 
   if ((int)blockIdx.x >= items) {       // the last workgroups write the statuses, a wave each
+    const int broken = first_broken(a.cu, a.batch, a.total_rows);
     const int b = ((int)blockIdx.x - items) * WAVES + wave;
     if (b >= a.batch) return;
     int st = request_status(a, b, broken, row0, rows, ctx);
@@ -465,6 +444,7 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
   const int h = it % a.kv_heads;
   it /= a.kv_heads;
   const int b = it % a.batch, chunk = a.chunks - 1 - it / a.batch;
+  const int broken = first_broken(a.cu, a.batch, a.total_rows);
   const int st = request_status(a, b, broken, row0, rows, ctx);
   if (st == SV_ROW_BAD_K) return;
   const int R = rows * G;
@@ -476,9 +456,12 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
   const float c = a.scale * LOG2E;
 
   A x;
-  x.init(a, row0, R, G, h, rb);
+  typename A::Raw raw;
   bool bad = st != SV_ROW_OK;
-  if (!bad) {
+  if (bad) {
+    A::ask(a, raw, row0, R, G, h, rb);
+    x.init(raw);
+  } else {
     const int32_t* tab = a.table + (int64_t)b * a.ld_table;
     const int64_t unit = unit_bytes(a.page, D), page_bytes = unit * a.kv_heads;
     const uint8_t* pool = a.pages + h * unit;
@@ -489,20 +472,15 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
     int id[2];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      id[hf] = 0;
       const int slot = (base_of(tbegin + lane) + 16 * hf) >> a.page_log2;
-      if (tbegin + lane < tend && page_needed(sp, slot, a.page_log2, a.sinks)) {
-        bool out = slot >= a.ld_table;
-        if (!out) {
-          id[hf] = tab[slot];
-          out = (uint32_t)id[hf] >= (uint64_t)a.num_pages;
-        }
-        if (out) {
-          id[hf] = 0;
-          bad = true;
-        }
-      }
+      const bool need = tbegin + lane < tend && page_needed(sp, slot, a.page_log2, a.sinks);
+      const bool have = need && slot < a.ld_table;
+      id[hf] = tab[have ? slot : 0];
+      const bool in_pool = have && (uint32_t)id[hf] < (uint64_t)a.num_pages;
+      bad |= need && !in_pool;
+      if (!in_pool) id[hf] = 0;
     }
+    A::ask(a, raw, row0, R, G, h, rb);
     bad = __any(bad);
     auto fetch = [&](Tile<D>& t, int i) {
       const int64_t i0 = __builtin_amdgcn_readlane(id[0], i - tbegin);
@@ -525,6 +503,7 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
     const int last = tend - 1;
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k) fetch(t[k], min(tbegin + wave + k * WAVES, last));
+    x.init(raw);
     for (int i = tbegin + wave; i < tend; i += DEPTH * WAVES) {
 #pragma unroll
       for (int k = 0; k < DEPTH; ++k) {
@@ -533,46 +512,62 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
       }
     }
   }
-  // a page id out of range: the request's rows are NaN
-  if (bad)
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) x.l[mt][0] = __builtin_nanf("");
-
   if (__any(x.poison != 0)) x.apply_poison();
-  // join the four waves: 2, 3 into 0, 1, then 1 into 0
-  if (wave >= 2) x.put(lds[wave - 2]);
-  __syncthreads();
-  if (wave < 2) x.join(lds[wave], c);
-  __syncthreads();
-  if (wave == 1) x.put(lds[0]);
-  __syncthreads();
-  if (wave != 0) return;
-  x.join(lds[0], c);
 
+  // join the four waves: each takes a quarter of every row's dims (those that are
+  // entry r = wave of the accumulators)
   const int n = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    if (g == 0) {
+      part_m[wave][mt][n] = x.m[mt];
+      // a page id out of range: the request's rows are NaN
+      part_l[wave][mt][n] = bad ? __builtin_nanf("") : x.l[mt][0];
+    }
+#pragma unroll
+    for (int f = 0; f < FR; ++f)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part_o[wave][(mt * FR + f) * 4 + r][lane] = x.o[mt][f][r];
+  }
+  __syncthreads();
+
   const bool whole = st != SV_ROW_OK || sp.tiles <= a.chunk_tiles;
   // this item's place among the partials
   const int64_t item = (((int64_t)chunk * a.batch + b) * a.kv_heads + h) * a.row_blocks + rb;
   float* part = a.part + item * (MT * 16) * D;
   float* stat = a.part + (int64_t)items * (MT * 16) * D + item * (MT * 16) * 2;
+  const int dim = g * (D / 4) + wave * FR;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const float sum = x.l[mt][0];
     const int r = (rb * MT + mt) * 16 + n;
+    float m = part_m[0][mt][n];
+#pragma unroll
+    for (int k = 1; k < WAVES; ++k) m = fmaxf(m, part_m[k][mt][n]);
+    float w[WAVES], sum = 0.f, y[FR];
+#pragma unroll
+    for (int k = 0; k < WAVES; ++k) {
+      const float mk = part_m[k][mt][n];
+      w[k] = mk == m ? 1.f : __builtin_amdgcn_exp2f((mk - m) * c);
+      sum += part_l[k][mt][n] * w[k];
+    }
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+      y[f] = 0.f;
+#pragma unroll
+      for (int k = 0; k < WAVES; ++k)
+        y[f] = __builtin_fmaf(part_o[k][(mt * FR + f) * 4 + wave][lane], w[k], y[f]);
+    }
     if (r >= R) continue;
-    float y[D / 4];
-    const float inv = whole ? 1.f / sum : 1.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int f = 0; f < A::FR; ++f) y[k * A::FR + f] = x.o[mt][f][k] * inv;
     if (whole) {
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int f = 0; f < FR; ++f) y[f] *= inv;
       const int j = r / G, hq = h * G + r - j * G;
-      store_row<T, D / 4>((T*)a.out + (int64_t)(row0 + j) * a.ld_out + (int64_t)hq * D + g * (D / 4), y);
+      store_row<T, FR>((T*)a.out + (int64_t)(row0 + j) * a.ld_out + (int64_t)hq * D + dim, y);
     } else {
-      store_row<float, D / 4>(part + (mt * 16 + n) * D + g * (D / 4), y);
-      if (g == 0) {
-        stat[(mt * 16 + n) * 2] = x.m[mt];
+      store_row<float, FR>(part + (mt * 16 + n) * D + dim, y);
+      if (wave == 0 && g == 0) {
+        stat[(mt * 16 + n) * 2] = m;
         stat[(mt * 16 + n) * 2 + 1] = sum;
       }
     }
