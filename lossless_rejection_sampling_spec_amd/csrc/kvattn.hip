@@ -51,7 +51,8 @@ struct AttnArgs {
   int64_t ld_out;
   int32_t* status;
   float* part;          // chunk partials: [item][rows][D], then [item][rows][2] (max, sum)
-  int chunks, chunk_tiles, row_blocks;
+  int chunks, chunk_tiles, row_blocks, block_rows;
+  struct Item* plan;    // [1 + items], the first holds how many there are; or NULL
 };
 
 // The tiles a request reads: tokens that some row sees, in steps of 32.
@@ -407,6 +408,100 @@ __device__ __forceinline__ void store_row(T* dst, const float* x) {
   __builtin_memcpy(dst, y, sizeof(y));
 }
 
+// One workgroup's share: rows from 16 MT rb on, KV head h, one chunk of request b.
+struct Item {
+  int b, row0, rows, ctx, status, chunk, h, rb;
+};
+
+// The items of a call that has room for more than the device runs at once: the
+// full chunks of all requests, then the chunks 0, which hold what is left over of
+// full ones.  So the shortest start last, and workgroups without an item come
+// after all others (a batch of ragged contexts has a third of the items that its
+// sizes allow).  One workgroup of 1,024, a thread per request, then per item.
+__global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
+  __shared__ int wred[3][16], sfull[MAX_BATCH + 1], srest[MAX_BATCH + 1], seach[MAX_BATCH];
+  __shared__ int srow0[MAX_BATCH], srows[MAX_BATCH], sctx[MAX_BATCH];
+  const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
+  const int G = a.heads / a.kv_heads;
+  int c0 = 0, c1 = 0, ctx = 0, broken = a.batch;
+  if (b < a.batch) {
+    c0 = a.cu[b];
+    c1 = a.cu[b + 1];
+    ctx = a.ctx[b];
+    if (c0 < 0 || c1 < c0 || c1 > a.total_rows) broken = b;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) broken = min(broken, __shfl_xor(broken, d));
+  if (lane == 0) wred[0][wave] = broken;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 16; ++w) broken = min(broken, wred[0][w]);
+  const int rows = c1 - c0;
+  int full = 0, rest = 0;
+  if (b < broken && rows >= 1 && rows <= a.max_k + 1) {
+    rest = a.kv_heads * ((rows * G + a.block_rows - 1) / a.block_rows);
+    if (ctx >= 0 && (int64_t)ctx + rows <= a.max_context)
+      full = (span_of(ctx, rows, a.window, a.sinks).tiles - 1) / a.chunk_tiles * rest;
+  }
+  int f = full, r = rest;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int yf = __shfl_up(f, d), yr = __shfl_up(r, d);
+    if (lane >= d) {
+      f += yf;
+      r += yr;
+    }
+  }
+  if (lane == 63) {
+    wred[1][wave] = f;
+    wred[2][wave] = r;
+  }
+  __syncthreads();
+  int all_full = 0, all_rest = 0;
+  for (int w = 0; w < 16; ++w) {
+    if (w == wave) {
+      f += all_full;
+      r += all_rest;
+    }
+    all_full += wred[1][w];
+    all_rest += wred[2][w];
+  }
+  sfull[b] = f - full;
+  srest[b] = r - rest;
+  seach[b] = rest;
+  srow0[b] = c0;
+  srows[b] = rows;
+  sctx[b] = ctx;
+  if (b == 0) {
+    sfull[MAX_BATCH] = all_full;
+    srest[MAX_BATCH] = all_rest;
+    a.plan[0].b = all_full + all_rest;
+  }
+  __syncthreads();
+  for (int i = b; i < all_full + all_rest; i += 1024) {
+    const bool rem = i >= all_full;
+    const int* start = rem ? srest : sfull;
+    const int at = rem ? i - all_full : i;
+    int lo = 0, hi = MAX_BATCH;               // the request whose range holds it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= at) lo = mid;
+      else hi = mid;
+    }
+    const int in = at - start[lo], each = seach[lo], local = in % each, blocks = each / a.kv_heads;
+    Item it;
+    it.b = lo;
+    it.row0 = srow0[lo];
+    it.rows = srows[lo];
+    it.ctx = sctx[lo];
+    it.status = it.ctx < 0 || (int64_t)it.ctx + it.rows > a.max_context ? SV_ROW_BAD_PARAM : SV_ROW_OK;
+    it.chunk = rem ? 0 : 1 + in / each;
+    it.h = local / blocks;
+    it.rb = local % blocks;
+    a.plan[1 + i] = it;
+  }
+}
+
 template <int D, int MT, int DEPTH, typename T>
 __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) void k_attn(AttnArgs a) {
   using A = Attn<D, MT, T>;
@@ -416,12 +511,13 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = a.heads / a.kv_heads;
   const int items = a.batch * a.kv_heads * a.row_blocks * a.chunks;
-  int row0, rows, ctx;
+  const int status_blocks = (a.batch + WAVES - 1) / WAVES;
 
-  if ((int)blockIdx.x >= items) {       // the last workgroups write the statuses, a wave each
+  if ((int)blockIdx.x < status_blocks) {      // a request's status, a wave each
     const int broken = first_broken(a.cu, a.batch, a.total_rows);
-    const int b = ((int)blockIdx.x - items) * WAVES + wave;
+    const int b = (int)blockIdx.x * WAVES + wave;
     if (b >= a.batch) return;
+    int row0, rows, ctx;
     int st = request_status(a, b, broken, row0, rows, ctx);
     if (st == SV_ROW_OK) {
       const Span sp = span_of(ctx, rows, a.window, a.sinks);
@@ -436,19 +532,30 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
     return;
   }
 
-  // chunk is the slowest index, the last ones first: a request's chunk 0 holds what
-  // is left over of full ones, so the shortest items start last
-  int it = blockIdx.x;
-  const int rb = it % a.row_blocks;
-  it /= a.row_blocks;
-  const int h = it % a.kv_heads;
-  it /= a.kv_heads;
-  const int b = it % a.batch, chunk = a.chunks - 1 - it / a.batch;
-  const int broken = first_broken(a.cu, a.batch, a.total_rows);
-  const int st = request_status(a, b, broken, row0, rows, ctx);
-  if (st == SV_ROW_BAD_K) return;
+  int b, row0, rows, ctx, st, chunk, h, rb, it = (int)blockIdx.x - status_blocks;
+  if (a.plan) {
+    if (it >= a.plan[0].b) return;
+    const Item x = a.plan[1 + it];
+    b = x.b;
+    row0 = x.row0;
+    rows = x.rows;
+    ctx = x.ctx;
+    st = x.status;
+    chunk = x.chunk;
+    h = x.h;
+    rb = x.rb;
+  } else {
+    rb = it % a.row_blocks;
+    it /= a.row_blocks;
+    h = it % a.kv_heads;
+    it /= a.kv_heads;
+    b = it % a.batch;
+    chunk = a.chunks - 1 - it / a.batch;
+    const int broken = first_broken(a.cu, a.batch, a.total_rows);
+    st = request_status(a, b, broken, row0, rows, ctx);
+    if (st == SV_ROW_BAD_K || rb * MT * 16 >= rows * G) return;
+  }
   const int R = rows * G;
-  if (rb * MT * 16 >= R) return;
   const Span sp = span_of(ctx, rows, a.window, a.sinks);
   const int over = (sp.tiles - 1) % a.chunk_tiles + 1;
   const int tend = over + chunk * a.chunk_tiles, tbegin = max(0, tend - a.chunk_tiles);
@@ -656,7 +763,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 struct Plan {
   int mt, row_blocks, chunks, chunk_tiles;
-  size_t bytes;
+  size_t part_bytes, bytes;
+  bool plan;
 };
 
 // Rows per workgroup and the split over the context, by the call's sizes alone.
@@ -683,7 +791,9 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
   p.chunks = (int)((tiles + ct - 1) / ct);
   const int64_t items = wide * p.chunks;
   if (items * (p.mt * 16) >= (1ll << 31) - 4096) return false;
-  p.bytes = p.chunks > 1 ? (size_t)items * (p.mt * 16) * (d + 2) * sizeof(float) : 0;
+  p.part_bytes = p.chunks > 1 ? (size_t)items * (p.mt * 16) * (d + 2) * sizeof(float) : 0;
+  p.plan = items > 1024;
+  p.bytes = p.part_bytes + (p.plan ? (size_t)(items + 1) * sizeof(Item) : 0);
   return true;
 }
 
@@ -698,6 +808,10 @@ static bool sizes_ok(int dtype, int batch, int max_k, int heads, int kv_heads, i
 template <int D, int MT, int DEPTH, typename T>
 static int launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
   const int items = a.batch * a.kv_heads * p.row_blocks * p.chunks;
+  if (a.plan) {
+    hipLaunchKernelGGL(k_attn_plan, dim3(1), dim3(1024), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
+  }
   hipLaunchKernelGGL((k_attn<D, MT, DEPTH, T>), dim3(items + (a.batch + WAVES - 1) / WAVES),
                      dim3(64 * WAVES), 0, s, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
@@ -775,6 +889,8 @@ int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_
   a.chunks = p.chunks;
   a.chunk_tiles = p.chunk_tiles;
   a.row_blocks = p.row_blocks;
+  a.block_rows = p.mt * 16;
+  a.plan = p.plan ? (Item*)((uint8_t*)workspace + p.part_bytes) : nullptr;
   hipStream_t s = (hipStream_t)stream;
 #define SVK_CASE(DD, MM, KK, TT) \
   if (head_dim == DD && p.mt == MM) return launch<DD, MM, KK, TT>(a, p, s)
