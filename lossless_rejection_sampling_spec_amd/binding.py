@@ -381,7 +381,7 @@ def kv_page_bytes(kv_heads: int, head_dim: int, page_size: int) -> int:
     return int(lib().spec_kv_page_bytes(kv_heads, head_dim, page_size))
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True, eq=False)
 class KVCache:
     """The device state of a 4-bit paged KV cache (see include/specverify.h).
 
@@ -418,6 +418,14 @@ class KVCache:
         _check_vec(self.ref_counts, "ref_counts", torch.int32, p.shape[1])
         if self.seq_lens.device != p.device or self.ref_counts.device != p.device:
             raise ValueError("seq_lens and ref_counts must be on the pages' device")
+        # sizes the calls pass on every time
+        object.__setattr__(self, "device", p.device)
+        object.__setattr__(self, "layers", p.shape[0])
+        object.__setattr__(self, "num_pages", p.shape[1])
+        object.__setattr__(self, "page_bytes", n)
+        object.__setattr__(self, "layer_bytes", p.stride(0) if p.shape[0] > 1 else p.shape[1] * n)
+        object.__setattr__(self, "requests", t.shape[0])
+        object.__setattr__(self, "ld_table", t.stride(0))
 
     @classmethod
     def create(cls, *, layers: int, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
@@ -442,7 +450,7 @@ def _kv_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
     stream only, behind the work that still reads it."""
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
     ws = _kv_ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
@@ -450,26 +458,55 @@ def _kv_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
     return ws
 
 
+class _on:
+    """The device guard of a call, which costs nothing where the device is current."""
+    __slots__ = ("device", "guard")
+
+    def __init__(self, device):
+        self.device, self.guard = device, None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _check_ints(t: torch.Tensor | None, name: str, device, n: int) -> None:
+    if t is not None and (t.dtype != torch.int32 or t.device != device or not t.is_contiguous()
+                          or t.numel() < n):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n} elements on "
+                         "the cache's device")
+
+
 def _kv_batch(cache: KVCache, cu_seqlens: torch.Tensor) -> int:
     batch = cu_seqlens.numel() - 1
-    _check_vec(cu_seqlens, "cu_seqlens", torch.int32, 2)
-    if batch > cache.page_table.shape[0]:
-        raise ValueError(f"{batch} requests, but the page table has {cache.page_table.shape[0]}")
+    _check_ints(cu_seqlens, "cu_seqlens", cache.device, 2)
+    if batch > cache.requests:
+        raise ValueError(f"{batch} requests, but the page table has {cache.requests}")
     return batch
 
 
-def _check_heads(t: torch.Tensor, name: str, cache: KVCache, heads: int | None = None) -> None:
-    if (t.dim() != 3 or t.shape[2] != cache.head_dim or t.stride(2) != 1
-            or t.shape[1] > 1 and t.stride(1) != cache.head_dim or t.device != cache.pages.device):
-        raise ValueError(f"{name} must be [rows, heads, {cache.head_dim}] on the cache's device, "
-                         "heads side by side")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"{name} must have {heads} heads")
+def _heads_of(t: torch.Tensor, name: str, cache: KVCache, dtype) -> tuple:
+    """(rows, heads, elements from row to row) of a [rows, heads, head_dim] argument."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, {cache.head_dim}]")
+    rows, heads, dim = t.shape
+    s0, s1, s2 = t.stride()
+    if (dim != cache.head_dim or s2 != 1 or heads > 1 and s1 != dim or t.device != cache.device
+            or t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype} [rows, heads, {cache.head_dim}] on the cache's "
+                         "device, heads side by side")
+    # (a single row has no stride of its own)
+    return rows, heads, s0 if rows > 1 else heads * dim
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Elements from row to row of [rows, heads, dim] (a single row has no stride of its own)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _out_like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def kv_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -486,41 +523,46 @@ def kv_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 
     Returns (q_out, status[B]), and with want_values (q_out, status, k_values,
     v_values): the values the cache now stands for."""
-    dev = cache.pages.device
     batch = _kv_batch(cache, cu_seqlens)
-    _check_heads(q, "q", cache)
-    for t, name in ((k, "k"), (v, "v")):
-        _check_heads(t, name, cache, cache.kv_heads)
-        if t.dtype != q.dtype or t.shape[0] != q.shape[0]:
-            raise ValueError(f"{name} must have q's dtype and rows")
-    _check_vec(context_lens, "context_lens", torch.int32, batch)
-    _check_vec(q_weight, "q_weight", torch.float32, cache.head_dim)
-    _check_vec(k_weight, "k_weight", torch.float32, cache.head_dim)
+    code = _dtype_code(q)
+    rows, heads, ld_q = _heads_of(q, "q", cache, q.dtype)
+    k_rows, k_heads, ld_k = _heads_of(k, "k", cache, q.dtype)
+    v_rows, v_heads, ld_v = _heads_of(v, "v", cache, q.dtype)
+    if k_rows != rows or v_rows != rows or k_heads != cache.kv_heads or v_heads != cache.kv_heads:
+        raise ValueError(f"k and v must be [{rows}, {cache.kv_heads}, {cache.head_dim}]")
+    _check_ints(context_lens, "context_lens", cache.device, batch)
     rot = positions = 0
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight"), (cos_sin, "cos_sin")):
+        if t is not None and (t.dtype != torch.float32 or t.device != cache.device
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 tensor on the cache's device")
+    if (q_weight is not None and q_weight.numel() != cache.head_dim
+            or k_weight is not None and k_weight.numel() != cache.head_dim):
+        raise ValueError(f"the norms' weights must have {cache.head_dim} elements")
     if cos_sin is not None:
-        _check_vec(cos_sin, "cos_sin", torch.float32)
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [positions, rot_dim]")
         positions, rot = cos_sin.shape
-    if not 0 <= layer < cache.pages.shape[0]:
-        raise ValueError(f"layer {layer} of {cache.pages.shape[0]}")
+    if not 0 <= layer < cache.layers:
+        raise ValueError(f"layer {layer} of {cache.layers}")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _check_heads(out, "out", cache, q.shape[1])
-    if out.dtype != q.dtype or out.shape != q.shape:
-        raise ValueError("out must match q's shape and dtype")
-    status = torch.empty(batch, dtype=torch.int32, device=dev)
-    kv = [torch.empty(k.shape, dtype=k.dtype, device=dev) if want_values else None
-          for _ in range(2)]
-    with torch.cuda.device(dev):
+        out = _out_like(q)
+        ld_out = heads * cache.head_dim
+    else:
+        o_rows, o_heads, ld_out = _heads_of(out, "out", cache, q.dtype)
+        if o_rows != rows or o_heads != heads:
+            raise ValueError("out must match q's shape")
+    status = context_lens.new_empty(batch)
+    k_values, v_values = (_out_like(k), _out_like(v)) if want_values else (None, None)
+    with _on(cache.device) as stream:
         _raise(lib().spec_kv_append(
-            _ptr(q), _ld(q), _ptr(k), _ld(k), _ptr(v), _ld(v), _dtype_code(q), _ptr(q_weight),
-            _ptr(k_weight), float(eps), _ptr(cos_sin), positions, rot, int(interleaved),
-            _ptr(cu_seqlens), _ptr(context_lens), batch, q.shape[0], q.shape[1], cache.kv_heads,
-            cache.head_dim, _ptr(cache.pages[layer]), cache.pages.shape[1], cache.page_size,
-            _ptr(cache.page_table), cache.page_table.stride(0), _ptr(out), _ld(out), _ptr(kv[0]),
-            _ptr(kv[1]), _ptr(status), _stream(dev)))
-    return (out, status, *kv) if want_values else (out, status)
+            q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, code, _ptr(q_weight),
+            _ptr(k_weight), eps, _ptr(cos_sin), positions, rot, interleaved,
+            cu_seqlens.data_ptr(), context_lens.data_ptr(), batch, rows, heads, cache.kv_heads,
+            cache.head_dim, cache.pages.data_ptr() + layer * cache.layer_bytes, cache.num_pages,
+            cache.page_size, cache.page_table.data_ptr(), cache.ld_table, out.data_ptr(), ld_out,
+            _ptr(k_values), _ptr(v_values), status.data_ptr(), stream))
+    return (out, status, k_values, v_values) if want_values else (out, status)
 
 
 def kv_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -530,75 +572,75 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor,
     """spec_kv_attention: attention of the k+1 verify rows of each request over
     the cache (k = 0: decode).  scale defaults to head_dim ** -0.5.  Returns
     (out [rows, heads, D], status[B])."""
-    dev = cache.pages.device
     batch = _kv_batch(cache, cu_seqlens)
-    _check_heads(q, "q", cache)
-    _check_vec(context_lens, "context_lens", torch.int32, batch)
-    if not 0 <= layer < cache.pages.shape[0]:
-        raise ValueError(f"layer {layer} of {cache.pages.shape[0]}")
+    code = _dtype_code(q)
+    rows, heads, ld_q = _heads_of(q, "q", cache, q.dtype)
+    _check_ints(context_lens, "context_lens", cache.device, batch)
+    if not 0 <= layer < cache.layers:
+        raise ValueError(f"layer {layer} of {cache.layers}")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _check_heads(out, "out", cache, q.shape[1])
-    if out.dtype != q.dtype or out.shape != q.shape:
-        raise ValueError("out must match q's shape and dtype")
-    status = torch.empty(batch, dtype=torch.int32, device=dev)
-    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
-    need = int(lib().spec_kv_attention_workspace_bytes(
-        _dtype_code(q), batch, max_k, q.shape[1], cache.kv_heads, cache.head_dim, max_context,
-        window, sinks))
+        out = _out_like(q)
+        ld_out = heads * cache.head_dim
+    else:
+        o_rows, o_heads, ld_out = _heads_of(out, "out", cache, q.dtype)
+        if o_rows != rows or o_heads != heads:
+            raise ValueError("out must match q's shape")
+    status = context_lens.new_empty(batch)
+    scale = cache.head_dim ** -0.5 if scale is None else scale
+    L = lib()
+    need = L.spec_kv_attention_workspace_bytes(code, batch, max_k, heads, cache.kv_heads,
+                                               cache.head_dim, max_context, window, sinks)
     if need == 0:
         raise ValueError("invalid sizes for spec_kv_attention")
-    with torch.cuda.device(dev):
-        ws = _kv_workspace(dev, need) if workspace is None else workspace
-        _raise(lib().spec_kv_attention(
-            _ptr(q), _ld(q), _dtype_code(q), _ptr(cu_seqlens), _ptr(context_lens), batch,
-            q.shape[0], max_k, q.shape[1], cache.kv_heads, cache.head_dim,
-            _ptr(cache.pages[layer]), cache.pages.shape[1], cache.page_size,
-            _ptr(cache.page_table), cache.page_table.stride(0), max_context, scale, window, sinks,
-            _ptr(out), _ld(out), _ptr(status), _ptr(ws), ws.numel(), _stream(dev)))
+    with _on(cache.device) as stream:
+        ws = _kv_workspace(cache.device, need) if workspace is None else workspace
+        _raise(L.spec_kv_attention(
+            q.data_ptr(), ld_q, code, cu_seqlens.data_ptr(), context_lens.data_ptr(), batch, rows,
+            max_k, heads, cache.kv_heads, cache.head_dim,
+            cache.pages.data_ptr() + layer * cache.layer_bytes, cache.num_pages, cache.page_size,
+            cache.page_table.data_ptr(), cache.ld_table, max_context, scale, window, sinks,
+            out.data_ptr(), ld_out, status.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size(), stream))
     return out, status
 
 
 def _pages_workspace(cache: KVCache, seqs: int, workspace):
-    need = int(lib().spec_kv_pages_workspace_bytes(seqs, cache.pages.shape[1]))
+    need = lib().spec_kv_pages_workspace_bytes(seqs, cache.num_pages)
     if need == 0:
         raise ValueError("invalid sizes: at most 1024 requests and 2^24 pages")
-    return _kv_workspace(cache.pages.device, need) if workspace is None else workspace
+    return _kv_workspace(cache.device, need) if workspace is None else workspace
 
 
 def kv_reserve(cache: KVCache, cu_seqlens: torch.Tensor, *, workspace: torch.Tensor | None = None):
     """spec_kv_reserve: pages for the rows of a call (shared last pages are
     copied).  Returns (context_lens[B], status[B])."""
-    dev = cache.pages.device
     batch = _kv_batch(cache, cu_seqlens)
-    context = torch.empty(batch, dtype=torch.int32, device=dev)
-    status = torch.empty(batch, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    context, status = cu_seqlens.new_empty(batch), cu_seqlens.new_empty(batch)
+    with _on(cache.device) as stream:
         ws = _pages_workspace(cache, batch, workspace)
         _raise(lib().spec_kv_reserve(
-            _ptr(cu_seqlens), batch, cache.page_size, _ptr(cache.seq_lens),
-            _ptr(cache.page_table), cache.page_table.stride(0), _ptr(cache.ref_counts),
-            cache.pages.shape[1], _ptr(cache.pages), cache.pages.shape[2], cache.pages.shape[0],
-            cache.pages.stride(0), _ptr(context), _ptr(status), _ptr(ws), ws.numel(),
-            _stream(dev)))
+            cu_seqlens.data_ptr(), batch, cache.page_size, cache.seq_lens.data_ptr(),
+            cache.page_table.data_ptr(), cache.ld_table, cache.ref_counts.data_ptr(),
+            cache.num_pages, cache.pages.data_ptr(), cache.page_bytes, cache.layers,
+            cache.layer_bytes, context.data_ptr(), status.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size(), stream))
     return context, status
 
 
 def kv_release(cache: KVCache, rollback: torch.Tensor, context_lens: torch.Tensor | None = None):
     """spec_kv_release: gives positions back (rollback as drain returns it, with
     the context_lens of the reserve before it).  Returns status[B]."""
-    dev = cache.pages.device
     batch = rollback.numel()
-    _check_vec(rollback, "rollback", torch.int32, 1)
-    _check_vec(context_lens, "context_lens", torch.int32, batch)
-    if batch > cache.page_table.shape[0]:
-        raise ValueError(f"{batch} requests, but the page table has {cache.page_table.shape[0]}")
-    status = torch.empty(batch, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    _check_ints(rollback, "rollback", cache.device, 1)
+    _check_ints(context_lens, "context_lens", cache.device, batch)
+    if batch > cache.requests:
+        raise ValueError(f"{batch} requests, but the page table has {cache.requests}")
+    status = rollback.new_empty(batch)
+    with _on(cache.device) as stream:
         _raise(lib().spec_kv_release(
-            _ptr(rollback), _ptr(context_lens), batch, cache.page_size, _ptr(cache.seq_lens),
-            _ptr(cache.page_table), cache.page_table.stride(0), _ptr(cache.ref_counts),
-            cache.pages.shape[1], _ptr(status), _stream(dev)))
+            rollback.data_ptr(), _ptr(context_lens), batch, cache.page_size,
+            cache.seq_lens.data_ptr(), cache.page_table.data_ptr(), cache.ld_table,
+            cache.ref_counts.data_ptr(), cache.num_pages, status.data_ptr(), stream))
     return status
 
 
@@ -606,33 +648,31 @@ def kv_fork(cache: KVCache, src: torch.Tensor, dst: torch.Tensor,
             lens: torch.Tensor | None = None):
     """spec_kv_fork: row dst[i] starts as the first lens[i] positions (None: all)
     of row src[i], sharing its pages.  Returns status[pairs]."""
-    dev = cache.pages.device
     pairs = src.numel()
-    _check_vec(src, "src", torch.int32, 1)
-    _check_vec(dst, "dst", torch.int32, pairs)
-    _check_vec(lens, "lens", torch.int32, pairs)
-    status = torch.empty(pairs, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    _check_ints(src, "src", cache.device, 1)
+    _check_ints(dst, "dst", cache.device, pairs)
+    _check_ints(lens, "lens", cache.device, pairs)
+    status = src.new_empty(pairs)
+    with _on(cache.device) as stream:
         _raise(lib().spec_kv_fork(
-            _ptr(src), _ptr(dst), _ptr(lens), pairs, cache.page_table.shape[0], cache.page_size,
-            _ptr(cache.seq_lens), _ptr(cache.page_table), cache.page_table.stride(0),
-            _ptr(cache.ref_counts), cache.pages.shape[1], _ptr(status), _stream(dev)))
+            src.data_ptr(), dst.data_ptr(), _ptr(lens), pairs, cache.requests, cache.page_size,
+            cache.seq_lens.data_ptr(), cache.page_table.data_ptr(), cache.ld_table,
+            cache.ref_counts.data_ptr(), cache.num_pages, status.data_ptr(), stream))
     return status
 
 
 def kv_compact(cache: KVCache, *, workspace: torch.Tensor | None = None):
     """spec_kv_compact: moves the pages in use to the front of the pool.
     Returns live (int32 [1]): pages live .. num_pages-1 are free afterwards."""
-    dev = cache.pages.device
-    live = torch.empty(1, dtype=torch.int32, device=dev)
-    seqs = cache.page_table.shape[0]
-    with torch.cuda.device(dev):
-        ws = _pages_workspace(cache, seqs, workspace)
+    live = cache.seq_lens.new_empty(1)
+    with _on(cache.device) as stream:
+        ws = _pages_workspace(cache, cache.requests, workspace)
         _raise(lib().spec_kv_compact(
-            seqs, cache.page_size, _ptr(cache.seq_lens), _ptr(cache.page_table),
-            cache.page_table.stride(0), _ptr(cache.ref_counts), cache.pages.shape[1],
-            _ptr(cache.pages), cache.pages.shape[2], cache.pages.shape[0], cache.pages.stride(0),
-            _ptr(live), _ptr(ws), ws.numel(), _stream(dev)))
+            cache.requests, cache.page_size, cache.seq_lens.data_ptr(),
+            cache.page_table.data_ptr(), cache.ld_table, cache.ref_counts.data_ptr(),
+            cache.num_pages, cache.pages.data_ptr(), cache.page_bytes, cache.layers,
+            cache.layer_bytes, live.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+            stream))
     return live
 
 
