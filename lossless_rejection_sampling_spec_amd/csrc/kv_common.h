@@ -53,15 +53,23 @@ __device__ __forceinline__ V load_any(const void* p) {   // no alignment beyond 
 // later one are BAD_K.  One wave, all lanes active; every lane gets the answer.
 __device__ __forceinline__ int first_broken(const int32_t* cu, int batch, int total_rows) {
   const int lane = threadIdx.x & 63;
-  for (int b0 = 0; b0 < batch; b0 += 64) {
-    const int b = b0 + lane;
-    bool bad = false;
-    if (b < batch) {
-      const int c0 = cu[b], c1 = cu[b + 1];
-      bad = c0 < 0 || c1 < c0 || c1 > total_rows;
+  for (int b0 = 0; b0 < batch; b0 += 512) {
+    int c0[8], c1[8];                          // (the loads of 512 requests go out together)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int b = min(b0 + 64 * i + lane, batch - 1);
+      c0[i] = cu[b];
+      c1[i] = cu[b + 1];
+      if (b0 + 64 * (i + 1) >= batch) break;
     }
-    const unsigned long long m = __ballot(bad);
-    if (m) return b0 + __builtin_ctzll(m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int b = b0 + 64 * i + lane;
+      const bool bad = b < batch && (c0[i] < 0 || c1[i] < c0[i] || c1[i] > total_rows);
+      const unsigned long long m = __ballot(bad);
+      if (m) return b0 + 64 * i + __builtin_ctzll(m);
+      if (b0 + 64 * (i + 1) >= batch) break;
+    }
   }
   return batch;
 }

@@ -45,6 +45,22 @@ struct AppendArgs {
   int data_blocks;
 };
 
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, false));
+}
+// lane ^ 1, lane ^ 2, and the mirrors of 8 and 16 lanes, which reach the other half
+// once the lanes of a half agree
+constexpr int DPP_XOR1 = 0xb1, DPP_XOR2 = 0x4e, DPP_MIRROR8 = 0x141, DPP_MIRROR16 = 0x140;
+
 __device__ __forceinline__ double shfl_xor_f64(double x, int m) {
   const uint64_t u = __builtin_bit_cast(uint64_t, x);
   const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)u, m);
@@ -67,6 +83,27 @@ __device__ __forceinline__ float sticky_f32(double x) {
   const double ax = __builtin_fabs(x), af = __builtin_fabs((double)f);
   if ((u & 0xfffu) == 0 && ax != af && af < __builtin_inf()) u += ax > af ? 1u : ~0u;
   return __builtin_bit_cast(float, u);
+}
+
+// 1 / sqrt(s): the hardware's estimate and two steps of Newton's method (the first
+// brings its error to about 2^-45, the second to fp64's own).
+__device__ __forceinline__ double rsqrt_f64(double s) {
+  double r = __builtin_amdgcn_rsq(s);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const double e = __builtin_fma(-s * r, r, 1.0);
+    r = __builtin_fma(r * e, 0.5, r);
+  }
+  return s < __builtin_inf() ? r : 1.0 / s;    // 0 at infinity, NaN for NaN
+}
+
+// 8 codes, the first in the lowest four bits, nearest with ties to the even code.
+__device__ __forceinline__ uint32_t pack_codes(const float* z) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, z[0], z[1], 1.f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, z[2], z[3], 1.f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, z[4], z[5], 1.f, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, z[6], z[7], 1.f, 3);
 }
 
 template <typename T>
@@ -144,103 +181,146 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
     const T* src = is_q   ? (const T*)a.q + (int64_t)row * a.ld_q + (int64_t)hh * D
                    : is_k ? (const T*)a.k + (int64_t)row * a.ld_k + (int64_t)kh * D
                           : (const T*)a.v + (int64_t)row * a.ld_v + (int64_t)kh * D;
-    double x[8];
-    {
-      T raw[8];
-      if (live) __builtin_memcpy(raw, src + 8 * c, sizeof(raw));
+    T raw[8];
+    if (live) {
+      __builtin_memcpy(raw, src + 8 * c, sizeof(raw));
+    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = live ? (double)(float)raw[i] : 0.0;
-    }
-    const float* w = is_q ? a.qw : is_k ? a.kw : nullptr;
-    double ss = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = __builtin_fma(x[i], x[i], ss);
-#pragma unroll
-    for (int d = 1; d < LPH; d <<= 1) ss += shfl_xor_f64(ss, d);
-    if (w) {
-      const double inv = 1.0 / __builtin_sqrt(ss / D + (double)a.eps);
-      float wf[8];
-      __builtin_memcpy(wf, w + 8 * c, sizeof(wf));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * (double)wf[i];
-    }
-    if (a.rot) {
-      const int half = a.rot / 2;
-      const bool turn = live && (is_q || is_k) && 8 * c < a.rot;
-      const float* cs = a.cos_sin + (turn ? pos : 0) * a.rot;
-      if (a.interleaved) {
-        if (turn) {
-          float co[4], si[4];
-          __builtin_memcpy(co, cs + 4 * c, sizeof(co));
-          __builtin_memcpy(si, cs + half + 4 * c, sizeof(si));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const double u = x[2 * i], v = x[2 * i + 1];
-            x[2 * i] = u * co[i] - v * si[i];
-            x[2 * i + 1] = v * co[i] + u * si[i];
-          }
-        }
-      } else {
-        // dim i of the first half turns with dim i + half: half/8 lanes away
-        const bool second = 8 * c >= half;
-        const int partner = lane + (turn ? (second ? -half / 8 : half / 8) : 0);
-        double y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = shfl_f64(x[i], partner);
-        if (turn) {
-          float co[8], si[8];
-          const int at = 8 * c - (second ? half : 0);
-          __builtin_memcpy(co, cs + at, sizeof(co));
-          __builtin_memcpy(si, cs + half + at, sizeof(si));
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            x[i] = second ? x[i] * co[i] + y[i] * si[i] : x[i] * co[i] - y[i] * si[i];
-        }
-      }
-    }
-    if (is_q && live) {
-      T y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = round_to<T>(x[i]);
-      __builtin_memcpy((T*)a.q_out + (int64_t)row * a.ld_qout + (int64_t)hh * D + 8 * c, y, sizeof(y));
+      for (int i = 0; i < 8; ++i) raw[i] = (T)0.f;
     }
 
-    // the block of 32 dims: smallest power of two that holds its largest
-    // magnitude as 6 (codes end at 6), within [2^-126, 2^125]
-    double amax = 0;
-    bool bad = false;
+    uint32_t word = 0;       // the lane's 8 codes
+    int byte = 1;            // the scale of its block of 32 dims
+    if (!is_q && !is_k) {
+      // V goes in as it is: fp32 holds it, and scaling by a power of two is exact
+      // (what underflows is far below the first border; its sign is kept)
+      float amax = 0;
+      bool bad = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      amax = __builtin_fmax(amax, __builtin_fabs(x[i]));
-      bad |= !(__builtin_fabs(x[i]) < __builtin_inf());
-    }
+      for (int i = 0; i < 8; ++i) {
+        const float v = __builtin_fabsf((float)raw[i]);
+        amax = __builtin_fmaxf(amax, v);
+        bad |= !(v < __builtin_inff());
+      }
+      amax = __builtin_fmaxf(amax, dpp_f32<DPP_XOR1>(amax));
+      amax = __builtin_fmaxf(amax, dpp_f32<DPP_XOR2>(amax));
+      float nan = bad ? 1.f : 0.f;
+      nan = __builtin_fmaxf(nan, dpp_f32<DPP_XOR1>(nan));
+      nan = __builtin_fmaxf(nan, dpp_f32<DPP_XOR2>(nan));
+      bad = nan != 0.f;
+      if (amax > 0 && !bad) {
+        const int e = __builtin_amdgcn_frexp_expf(amax) - 1;
+        const float f = __builtin_amdgcn_ldexpf(amax, -e);
+        byte = e + 127 - (f > 1.5f ? 1 : 2);
+        byte = byte < 1 ? 1 : byte > 252 ? 252 : byte;
+      }
+      float z[8];
 #pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      amax = __builtin_fmax(amax, shfl_xor_f64(amax, d));
-      bad |= __shfl_xor((int)bad, d) != 0;
-    }
-    int byte = 1;
-    if (amax > 0 && !bad) {
-      // amax = f 2^e, f in [1, 2): f <= 1.5 fits 6 * 2^(e-2), else 6 * 2^(e-1)
-      const int e = __builtin_amdgcn_frexp_exp(amax) - 1;
-      const double f = __builtin_amdgcn_ldexp(amax, -e);
-      byte = e + 127 - (f > 1.5 ? 1 : 2);
-      byte = byte < 1 ? 1 : byte > 252 ? 252 : byte;
-    }
-    uint32_t word = 0;
-    float z[8];
+      for (int i = 0; i < 8; ++i) {
+        const float v = (float)raw[i];
+        const float y = __builtin_amdgcn_ldexpf(v, 127 - byte);
+        z[i] = bad ? 0.f : v < 0.f ? __builtin_fminf(y, -1e-30f) : y + 0.f;
+      }
+      word = pack_codes(z);
+      if (bad) byte = 255;
+    } else {
+      double x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // |x| may pass the largest code where the scale stopped at 2^125
-      const double y = __builtin_amdgcn_ldexp(x[i], 127 - byte);
-      z[i] = bad ? 0.f : sticky_f32(__builtin_fmin(__builtin_fmax(y, -8.0), 8.0)) + 0.f;
+      for (int i = 0; i < 8; ++i) x[i] = (double)(float)raw[i];
+      const float* w = is_q ? a.qw : a.kw;
+      if (w) {
+        double ss = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = __builtin_fma(x[i], x[i], ss);
+        ss += dpp_f64<DPP_XOR1>(ss);
+        ss += dpp_f64<DPP_XOR2>(ss);
+        ss += dpp_f64<DPP_MIRROR8>(ss);
+        if constexpr (LPH >= 16) ss += dpp_f64<DPP_MIRROR16>(ss);
+        if constexpr (LPH >= 32) ss += shfl_xor_f64(ss, 16);
+        const double inv = rsqrt_f64(ss * (1.0 / D) + (double)a.eps);
+        float wf[8];
+        __builtin_memcpy(wf, w + 8 * c, sizeof(wf));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * (inv * (double)wf[i]);
+      }
+      if (a.rot) {
+        const int half = a.rot / 2;
+        const bool turn = live && 8 * c < a.rot;
+        const float* cs = a.cos_sin + (turn ? pos : 0) * a.rot;
+        if (a.interleaved) {
+          if (turn) {
+            float co[4], si[4];
+            __builtin_memcpy(co, cs + 4 * c, sizeof(co));
+            __builtin_memcpy(si, cs + half + 4 * c, sizeof(si));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const double u = x[2 * i], v = x[2 * i + 1];
+              x[2 * i] = u * co[i] - v * si[i];
+              x[2 * i + 1] = v * co[i] + u * si[i];
+            }
+          }
+        } else {
+          // dim i of the first half turns with dim i + half: half/8 lanes away
+          const bool second = 8 * c >= half;
+          const int partner = lane + (turn ? (second ? -half / 8 : half / 8) : 0);
+          double y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = shfl_f64(x[i], partner);
+          if (turn) {
+            float co[8], si[8];
+            const int at = 8 * c - (second ? half : 0);
+            __builtin_memcpy(co, cs + at, sizeof(co));
+            __builtin_memcpy(si, cs + half + at, sizeof(si));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              x[i] = __builtin_fma(y[i], (double)(second ? si[i] : -si[i]), x[i] * (double)co[i]);
+          }
+        }
+      }
+      if (is_q) {
+        if (live) {
+          T y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = round_to<T>(x[i]);
+          __builtin_memcpy((T*)a.q_out + (int64_t)row * a.ld_qout + (int64_t)hh * D + 8 * c, y,
+                           sizeof(y));
+        }
+        continue;
+      }
+      // the block of 32 dims: smallest power of two that holds its largest
+      // magnitude as 6 (codes end at 6), within [2^-126, 2^125]
+      double amax = 0;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        amax = __builtin_fmax(amax, __builtin_fabs(x[i]));
+        bad |= !(__builtin_fabs(x[i]) < __builtin_inf());
+      }
+      amax = __builtin_fmax(amax, dpp_f64<DPP_XOR1>(amax));
+      amax = __builtin_fmax(amax, dpp_f64<DPP_XOR2>(amax));
+      float nan = bad ? 1.f : 0.f;
+      nan = __builtin_fmaxf(nan, dpp_f32<DPP_XOR1>(nan));
+      nan = __builtin_fmaxf(nan, dpp_f32<DPP_XOR2>(nan));
+      bad = nan != 0.f;
+      if (amax > 0 && !bad) {
+        // amax = f 2^e, f in [1, 2): f <= 1.5 fits 6 * 2^(e-2), else 6 * 2^(e-1)
+        const int e = __builtin_amdgcn_frexp_exp(amax) - 1;
+        const double f = __builtin_amdgcn_ldexp(amax, -e);
+        byte = e + 127 - (f > 1.5 ? 1 : 2);
+        byte = byte < 1 ? 1 : byte > 252 ? 252 : byte;
+      }
+      float z[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // |x| may pass the largest code where the scale stopped at 2^125
+        const double y = __builtin_amdgcn_ldexp(x[i], 127 - byte);
+        z[i] = bad ? 0.f : sticky_f32(__builtin_fmin(__builtin_fmax(y, -8.0), 8.0)) + 0.f;
+      }
+      word = pack_codes(z);
+      if (bad) byte = 255;
     }
-    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, z[0], z[1], 1.f, 0);
-    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, z[2], z[3], 1.f, 1);
-    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, z[4], z[5], 1.f, 2);
-    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, z[6], z[7], 1.f, 3);
-    if (is_q || !live) continue;
-    if (bad) byte = 255;
+    if (!live) continue;
+    const bool bad = byte == 255;
 
     if (a.k_val) {                            // the values the cache now stands for
       const float sc = bad ? __builtin_nanf("") : __builtin_bit_cast(float, (uint32_t)byte << 23);
@@ -279,6 +359,7 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
 
 // -------------------------------------------------------------------- pages
 
+constexpr int MAX_PAGES = 1 << 24;
 constexpr int CHUNK = 4096;                   // counts a workgroup looks at
 constexpr int PER_THREAD = CHUNK / 256;
 
@@ -342,7 +423,8 @@ struct PageArgs {
   int32_t *ctx, *status;
   // workspace
   int32_t* used;          // [chunks]
-  int64_t* first;         // [batch + 1] rank of a request's first new page among the free ones
+  uint64_t* bits;         // [words], in its place for small pools
+  int32_t* first;         // [batch + 1] rank of a request's first new page among the free ones
   int32_t* copy;          // [batch] page to copy into the request's first new page, or -1
 };
 
@@ -350,90 +432,172 @@ __device__ __forceinline__ int pages_of(int64_t n, int page_log2) {
   return (int)((n + (1 << page_log2) - 1) >> page_log2);
 }
 
-// One workgroup, a thread per request: what each needs, in request order.
-__global__ __launch_bounds__(1024) void k_reserve_plan(PageArgs a) {
-  __shared__ int64_t wsum[16];
+// What a request needs (a thread per request): its status without regard to the
+// others, its new pages and the shared last page among them.
+struct Need {
+  int st, len, rows, tail, pages;
+};
+__device__ __forceinline__ Need need_of(const PageArgs& a) {
   const int b = threadIdx.x;
-  int64_t free_pages = 0;
-  for (int i = b; i < a.chunks; i += 1024) free_pages -= a.used[i];
-  int64_t all;
-  block_scan<1024, int64_t>(free_pages, wsum, all);
-  all += a.num_pages;
-  const int broken = first_broken(a.cu, a.batch, 0x7fffffff);
-  int st = SV_ROW_BAD_K, len = 0, rows = 0, tail = -1;
-  int64_t need = 0;
-  if (b < broken) {
-    rows = a.cu[b + 1] - a.cu[b];
-    len = a.seq_lens[b];
-    if (rows > 0) {
-      const int64_t want = ((int64_t)len + rows + (1 << a.page_log2) - 1) >> a.page_log2;
-      const int have = len < 0 ? 0 : pages_of(len, a.page_log2);
-      if (len < 0) st = SV_ROW_BAD_PARAM;
-      else if (want > a.ld_table) st = SV_ROW_NO_PAGES;
-      else {
-        st = SV_ROW_OK;
-        need = want - have;
-        if (len & ((1 << a.page_log2) - 1)) {
-          const int32_t id = a.table[(int64_t)b * a.ld_table + have - 1];
-          if ((uint32_t)id >= (uint32_t)a.num_pages) {
-            st = SV_ROW_BAD_PAGE;
-            need = 0;
-          } else if (a.refs[id] > 1) {
-            tail = id;
-            need += 1;
-          }
-        }
-      }
+  Need n = {SV_ROW_BAD_K, 0, 0, -1, 0};
+  if (b >= a.batch) return n;
+  const int c0 = a.cu[b], c1 = a.cu[b + 1];
+  n.len = a.seq_lens[b];
+  if (c0 < 0 || c1 <= c0) return n;
+  n.rows = c1 - c0;
+  if (n.len < 0) {
+    n.st = SV_ROW_BAD_PARAM;
+    return n;
+  }
+  const int64_t want = ((int64_t)n.len + n.rows + (1 << a.page_log2) - 1) >> a.page_log2;
+  const int have = pages_of(n.len, a.page_log2);
+  if (want > a.ld_table) {
+    n.st = SV_ROW_NO_PAGES;
+    return n;
+  }
+  n.st = SV_ROW_OK;
+  n.pages = (int)want - have;
+  if (n.len & ((1 << a.page_log2) - 1)) {
+    const int32_t id = a.table[(int64_t)b * a.ld_table + have - 1];
+    if ((uint32_t)id >= (uint32_t)a.num_pages) {
+      n.st = SV_ROW_BAD_PAGE;
+      n.pages = 0;
+    } else if (a.refs[id] > 1) {
+      n.tail = id;
+      n.pages += 1;
     }
   }
+  return n;
+}
+
+// Ranks of the free pages for every request, in request order, by a workgroup of
+// 1,024.  first, ctx, copy: in LDS, for the caller.
+__device__ __forceinline__ void plan_requests(const PageArgs& a, Need n, int64_t free_pages,
+                                              int64_t* wsum, int* first, int* ctx, int* copy) {
+  const int b = threadIdx.x;
+  // the first request whose offsets break the packing rule, and all behind it
+  if (b == 0) first[MAX_BATCH] = a.batch;
+  __syncthreads();
+  if (b < a.batch && (a.cu[b] < 0 || a.cu[b + 1] < a.cu[b])) atomicMin(&first[MAX_BATCH], b);
+  __syncthreads();
+  if (b >= first[MAX_BATCH]) n = {SV_ROW_BAD_K, 0, 0, -1, 0};
   int64_t total;
-  const int64_t end = block_scan<1024, int64_t>(need, wsum, total);
+  const int64_t need = n.pages, end = block_scan<1024, int64_t>(need, wsum, total);
   if (b < a.batch) {
-    if (st == SV_ROW_OK && need > 0 && end > all) st = SV_ROW_NO_PAGES;
-    a.first[b] = end - need;
-    if (b == a.batch - 1) a.first[a.batch] = end;
-    a.copy[b] = st == SV_ROW_OK ? tail : -1;
-    a.status[b] = st;
-    a.ctx[b] = st == SV_ROW_OK ? len : -1;
-    if (st == SV_ROW_OK) a.seq_lens[b] = len + rows;
+    if (n.st == SV_ROW_OK && need > 0 && end > free_pages) n.st = SV_ROW_NO_PAGES;
+    // (ranks past the pool are never handed out)
+    first[b] = (int)min(end - need, (int64_t)MAX_PAGES);
+    if (b == a.batch - 1) first[a.batch] = (int)min(end, (int64_t)MAX_PAGES);
+    copy[b] = n.st == SV_ROW_OK ? n.tail : -1;
+    ctx[b] = n.st == SV_ROW_OK ? n.len : -1;
+    a.copy[b] = copy[b];
+    a.ctx[b] = ctx[b];
+    a.status[b] = n.st;
+    if (n.st == SV_ROW_OK) a.seq_lens[b] = n.len + n.rows;
   }
+}
+
+__global__ __launch_bounds__(1024) void k_reserve_plan(PageArgs a) {
+  __shared__ int64_t wsum[16];
+  __shared__ int first[MAX_BATCH + 1], ctx[MAX_BATCH], copy[MAX_BATCH];
+  int64_t free_pages = 0, all;
+  for (int i = threadIdx.x; i < a.chunks; i += 1024) free_pages -= a.used[i];
+  block_scan<1024, int64_t>(free_pages, wsum, all);
+  plan_requests(a, need_of(a), all + a.num_pages, wsum, first, ctx, copy);
+  __syncthreads();
+  for (int i = threadIdx.x; i <= a.batch; i += 1024) a.first[i] = first[i];
+}
+
+// Free page p has rank `rank` among the free ones: it goes to the request whose
+// range first[b] .. first[b+1] holds the rank (first, ctx and copy in LDS; ctx -1:
+// the request failed, its pages stay free; copy >= 0: its first new page replaces
+// the last it has).
+__device__ __forceinline__ void give_page(const PageArgs& a, int p, int rank, const int* first,
+                                          const int* ctx, const int* copy) {
+  int lo = 0, hi = a.batch;                   // (ranges can be empty: the last start <= rank)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= rank) lo = mid;
+    else hi = mid;
+  }
+  const int len = ctx[lo];
+  if (len < 0) return;
+  const int slot = pages_of(len, a.page_log2) - (copy[lo] >= 0) + rank - first[lo];
+  a.table[(int64_t)lo * a.ld_table + slot] = p;
+  a.refs[p] = 1;
 }
 
 // Hands out the free pages of a chunk by their rank.
 __global__ __launch_bounds__(256) void k_reserve_assign(PageArgs a) {
   __shared__ int wsum[4];
+  __shared__ int first[MAX_BATCH + 1], ctx[MAX_BATCH], copy[MAX_BATCH];
   int before, all;
   used_before(a.used, a.chunks, blockIdx.x, wsum, before, all);
-  const int64_t rank0 = (int64_t)blockIdx.x * CHUNK - before;
-  const int64_t want = a.first[a.batch];
-  if (rank0 >= want) return;
-  const int p0 = blockIdx.x * CHUNK + threadIdx.x * PER_THREAD;
-  int n = 0;
-  uint32_t free_bits = 0;
-  for (int i = 0; i < PER_THREAD; ++i)
-    if (p0 + i < a.num_pages && a.refs[p0 + i] == 0) {
-      ++n;
-      free_bits |= 1u << i;
-    }
-  int total;
-  int64_t rank = rank0 + block_scan<256, int>(n, wsum, total) - n;
-  for (int i = 0; i < PER_THREAD; ++i) {
-    if (!(free_bits >> i & 1)) continue;
-    if (rank >= want) break;
-    int lo = 0, hi = a.batch;                 // the request whose range holds this rank
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.first[mid] <= rank) lo = mid;
-      else hi = mid;
-    }
-    // (ranges of requests that need nothing are empty: the last start <= rank has the rank)
-    const int j = (int)(rank - a.first[lo]);
-    ++rank;
-    const int ctx = a.ctx[lo];
-    if (ctx < 0) continue;                    // it failed: the page stays free
-    const int have = pages_of(ctx, a.page_log2), cow = a.copy[lo] >= 0;
-    a.table[(int64_t)lo * a.ld_table + have - cow + j] = p0 + i;
-    a.refs[p0 + i] = 1;
+  const int rank0 = (int)blockIdx.x * CHUNK - before;
+  if (rank0 >= a.first[a.batch]) return;
+  for (int i = threadIdx.x; i <= a.batch; i += 256) first[i] = a.first[i];
+  for (int i = threadIdx.x; i < a.batch; i += 256) {
+    ctx[i] = a.ctx[i];
+    copy[i] = a.copy[i];
+  }
+  // a wave looks at 1,024 pages, 64 at a time, a page per lane
+  const int lane = threadIdx.x & 63;
+  const int w0 = blockIdx.x * CHUNK + (threadIdx.x >> 6) * (CHUNK / 4);
+  uint64_t mask[16];
+  int n = 0, total;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int p = w0 + 64 * i + lane;
+    mask[i] = __ballot(p < a.num_pages && a.refs[p] == 0);
+    n += __builtin_popcountll(mask[i]);
+  }
+  int rank = rank0 + (block_scan<256, int>(lane == 0 ? n : 0, wsum, total) - n);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int mine = rank + __builtin_popcountll(mask[i] & ((1ull << lane) - 1));
+    if ((mask[i] >> lane & 1) && mine < first[a.batch])
+      give_page(a, w0 + 64 * i + lane, mine, first, ctx, copy);
+    rank += __builtin_popcountll(mask[i]);
+  }
+}
+
+// Free bits of a pool, 64 pages per word, a wave per 4 words.
+__global__ __launch_bounds__(256) void k_pool_bits(const int32_t* __restrict__ refs, int num_pages,
+                                                   uint64_t* __restrict__ bits) {
+  const int lane = threadIdx.x & 63;
+  const int w0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int p = 64 * (w0 + i) + lane;
+    const uint64_t m = __ballot(refs[min(p, num_pages - 1)] == 0 && p < num_pages);
+    if (lane == 0) bits[w0 + i] = m;
+  }
+}
+
+// Pools of at most 65,536 pages: plan and assignment in one workgroup over the
+// pool's free bits.  (The counts themselves are 256 KB, which one workgroup takes
+// 20 us to read; larger pools count and assign by many workgroups.)
+constexpr int SMALL_POOL = 65536;
+__global__ __launch_bounds__(1024) void k_reserve_small(PageArgs a) {
+  __shared__ int64_t wsum[16];
+  __shared__ uint64_t bits[SMALL_POOL / 64];
+  __shared__ int rank[SMALL_POOL / 64];
+  __shared__ int first[MAX_BATCH + 1], ctx[MAX_BATCH], copy[MAX_BATCH];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int words = (a.num_pages + 63) / 64;
+  const uint64_t mine = tid < words ? a.bits[tid] : 0;
+  const Need need = need_of(a);
+  bits[tid] = mine;
+  const int n = __builtin_popcountll(mine);
+  int64_t free_pages;
+  rank[tid] = (int)block_scan<1024, int64_t>(n, wsum, free_pages) - n;
+  plan_requests(a, need, free_pages, wsum, first, ctx, copy);
+  __syncthreads();
+  const int want = first[a.batch];
+  for (int w = wave; w < words && rank[w] < want; w += 16) {
+    const uint64_t m = bits[w];
+    const int r = rank[w] + __builtin_popcountll(m & ((1ull << lane) - 1));
+    if ((m >> lane & 1) && r < want) give_page(a, 64 * w + lane, r, first, ctx, copy);
   }
 }
 
@@ -479,14 +643,16 @@ __global__ __launch_bounds__(256) void k_release(const int32_t* __restrict__ giv
   }
 }
 
-// One workgroup per pair.  Each looks at all pairs, so that what it decides does
-// not depend on what another has already written.
-__global__ __launch_bounds__(256) void k_fork(const int32_t* __restrict__ src,
-                                              const int32_t* __restrict__ dst,
-                                              const int32_t* __restrict__ lens, int pairs, int seqs,
-                                              int page_log2, int32_t* seq_lens, int32_t* table,
-                                              int64_t ld_table, int32_t* refs, int num_pages,
-                                              int32_t* __restrict__ status) {
+// One workgroup per pair: its status.  Nothing is changed yet, so the checks see
+// the tables as the call found them.
+__global__ __launch_bounds__(256) void k_fork_check(const int32_t* __restrict__ src,
+                                                    const int32_t* __restrict__ dst,
+                                                    const int32_t* __restrict__ lens, int pairs,
+                                                    int seqs, int page_log2,
+                                                    const int32_t* __restrict__ seq_lens,
+                                                    const int32_t* __restrict__ table,
+                                                    int64_t ld_table, int num_pages,
+                                                    int32_t* __restrict__ status) {
   const int i = blockIdx.x, s = src[i], d = dst[i];
   bool clash = false;       // an earlier pair writes d, or some pair writes s
   for (int k = threadIdx.x; k < pairs; k += 256) {
@@ -496,34 +662,58 @@ __global__ __launch_bounds__(256) void k_fork(const int32_t* __restrict__ src,
   int st = SV_ROW_OK;
   if (__syncthreads_or(clash) || (uint32_t)s >= (uint32_t)seqs || (uint32_t)d >= (uint32_t)seqs)
     st = SV_ROW_BAD_PARAM;
-  int n = 0, held = 0;
-  const int32_t* from = table;
-  int32_t* to = table;
   if (st == SV_ROW_OK) {
-    const int have = seq_lens[s];
-    n = lens ? lens[i] : have;
+    const int have = seq_lens[s], n = lens ? lens[i] : have;
     if (seq_lens[d] != 0 || n < 0 || n > have) st = SV_ROW_BAD_PARAM;
     else {
-      held = pages_of(n, page_log2);
-      from = table + (int64_t)s * ld_table;
-      to = table + (int64_t)d * ld_table;
+      const int held = pages_of(n, page_log2);
       bool bad = held > ld_table;
       if (!bad)
         for (int k = threadIdx.x; k < held; k += 256)
-          bad |= (uint32_t)from[k] >= (uint32_t)num_pages;
+          bad |= (uint32_t)table[(int64_t)s * ld_table + k] >= (uint32_t)num_pages;
       if (__syncthreads_or(bad)) st = SV_ROW_BAD_PAGE;
     }
   }
-  if (st == SV_ROW_OK)
-    for (int k = threadIdx.x; k < held; k += 256) {
-      const int32_t id = from[k];
-      to[k] = id;
-      atomicAdd(&refs[id], 1);
-    }
+  if (threadIdx.x == 0) status[i] = st;
+}
+
+// Workgroup (i, j): where pair i is the first good one of its src, every gridDim.y-th
+// 256 entries of that row go to every good dst of the src, and each page's count goes up once
+// by how many took it (device-wide atomics are what bounds a fork: one per page and
+// pair took twice the time).
+__global__ __launch_bounds__(256) void k_fork_copy(const int32_t* __restrict__ src,
+                                                   const int32_t* __restrict__ dst,
+                                                   const int32_t* __restrict__ lens, int pairs,
+                                                   int page_log2, int32_t* seq_lens, int32_t* table,
+                                                   int64_t ld_table, int32_t* refs,
+                                                   const int32_t* __restrict__ status) {
+  __shared__ int to[MAX_BATCH], held[MAX_BATCH], count;
+  const int i = blockIdx.x;
+  if (status[i] != SV_ROW_OK) return;
+  const int s = src[i];
+  if (threadIdx.x == 0) count = 0;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    status[i] = st;
-    if (st == SV_ROW_OK) seq_lens[d] = n;
+  bool later = false;
+  const int have = seq_lens[s];               // (a src is nobody's dst)
+  for (int k = threadIdx.x; k < pairs; k += 256)
+    if (src[k] == s && status[k] == SV_ROW_OK) {
+      later |= k < i;
+      const int n = lens ? lens[k] : have, at = atomicAdd(&count, 1);
+      to[at] = dst[k];
+      held[at] = pages_of(n, page_log2);
+      if (blockIdx.y == 0 && k >= i) seq_lens[dst[k]] = n;
+    }
+  if (__syncthreads_or(later)) return;
+  const int pages = pages_of(have, page_log2);
+  for (int k = (int)blockIdx.y * 256 + threadIdx.x; k < pages; k += (int)gridDim.y * 256) {
+    const int32_t id = table[(int64_t)s * ld_table + k];
+    int took = 0;
+    for (int m = 0; m < count; ++m)
+      if (k < held[m]) {
+        table[(int64_t)to[m] * ld_table + k] = id;
+        ++took;
+      }
+    if (took) atomicAdd(&refs[id], took);
   }
 }
 
@@ -623,10 +813,14 @@ __global__ __launch_bounds__(256) void k_compact_move(CompactArgs a) {
 
 // ---- host side
 
-constexpr int MAX_PAGES = 1 << 24;
-
 static size_t round16(size_t x) { return (x + 15) / 16 * 16; }
 static int chunks_of(int64_t num_pages) { return (int)((num_pages + CHUNK - 1) / CHUNK); }
+
+// Reserve's free bits (small pools; whole workgroups of 16 words) or chunk counts.
+static size_t head_bytes(int64_t num_pages) {
+  return num_pages <= SMALL_POOL ? 128 * (size_t)((num_pages + 1023) / 1024)
+                                 : round16(4 * (size_t)chunks_of(num_pages));
+}
 
 static bool pool_ok(int seqs, int page, int64_t ld_table, int64_t num_pages) {
   return seqs >= 1 && seqs <= MAX_BATCH && page_ok(page) && ld_table >= 1 &&
@@ -720,7 +914,7 @@ size_t spec_kv_pages_workspace_bytes(int seqs, int64_t num_pages) {
   if (!pool_ok(seqs, 16, 1, num_pages)) return 0;
   // reserve: used, first, copy; compact: used, one count, three words per page
   const size_t used = round16(4 * (size_t)chunks_of(num_pages));
-  const size_t reserve = used + round16(8 * ((size_t)seqs + 1)) + round16(4 * (size_t)seqs);
+  const size_t reserve = head_bytes(num_pages) + round16(4 * ((size_t)seqs + 1)) + round16(4 * (size_t)seqs);
   const size_t compact = used + 16 + 3 * round16(4 * (size_t)num_pages);
   return reserve > compact ? reserve : compact;
 }
@@ -757,14 +951,21 @@ int spec_kv_reserve(const int32_t* cu_seqlens, int batch, int page_size, int32_t
   a.status = status;
   uint8_t* w = (uint8_t*)workspace;
   a.used = (int32_t*)w;
-  w += round16(4 * (size_t)a.chunks);
-  a.first = (int64_t*)w;
-  w += round16(8 * ((size_t)batch + 1));
+  a.bits = (uint64_t*)w;
+  w += head_bytes(num_pages);
+  a.first = (int32_t*)w;
+  w += round16(4 * ((size_t)batch + 1));
   a.copy = (int32_t*)w;
   hipStream_t s = (hipStream_t)stream;
-  hipLaunchKernelGGL(k_count, dim3(a.chunks), dim3(256), 0, s, a.refs, a.num_pages, a.used);
-  hipLaunchKernelGGL(k_reserve_plan, dim3(1), dim3(1024), 0, s, a);
-  hipLaunchKernelGGL(k_reserve_assign, dim3(a.chunks), dim3(256), 0, s, a);
+  if (a.num_pages <= SMALL_POOL) {
+    hipLaunchKernelGGL(k_pool_bits, dim3((a.num_pages + 1023) / 1024), dim3(256), 0, s, a.refs,
+                       a.num_pages, a.bits);
+    hipLaunchKernelGGL(k_reserve_small, dim3(1), dim3(1024), 0, s, a);
+  } else {
+    hipLaunchKernelGGL(k_count, dim3(a.chunks), dim3(256), 0, s, a.refs, a.num_pages, a.used);
+    hipLaunchKernelGGL(k_reserve_plan, dim3(1), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(k_reserve_assign, dim3(a.chunks), dim3(256), 0, s, a);
+  }
   hipLaunchKernelGGL(k_copy_tails, dim3(batch, layers), dim3(256), 0, s, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
 }
@@ -786,9 +987,14 @@ int spec_kv_fork(const int32_t* src, const int32_t* dst, const int32_t* lens, in
   if (!src || !dst || !seq_lens || !page_table || !ref_counts || !status) return SV_ERR_NULL;
   if (!pool_ok(seqs, page_size, ld_table, num_pages) || pairs < 1 || pairs > MAX_BATCH)
     return SV_ERR_SHAPE;
-  hipLaunchKernelGGL(k_fork, dim3(pairs), dim3(256), 0, (hipStream_t)stream, src, dst, lens, pairs,
-                     seqs, __builtin_ctz((unsigned)page_size), seq_lens, page_table, ld_table,
-                     ref_counts, (int)num_pages, status);
+  const int log2 = __builtin_ctz((unsigned)page_size);
+  hipStream_t s = (hipStream_t)stream;
+  hipLaunchKernelGGL(k_fork_check, dim3(pairs), dim3(256), 0, s, src, dst, lens, pairs, seqs, log2,
+                     seq_lens, page_table, ld_table, (int)num_pages, status);
+  const int64_t splits = (ld_table + 255) / 256;
+  hipLaunchKernelGGL(k_fork_copy, dim3(pairs, (unsigned)(splits < 16 ? splits : 16)), dim3(256), 0, s,
+                     src, dst, lens, pairs, log2, seq_lens, page_table, ld_table, ref_counts,
+                     status);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
 }
 

@@ -528,7 +528,8 @@ class World:
 
 
 @pytest.mark.parametrize("seqs,width,num,page", [(1, 4, 3, 16), (7, 9, 40, 16), (40, 30, 500, 32),
-                                                 (300, 12, 9000, 16), (1024, 6, 4097, 256)])
+                                                 (300, 12, 9000, 16), (1024, 6, 4097, 256),
+                                                 (50, 900, 70001, 16)])
 def test_page_calls_in_random_order(seqs, width, num, page):
     w = World(seqs, width, num, page, layers=1 if num > 1000 else 2, seed=num)
     rng = w.rng
