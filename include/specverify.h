@@ -336,7 +336,8 @@ int spec_verify_sampled_noalloc(const void* target_logits, int target_dtype, int
  *   4-bit code, sign bit then {0, .5, 1, 1.5, 2, 3, 4, 6}.  A block's scale is
  *   the smallest power of two s with amax <= 6 s (byte held to [1, 252]; larger
  *   magnitudes saturate), codes round to nearest, ties to the even code.  A
- *   block with a NaN or an infinity is stored with byte 255 and reads as NaN.
+ *   block with a NaN, an infinity or a magnitude past fp32's range is stored
+ *   with byte 255 and reads as NaN.
  * Pages: one layer's pool is [num_pages][kv_heads] units; a unit holds
  *   page_size tokens (16, 32, 64, 128 or 256) of one KV head of dimension
  *   D = head_dim (64, 128 or 256), P = page_size, without gaps:
@@ -388,7 +389,8 @@ size_t spec_kv_page_bytes(int kv_heads, int head_dim, int page_size);
  *                  missing are not stored; q_out and the others are)
  * Rows of no request are left as they were.
  * Returns SV_ERR_SHAPE for heads not a multiple of kv_heads, heads > 1024, an
- * ld shorter than its row, and sizes outside the limits above.
+ * ld shorter than its row, total_rows * (heads + 2 kv_heads) past 2^31 - 65,537,
+ * and sizes outside the limits above.
  */
 int spec_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
                    int64_t ld_v, int dtype, const float* q_weight, const float* k_weight, float eps,

@@ -74,15 +74,13 @@ __device__ __forceinline__ double shfl_f64(double x, int src) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// x as a float that a further rounding to fewer bits treats as x itself: where
-// the conversion was inexact and the float sits on one of its 13 or more coarse
-// positions, it moves one step back towards x (so no tie that x is not).
-__device__ __forceinline__ float sticky_f32(double x) {
-  const float f = (float)x;
-  uint32_t u = __builtin_bit_cast(uint32_t, f);
-  const double ax = __builtin_fabs(x), af = __builtin_fabs((double)f);
-  if ((u & 0xfffu) == 0 && ax != af && af < __builtin_inf()) u += ax > af ? 1u : ~0u;
-  return __builtin_bit_cast(float, u);
+// x as a float that a further rounding to 18 bits or fewer treats as x itself: the
+// 20 mantissa bits of its upper word, the last one set if anything follows (rounding
+// to odd), so that x lands on no tie or border that it is not on.
+__device__ __forceinline__ float odd_f32(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t hi = (uint32_t)(u >> 32) | min((uint32_t)u, 1u);
+  return (float)__builtin_bit_cast(double, (uint64_t)hi << 32);
 }
 
 // 1 / sqrt(s): the hardware's estimate and two steps of Newton's method (the first
@@ -111,13 +109,14 @@ __device__ __forceinline__ T round_to(double x);
 template <>
 __device__ __forceinline__ float round_to<float>(double x) { return (float)x; }
 template <>
-__device__ __forceinline__ __bf16 round_to<__bf16>(double x) { return (__bf16)sticky_f32(x); }
+__device__ __forceinline__ __bf16 round_to<__bf16>(double x) { return (__bf16)odd_f32(x); }
 
 template <int D, typename T>
 __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
   constexpr int LPH = D / 8;                  // lanes per head
   constexpr int TASKS = 256 / LPH;
-  __shared__ int32_t scu[MAX_BATCH + 1];
+  __shared__ int32_t scu[MAX_BATCH + 1], sctx[MAX_BATCH];
+  __shared__ double sw[2][D];                 // the norms' weights
   __shared__ int sbroken;
   const int tid = threadIdx.x, lane = tid & 63;
 
@@ -143,23 +142,58 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
     return;
   }
 
-  for (int i = tid; i <= a.batch; i += 256) scu[i] = a.cu[i];
-  if (tid < 64) {
-    const int broken = first_broken(a.cu, a.batch, a.total_rows);
-    if (tid == 0) sbroken = broken;
+  const int per_row = a.heads + 2 * a.kv_heads;
+  const uint32_t tasks = (uint32_t)a.total_rows * (uint32_t)per_row;   // (host: below 2^31)
+  const uint32_t step = (uint32_t)a.data_blocks * TASKS;
+  const float inv_row = 1.f / (float)per_row;
+  const int c = tid % LPH;                    // dims 8c .. 8c+7
+  // the lane's row and head of the tasks from t0 on
+  auto locate = [&](uint32_t t0, int& row, int& hh) {
+    const uint32_t r = t0 / (uint32_t)per_row;
+    // (the head is below per_row + TASKS here, so fp32 divides it right)
+    hh = (int)(t0 - r * (uint32_t)per_row) + tid / LPH;
+    const int up = (int)(((float)hh + 0.5f) * inv_row);
+    hh -= up * per_row;
+    row = (int)r + up;
+  };
+  auto ask = [&](int row, int hh, T* raw) {
+    const int64_t r = min(row, a.total_rows - 1);
+    const int kh = hh < a.heads + a.kv_heads ? hh - a.heads : hh - a.heads - a.kv_heads;
+    const T* src = hh < a.heads                ? (const T*)a.q + r * a.ld_q + (int64_t)hh * D
+                   : hh < a.heads + a.kv_heads ? (const T*)a.k + r * a.ld_k + (int64_t)kh * D
+                                               : (const T*)a.v + r * a.ld_v + (int64_t)kh * D;
+    __builtin_memcpy(raw, src + 8 * c, 8 * sizeof(T));
+  };
+  // the first heads are on their way while the offsets are checked
+  T next[8];
+  int next_row, next_hh;
+  locate(blockIdx.x * TASKS, next_row, next_hh);
+  ask(next_row, next_hh, next);
+  if (tid == 0) sbroken = a.batch;
+  for (int i = tid; i < D; i += 256) {
+    sw[0][i] = a.qw ? (double)a.qw[i] : 1.0;
+    sw[1][i] = a.kw ? (double)a.kw[i] : 1.0;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.batch; i += 256) {
+    const int c0 = a.cu[i], c1 = a.cu[i + 1];
+    scu[i] = c0;
+    sctx[i] = a.ctx[i];
+    if (i == a.batch - 1) scu[a.batch] = c1;
+    if (c0 < 0 || c1 < c0 || c1 > a.total_rows) atomicMin(&sbroken, i);
   }
   __syncthreads();
   const int broken = sbroken;
-  const int per_row = a.heads + 2 * a.kv_heads;
-  const int64_t tasks = (int64_t)a.total_rows * per_row;
-  const int c = tid % LPH;                    // dims 8c .. 8c+7
 
   // the lanes of a head go through the loop together; a head never crosses a wave
-  for (int64_t t0 = (int64_t)blockIdx.x * TASKS; t0 < tasks; t0 += (int64_t)a.data_blocks * TASKS) {
-    const int64_t task = t0 + tid / LPH;
-    bool live = task < tasks;
-    const int row = live ? (int)(task / per_row) : 0;
-    const int hh = live ? (int)(task - (int64_t)row * per_row) : 0;
+  for (uint32_t t0 = blockIdx.x * TASKS; t0 < tasks; t0 += step) {
+    const int row = next_row, hh = next_hh;
+    T raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = next[i];
+    // (behind the last task the last row once more: no branch around the loads)
+    locate(min(t0 + step, tasks - 1), next_row, next_hh);
+    ask(next_row, next_hh, next);
     // its request: the last with cu[b] <= row (good up to `broken`)
     int lo = 0, hi = broken;
     while (lo < hi) {
@@ -167,68 +201,43 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
       if (scu[mid + 1] <= row) lo = mid + 1;
       else hi = mid;
     }
-    const int b = lo;
-    live = live && b < broken && row >= scu[b];
-    int64_t pos = 0;
-    if (live) {
-      const int ctx = a.ctx[b];
-      pos = (int64_t)ctx + (row - scu[b]);
-      live = ctx >= 0 && pos < a.max_position;
-    }
+    const int b = lo, ctx = sctx[min(b, a.batch - 1)], row0 = scu[min(b, a.batch - 1)];
+    const int64_t pos = (int64_t)ctx + (row - row0);
+    const bool live = row < a.total_rows && b < broken && row >= row0 && ctx >= 0 &&
+                      pos < a.max_position;
     const bool is_q = hh < a.heads;
     const bool is_k = !is_q && hh < a.heads + a.kv_heads;
     const int kh = is_q ? 0 : is_k ? hh - a.heads : hh - a.heads - a.kv_heads;
-    const T* src = is_q   ? (const T*)a.q + (int64_t)row * a.ld_q + (int64_t)hh * D
-                   : is_k ? (const T*)a.k + (int64_t)row * a.ld_k + (int64_t)kh * D
-                          : (const T*)a.v + (int64_t)row * a.ld_v + (int64_t)kh * D;
-    T raw[8];
-    if (live) {
-      __builtin_memcpy(raw, src + 8 * c, sizeof(raw));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) raw[i] = (T)0.f;
+    // requested ahead of their use: the page and the angles
+    const int64_t slot = pos >> a.page_log2;
+    const bool held = live && !is_q && slot < a.ld_table;
+    const uint32_t id = (uint32_t)a.table[held ? (int64_t)b * a.ld_table + slot : 0];
+    const int half = a.rot / 2;
+    const bool turn = live && (is_q || is_k) && 8 * c < a.rot;
+    const bool second = 8 * c >= half;
+    float co[8], si[8];
+    if (a.rot) {
+      const float* cs = a.cos_sin + (turn ? pos : 0) * a.rot;
+      if (a.interleaved) {
+        const int at = turn ? 4 * c : 0;
+        __builtin_memcpy(co, cs + at, 16);
+        __builtin_memcpy(si, cs + half + at, 16);
+      } else {
+        const int at = turn ? 8 * c - (second ? half : 0) : 0;
+        __builtin_memcpy(co, cs + at, sizeof(co));
+        __builtin_memcpy(si, cs + half + at, sizeof(si));
+      }
     }
 
-    uint32_t word = 0;       // the lane's 8 codes
-    int byte = 1;            // the scale of its block of 32 dims
+    float y[8];
     if (!is_q && !is_k) {
-      // V goes in as it is: fp32 holds it, and scaling by a power of two is exact
-      // (what underflows is far below the first border; its sign is kept)
-      float amax = 0;
-      bool bad = false;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = __builtin_fabsf((float)raw[i]);
-        amax = __builtin_fmaxf(amax, v);
-        bad |= !(v < __builtin_inff());
-      }
-      amax = __builtin_fmaxf(amax, dpp_f32<DPP_XOR1>(amax));
-      amax = __builtin_fmaxf(amax, dpp_f32<DPP_XOR2>(amax));
-      float nan = bad ? 1.f : 0.f;
-      nan = __builtin_fmaxf(nan, dpp_f32<DPP_XOR1>(nan));
-      nan = __builtin_fmaxf(nan, dpp_f32<DPP_XOR2>(nan));
-      bad = nan != 0.f;
-      if (amax > 0 && !bad) {
-        const int e = __builtin_amdgcn_frexp_expf(amax) - 1;
-        const float f = __builtin_amdgcn_ldexpf(amax, -e);
-        byte = e + 127 - (f > 1.5f ? 1 : 2);
-        byte = byte < 1 ? 1 : byte > 252 ? 252 : byte;
-      }
-      float z[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = (float)raw[i];
-        const float y = __builtin_amdgcn_ldexpf(v, 127 - byte);
-        z[i] = bad ? 0.f : v < 0.f ? __builtin_fminf(y, -1e-30f) : y + 0.f;
-      }
-      word = pack_codes(z);
-      if (bad) byte = 255;
+      for (int i = 0; i < 8; ++i) y[i] = (float)raw[i];         // V goes in as it is
     } else {
       double x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = (double)(float)raw[i];
-      const float* w = is_q ? a.qw : a.kw;
-      if (w) {
+      if (is_q ? a.qw != nullptr : a.kw != nullptr) {
         double ss = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __builtin_fma(x[i], x[i], ss);
@@ -238,89 +247,76 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
         if constexpr (LPH >= 16) ss += dpp_f64<DPP_MIRROR16>(ss);
         if constexpr (LPH >= 32) ss += shfl_xor_f64(ss, 16);
         const double inv = rsqrt_f64(ss * (1.0 / D) + (double)a.eps);
-        float wf[8];
-        __builtin_memcpy(wf, w + 8 * c, sizeof(wf));
+        const double* w = sw[is_q ? 0 : 1] + 8 * c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * (inv * (double)wf[i]);
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * (inv * w[i]);
       }
       if (a.rot) {
-        const int half = a.rot / 2;
-        const bool turn = live && 8 * c < a.rot;
-        const float* cs = a.cos_sin + (turn ? pos : 0) * a.rot;
         if (a.interleaved) {
           if (turn) {
-            float co[4], si[4];
-            __builtin_memcpy(co, cs + 4 * c, sizeof(co));
-            __builtin_memcpy(si, cs + half + 4 * c, sizeof(si));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const double u = x[2 * i], v = x[2 * i + 1];
-              x[2 * i] = u * co[i] - v * si[i];
-              x[2 * i + 1] = v * co[i] + u * si[i];
+              x[2 * i] = __builtin_fma(v, -(double)si[i], u * (double)co[i]);
+              x[2 * i + 1] = __builtin_fma(u, (double)si[i], v * (double)co[i]);
             }
           }
         } else {
           // dim i of the first half turns with dim i + half: half/8 lanes away
-          const bool second = 8 * c >= half;
           const int partner = lane + (turn ? (second ? -half / 8 : half / 8) : 0);
-          double y[8];
+          double y2[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = shfl_f64(x[i], partner);
+          for (int i = 0; i < 8; ++i) y2[i] = shfl_f64(x[i], partner);
           if (turn) {
-            float co[8], si[8];
-            const int at = 8 * c - (second ? half : 0);
-            __builtin_memcpy(co, cs + at, sizeof(co));
-            __builtin_memcpy(si, cs + half + at, sizeof(si));
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              x[i] = __builtin_fma(y[i], (double)(second ? si[i] : -si[i]), x[i] * (double)co[i]);
+              x[i] = __builtin_fma(y2[i], (double)(second ? si[i] : -si[i]), x[i] * (double)co[i]);
           }
         }
       }
       if (is_q) {
         if (live) {
-          T y[8];
+          T r[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = round_to<T>(x[i]);
-          __builtin_memcpy((T*)a.q_out + (int64_t)row * a.ld_qout + (int64_t)hh * D + 8 * c, y,
-                           sizeof(y));
+          for (int i = 0; i < 8; ++i) r[i] = round_to<T>(x[i]);
+          __builtin_memcpy((T*)a.q_out + (int64_t)row * a.ld_qout + (int64_t)hh * D + 8 * c, r,
+                           sizeof(r));
         }
         continue;
       }
-      // the block of 32 dims: smallest power of two that holds its largest
-      // magnitude as 6 (codes end at 6), within [2^-126, 2^125]
-      double amax = 0;
-      bool bad = false;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        amax = __builtin_fmax(amax, __builtin_fabs(x[i]));
-        bad |= !(__builtin_fabs(x[i]) < __builtin_inf());
-      }
-      amax = __builtin_fmax(amax, dpp_f64<DPP_XOR1>(amax));
-      amax = __builtin_fmax(amax, dpp_f64<DPP_XOR2>(amax));
-      float nan = bad ? 1.f : 0.f;
-      nan = __builtin_fmaxf(nan, dpp_f32<DPP_XOR1>(nan));
-      nan = __builtin_fmaxf(nan, dpp_f32<DPP_XOR2>(nan));
-      bad = nan != 0.f;
-      if (amax > 0 && !bad) {
-        // amax = f 2^e, f in [1, 2): f <= 1.5 fits 6 * 2^(e-2), else 6 * 2^(e-1)
-        const int e = __builtin_amdgcn_frexp_exp(amax) - 1;
-        const double f = __builtin_amdgcn_ldexp(amax, -e);
-        byte = e + 127 - (f > 1.5 ? 1 : 2);
-        byte = byte < 1 ? 1 : byte > 252 ? 252 : byte;
-      }
-      float z[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // |x| may pass the largest code where the scale stopped at 2^125
-        const double y = __builtin_amdgcn_ldexp(x[i], 127 - byte);
-        z[i] = bad ? 0.f : sticky_f32(__builtin_fmin(__builtin_fmax(y, -8.0), 8.0)) + 0.f;
-      }
-      word = pack_codes(z);
-      if (bad) byte = 255;
+      for (int i = 0; i < 8; ++i) y[i] = odd_f32(x[i]);
     }
+
+    // the block of 32 dims (four lanes): smallest power of two that holds its largest
+    // magnitude as 6 (codes end at 6), within [2^-126, 2^125]; 255 if one is not finite
+    float amax = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      amax = __builtin_fmaxf(amax, __builtin_fabsf(y[i]));
+      bad |= !(__builtin_fabsf(y[i]) < __builtin_inff());
+    }
+    amax = bad ? __builtin_inff() : amax;
+    amax = __builtin_fmaxf(amax, dpp_f32<DPP_XOR1>(amax));
+    amax = __builtin_fmaxf(amax, dpp_f32<DPP_XOR2>(amax));
+    bad = amax == __builtin_inff();
+    // amax = f 2^e, f in [1, 2): f <= 1.5 fits 6 * 2^(e-2), else 6 * 2^(e-1)
+    const int e = __builtin_amdgcn_frexp_expf(amax) - 1;
+    const float f = __builtin_amdgcn_ldexpf(amax, -e);
+    int byte = e + 127 - (f > 1.5f ? 1 : 2);
+    byte = amax > 0.f ? min(max(byte, 1), 252) : 1;
+    // scaling by a power of two is exact down to where fp32 underflows, far below the
+    // first border (only the sign is kept there); past the largest code it saturates
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float z = __builtin_amdgcn_ldexpf(y[i], 127 - byte);
+      z = y[i] < 0.f ? __builtin_fminf(z, -1e-30f) : z + 0.f;
+      y[i] = bad ? 0.f : z;
+    }
+    const uint32_t word = pack_codes(y);                      // the lane's 8 codes
+    if (bad) byte = 255;
     if (!live) continue;
-    const bool bad = byte == 255;
 
     if (a.k_val) {                            // the values the cache now stands for
       const float sc = bad ? __builtin_nanf("") : __builtin_bit_cast(float, (uint32_t)byte << 23);
@@ -328,15 +324,12 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
       const f32x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.f, 1);
       const f32x2 y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.f, 2);
       const f32x2 y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.f, 3);
-      const T y[8] = {(T)(y0[0] * sc), (T)(y0[1] * sc), (T)(y1[0] * sc), (T)(y1[1] * sc),
+      const T r[8] = {(T)(y0[0] * sc), (T)(y0[1] * sc), (T)(y1[0] * sc), (T)(y1[1] * sc),
                       (T)(y2[0] * sc), (T)(y2[1] * sc), (T)(y3[0] * sc), (T)(y3[1] * sc)};
       T* dst = (T*)(is_k ? a.k_val : a.v_val) + ((int64_t)row * a.kv_heads + kh) * D + 8 * c;
-      __builtin_memcpy(dst, y, sizeof(y));
+      __builtin_memcpy(dst, r, sizeof(r));
     }
-    const int64_t slot = pos >> a.page_log2;
-    if (slot >= a.ld_table) continue;
-    const uint32_t id = (uint32_t)a.table[(int64_t)b * a.ld_table + slot];
-    if (id >= (uint64_t)a.num_pages) continue;
+    if (!held || id >= (uint64_t)a.num_pages) continue;
     const int P = a.page, t = (int)pos & (P - 1);
     uint8_t* u = a.pages + ((int64_t)id * a.kv_heads + kh) * unit_bytes(P, D);
     uint8_t* sc = u + (is_k ? off_ks(P, D) : off_vs(P, D)) + (t >> 3) * (D / 4) + (t & 7);
@@ -866,7 +859,8 @@ int spec_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, con
       kv_heads < 1 || heads < kv_heads || heads > 1024 || heads % kv_heads != 0 ||
       ld_q < heads * d || ld_k < kv_heads * d || ld_v < kv_heads * d || ld_qout < heads * d ||
       rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0 || (rot_dim && max_position < 1) ||
-      !(eps >= 0.f) || !(eps <= 1.f) || !aligned16(pages))
+      !(eps >= 0.f) || !(eps <= 1.f) || !aligned16(pages) ||
+      (int64_t)total_rows * (heads + 2 * kv_heads) >= (1ll << 31) - 65536)
     return SV_ERR_SHAPE;
   AppendArgs a;
   a.q = q;

@@ -110,7 +110,8 @@ def _append(**kw):
     (dict(ldt=(1 << 26) + 1), 2), (dict(ldq=511), 2), (dict(ldk=255), 2), (dict(ldv=255), 2),
     (dict(ldo=511), 2), (dict(cs=F, rot=24, maxp=4), 2), (dict(cs=F, rot=144, maxp=4), 2),
     (dict(cs=F, rot=-16, maxp=4), 2), (dict(cs=F, rot=64, maxp=0), 2), (dict(eps=-1.0), 2),
-    (dict(eps=float("nan")), 2), (dict(eps=2.0), 2), (dict(pages=F + 8), 2)])
+    (dict(eps=float("nan")), 2), (dict(eps=2.0), 2), (dict(pages=F + 8), 2),
+    (dict(rows=1 << 28), 2)])
 def test_append_refuses(kw, rc):
     assert _append(**kw) == rc
 
