@@ -43,6 +43,7 @@ struct AppendArgs {
   void *k_val, *v_val;
   int32_t* status;
   int data_blocks;
+  int tasks, slices, slice_groups;   // waves' shares: rows * slices of the rows' head groups
 };
 
 template <int CTRL>
@@ -111,10 +112,21 @@ __device__ __forceinline__ float round_to<float>(double x) { return (float)x; }
 template <>
 __device__ __forceinline__ __bf16 round_to<__bf16>(double x) { return (__bf16)odd_f32(x); }
 
+// Requests 8 dims of head hh of a row's q, k and v (past the last head: that one).
 template <int D, typename T>
-__global__ __launch_bounds__(256) void k_append(AppendArgs a) {
+__device__ __forceinline__ void ask_head(T* raw, const T* qrow, const T* krow, const T* vrow, int hh,
+                                         int c, int heads, int kv_heads) {
+  hh = min(hh, heads + 2 * kv_heads - 1);
+  const bool q = hh < heads, k = hh < heads + kv_heads;
+  const T* src = q ? qrow : k ? krow : vrow;
+  const int at = hh - (q ? 0 : k ? heads : heads + kv_heads);
+  __builtin_memcpy(raw, src + (uint32_t)(at * D + 8 * c), 8 * sizeof(T));
+}
+
+template <int D, typename T>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : D == 256 ? 2 : 3) void k_append(AppendArgs a) {
   constexpr int LPH = D / 8;                  // lanes per head
-  constexpr int TASKS = 256 / LPH;
+  constexpr int HPW = 64 / LPH;               // heads of a wave
   __shared__ int32_t scu[MAX_BATCH + 1], sctx[MAX_BATCH];
   __shared__ double sw[2][D];                 // the norms' weights
   __shared__ int sbroken;
@@ -142,33 +154,6 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
     return;
   }
 
-  const int per_row = a.heads + 2 * a.kv_heads;
-  const uint32_t tasks = (uint32_t)a.total_rows * (uint32_t)per_row;   // (host: below 2^31)
-  const uint32_t step = (uint32_t)a.data_blocks * TASKS;
-  const float inv_row = 1.f / (float)per_row;
-  const int c = tid % LPH;                    // dims 8c .. 8c+7
-  // the lane's row and head of the tasks from t0 on
-  auto locate = [&](uint32_t t0, int& row, int& hh) {
-    const uint32_t r = t0 / (uint32_t)per_row;
-    // (the head is below per_row + TASKS here, so fp32 divides it right)
-    hh = (int)(t0 - r * (uint32_t)per_row) + tid / LPH;
-    const int up = (int)(((float)hh + 0.5f) * inv_row);
-    hh -= up * per_row;
-    row = (int)r + up;
-  };
-  auto ask = [&](int row, int hh, T* raw) {
-    const int64_t r = min(row, a.total_rows - 1);
-    const int kh = hh < a.heads + a.kv_heads ? hh - a.heads : hh - a.heads - a.kv_heads;
-    const T* src = hh < a.heads                ? (const T*)a.q + r * a.ld_q + (int64_t)hh * D
-                   : hh < a.heads + a.kv_heads ? (const T*)a.k + r * a.ld_k + (int64_t)kh * D
-                                               : (const T*)a.v + r * a.ld_v + (int64_t)kh * D;
-    __builtin_memcpy(raw, src + 8 * c, 8 * sizeof(T));
-  };
-  // the first heads are on their way while the offsets are checked
-  T next[8];
-  int next_row, next_hh;
-  locate(blockIdx.x * TASKS, next_row, next_hh);
-  ask(next_row, next_hh, next);
   if (tid == 0) sbroken = a.batch;
   for (int i = tid; i < D; i += 256) {
     sw[0][i] = a.qw ? (double)a.qw[i] : 1.0;
@@ -184,50 +169,62 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
   }
   __syncthreads();
   const int broken = sbroken;
+  const int per_row = a.heads + 2 * a.kv_heads;
+  const int c = tid % LPH;                    // dims 8c .. 8c+7 of the lane's head
+  const int half = a.rot / 2;
+  const bool second = 8 * c >= half, in_rot = 8 * c < a.rot;
+  const int partner = lane + (in_rot ? (second ? -half / 8 : half / 8) : 0);
 
-  // the lanes of a head go through the loop together; a head never crosses a wave
-  for (uint32_t t0 = blockIdx.x * TASKS; t0 < tasks; t0 += step) {
-    const int row = next_row, hh = next_hh;
-    T raw[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = next[i];
-    // (behind the last task the last row once more: no branch around the loads)
-    locate(min(t0 + step, tasks - 1), next_row, next_hh);
-    ask(next_row, next_hh, next);
+  // a wave takes a row's groups of HPW heads, or a slice of them where rows are few:
+  // what belongs to the row is found once and stays scalar
+  const int wave0 = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int task = wave0; task < a.tasks; task += a.data_blocks * 4) {
+    const int row = task / a.slices, slice = task - row * a.slices;
     // its request: the last with cu[b] <= row (good up to `broken`)
     int lo = 0, hi = broken;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (scu[mid + 1] <= row) lo = mid + 1;
+      if (__builtin_amdgcn_readfirstlane(scu[mid + 1]) <= row) lo = mid + 1;
       else hi = mid;
     }
-    const int b = lo, ctx = sctx[min(b, a.batch - 1)], row0 = scu[min(b, a.batch - 1)];
+    if (lo >= broken) continue;
+    const int b = lo, row0 = __builtin_amdgcn_readfirstlane(scu[b]);
+    const int ctx = __builtin_amdgcn_readfirstlane(sctx[b]);
     const int64_t pos = (int64_t)ctx + (row - row0);
-    const bool live = row < a.total_rows && b < broken && row >= row0 && ctx >= 0 &&
-                      pos < a.max_position;
+    if (row < row0 || ctx < 0 || pos >= a.max_position) continue;
+    // requested ahead of their use: the page and the angles
+    const int64_t slot = pos >> a.page_log2;
+    const uint32_t id = slot < a.ld_table ? (uint32_t)a.table[(int64_t)b * a.ld_table + slot]
+                                          : 0xffffffffu;
+    f32x4 co[2] = {}, si[2] = {};             // pairs of the lane's dims: 8, or 4 interleaved
+    if (a.rot) {
+      const float* cs = a.cos_sin + pos * a.rot;
+      const int at = !in_rot ? 0 : a.interleaved ? 4 * c : 8 * c - (second ? half : 0);
+      const int more = a.interleaved ? 0 : 4;
+      co[0] = load_any<f32x4>(cs + at);
+      co[1] = load_any<f32x4>(cs + at + more);
+      si[0] = load_any<f32x4>(cs + half + at);
+      si[1] = load_any<f32x4>(cs + half + at + more);
+    }
+    const T* qrow = (const T*)a.q + (int64_t)row * a.ld_q;
+    const T* krow = (const T*)a.k + (int64_t)row * a.ld_k;
+    const T* vrow = (const T*)a.v + (int64_t)row * a.ld_v;
+    const int g0 = slice * a.slice_groups;
+    const int g1 = min(g0 + a.slice_groups, (per_row + HPW - 1) / HPW);
+    T next[8];
+    ask_head<D, T>(next, qrow, krow, vrow, g0 * HPW + lane / LPH, c, a.heads, a.kv_heads);
+    for (int g = g0; g < g1; ++g) {
+    T raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = next[i];
+    ask_head<D, T>(next, qrow, krow, vrow, min(g + 1, g1 - 1) * HPW + lane / LPH, c, a.heads,
+                   a.kv_heads);
+    const int hh = g * HPW + lane / LPH;
+    const bool live = hh < per_row;
     const bool is_q = hh < a.heads;
     const bool is_k = !is_q && hh < a.heads + a.kv_heads;
     const int kh = is_q ? 0 : is_k ? hh - a.heads : hh - a.heads - a.kv_heads;
-    // requested ahead of their use: the page and the angles
-    const int64_t slot = pos >> a.page_log2;
-    const bool held = live && !is_q && slot < a.ld_table;
-    const uint32_t id = (uint32_t)a.table[held ? (int64_t)b * a.ld_table + slot : 0];
-    const int half = a.rot / 2;
-    const bool turn = live && (is_q || is_k) && 8 * c < a.rot;
-    const bool second = 8 * c >= half;
-    float co[8], si[8];
-    if (a.rot) {
-      const float* cs = a.cos_sin + (turn ? pos : 0) * a.rot;
-      if (a.interleaved) {
-        const int at = turn ? 4 * c : 0;
-        __builtin_memcpy(co, cs + at, 16);
-        __builtin_memcpy(si, cs + half + at, 16);
-      } else {
-        const int at = turn ? 8 * c - (second ? half : 0) : 0;
-        __builtin_memcpy(co, cs + at, sizeof(co));
-        __builtin_memcpy(si, cs + half + at, sizeof(si));
-      }
-    }
+    const bool turn = in_rot;
 
     float y[8];
     if (!is_q && !is_k) {
@@ -257,20 +254,20 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const double u = x[2 * i], v = x[2 * i + 1];
-              x[2 * i] = __builtin_fma(v, -(double)si[i], u * (double)co[i]);
-              x[2 * i + 1] = __builtin_fma(u, (double)si[i], v * (double)co[i]);
+              x[2 * i] = __builtin_fma(v, -(double)si[0][i], u * (double)co[0][i]);
+              x[2 * i + 1] = __builtin_fma(u, (double)si[0][i], v * (double)co[0][i]);
             }
           }
         } else {
           // dim i of the first half turns with dim i + half: half/8 lanes away
-          const int partner = lane + (turn ? (second ? -half / 8 : half / 8) : 0);
           double y2[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) y2[i] = shfl_f64(x[i], partner);
           if (turn) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              x[i] = __builtin_fma(y2[i], (double)(second ? si[i] : -si[i]), x[i] * (double)co[i]);
+              x[i] = __builtin_fma(y2[i], (double)(second ? si[i / 4][i % 4] : -si[i / 4][i % 4]),
+                                   x[i] * (double)co[i / 4][i % 4]);
           }
         }
       }
@@ -329,7 +326,7 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
       T* dst = (T*)(is_k ? a.k_val : a.v_val) + ((int64_t)row * a.kv_heads + kh) * D + 8 * c;
       __builtin_memcpy(dst, r, sizeof(r));
     }
-    if (!held || id >= (uint64_t)a.num_pages) continue;
+    if (id >= (uint64_t)a.num_pages) continue;
     const int P = a.page, t = (int)pos & (P - 1);
     uint8_t* u = a.pages + ((int64_t)id * a.kv_heads + kh) * unit_bytes(P, D);
     uint8_t* sc = u + (is_k ? off_ks(P, D) : off_vs(P, D)) + (t >> 3) * (D / 4) + (t & 7);
@@ -346,6 +343,7 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
       } else {                                // half a 16th per lane
         *(uint32_t*)(d + (c >> 1) * 64 + (c & 1) * 4) = word;
       }
+    }
     }
   }
 }
@@ -822,11 +820,17 @@ static bool pool_ok(int seqs, int page, int64_t ld_table, int64_t num_pages) {
 
 template <int D, typename T>
 static int launch_append(AppendArgs a, hipStream_t s) {
-  constexpr int TASKS = 256 / (D / 8);
-  const int64_t tasks = (int64_t)a.total_rows * (a.heads + 2 * a.kv_heads);
-  int64_t blocks = (tasks + TASKS - 1) / TASKS;
-  if (blocks > 4096) blocks = 4096;
-  a.data_blocks = (int)blocks;
+  // a row per wave where that fills the device (4 waves per SIMD), else slices of rows
+  constexpr int HPW = 512 / D;
+  const int groups = (a.heads + 2 * a.kv_heads + HPW - 1) / HPW;
+  int slices = 4096 / a.total_rows + 1;
+  if (slices > groups) slices = groups;
+  a.slice_groups = (groups + slices - 1) / slices;
+  a.slices = (groups + a.slice_groups - 1) / a.slice_groups;
+  a.tasks = a.total_rows * a.slices;          // (the caller: below 2^31)
+  const int most = sizeof(T) == 2 ? 1024 : D == 256 ? 512 : 768;   // what the device holds at once
+  const int blocks = min((a.tasks + 3) / 4, most);
+  a.data_blocks = blocks;
   hipLaunchKernelGGL((k_append<D, T>), dim3((unsigned)blocks + (a.batch + 3) / 4), dim3(256), 0, s, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
 }
