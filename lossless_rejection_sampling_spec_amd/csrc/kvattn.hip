@@ -12,9 +12,9 @@
 //   S^T[token][row] = K Q^T   then   O^T[dim][row] += V^T P^T
 // with v_mfma_f32_16x16x32_bf16.  With tokens as the rows of S^T, a lane holds
 // the scores of ONE query row (its column), for 8 tokens (4 of each half of the
-// tile) that are exactly the 8 contraction entries of its P^T operand: softmax statistics are per lane
-// and the probabilities go from accumulator to operand without LDS or
-// shuffles.  K and V come as e2m1 codes and are widened to bf16 by the
+// tile) that are exactly the 8 contraction entries of its P^T operand: softmax
+// statistics are per lane and the probabilities go from accumulator to operand
+// without LDS or shuffles.  K and V come as e2m1 codes and are widened to bf16 by the
 // hardware conversion, which applies the power-of-two block scale (exact).
 //
 // What bounds it: HBM reads of the cache (D*17/16 bytes per token and KV head)
@@ -39,9 +39,11 @@ struct AttnArgs {
   const int32_t* cu;
   const int32_t* ctx;
   int batch, total_rows, max_k, heads, kv_heads;
+  int group;            // heads / kv_heads
+  float inv_group;
   const uint8_t* pages;
   int64_t num_pages;
-  int page, page_log2;
+  int page, page_log2, unit;        // tokens of a page; bytes of a page's KV head
   const int32_t* table;
   int64_t ld_table;
   int max_context;
@@ -121,10 +123,21 @@ struct Tile {
   uint32_t vs[2];                     // their scale bytes
 };
 
+// A workgroup's share, the same for all its threads.
+struct Share {
+  Span sp;
+  int row0, ctx, rows, R;       // query rows: first in the call, position, count, times G
+  int rb, tbegin, tend;         // row block, tiles
+  float c;                      // scale log2 e
+  const uint8_t* pool;          // the KV head's unit of page 0
+  uint32_t page_bytes;
+};
+
 template <int D, int MT, typename T>
 struct Attn {
   static constexpr int STEPS = D / 32;           // contraction steps of K Q^T
   static constexpr int FR = D / 16;              // output fragments of 16 dims
+  static constexpr int KB = (D + 127) / 128;     // scale blocks of a lane's K dims
   // fp32 queries and weights are split into three bf16 terms (3 x 8 bits hold
   // fp32's 24): products with the exact bf16 K and V then lose nothing
   static constexpr int NT = sizeof(T) == 4 ? 3 : 1;
@@ -132,8 +145,12 @@ struct Attn {
   bf16x8 q[MT][STEPS][NT];
   f32x4 o[MT][FR];
   f32x4 l[MT];            // sums of the weights: a row of ones among the products (4 equal)
-  float m[MT], mc[MT];    // running max of the raw scores; times scale log2 e, or 0
-  uint32_t poison = 0;    // outputs that saw a V block stored as NaN
+  // running max m of the raw scores: m, m scale log2 e (0 before the first visible
+  // score) and what a score has to pass to raise it
+  float m[MT], mc[MT], over[MT];
+  // rows that saw a block stored as NaN.  V: bit 4 mt + r, dims g*D/4 + r*D/16 ...;
+  // K: bit 16 + mt, all dims
+  uint32_t poison = 0;
 
   static __device__ __forceinline__ void split(float x, __bf16* t) {
     float r = x;
@@ -144,18 +161,23 @@ struct Attn {
     }
   }
 
+  // Row r of a request's R: verify row r / G, query head r % G of the KV head's G
+  // (fp32 divides these right: r < 2^16).
+  static __device__ __forceinline__ int row_of(const AttnArgs& a, int r) {
+    return (int)(((float)r + 0.5f) * a.inv_group);
+  }
+
   // The query rows' operands: requested first, taken over once they are there.
   struct Raw {
     T x[MT][STEPS][8];
   };
-  static __device__ __forceinline__ void ask(const AttnArgs& a, Raw& raw, int row0, int R, int G,
-                                             int h, int rb) {
+  static __device__ __forceinline__ void ask(const AttnArgs& a, Raw& raw, const Share& w, int h) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int r = min((rb * MT + mt) * 16 + n, R - 1);
-      const int j = r / G, hq = h * G + r - j * G;
-      const T* src = (const T*)a.q + (int64_t)(row0 + j) * a.ld_q + (int64_t)hq * D + g * (D / 4);
+      const int r = min((w.rb * MT + mt) * 16 + n, w.R - 1);
+      const int j = row_of(a, r), hq = h * a.group + r - j * a.group;
+      const T* src = (const T*)a.q + (int64_t)(w.row0 + j) * a.ld_q + (uint32_t)(hq * D + g * (D / 4));
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) __builtin_memcpy(raw.x[mt][s], src + 8 * s, sizeof(raw.x[mt][s]));
     }
@@ -163,7 +185,7 @@ struct Attn {
   __device__ __forceinline__ void init(const Raw& raw) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      m[mt] = -INFINITY;
+      m[mt] = over[mt] = -INFINITY;
       mc[mt] = 0.f;
       l[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -181,34 +203,59 @@ struct Attn {
     }
   }
 
-  // Half hf of a tile: 16 tokens at token `tb` of unit p.  The unit's address is
-  // scalar and the lane's offsets are the same in every tile, so the loads need
-  // no vector arithmetic.
-  static __device__ __forceinline__ void load(Tile<D>& t, int hf, const uint8_t* p, int P, int tb) {
+  // Half hf of a tile: 16 tokens at token `tb` of a page's unit.  The unit is a
+  // buffer resource with a scalar base, the token a scalar offset, and the lane's
+  // offsets are the same in every tile: a load costs no vector arithmetic.
+  struct Lane {
+    uint32_t k, ks, v, vs;
+  };
+  static __device__ __forceinline__ Lane lane_offsets(int P) {
     const uint32_t lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    constexpr int KA = D == 64 ? 8 : 16;
-    const uint8_t* k = p + tb * (D / 2);
-    __builtin_memcpy(t.k[hf], __builtin_assume_aligned(k + (n * (D / 2) + g * (D / 8)), KA), D / 8);
-    const uint8_t* ks = p + off_ks(P, D) + tb * (D / 32);
+    Lane o;
+    o.k = n * (D / 2) + g * (D / 8);
+    o.ks = off_ks(P, D) + (n >> 3) * (D / 4) + (g * (D / 4) / 32) * 8 + (n & 7);
+    o.v = off_v(P, D) + (g >> 1) * (4 * D) + n * (D / 4) + (g & 1) * (D / 8);
+    o.vs = off_vs(P, D) + (g >> 1) * (D / 4) + (n * D / 512) * 8 + (g & 1) * 4;
+    return o;
+  }
+  static __device__ __forceinline__ void load(Tile<D>& t, int hf, const uint8_t* unit, int bytes,
+                                              const Lane& at, int tb) {
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc((void*)unit, 0, bytes, 0x00020000);
+    const int sk = tb * (D / 2), ss = tb * (D / 32);
+    if constexpr (D == 64) {
+      const u32x2 k = __builtin_amdgcn_raw_buffer_load_b64(r, at.k, sk, 0);
+      t.k[hf][0] = k[0];
+      t.k[hf][1] = k[1];
+      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, at.v, sk, 0);
+      t.v[hf * 2] = v[0];
+      t.v[hf * 2 + 1] = v[1];
+    } else {
 #pragma unroll
-    for (uint32_t i = 0; i < (D + 127) / 128; ++i)
-      t.ks[hf][i] = ks[(n >> 3) * (D / 4) + (g * (D / 4) / 32 + i) * 8 + (n & 7)];
-    const uint8_t* v = p + off_v(P, D) + tb * (D / 2);
-    __builtin_memcpy(t.v + hf * (D / 32),
-                     __builtin_assume_aligned(
-                         v + ((g >> 1) * (4 * D) + n * (D / 4) + (g & 1) * (D / 8)), KA), D / 8);
-    const uint8_t* vs = p + off_vs(P, D) + tb * (D / 32);
-    __builtin_memcpy(&t.vs[hf], __builtin_assume_aligned(
-        vs + ((g >> 1) * (D / 4) + (n * D / 512) * 8 + (g & 1) * 4), 4), 4);
+      for (int i = 0; i < D / 128; ++i) {
+        const u32x4 k = __builtin_amdgcn_raw_buffer_load_b128(r, at.k + 16 * i, sk, 0);
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, at.v + 16 * i, sk, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          t.k[hf][4 * i + j] = k[j];
+          t.v[hf * (D / 32) + 4 * i + j] = v[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KB; ++i)
+      t.ks[hf][i] = __builtin_amdgcn_raw_buffer_load_b8(r, at.ks + 8 * i, ss, 0);
+    t.vs[hf] = __builtin_amdgcn_raw_buffer_load_b32(r, at.vs, ss, 0);
   }
   // Entry i of a lane's 8 tokens, relative to the tile.
   static __device__ __forceinline__ int token(int g, int i) {
     return 16 * (i >> 2) + 4 * g + (i & 3);
   }
 
-  // masked: some row does not see some token of the tile.
+  // One tile for the first M row tiles.  masked: some row does not see some token.
+  template <int M>
   __device__ __forceinline__ void step(const AttnArgs& a, Tile<D>& t, bool masked, int base,
-                                       int ctx, int R, int G, int rb, const Span& sp, float c) {
+                                       const Share& w) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     auto sees = [&](int tok, int pos) {
       return tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
@@ -219,13 +266,12 @@ struct Attn {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int tok = base + token(g, i);
-        if (tok >= sp.n || (tok < sp.first && tok >= a.sinks)) {
+        if (tok >= w.sp.n || (tok < w.sp.first && tok >= a.sinks)) {
           const int sh = 8 * (i & 3);
           t.vs[i >> 2] = (t.vs[i >> 2] & ~(255u << sh)) | (127u << sh);
         }
       }
     }
-    constexpr int KB = (D + 127) / 128;
     float ksc[2][KB], vsc[8];
     uint32_t top = 0;
 #pragma unroll
@@ -240,86 +286,68 @@ struct Attn {
       vsc[i] = scale_of(t.vs[i >> 2], i & 3);
       top = max(top, __builtin_bit_cast(uint32_t, vsc[i]));
     }
-    // a scale of 255: some block of the tile is stored as NaN
-    const bool odd = __any(top == 0x7f800000u);
+    if (__any(top == 0x7f800000u)) {          // a scale of 255: a block stored as NaN
+      nan_blocks<M>(a, t, base, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vsc[i] = scale_of(t.vs[i >> 2], i & 3);
+    }
     // scores: s[half][mt], lane: row n, tokens base + 16*half + 4g + r
-    f32x4 s[2][MT];
+    f32x4 s[2][M];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) s[hf][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int mt = 0; mt < M; ++mt) s[hf][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
         const float sc = ksc[hf][st / 4];
-        const uint32_t w = t.k[hf][st];
+        const uint32_t x = t.k[hf][st];
         u32x4 kb;
-        kb[0] = widen<0>(w, sc);
-        kb[1] = widen<1>(w, sc);
-        kb[2] = widen<2>(w, sc);
-        kb[3] = widen<3>(w, sc);
+        kb[0] = widen<0>(x, sc);
+        kb[1] = widen<1>(x, sc);
+        kb[2] = widen<2>(x, sc);
+        kb[3] = widen<3>(x, sc);
         const bf16x8 ka = __builtin_bit_cast(bf16x8, kb);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < M; ++mt)
 #pragma unroll
           for (int k = NT - 1; k >= 0; --k)
             s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, q[mt][st][k], s[hf][mt], 0, 0, 0);
       }
     }
-    if (odd) {
-      // a K block stored as NaN: the token's scores are NaN
-      uint32_t any = 0;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int i = 0; i < KB; ++i) any |= (t.ks[hf][i] == 255u ? 1u : 0u) << hf;
-      any |= (uint32_t)__shfl_xor((int)any, 16);
-      any |= (uint32_t)__shfl_xor((int)any, 32);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t f = (uint32_t)__shfl((int)any, 4 * g + r);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-          if (f >> hf & 1)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) s[hf][mt][r] = __builtin_nanf("");
-      }
-      nan_values(a, t, base, ctx, G, rb);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) vsc[i] = scale_of(t.vs[i >> 2], i & 3);
-    }
     if (masked) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int pos = ctx + ((rb * MT + mt) * 16 + n) / G;
+      for (int mt = 0; mt < M; ++mt) {
+        const int pos = w.ctx + row_of(a, (w.rb * MT + mt) * 16 + n);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (!sees(base + token(g, i), pos)) s[i >> 2][mt][i & 3] = -INFINITY;
       }
     }
-    bf16x8 p[MT][NT];
+    bf16x8 p[M][NT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int mt = 0; mt < M; ++mt) {
       float mx = fmaxf(fmaxf(s[0][mt][0], s[0][mt][1]), s[0][mt][2]);
       mx = fmaxf(fmaxf(mx, s[0][mt][3]), s[1][mt][0]);
       mx = fmaxf(fmaxf(mx, s[1][mt][1]), s[1][mt][2]);
       mx = fmaxf(mx, s[1][mt][3]);
       // (a first visible score raises -inf; a row that has seen nothing stays there)
-      if (__any((mx - m[mt]) * c > RAISE)) {
+      if (__any(mx > over[mt])) {
         const float nm = fmaxf(m[mt], row_max(mx));
-        const float w = nm == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[mt] - nm) * c);
-        l[mt] *= w;
+        const float f = nm == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[mt] - nm) * w.c);
+        l[mt] *= f;
 #pragma unroll
-        for (int f = 0; f < FR; ++f) o[mt][f] *= w;
+        for (int k = 0; k < FR; ++k) o[mt][k] *= f;
         m[mt] = nm;
-        mc[mt] = nm == -INFINITY ? 0.f : nm * c;
+        mc[mt] = nm == -INFINITY ? 0.f : nm * w.c;
+        over[mt] = nm + RAISE / w.c;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc[mt]));
-        __bf16 w[NT];
-        split(e, w);
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], w.c, -mc[mt]));
+        __bf16 x[NT];
+        split(e, x);
 #pragma unroll
-        for (int k = 0; k < NT; ++k) p[mt][k][i] = w[k];
+        for (int k = 0; k < NT; ++k) p[mt][k][i] = x[k];
       }
     }
     {
@@ -327,7 +355,7 @@ struct Attn {
 #pragma unroll
       for (int i = 0; i < 8; ++i) one[i] = (__bf16)1.f;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < M; ++mt)
 #pragma unroll
         for (int k = NT - 1; k >= 0; --k)
           l[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, p[mt][k], l[mt], 0, 0, 0);
@@ -335,22 +363,22 @@ struct Attn {
     // fragment pair c2: dims 2*c2 and 2*c2+1 of every lane's D/16
 #pragma unroll
     for (int c2 = 0; c2 < FR / 2; ++c2) {
-      uint32_t w[8];
+      uint32_t x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int byte = i * (D / 32) + c2;
-        const uint32_t x = t.v[byte / 4];
-        w[i] = byte % 4 == 0 ? widen<0>(x, vsc[i]) : byte % 4 == 1 ? widen<1>(x, vsc[i])
-             : byte % 4 == 2 ? widen<2>(x, vsc[i]) : widen<3>(x, vsc[i]);
+        const uint32_t v = t.v[byte / 4];
+        x[i] = byte % 4 == 0 ? widen<0>(v, vsc[i]) : byte % 4 == 1 ? widen<1>(v, vsc[i])
+             : byte % 4 == 2 ? widen<2>(v, vsc[i]) : widen<3>(v, vsc[i]);
       }
       u32x4 lo, hi;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        lo[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x05040100u);
-        hi[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x07060302u);
+        lo[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100u);
+        hi[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
       }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < M; ++mt)
 #pragma unroll
         for (int k = NT - 1; k >= 0; --k) {
           o[mt][2 * c2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -361,28 +389,44 @@ struct Attn {
     }
   }
 
-  // V blocks stored as NaN: rows that see the token get NaN in those dims, the
-  // others must not (0 * NaN), so the block is made finite for the product and
-  // `poison` keeps who saw it: bit 4 mt + r, dims g*D/4 + r*D/16 ...
-  __device__ __forceinline__ void nan_values(const AttnArgs& a, Tile<D>& t, int base, int ctx, int G,
-                                             int rb) {
+  // Blocks stored as NaN.  K: every row that sees the token is NaN.  V: such a row
+  // gets NaN in the block's dims.  The others must not (0 * NaN), so `poison` keeps
+  // who saw what and V is made finite for the products; the scores that a K block
+  // spoils are those of rows that are NaN anyway or that the mask replaces.
+  template <int M>
+  __device__ __forceinline__ void nan_blocks(const AttnArgs& a, Tile<D>& t, int base,
+                                             const Share& w) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    auto sees = [&](int tok, int mt) {
+      const int pos = w.ctx + row_of(a, (w.rb * MT + mt) * 16 + n);
+      return tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
+    };
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < KB; ++i) odd |= t.ks[hf][i] == 255u;
+      uint64_t b = __ballot(odd);             // bit 16 g + n: token n
+      b |= b >> 32;
+      b = (b | b >> 16) & 0xffffu;
+      for (; b; b &= b - 1)
+#pragma nounroll
+        for (int mt = 0; mt < M; ++mt)
+          if (sees(base + 16 * hf + __builtin_ctzll(b), mt)) poison |= 0x10000u << mt;
+    }
 #pragma nounroll
     for (int src = 0; src < 64; ++src) {
       if (src & 15 & (16 / STEPS - 1)) continue;        // one lane per block of 32 dims
       const int block = (src & 15) / (16 / STEPS);
 #pragma nounroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t w = (uint32_t)__builtin_amdgcn_readlane((int)(i < 4 ? t.vs[0] : t.vs[1]), src);
-        if (((w >> (8 * (i & 3))) & 255u) != 255u) continue;
+        const uint32_t x = (uint32_t)__builtin_amdgcn_readlane((int)(i < 4 ? t.vs[0] : t.vs[1]), src);
+        if (((x >> (8 * (i & 3))) & 255u) != 255u) continue;
         const int tok = base + token(src >> 4, i);
 #pragma nounroll
-        for (int bit = 0; bit < 4 * MT; ++bit) {
-          const int pos = ctx + ((rb * MT + (bit >> 2)) * 16 + n) / G;
-          const bool sees =
-              tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
+        for (int bit = 0; bit < 4 * M; ++bit) {
           const int mine = (g * (D / 4) + (bit & 3) * (D / 16)) / 32;
-          if (sees && mine == block) poison |= 1u << bit;
+          if (mine == block && sees(tok, bit >> 2)) poison |= 1u << bit;
         }
       }
     }
@@ -392,12 +436,47 @@ struct Attn {
   }
   __device__ __forceinline__ void apply_poison() {
 #pragma unroll
-    for (int bit = 0; bit < 4 * MT; ++bit)
-      if (poison >> bit & 1)
+    for (int mt = 0; mt < MT; ++mt) {
+      if (poison >> (16 + mt) & 1) l[mt][0] = __builtin_nanf("");
 #pragma unroll
-        for (int f = 0; f < FR; ++f) o[bit >> 2][f][bit & 3] = __builtin_nanf("");
+      for (int r = 0; r < 4; ++r)
+        if (poison >> (4 * mt + r) & 1)
+#pragma unroll
+          for (int f = 0; f < FR; ++f) o[mt][f][r] = __builtin_nanf("");
+    }
   }
 
+  // The wave's tiles: every WAVES-th of the share, for the first M row tiles.
+  // id: lane i holds the pages of tile tbegin + i (its two halves).
+  template <int M, int DEPTH>
+  __device__ __forceinline__ void run(const AttnArgs& a, const Share& w, Tile<D> (&t)[DEPTH],
+                                      const int (&id)[2], const Lane& at, int wave) {
+    const int last = w.tend - 1;
+    for (int i = w.tbegin + wave; i < w.tend; i += DEPTH * WAVES) {
+#pragma unroll
+      for (int k = 0; k < DEPTH; ++k) {
+        if (i + k * WAVES < w.tend) {
+          const int base = base_of(w.sp, i + k * WAVES);
+          const bool masked =
+              base + TILE - 1 > w.ctx ||
+              (a.window > 0 && base <= w.ctx + w.rows - 1 - a.window && base + TILE > a.sinks);
+          step<M>(a, t[k], masked, base, w);
+        }
+        fetch(a, w, t[k], id, at, min(i + (k + DEPTH) * WAVES, last));
+      }
+    }
+  }
+  static __device__ __forceinline__ int base_of(const Span& sp, int i) {
+    return (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.tile0) * TILE;
+  }
+  static __device__ __forceinline__ void fetch(const AttnArgs& a, const Share& w, Tile<D>& t,
+                                               const int (&id)[2], const Lane& at, int i) {
+    const uint32_t i0 = (uint32_t)__builtin_amdgcn_readlane(id[0], i - w.tbegin);
+    const uint32_t i1 = (uint32_t)__builtin_amdgcn_readlane(id[1], i - w.tbegin);
+    const int tb = base_of(w.sp, i) & (a.page - 1);
+    load(t, 0, w.pool + (uint64_t)i0 * w.page_bytes, a.unit, at, tb);
+    load(t, 1, w.pool + (uint64_t)i1 * w.page_bytes, a.unit, at, (tb + 16) & (a.page - 1));
+  }
 };
 
 template <typename T, int N>
@@ -509,7 +588,6 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
   __shared__ float part_o[WAVES][MT * FR * 4][64];
   __shared__ float part_m[WAVES][MT][16], part_l[WAVES][MT][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = a.heads / a.kv_heads;
   const int items = a.batch * a.kv_heads * a.row_blocks * a.chunks;
   const int status_blocks = (a.batch + WAVES - 1) / WAVES;
 
@@ -553,71 +631,63 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
     chunk = a.chunks - 1 - it / a.batch;
     const int broken = first_broken(a.cu, a.batch, a.total_rows);
     st = request_status(a, b, broken, row0, rows, ctx);
-    if (st == SV_ROW_BAD_K || rb * MT * 16 >= rows * G) return;
+    if (st == SV_ROW_BAD_K || rb * MT * 16 >= rows * a.group) return;
   }
-  const int R = rows * G;
-  const Span sp = span_of(ctx, rows, a.window, a.sinks);
-  const int over = (sp.tiles - 1) % a.chunk_tiles + 1;
-  const int tend = over + chunk * a.chunk_tiles, tbegin = max(0, tend - a.chunk_tiles);
-  if (st == SV_ROW_OK ? tend > sp.tiles : chunk > 0) return;
-  const float c = a.scale * LOG2E;
+  Share w;
+  w.sp = span_of(ctx, rows, a.window, a.sinks);
+  const int over = (w.sp.tiles - 1) % a.chunk_tiles + 1;
+  w.tend = over + chunk * a.chunk_tiles;
+  w.tbegin = max(0, w.tend - a.chunk_tiles);
+  if (st == SV_ROW_OK ? w.tend > w.sp.tiles : chunk > 0) return;
+  w.row0 = row0;
+  w.ctx = ctx;
+  w.rows = rows;
+  w.R = rows * a.group;
+  w.rb = rb;
+  w.c = a.scale * LOG2E;
+  w.pool = a.pages + (int64_t)h * a.unit;
+  w.page_bytes = (uint32_t)a.unit * (uint32_t)a.kv_heads;
+  const float c = w.c;
+  const int R = w.R;
 
   A x;
   typename A::Raw raw;
   bool bad = st != SV_ROW_OK;
   if (bad) {
-    A::ask(a, raw, row0, R, G, h, rb);
+    A::ask(a, raw, w, h);
     x.init(raw);
   } else {
     const int32_t* tab = a.table + (int64_t)b * a.ld_table;
-    const int64_t unit = unit_bytes(a.page, D), page_bytes = unit * a.kv_heads;
-    const uint8_t* pool = a.pages + h * unit;
-    auto base_of = [&](int i) {
-      return (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.tile0) * TILE;
-    };
     // lane i: the pages of the chunk's tile i (its first and second 16 tokens)
     int id[2];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const int slot = (base_of(tbegin + lane) + 16 * hf) >> a.page_log2;
-      const bool need = tbegin + lane < tend && page_needed(sp, slot, a.page_log2, a.sinks);
+      const int slot = (A::base_of(w.sp, w.tbegin + lane) + 16 * hf) >> a.page_log2;
+      const bool need = w.tbegin + lane < w.tend && page_needed(w.sp, slot, a.page_log2, a.sinks);
       const bool have = need && slot < a.ld_table;
       id[hf] = tab[have ? slot : 0];
       const bool in_pool = have && (uint32_t)id[hf] < (uint64_t)a.num_pages;
       bad |= need && !in_pool;
       if (!in_pool) id[hf] = 0;
     }
-    A::ask(a, raw, row0, R, G, h, rb);
+    A::ask(a, raw, w, h);
     bad = __any(bad);
-    auto fetch = [&](Tile<D>& t, int i) {
-      const int64_t i0 = __builtin_amdgcn_readlane(id[0], i - tbegin);
-      const int64_t i1 = __builtin_amdgcn_readlane(id[1], i - tbegin);
-      const int tb = base_of(i) & (a.page - 1);
-      A::load(t, 0, pool + i0 * page_bytes, a.page, tb);
-      A::load(t, 1, pool + i1 * page_bytes, a.page, (tb + 16) & (a.page - 1));
-    };
-    auto work = [&](Tile<D>& t, int i) {
-      const int base = base_of(i);
-      const bool masked = base + TILE - 1 > ctx ||
-                          (a.window > 0 && base <= ctx + rows - 1 - a.window && base + TILE > a.sinks);
-      x.step(a, t, masked, base, ctx, R, G, rb, sp, c);
-    };
+    const typename A::Lane at = A::lane_offsets(a.page);
     // DEPTH tiles are on their way at any time: a buffer is filled again as soon
     // as its tile is done.  Past the end the last tile is loaded once more: with a
     // branch around the loads the compiler could not count those in flight and
     // would wait for all of them at every tile.
     Tile<D> t[DEPTH];
-    const int last = tend - 1;
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k) fetch(t[k], min(tbegin + wave + k * WAVES, last));
+    for (int k = 0; k < DEPTH; ++k)
+      A::fetch(a, w, t[k], id, at, min(w.tbegin + wave + k * WAVES, w.tend - 1));
     x.init(raw);
-    for (int i = tbegin + wave; i < tend; i += DEPTH * WAVES) {
-#pragma unroll
-      for (int k = 0; k < DEPTH; ++k) {
-        if (i + k * WAVES < tend) work(t[k], i + k * WAVES);
-        fetch(t[k], min(i + (k + DEPTH) * WAVES, last));
-      }
-    }
+    // row tiles that hold rows: a short request does not pay for a long one's
+    const int tiles = (min(R - rb * MT * 16, MT * 16) + 15) / 16;
+    if (MT == 1 || tiles == 1) x.template run<1>(a, w, t, id, at, wave);
+    else if (MT == 2 || tiles == 2) x.template run<MT < 2 ? 1 : 2>(a, w, t, id, at, wave);
+    else if (tiles == 3) x.template run<MT < 3 ? 1 : 3>(a, w, t, id, at, wave);
+    else x.template run<MT>(a, w, t, id, at, wave);
   }
   if (__any(x.poison != 0)) x.apply_poison();
 
@@ -638,7 +708,7 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
   }
   __syncthreads();
 
-  const bool whole = st != SV_ROW_OK || sp.tiles <= a.chunk_tiles;
+  const bool whole = st != SV_ROW_OK || w.sp.tiles <= a.chunk_tiles;
   // this item's place among the partials
   const int64_t item = (((int64_t)chunk * a.batch + b) * a.kv_heads + h) * a.row_blocks + rb;
   float* part = a.part + item * (MT * 16) * D;
@@ -650,26 +720,26 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
     float m = part_m[0][mt][n];
 #pragma unroll
     for (int k = 1; k < WAVES; ++k) m = fmaxf(m, part_m[k][mt][n]);
-    float w[WAVES], sum = 0.f, y[FR];
+    float part_w[WAVES], sum = 0.f, y[FR];
 #pragma unroll
     for (int k = 0; k < WAVES; ++k) {
       const float mk = part_m[k][mt][n];
-      w[k] = mk == m ? 1.f : __builtin_amdgcn_exp2f((mk - m) * c);
-      sum += part_l[k][mt][n] * w[k];
+      part_w[k] = mk == m ? 1.f : __builtin_amdgcn_exp2f((mk - m) * c);
+      sum += part_l[k][mt][n] * part_w[k];
     }
 #pragma unroll
     for (int f = 0; f < FR; ++f) {
       y[f] = 0.f;
 #pragma unroll
       for (int k = 0; k < WAVES; ++k)
-        y[f] = __builtin_fmaf(part_o[k][(mt * FR + f) * 4 + wave][lane], w[k], y[f]);
+        y[f] = __builtin_fmaf(part_o[k][(mt * FR + f) * 4 + wave][lane], part_w[k], y[f]);
     }
     if (r >= R) continue;
     if (whole) {
       const float inv = 1.f / sum;
 #pragma unroll
       for (int f = 0; f < FR; ++f) y[f] *= inv;
-      const int j = r / G, hq = h * G + r - j * G;
+      const int j = A::row_of(a, r), hq = h * a.group + r - j * a.group;
       store_row<T, FR>((T*)a.out + (int64_t)(row0 + j) * a.ld_out + (int64_t)hq * D + dim, y);
     } else {
       store_row<float, FR>(part + (mt * 16 + n) * D + dim, y);
@@ -872,6 +942,9 @@ int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_
   a.max_k = max_k;
   a.heads = heads;
   a.kv_heads = kv_heads;
+  a.group = heads / kv_heads;
+  a.inv_group = 1.f / (float)a.group;
+  a.unit = (int)unit_bytes(page_size, head_dim);
   a.pages = (const uint8_t*)pages;
   a.num_pages = num_pages;
   a.page = page_size;
