@@ -496,7 +496,9 @@ struct Item {
 // full chunks of all requests, then the chunks 0, which hold what is left over of
 // full ones.  So the shortest start last, and workgroups without an item come
 // after all others (a batch of ragged contexts has a third of the items that its
-// sizes allow).  One workgroup of 1,024, a thread per request, then per item.
+// sizes allow).  (Starting every compute unit with a full chunk
+// beside a chunk 0, so that they do not end together, changed nothing.)  One
+// workgroup of 1,024, a thread per request, then per item.
 __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
   __shared__ int wred[3][16], sfull[MAX_BATCH + 1], srest[MAX_BATCH + 1], seach[MAX_BATCH];
   __shared__ int srow0[MAX_BATCH], srows[MAX_BATCH], sctx[MAX_BATCH];
@@ -561,7 +563,7 @@ __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
     const bool rem = i >= all_full;
     const int* start = rem ? srest : sfull;
     const int at = rem ? i - all_full : i;
-    int lo = 0, hi = MAX_BATCH;               // the request whose range holds it
+    int lo = 0, hi = a.batch;                 // the request whose range holds it
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (start[mid] <= at) lo = mid;
@@ -751,18 +753,16 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
   }
 }
 
-// Joins the chunks of requests longer than one: WR waves per row.
-template <int D, int MT, int WR, typename T>
+// Joins the chunks of requests longer than one: a workgroup per row.
+template <int D, int MT, typename T>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int E = D / 64;                  // dims per lane
   __shared__ float red[WAVES][D + 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int broken = first_broken(a.cu, a.batch, a.total_rows);
-  const int G = a.heads / a.kv_heads;
-  constexpr int PER = MT * 16 / (WAVES / WR);      // workgroups of one item
   int it = blockIdx.x;
-  const int local = (it % PER) * (WAVES / WR) + wave / WR;
-  it /= PER;
+  const int local = it % (MT * 16);          // the row in its item
+  it /= MT * 16;
   const int first = it;                      // its item of chunk 0
   const int rb = it % a.row_blocks;
   it /= a.row_blocks;
@@ -772,21 +772,19 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   const Span sp = span_of(ctx, rows, a.window, a.sinks);
   const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
   const int r = rb * MT * 16 + local;
-  if (n < 2) return;
-  const bool live = r < rows * G;
+  if (n < 2 || r >= rows * a.group) return;
   const int64_t per_chunk = (int64_t)a.batch * a.kv_heads * a.row_blocks;
   const float* part = a.part + ((int64_t)first * (MT * 16) + local) * D + lane * E;
   const float* stat = a.part + per_chunk * a.chunks * (MT * 16) * D + ((int64_t)first * (MT * 16) + local) * 2;
   const int64_t step = per_chunk * (MT * 16);
   const float c = a.scale * LOG2E;
   float m = -INFINITY;
-  if (live)
-    for (int k = lane; k < n; k += 64) m = fmaxf(m, stat[k * step * 2]);
+  for (int k = lane; k < n; k += 64) m = fmaxf(m, stat[k * step * 2]);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  // every wave of the row weighs the chunks the same; it adds up every WR-th
+  // every wave weighs the chunks the same; it adds up every fourth
   float acc[E] = {}, sum = 0.f;
-  for (int k0 = 0; k0 < n && live; k0 += 64) {
+  for (int k0 = 0; k0 < n; k0 += 64) {
     float w = 0.f;
     if (k0 + lane < n) {
       const float mk = stat[(k0 + lane) * step * 2];
@@ -794,14 +792,14 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
       sum += w * stat[(k0 + lane) * step * 2 + 1];
     }
     const int most = min(64, n - k0);
-    for (int k1 = wave % WR; k1 < most; k1 += 8 * WR) {
+    for (int k1 = wave; k1 < most; k1 += 8 * WAVES) {
       float y[8][E];
 #pragma unroll
       for (int u = 0; u < 8; ++u)             // (past the end: the last chunk once more, weight 0)
-        __builtin_memcpy(y[u], part + (k0 + min(k1 + u * WR, most - 1)) * step * D, sizeof(y[u]));
+        __builtin_memcpy(y[u], part + (k0 + min(k1 + u * WAVES, most - 1)) * step * D, sizeof(y[u]));
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int k = k1 + u * WR;
+        const int k = k1 + u * WAVES;
         const float wk = __builtin_bit_cast(
             float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), min(k, most - 1)));
         if (k < most)
@@ -812,21 +810,74 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-  if constexpr (WR > 1) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) red[wave][lane * E + e] = acc[e];
-    __syncthreads();
-    if (wave != 0) return;
+  for (int e = 0; e < E; ++e) red[wave][lane * E + e] = acc[e];
+  __syncthreads();
+  if (wave != 0) return;
 #pragma unroll
-    for (int w = 1; w < WR; ++w)
+  for (int w = 1; w < WAVES; ++w)
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += red[w][lane * E + e];
-  }
-  if (!live) return;
-  const int j = r / G, hq = h * G + r - j * G;
+    for (int e = 0; e < E; ++e) acc[e] += red[w][lane * E + e];
+  const int j = r / a.group, hq = h * a.group + r - j * a.group;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] /= sum;
   store_row<T, E>((T*)a.out + (int64_t)(row0 + j) * a.ld_out + (int64_t)hq * D + lane * E, acc);
+}
+
+// The same where rows are many and chunks few: 16 threads per row, 16 rows per
+// workgroup, every chunk's part on its way at once.
+template <int D, int MT, typename T>
+__global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
+  constexpr int E = D / 16;                  // dims per thread
+  const int lane = threadIdx.x & 63, j16 = threadIdx.x & 15;
+  const int mt = blockIdx.x % MT, first = blockIdx.x / MT;
+  const int rb = first % a.row_blocks, h = first / a.row_blocks % a.kv_heads;
+  const int b = first / a.row_blocks / a.kv_heads;
+  const int broken = first_broken(a.cu, a.batch, a.total_rows);
+  int row0, rows, ctx;
+  if (request_status(a, b, broken, row0, rows, ctx) != SV_ROW_OK) return;
+  const Span sp = span_of(ctx, rows, a.window, a.sinks);
+  const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+  const int local = mt * 16 + (threadIdx.x >> 4), r = rb * MT * 16 + local;
+  if (n < 2 || r >= rows * a.group) return;  // (whole groups of 16 lanes)
+  const int64_t per_chunk = (int64_t)a.batch * a.kv_heads * a.row_blocks;
+  const int64_t step = per_chunk * (MT * 16);
+  const float* part = a.part + ((int64_t)first * (MT * 16) + local) * D + j16 * E;
+  const float* stat = a.part + step * a.chunks * D + ((int64_t)first * (MT * 16) + local) * 2;
+  const float c = a.scale * LOG2E;
+  float m = -INFINITY;
+  for (int k = j16; k < n; k += 16) m = fmaxf(m, stat[k * step * 2]);
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  float acc[E] = {}, sum = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 16) {
+    float w = 0.f;
+    if (k0 + j16 < n) {
+      const float mk = stat[(k0 + j16) * step * 2];
+      w = mk == m ? 1.f : __builtin_amdgcn_exp2f((mk - m) * c);
+      sum += w * stat[(k0 + j16) * step * 2 + 1];
+    }
+    const int most = min(16, n - k0);
+    for (int k1 = 0; k1 < most; k1 += 4) {
+      float y[4][E];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)             // (past the end: the last chunk once more, unused)
+        __builtin_memcpy(y[u], part + (k0 + min(k1 + u, most - 1)) * step * D, sizeof(y[u]));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float wk = __shfl(w, (lane & 48) | min(k1 + u, 15));
+        if (k1 + u < most)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(y[u][e], wk, acc[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor(sum, d);
+  const int j = r / a.group, hq = h * a.group + r - j * a.group;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] /= sum;
+  store_row<T, E>((T*)a.out + (int64_t)(row0 + j) * a.ld_out + (int64_t)hq * D + j16 * E, acc);
 }
 
 // ---- host side
@@ -841,7 +892,8 @@ struct Plan {
 static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, int d,
                     int max_context, int window, int sinks, Plan& p) {
   const int64_t R = (int64_t)(max_k + 1) * (heads / kv_heads);
-  const int most = dtype == SV_F32 ? (d == 256 ? 1 : 2) : (d == 256 ? 2 : 4);
+  // (three terms fill the registers: fp32 rows go 16 to a workgroup)
+  const int most = dtype == SV_F32 ? 1 : d == 256 ? 2 : 4;
   p.mt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   if (p.mt > most) p.mt = most;
   p.row_blocks = (int)((R + p.mt * 16 - 1) / (p.mt * 16));
@@ -853,10 +905,11 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
   }
   const int64_t tiles = (tokens + TILE - 1) / TILE;
   const int64_t wide = (int64_t)batch * kv_heads * p.row_blocks;
-  // chunks of 64 tiles (a lane of a wave each), halved down to 256 tokens while the grid stays under two
-  // workgroups per compute unit
+  // chunks of 64 tiles (a lane of a wave each), halved down to 256 tokens while
+  // there is less than a workgroup per compute unit.  (One user over 32,000
+  // positions: 18.5 us with 256 workgroups, 21.5 with 512, 26 with 1,024.)
   int64_t ct = 64;
-  while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 512) ct /= 2;
+  while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 256) ct /= 2;
   p.chunk_tiles = (int)ct;
   p.chunks = (int)((tiles + ct - 1) / ct);
   const int64_t items = wide * p.chunks;
@@ -887,12 +940,12 @@ static int launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   if (p.chunks > 1) {
     const int wide = a.batch * a.kv_heads * p.row_blocks;
-    // one row per workgroup where few rows have many chunks, else one per wave
+    // a workgroup per row where few rows have many chunks (one user over 32,000
+    // positions: 5.4 us, the other form 9), else per 16 rows
     if (p.chunks > 8 && wide * MT * 16 <= 2048)
-      hipLaunchKernelGGL((k_attn_join<D, MT, 4, T>), dim3(wide * (MT * 16)), dim3(64 * WAVES), 0, s, a);
+      hipLaunchKernelGGL((k_attn_join<D, MT, T>), dim3(wide * (MT * 16)), dim3(64 * WAVES), 0, s, a);
     else
-      hipLaunchKernelGGL((k_attn_join<D, MT, 1, T>), dim3(wide * (MT * 16 / WAVES)), dim3(64 * WAVES),
-                         0, s, a);
+      hipLaunchKernelGGL((k_attn_join_rows<D, MT, T>), dim3(wide * MT), dim3(256), 0, s, a);
     if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   }
   return SV_OK;
@@ -978,9 +1031,7 @@ int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_
     SVK_CASE(256, 2, 2, __bf16);
   } else {
     SVK_CASE(64, 1, 2, float);
-    SVK_CASE(64, 2, 2, float);
     SVK_CASE(128, 1, 2, float);
-    SVK_CASE(128, 2, 2, float);
     SVK_CASE(256, 1, 2, float);
   }
 #undef SVK_CASE
