@@ -26,7 +26,6 @@
 namespace svk {
 
 constexpr int TILE = 32;          // tokens per wave step
-constexpr int WAVES = 4;
 constexpr float LOG2E = 1.44269504088896340736f;
 // the running maximum is raised only when a score passes it by this much (in
 // powers of two): until then weights stay below 2^8, which fp32 sums and bf16
@@ -448,7 +447,7 @@ struct Attn {
 
   // The wave's tiles: every WAVES-th of the share, for the first M row tiles.
   // id: lane i holds the pages of tile tbegin + i (its two halves).
-  template <int M, int DEPTH>
+  template <int M, int WAVES, int DEPTH>
   __device__ __forceinline__ void run(const AttnArgs& a, const Share& w, Tile<D> (&t)[DEPTH],
                                       const int (&id)[2], const Lane& at, int wave) {
     const int last = w.tend - 1;
@@ -583,8 +582,8 @@ __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
   }
 }
 
-template <int D, int MT, int DEPTH, typename T>
-__global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) void k_attn(AttnArgs a) {
+template <int D, int MT, int DEPTH, int WAVES, typename T>
+__global__ __launch_bounds__(64 * WAVES, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) void k_attn(AttnArgs a) {
   using A = Attn<D, MT, T>;
   constexpr int FR = A::FR;
   __shared__ float part_o[WAVES][MT * FR * 4][64];
@@ -686,15 +685,15 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
     x.init(raw);
     // row tiles that hold rows: a short request does not pay for a long one's
     const int tiles = (min(R - rb * MT * 16, MT * 16) + 15) / 16;
-    if (MT == 1 || tiles == 1) x.template run<1>(a, w, t, id, at, wave);
-    else if (MT == 2 || tiles == 2) x.template run<MT < 2 ? 1 : 2>(a, w, t, id, at, wave);
-    else if (tiles == 3) x.template run<MT < 3 ? 1 : 3>(a, w, t, id, at, wave);
-    else x.template run<MT>(a, w, t, id, at, wave);
+    if (MT == 1 || tiles == 1) x.template run<1, WAVES>(a, w, t, id, at, wave);
+    else if (MT == 2 || tiles == 2) x.template run<(MT < 2 ? 1 : 2), WAVES>(a, w, t, id, at, wave);
+    else if (tiles == 3) x.template run<(MT < 3 ? 1 : 3), WAVES>(a, w, t, id, at, wave);
+    else x.template run<MT, WAVES>(a, w, t, id, at, wave);
   }
   if (__any(x.poison != 0)) x.apply_poison();
 
-  // join the four waves: each takes a quarter of every row's dims (those that are
-  // entry r = wave of the accumulators)
+  // join the waves: each takes its share of every row's dims (those that are entry r
+  // of the accumulators, r = wave + WAVES i)
   const int n = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -715,39 +714,43 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
   const int64_t item = (((int64_t)chunk * a.batch + b) * a.kv_heads + h) * a.row_blocks + rb;
   float* part = a.part + item * (MT * 16) * D;
   float* stat = a.part + (int64_t)items * (MT * 16) * D + item * (MT * 16) * 2;
-  const int dim = g * (D / 4) + wave * FR;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int r = (rb * MT + mt) * 16 + n;
     float m = part_m[0][mt][n];
 #pragma unroll
     for (int k = 1; k < WAVES; ++k) m = fmaxf(m, part_m[k][mt][n]);
-    float part_w[WAVES], sum = 0.f, y[FR];
+    float part_w[WAVES], sum = 0.f;
 #pragma unroll
     for (int k = 0; k < WAVES; ++k) {
       const float mk = part_m[k][mt][n];
       part_w[k] = mk == m ? 1.f : __builtin_amdgcn_exp2f((mk - m) * c);
       sum += part_l[k][mt][n] * part_w[k];
     }
+    const float inv = 1.f / sum;
+    const int j = A::row_of(a, r), hq = h * a.group + r - j * a.group;
 #pragma unroll
-    for (int f = 0; f < FR; ++f) {
-      y[f] = 0.f;
+    for (int q = 0; q < 4 / WAVES; ++q) {
+      const int e = wave + q * WAVES, dim = g * (D / 4) + e * FR;
+      float y[FR];
 #pragma unroll
-      for (int k = 0; k < WAVES; ++k)
-        y[f] = __builtin_fmaf(part_o[k][(mt * FR + f) * 4 + wave][lane], part_w[k], y[f]);
-    }
-    if (r >= R) continue;
-    if (whole) {
-      const float inv = 1.f / sum;
+      for (int f = 0; f < FR; ++f) {
+        y[f] = 0.f;
 #pragma unroll
-      for (int f = 0; f < FR; ++f) y[f] *= inv;
-      const int j = A::row_of(a, r), hq = h * a.group + r - j * a.group;
-      store_row<T, FR>((T*)a.out + (int64_t)(row0 + j) * a.ld_out + (int64_t)hq * D + dim, y);
-    } else {
-      store_row<float, FR>(part + (mt * 16 + n) * D + dim, y);
-      if (wave == 0 && g == 0) {
-        stat[(mt * 16 + n) * 2] = m;
-        stat[(mt * 16 + n) * 2 + 1] = sum;
+        for (int k = 0; k < WAVES; ++k)
+          y[f] = __builtin_fmaf(part_o[k][(mt * FR + f) * 4 + e][lane], part_w[k], y[f]);
+      }
+      if (r >= R) continue;
+      if (whole) {
+#pragma unroll
+        for (int f = 0; f < FR; ++f) y[f] *= inv;
+        store_row<T, FR>((T*)a.out + (int64_t)(row0 + j) * a.ld_out + (int64_t)hq * D + dim, y);
+      } else {
+        store_row<float, FR>(part + (mt * 16 + n) * D + dim, y);
+        if (e == 0 && g == 0) {
+          stat[(mt * 16 + n) * 2] = m;
+          stat[(mt * 16 + n) * 2 + 1] = sum;
+        }
       }
     }
   }
@@ -756,7 +759,7 @@ __global__ __launch_bounds__(256, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) voi
 // Joins the chunks of requests longer than one: a workgroup per row.
 template <int D, int MT, typename T>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int E = D / 64;                  // dims per lane
+  constexpr int E = D / 64, WAVES = 4;       // dims per lane
   __shared__ float red[WAVES][D + 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int broken = first_broken(a.cu, a.batch, a.total_rows);
@@ -883,7 +886,7 @@ __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
 // ---- host side
 
 struct Plan {
-  int mt, row_blocks, chunks, chunk_tiles;
+  int mt, row_blocks, chunks, chunk_tiles, waves;
   size_t part_bytes, bytes;
   bool plan;
 };
@@ -916,6 +919,9 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
   if (items * (p.mt * 16) >= (1ll << 31) - 4096) return false;
   p.part_bytes = p.chunks > 1 ? (size_t)items * (p.mt * 16) * (d + 2) * sizeof(float) : 0;
   p.plan = items > 1024;
+  // two waves per workgroup where items are many and short (B=512 over 1 to 2,000
+  // positions 97 us, with four 108; all at 2,000, the longest unsplit, 145 and 142)
+  p.waves = p.plan && p.chunks == 1 ? 2 : 4;
   p.bytes = p.part_bytes + (p.plan ? (size_t)(items + 1) * sizeof(Item) : 0);
   return true;
 }
@@ -935,15 +941,17 @@ static int launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
     hipLaunchKernelGGL(k_attn_plan, dim3(1), dim3(1024), 0, s, a);
     if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   }
-  hipLaunchKernelGGL((k_attn<D, MT, DEPTH, T>), dim3(items + (a.batch + WAVES - 1) / WAVES),
-                     dim3(64 * WAVES), 0, s, a);
+  if (p.waves == 2)
+    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 2, T>), dim3(items + (a.batch + 1) / 2), dim3(128), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 4, T>), dim3(items + (a.batch + 3) / 4), dim3(256), 0, s, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   if (p.chunks > 1) {
     const int wide = a.batch * a.kv_heads * p.row_blocks;
     // a workgroup per row where few rows have many chunks (one user over 32,000
     // positions: 5.4 us, the other form 9), else per 16 rows
     if (p.chunks > 8 && wide * MT * 16 <= 2048)
-      hipLaunchKernelGGL((k_attn_join<D, MT, T>), dim3(wide * (MT * 16)), dim3(64 * WAVES), 0, s, a);
+      hipLaunchKernelGGL((k_attn_join<D, MT, T>), dim3(wide * (MT * 16)), dim3(256), 0, s, a);
     else
       hipLaunchKernelGGL((k_attn_join_rows<D, MT, T>), dim3(wide * MT), dim3(256), 0, s, a);
     if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
