@@ -352,7 +352,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : D == 256 ? 2 : 3) void k_
 
 constexpr int MAX_PAGES = 1 << 24;
 constexpr int CHUNK = 4096;                   // counts a workgroup looks at
-constexpr int PER_THREAD = CHUNK / 256;
 
 // Sums over a workgroup of NT threads: inclusive in thread order, and the total.
 template <int NT, typename I>
@@ -375,17 +374,32 @@ __device__ __forceinline__ I block_scan(I x, I* wsum, I& total) {
   return x + carry;
 }
 
+// The pages in use among a wave's 1,024 of a chunk: 64 at a time, a page per lane.
+__device__ __forceinline__ void used_masks(const int32_t* refs, int num_pages, int w0,
+                                           uint64_t (&mask)[16]) {
+  const int lane = threadIdx.x & 63;
+  int32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = refs[min(w0 + 64 * i + lane, num_pages - 1)];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) mask[i] = __ballot(w0 + 64 * i + lane < num_pages && r[i] != 0);
+}
+__device__ __forceinline__ int wave_pages() {
+  return blockIdx.x * CHUNK + (threadIdx.x >> 6) * (CHUNK / 4);
+}
+
 // Pages in use in each chunk of the pool.
 __global__ __launch_bounds__(256) void k_count(const int32_t* __restrict__ refs, int num_pages,
                                                int32_t* __restrict__ used) {
   __shared__ int wsum[4];
-  const int p0 = blockIdx.x * CHUNK + threadIdx.x * PER_THREAD;
+  uint64_t mask[16];
+  used_masks(refs, num_pages, wave_pages(), mask);
   int n = 0;
-  for (int i = 0; i < PER_THREAD; ++i)
-    if (p0 + i < num_pages) n += refs[p0 + i] != 0;
-  int total;
-  block_scan<256, int>(n, wsum, total);
-  if (threadIdx.x == 0) used[blockIdx.x] = total;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) n += __builtin_popcountll(mask[i]);
+  if ((threadIdx.x & 63) == 0) wsum[threadIdx.x >> 6] = n;
+  __syncthreads();
+  if (threadIdx.x == 0) used[blockIdx.x] = wsum[0] + wsum[1] + wsum[2] + wsum[3];
 }
 
 // Sum of used[0 .. upto) by a workgroup of 256, and of all of it.
@@ -531,15 +545,14 @@ __global__ __launch_bounds__(256) void k_reserve_assign(PageArgs a) {
     ctx[i] = a.ctx[i];
     copy[i] = a.copy[i];
   }
-  // a wave looks at 1,024 pages, 64 at a time, a page per lane
-  const int lane = threadIdx.x & 63;
-  const int w0 = blockIdx.x * CHUNK + (threadIdx.x >> 6) * (CHUNK / 4);
+  const int lane = threadIdx.x & 63, w0 = wave_pages();
   uint64_t mask[16];
+  used_masks(a.refs, a.num_pages, w0, mask);
   int n = 0, total;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const int p = w0 + 64 * i + lane;
-    mask[i] = __ballot(p < a.num_pages && a.refs[p] == 0);
+    const int in_pool = min(max(a.num_pages - (w0 + 64 * i), 0), 64);     // the others are free
+    mask[i] = ~mask[i] & (in_pool == 64 ? ~0ull : (1ull << in_pool) - 1);
     n += __builtin_popcountll(mask[i]);
   }
   int rank = rank0 + (block_scan<256, int>(lane == 0 ? n : 0, wsum, total) - n);
@@ -746,27 +759,28 @@ __global__ __launch_bounds__(256) void k_compact_rank(CompactArgs a) {
   __shared__ int wsum[4];
   int before, live;
   used_before(a.used, a.chunks, blockIdx.x, wsum, before, live);
-  const int p0 = blockIdx.x * CHUNK + threadIdx.x * PER_THREAD;
-  int n = 0;
-  uint32_t bits = 0;
-  for (int i = 0; i < PER_THREAD; ++i)
-    if (p0 + i < a.num_pages && a.refs[p0 + i] != 0) {
-      ++n;
-      bits |= 1u << i;
+  const int lane = threadIdx.x & 63, w0 = wave_pages();
+  uint64_t mask[16];
+  used_masks(a.refs, a.num_pages, w0, mask);
+  int n = 0, total;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) n += __builtin_popcountll(mask[i]);
+  // used pages before the wave's
+  int rank = before + block_scan<256, int>(lane == 0 ? n : 0, wsum, total) - n;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int p = w0 + 64 * i + lane;
+    const int r = rank + __builtin_popcountll(mask[i] & ((1ull << lane) - 1));
+    const bool used = mask[i] >> lane & 1;
+    if (p < a.num_pages) {
+      if (p == live) a.counts[0] = live - r;
+      if (p < live && !used) a.hole[p - r] = p;
+      if (p >= live && used) {
+        a.mover[live - 1 - r] = p;
+        a.place[p] = live - 1 - r;
+      }
     }
-  int total;
-  int rank = before + block_scan<256, int>(n, wsum, total) - n;   // used pages before p
-  for (int i = 0; i < PER_THREAD; ++i) {
-    const int p = p0 + i;
-    if (p >= a.num_pages) break;
-    const bool used = bits >> i & 1;
-    if (p == live) a.counts[0] = live - rank;
-    if (p < live && !used) a.hole[p - rank] = p;
-    if (p >= live && used) {
-      a.mover[live - 1 - rank] = p;
-      a.place[p] = live - 1 - rank;
-    }
-    rank += used;
+    rank += __builtin_popcountll(mask[i]);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.live[0] = live;
