@@ -28,6 +28,7 @@ _lib = None
 _lock = threading.Lock()
 _ws_cache: dict = {}
 _kv_ws_cache: dict = {}
+_kv_lock = threading.RLock()
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int
@@ -442,12 +443,17 @@ class KVCache:
                    page_size=page_size, kv_heads=kv_heads, head_dim=head_dim)
 
 
-def _kv_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
-    """Scratch of the cache calls, kept per (device, current stream): calls on
+def _kv_workspace(device: torch.device, nbytes: int,
+                  given: torch.Tensor | None = None) -> torch.Tensor:
+    """The caller's workspace, or scratch kept per (device, current stream): calls on
     one stream are ordered, so they share one.  While a graph is captured the
     call gets memory of the graph's own, so two graphs never share any.  An
     outgrown buffer goes back to torch's allocator, which reuses it on its own
     stream only, behind the work that still reads it."""
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        return given
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
@@ -459,13 +465,15 @@ def _kv_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
 
 
 class _on:
-    """The device guard of a call, which costs nothing where the device is current."""
+    """A call's launches: on the cache's device, and not between those of another
+    thread's call (a call is several launches that hand over in the workspace)."""
     __slots__ = ("device", "guard")
 
     def __init__(self, device):
         self.device, self.guard = device, None
 
     def __enter__(self):
+        _kv_lock.acquire()
         if torch.cuda.current_device() != self.device.index:
             self.guard = torch.cuda.device(self.device)
             self.guard.__enter__()
@@ -474,6 +482,7 @@ class _on:
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+        _kv_lock.release()
 
 
 def _check_ints(t: torch.Tensor | None, name: str, device, n: int) -> None:
@@ -593,7 +602,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor,
     if need == 0:
         raise ValueError("invalid sizes for spec_kv_attention")
     with _on(cache.device) as stream:
-        ws = _kv_workspace(cache.device, need) if workspace is None else workspace
+        ws = _kv_workspace(cache.device, need, workspace)
         _raise(L.spec_kv_attention(
             q.data_ptr(), ld_q, code, cu_seqlens.data_ptr(), context_lens.data_ptr(), batch, rows,
             max_k, heads, cache.kv_heads, cache.head_dim,
@@ -608,7 +617,7 @@ def _pages_workspace(cache: KVCache, seqs: int, workspace):
     need = lib().spec_kv_pages_workspace_bytes(seqs, cache.num_pages)
     if need == 0:
         raise ValueError("invalid sizes: at most 1024 requests and 2^24 pages")
-    return _kv_workspace(cache.device, need) if workspace is None else workspace
+    return _kv_workspace(cache.device, need, workspace)
 
 
 def kv_reserve(cache: KVCache, cu_seqlens: torch.Tensor, *, workspace: torch.Tensor | None = None):

@@ -721,7 +721,8 @@ __global__ __launch_bounds__(256) void k_fork_copy(const int32_t* __restrict__ s
       if (blockIdx.y == 0 && k >= i) seq_lens[dst[k]] = n;
     }
   if (__syncthreads_or(later)) return;
-  const int pages = pages_of(have, page_log2);
+  // (a length past the table row is nobody's held pages: they were checked)
+  const int pages = (int)min((int64_t)pages_of(have, page_log2), ld_table);
   for (int k = (int)blockIdx.y * 256 + threadIdx.x; k < pages; k += (int)gridDim.y * 256) {
     const int32_t id = table[(int64_t)s * ld_table + k];
     int took = 0;

@@ -333,6 +333,59 @@ def test_attention_peaked_scores(dtype):
     run_attention(dtype, 128, 16, 2, 1, [4, 1], [400, 90], loud=True, scale=1.0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,heads", [(64, 8), (128, 4), (256, 2)])
+def test_attention_of_many_short_items(dtype, d, heads):
+    """More items than the device holds at once, none split: the planned launch with two
+    waves per workgroup, rows of 1 to 4 tiles, with and without a window."""
+    rng = np.random.default_rng(d)
+    rows = [int(x) for x in rng.integers(0, 6, 520)]
+    rows[:3] = [6, 1, 5]
+    ctx = [int(x) for x in rng.integers(0, 90, 520)]
+    check_many(dtype, d, heads, 2, rows, ctx, 100, 0, 0, range(0, 520, 7))
+    check_many(dtype, d, heads, 2, rows, ctx, 100, 20, 3, range(3, 520, 7))
+
+
+def check_many(dtype, d, heads, kv, rows, ctx, max_context, window, sinks, some):
+    cache, K, V = make_attention(d, 16, kv, [max(r, 1) for r in rows], ctx, 1)
+    cu = _cu(rows)
+    q = torch.randn(int(cu[-1]), heads, d, device=DEV).to(DTYPES[dtype])
+    out, st = binding.kv_attention(cache, q, _i(cu), _i(ctx), max_k=7, max_context=max_context,
+                                   window=window, sinks=sinks)
+    assert st.cpu().tolist() == [0 if r else 3 for r in rows]
+    assert not torch.isnan(out).any()
+    check_attention(out, q, K, V, cu, ctx, rows, dtype, d ** -0.5, window, sinks,
+                    skip=set(range(len(rows))) - set(some))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_of_many_items_some_of_them_split(dtype, d):
+    """The planned launch with chunks: few long requests among many short ones, bad ones
+    between them, the same rows as calls that are not planned."""
+    rng = np.random.default_rng(d)
+    rows = [int(x) for x in rng.integers(1, 4, 60)]
+    ctx = [int(x) for x in rng.integers(0, 60, 60)]
+    for b, c in ((5, 6200), (17, 2049), (40, 4095), (59, 2047)):
+        ctx[b] = c
+    cache, K, V = make_attention(d, 32, 4, rows, ctx, 2)
+    ctx[8] = -1
+    cache.page_table[30, 0] = -5
+    cache.page_table[40, 100] = 1 << 29
+    cu = _cu(rows)
+    q = torch.randn(int(cu[-1]), 8, d, device=DEV).to(DTYPES[dtype])
+    out, st = binding.kv_attention(cache, q, _i(cu), _i(ctx), max_k=3, max_context=20000)
+    want = [0] * 60
+    want[8], want[30], want[40] = 5, 8, 8
+    assert st.cpu().tolist() == want
+    o = _f64(out)
+    for b in (8, 30, 40):
+        assert np.isnan(o[cu[b]:cu[b + 1]]).all()
+    check_attention(out, q, K, V, cu, ctx, rows, dtype, d ** -0.5, skip=(8, 30, 40))
+    again, _ = binding.kv_attention(cache, q, _i(cu), _i(ctx), max_k=3, max_context=20000)
+    assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
+
+
 def test_attention_does_not_depend_on_the_other_requests():
     a = run_attention("bf16", 128, 16, 4, 2, [3, 5, 1], [100, 900, 44], seed=9, max_k=7,
                       max_context=1000)
@@ -619,7 +672,94 @@ def test_compact_of_empty_full_and_one_page_pools():
         w.compact()
 
 
+def test_fork_of_lengths_past_the_table_row():
+    """A length that its table row cannot hold is refused, also where many pairs share it."""
+    w = World(300, 3, 40, 16, layers=1)
+    w.reserve([40] + [0] * 299)
+    w.cache.seq_lens[0] = 16 * 64
+    st = binding.kv_fork(w.cache, _i([0] * 299), _i(range(1, 300)))
+    assert st.cpu().tolist() == [8] * 299
+    st = binding.kv_fork(w.cache, _i([0] * 299), _i(range(1, 300)), _i([40] * 299))
+    assert st.cpu().tolist() == [0] * 299
+    assert w.cache.ref_counts.cpu().tolist()[:4] == [300, 300, 300, 0]
+
+
 # ------------------------------------------------------- streams and graphs
+
+def test_calls_of_two_threads_on_one_stream():
+    """The launches of a call do not mix with another thread's on the same stream."""
+    import threading
+    cache, q, cu, ctx, kw = _small()
+    want, _ = binding.kv_attention(cache, q, cu, ctx, **kw)
+    torch.cuda.synchronize()
+    outs = []
+
+    def work():
+        for _ in range(20):
+            outs.append(binding.kv_attention(cache, q, cu, ctx, **kw)[0])
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(outs) == 60 and all(torch.equal(o, want) for o in outs)
+
+
+def test_a_workspace_of_the_callers():
+    cache, q, cu, ctx, kw = _small()
+    want, _ = binding.kv_attention(cache, q, cu, ctx, **kw)
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV)     # any contents
+    out, _ = binding.kv_attention(cache, q, cu, ctx, workspace=ws, **kw)
+    assert torch.equal(out, want)
+    for bad in (ws[:64], ws[8:], ws[::2], ws.cpu()):
+        with pytest.raises(ValueError):
+            binding.kv_attention(cache, q, cu, ctx, workspace=bad, **kw)
+    w = World(3, 4, 12, 16)
+    for bad in (ws[:16], ws.cpu()):
+        with pytest.raises(ValueError):
+            binding.kv_reserve(w.cache, _i([0, 1, 1, 1]), workspace=bad)
+        with pytest.raises(ValueError):
+            binding.kv_compact(w.cache, workspace=bad)
+
+
+def test_the_binding_refuses_arguments_that_do_not_fit():
+    cache, q, cu, ctx, kw = _small()
+    x = torch.randn(9, 8, 128, device=DEV, dtype=torch.bfloat16)
+    ok = dict(q=x[:, :4], k=x[:, 4:6], v=x[:, 6:], cu_seqlens=cu, context_lens=ctx)
+    binding.kv_append(cache, **ok)
+    cs = torch.zeros(800, 64, device=DEV)
+    for change in (dict(q=x[:, :3]), dict(k=x[:, 4:7]), dict(v=x[:8, 6:]), dict(q=x[:, :4].float()),
+                   dict(q=x[:, :4, :64]), dict(q=x[:, 0:8:2]), dict(q=x[:, :4].cpu()),
+                   dict(cu_seqlens=cu.long()), dict(cu_seqlens=cu[:1]), dict(context_lens=ctx[:2]),
+                   dict(context_lens=ctx.float()), dict(q_weight=torch.ones(64, device=DEV)),
+                   dict(k_weight=torch.ones(128, device=DEV, dtype=torch.bfloat16)),
+                   dict(cos_sin=cs[:, :40]), dict(cos_sin=cs.double()), dict(cos_sin=cs[0]),
+                   dict(cos_sin=cs[:, :24].contiguous()), dict(layer=1), dict(layer=-1),
+                   dict(out=x[:8, :4]), dict(eps=-1.0), dict(q=x[0:1, :4].expand(9, -1, -1)),
+                   dict(cu_seqlens=torch.zeros(9, dtype=torch.int32, device=DEV)),
+                   dict(q=x[:0, :4], k=x[:0, 4:6], v=x[:0, 6:])):
+        with pytest.raises(ValueError):
+            binding.kv_append(cache, **{**ok, **change})
+    ok = dict(q=q, cu_seqlens=cu, context_lens=ctx, **kw)
+    for change in (dict(q=q.half()), dict(q=q[:, :3]), dict(max_k=64), dict(max_context=0),
+                   dict(window=-1), dict(scale=0.0), dict(layer=2), dict(out=q.float()),
+                   dict(context_lens=ctx[:1])):
+        with pytest.raises(ValueError):
+            binding.kv_attention(cache, **{**ok, **change})
+    with pytest.raises(ValueError):
+        binding.kv_release(cache, torch.zeros(4, dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError):
+        binding.kv_release(cache, _i([0, 0]), _i([0]))
+    with pytest.raises(ValueError):
+        binding.kv_fork(cache, _i([0, 1]), _i([2]))
+    for name, bad in (("pages", cache.pages[:, :, :-16]), ("page_table", cache.page_table.long()),
+                      ("seq_lens", cache.seq_lens[:1]), ("ref_counts", cache.ref_counts[:2])):
+        with pytest.raises(ValueError):
+            binding.KVCache(**{**{n: getattr(cache, n) for n in (
+                "pages", "page_table", "seq_lens", "ref_counts", "page_size", "kv_heads",
+                "head_dim")}, name: bad})
 
 def _small(seed=0, batch=3):
     rows, ctx = [3, 1, 5][:batch], [40, 7, 700][:batch]
