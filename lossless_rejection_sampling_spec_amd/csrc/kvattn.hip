@@ -5,10 +5,10 @@
 //   out = sum_t exp(scale q.k_t - m) v_t / sum_t exp(scale q.k_t - m)
 // over the visible t, in one pass with a running maximum m and sum.
 //
-// One workgroup (4 waves) takes one KV head, up to 16*MT of the R = (k+1)*G
-// rows that share it, and one chunk of the context; its waves take every
-// fourth tile of 32 tokens and work alone until the end, where their partial
-// results are joined through LDS.  A wave computes
+// One workgroup (2, 4 or 8 waves) takes one KV head, up to 16*MT of the
+// R = (k+1)*G rows that share it, and one chunk of the context; its waves take
+// the tiles of 32 tokens in turn and work alone until the end, where their
+// partial results are joined through LDS.  A wave computes
 //   S^T[token][row] = K Q^T   then   O^T[dim][row] += V^T P^T
 // with v_mfma_f32_16x16x32_bf16.  With tokens as the rows of S^T, a lane holds
 // the scores of ONE query row (its column), for 8 tokens (4 of each half of the
@@ -17,9 +17,14 @@
 // without LDS or shuffles.  K and V come as e2m1 codes and are widened to bf16 by the
 // hardware conversion, which applies the power-of-two block scale (exact).
 //
-// What bounds it: HBM reads of the cache (D*17/16 bytes per token and KV head)
-// as long as R <= 32; per 32-token tile a wave issues D*2/32*MT MFMAs and about
-// 120 + 110*MT vector instructions (D=128).
+// What bounds it: HBM reads of the cache (D*17/16 bytes per token and KV head) and
+// the vector instructions that widen it (half a conversion and, for V, half a byte
+// permutation per value of a tile and row block, besides the softmax) share the
+// time.  64 requests over 1 to 8,000 positions (k=6, 32 heads over 8 KV heads of
+// D=128): 94 us, of these plan 5, this kernel 78 (301 MB, 3.9 TB/s), join 7; with the
+// loads alone 81 in all.  One user over 32,000 positions, k=0: 18 us, of these join
+// 5; 64 requests over 4,000 with 64 heads (R=56, two row blocks that both read and
+// widen the cache): 133 us, 440 TFLOP/s.
 
 #include "kv_common.h"
 
@@ -73,15 +78,18 @@ __device__ __forceinline__ Span span_of(int ctx, int rows, int window, int sinks
   return s;
 }
 
-// SV_ROW_* of a request by its numbers alone (pages are checked where read).
-__device__ __forceinline__ int request_status(const AttnArgs& a, int b, int broken, int& row0,
-                                              int& rows, int& ctx) {
+// A request's numbers and its SV_ROW_* by them alone (pages are checked where
+// read).  One wave; its loads go out together with those of the offsets' check.
+__device__ __forceinline__ int request_status(const AttnArgs& a, int b, int& row0, int& rows,
+                                              int& ctx) {
+  const int c0 = a.cu[b], c1 = a.cu[b + 1], cx = a.ctx[b];
+  const int broken = first_broken(a.cu, a.batch, a.total_rows);
   row0 = rows = ctx = 0;
   if (b >= broken) return SV_ROW_BAD_K;
-  row0 = a.cu[b];
-  rows = a.cu[b + 1] - row0;
+  row0 = c0;
+  rows = c1 - c0;
   if (rows < 1 || rows > a.max_k + 1) return SV_ROW_BAD_K;
-  ctx = a.ctx[b];
+  ctx = cx;
   if (ctx < 0 || (int64_t)ctx + rows > a.max_context) return SV_ROW_BAD_PARAM;
   return SV_ROW_OK;
 }
@@ -551,7 +559,7 @@ __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
   seach[b] = rest;
   srow0[b] = c0;
   srows[b] = rows;
-  sctx[b] = ctx;
+  sctx[b] = ctx >= 0 && (int64_t)ctx + rows <= a.max_context ? ctx : -1;
   if (b == 0) {
     sfull[MAX_BATCH] = all_full;
     srest[MAX_BATCH] = all_rest;
@@ -573,8 +581,8 @@ __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
     it.b = lo;
     it.row0 = srow0[lo];
     it.rows = srows[lo];
-    it.ctx = sctx[lo];
-    it.status = it.ctx < 0 || (int64_t)it.ctx + it.rows > a.max_context ? SV_ROW_BAD_PARAM : SV_ROW_OK;
+    it.ctx = max(sctx[lo], 0);
+    it.status = sctx[lo] < 0 ? SV_ROW_BAD_PARAM : SV_ROW_OK;
     it.chunk = rem ? 0 : 1 + in / each;
     it.h = local / blocks;
     it.rb = local % blocks;
@@ -583,7 +591,7 @@ __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
 }
 
 template <int D, int MT, int DEPTH, int WAVES, typename T>
-__global__ __launch_bounds__(64 * WAVES, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 2)) void k_attn(AttnArgs a) {
+__global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
   using A = Attn<D, MT, T>;
   constexpr int FR = A::FR;
   __shared__ float part_o[WAVES][MT * FR * 4][64];
@@ -593,11 +601,10 @@ __global__ __launch_bounds__(64 * WAVES, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 
   const int status_blocks = (a.batch + WAVES - 1) / WAVES;
 
   if ((int)blockIdx.x < status_blocks) {      // a request's status, a wave each
-    const int broken = first_broken(a.cu, a.batch, a.total_rows);
     const int b = (int)blockIdx.x * WAVES + wave;
     if (b >= a.batch) return;
     int row0, rows, ctx;
-    int st = request_status(a, b, broken, row0, rows, ctx);
+    int st = request_status(a, b, row0, rows, ctx);
     if (st == SV_ROW_OK) {
       const Span sp = span_of(ctx, rows, a.window, a.sinks);
       const int32_t* tab = a.table + (int64_t)b * a.ld_table;
@@ -630,8 +637,7 @@ __global__ __launch_bounds__(64 * WAVES, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 
     it /= a.kv_heads;
     b = it % a.batch;
     chunk = a.chunks - 1 - it / a.batch;
-    const int broken = first_broken(a.cu, a.batch, a.total_rows);
-    st = request_status(a, b, broken, row0, rows, ctx);
+    st = request_status(a, b, row0, rows, ctx);
     if (st == SV_ROW_BAD_K || rb * MT * 16 >= rows * a.group) return;
   }
   Share w;
@@ -730,8 +736,9 @@ __global__ __launch_bounds__(64 * WAVES, (MT * D * (int)sizeof(T) >= 1024 ? 1 : 
     const float inv = 1.f / sum;
     const int j = A::row_of(a, r), hq = h * a.group + r - j * a.group;
 #pragma unroll
-    for (int q = 0; q < 4 / WAVES; ++q) {
+    for (int q = 0; q < (WAVES < 4 ? 4 / WAVES : 1); ++q) {
       const int e = wave + q * WAVES, dim = g * (D / 4) + e * FR;
+      if (e >= 4) continue;                    // (eight waves: four of them join)
       float y[FR];
 #pragma unroll
       for (int f = 0; f < FR; ++f) {
@@ -762,7 +769,6 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int E = D / 64, WAVES = 4;       // dims per lane
   __shared__ float red[WAVES][D + 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int broken = first_broken(a.cu, a.batch, a.total_rows);
   int it = blockIdx.x;
   const int local = it % (MT * 16);          // the row in its item
   it /= MT * 16;
@@ -771,7 +777,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   it /= a.row_blocks;
   const int h = it % a.kv_heads, b = it / a.kv_heads;
   int row0, rows, ctx;
-  if (request_status(a, b, broken, row0, rows, ctx) != SV_ROW_OK) return;
+  if (request_status(a, b, row0, rows, ctx) != SV_ROW_OK) return;
   const Span sp = span_of(ctx, rows, a.window, a.sinks);
   const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
   const int r = rb * MT * 16 + local;
@@ -836,9 +842,8 @@ __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
   const int mt = blockIdx.x % MT, first = blockIdx.x / MT;
   const int rb = first % a.row_blocks, h = first / a.row_blocks % a.kv_heads;
   const int b = first / a.row_blocks / a.kv_heads;
-  const int broken = first_broken(a.cu, a.batch, a.total_rows);
   int row0, rows, ctx;
-  if (request_status(a, b, broken, row0, rows, ctx) != SV_ROW_OK) return;
+  if (request_status(a, b, row0, rows, ctx) != SV_ROW_OK) return;
   const Span sp = span_of(ctx, rows, a.window, a.sinks);
   const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
   const int local = mt * 16 + (threadIdx.x >> 4), r = rb * MT * 16 + local;
@@ -895,8 +900,9 @@ struct Plan {
 static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, int d,
                     int max_context, int window, int sinks, Plan& p) {
   const int64_t R = (int64_t)(max_k + 1) * (heads / kv_heads);
-  // (three terms fill the registers: fp32 rows go 16 to a workgroup)
-  const int most = dtype == SV_F32 ? 1 : d == 256 ? 2 : 4;
+  // what fits the registers without spills: more rows per workgroup at D=128 or 256
+  // spilled, and the spilling code gave wrong rows; fp32 rows are three terms
+  const int most = dtype == SV_F32 ? 1 : 256 / d;
   p.mt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   if (p.mt > most) p.mt = most;
   p.row_blocks = (int)((R + p.mt * 16 - 1) / (p.mt * 16));
@@ -922,6 +928,11 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
   // two waves per workgroup where items are many and short (B=512 over 1 to 2,000
   // positions 97 us, with four 108; all at 2,000, the longest unsplit, 145 and 142)
   p.waves = p.plan && p.chunks == 1 ? 2 : 4;
+  // eight for fp32, whose waves are the slowest, where workgroups are few (32 requests
+  // over 1 to 2,000 positions 16.1 us, with four 18.0; 8 over 2,000 19.5 both ways).
+  // bf16 only loses by the longer join (4 over 500: 13.4 us against 12.0), and at
+  // D=256 the waves have no registers left to overlap (29.0 us against 28.1)
+  if (items < 512 && dtype == SV_F32 && d < 256) p.waves = 8;
   p.bytes = p.part_bytes + (p.plan ? (size_t)(items + 1) * sizeof(Item) : 0);
   return true;
 }
@@ -941,15 +952,21 @@ static int launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
     hipLaunchKernelGGL(k_attn_plan, dim3(1), dim3(1024), 0, s, a);
     if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   }
-  if (p.waves == 2)
-    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 2, T>), dim3(items + (a.batch + 1) / 2), dim3(128), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 4, T>), dim3(items + (a.batch + 3) / 4), dim3(256), 0, s, a);
+  const int grid = items + (a.batch + p.waves - 1) / p.waves;
+  if (p.waves == 2) {
+    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 2, T>), dim3(grid), dim3(128), 0, s, a);
+  } else if (p.waves == 4) {
+    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 4, T>), dim3(grid), dim3(256), 0, s, a);
+  } else {
+    if constexpr (sizeof(T) == 4 && D < 256)
+      hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 8, T>), dim3(grid), dim3(512), 0, s, a);
+  }
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   if (p.chunks > 1) {
     const int wide = a.batch * a.kv_heads * p.row_blocks;
     // a workgroup per row where few rows have many chunks (one user over 32,000
-    // positions: 5.4 us, the other form 9), else per 16 rows
+    // positions: 18.1 us a call, with the other form 21.8), else per 16 rows (8
+    // requests over 2,000: 16.5 us, a workgroup per row 20.8)
     if (p.chunks > 8 && wide * MT * 16 <= 2048)
       hipLaunchKernelGGL((k_attn_join<D, MT, T>), dim3(wide * (MT * 16)), dim3(256), 0, s, a);
     else
@@ -987,7 +1004,7 @@ int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_
   if (!sizes_ok(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks) ||
       total_rows < 1 || !page_ok(page_size) || num_pages < 1 || num_pages > 0x7fffffff ||
       ld_table < 1 || ld_table > (1 << 30) / page_size || ld_q < (int64_t)heads * head_dim ||
-      ld_out < (int64_t)heads * head_dim || !(scale > 0.f) || !(scale <= 3.0e38f) ||
+      ld_out < (int64_t)heads * head_dim || !(scale > 0.f) || !(scale <= 2.0e38f) ||
       !aligned16(pages) ||
       !plan_of(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks, p))
     return SV_ERR_SHAPE;
@@ -1034,13 +1051,11 @@ int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_
     SVK_CASE(64, 4, 2, __bf16);
     SVK_CASE(128, 1, 3, __bf16);
     SVK_CASE(128, 2, 2, __bf16);
-    SVK_CASE(128, 4, 2, __bf16);
     SVK_CASE(256, 1, 2, __bf16);
-    SVK_CASE(256, 2, 2, __bf16);
   } else {
     SVK_CASE(64, 1, 2, float);
     SVK_CASE(128, 1, 2, float);
-    SVK_CASE(256, 1, 2, float);
+    SVK_CASE(256, 1, 1, float);
   }
 #undef SVK_CASE
   return SV_ERR_SHAPE;
