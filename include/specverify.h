@@ -411,13 +411,16 @@ size_t spec_kv_attention_workspace_bytes(int dtype, int batch, int max_k, int he
  *   t <= p, and with window > 0 only t > p - window or t < sinks
  * and gets out = sum_t softmax_t(scale q.k_t) v_t per head; query head h reads
  * KV head h / (heads / kv_heads).  Statistics and sums in fp32, K and V exact
- * as stored, weights rounded to bf16 for bf16 rows (not for fp32 rows), the
- * result rounded once.  What a row does not see never reaches it, NaN included.
+ * as stored, weights rounded to bf16 for bf16 rows (not for fp32 rows, which
+ * enter as three bf16 terms: exact from 2^-110 up), the result rounded once.
+ * What a row does not see never reaches it, NaN included.  scale q.k log2 e, and
+ * sums of weights (up to 2^8 each before the division) times V, have to stay in
+ * fp32's range: past it a row is NaN or infinite.
  *   q, out         [total_rows][heads][head_dim] of dtype, rows ld_q / ld_out apart
  *   max_k          at most 63; requests with more drafts are SV_ROW_BAD_K
  *   max_context    bound of context_lens[b] + rows; requests past it are
  *                  SV_ROW_BAD_PARAM, like context_lens[b] < 0
- *   scale > 0, window >= 0 (0: off), sinks >= 0 (used with a window)
+ *   scale in (0, 2e38], window >= 0 (0: off), sinks >= 0 (used with a window)
  *   status         int32 [batch]: as above, SV_ROW_BAD_PAGE for a page id outside
  *                  the pool (or past the table row) at a position some row sees
  *   workspace      spec_kv_attention_workspace_bytes(), any contents; calls that

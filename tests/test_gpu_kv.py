@@ -254,7 +254,9 @@ def make_attention(d, page, kv, rows, ctx, seed=0, spare=2, loud=False):
 def check_attention(out, q, K, V, cu, ctx, rows, dtype, scale, window=0, sinks=0, skip=()):
     """Every element against float64.  fp32 scores are off by at most (D + 8) 2^-24 of
     scale sum|q||k|, weights by twice that and a step of exp2, sums by a step per term;
-    a bf16 row adds half a step for each weight, and the result its own rounding."""
+    a bf16 row adds half a step for each weight, and the result its own rounding.
+    Weights of less than 2^-126 of the largest may be 0 (fp32 ends there; the largest
+    counts at least 1 in the sum they are divided by): each off by at most that."""
     o, x = _f64(out), _f64(q)
     heads, d = x.shape[1:]
     for b in range(len(rows)):
@@ -271,6 +273,7 @@ def check_attention(out, q, K, V, cu, ctx, rows, dtype, scale, window=0, sinks=0
                 assert np.array_equal(np.isfinite(got), fine), (b, j, h)
                 tol = mass * ((HALF["bf16"] if dtype == "bf16" else 0) + 4 * (d + 8) * 2.0 ** -24 * slip
                               + (2 * n + 128) * 2.0 ** -24 + 2.0 ** -20) + HALF[dtype] * np.abs(want)
+                tol = tol + 2.0 ** -126 * np.abs(V[b][:, h // g]).sum(0)
                 bad = np.abs(got - want)[fine] > tol[fine]
                 assert not bad.any(), (b, j, h, np.abs(got - want)[fine].max(), tol.min())
 
@@ -370,18 +373,19 @@ def test_attention_of_many_items_some_of_them_split(dtype, d):
         ctx[b] = c
     cache, K, V = make_attention(d, 32, 4, rows, ctx, 2)
     ctx[8] = -1
+    ctx[9] = 2 ** 31 - 1
     cache.page_table[30, 0] = -5
     cache.page_table[40, 100] = 1 << 29
     cu = _cu(rows)
     q = torch.randn(int(cu[-1]), 8, d, device=DEV).to(DTYPES[dtype])
     out, st = binding.kv_attention(cache, q, _i(cu), _i(ctx), max_k=3, max_context=20000)
     want = [0] * 60
-    want[8], want[30], want[40] = 5, 8, 8
+    want[8], want[9], want[30], want[40] = 5, 5, 8, 8
     assert st.cpu().tolist() == want
     o = _f64(out)
-    for b in (8, 30, 40):
+    for b in (8, 9, 30, 40):
         assert np.isnan(o[cu[b]:cu[b + 1]]).all()
-    check_attention(out, q, K, V, cu, ctx, rows, dtype, d ** -0.5, skip=(8, 30, 40))
+    check_attention(out, q, K, V, cu, ctx, rows, dtype, d ** -0.5, skip=(8, 9, 30, 40))
     again, _ = binding.kv_attention(cache, q, _i(cu), _i(ctx), max_k=3, max_context=20000)
     assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
 
@@ -442,6 +446,18 @@ def test_attention_rows_with_infinite_or_nan_queries_stay_alone():
     assert torch.isnan(out[1, 0]).all() and torch.isnan(out[2, 1]).all()
     for j, h in ((0, 0), (0, 1), (1, 1), (2, 0), (3, 0), (3, 1)):
         assert torch.equal(out[j, h], clean[j, h])
+
+
+@pytest.mark.parametrize("dtype,scale,shift", [("bf16", 1e-38, 0), ("bf16", 2e38, 120),
+                                               ("f32", 1e-38, 0), ("f32", 1.5e32, 100)])
+def test_attention_scales_from_the_smallest_to_the_largest(dtype, scale, shift):
+    """The smallest gives the mean of V; the largest meet queries so small that the
+    scores stay in range."""
+    cache, K, V = make_attention(64, 16, 1, [2], [70], 3)
+    q = (torch.randn(2, 4, 64, device=DEV) * 2.0 ** -shift).to(DTYPES[dtype])
+    out, st = binding.kv_attention(cache, q, _i([0, 2]), _i([70]), max_k=1, max_context=72, scale=scale)
+    assert st.cpu().tolist() == [0]
+    check_attention(out, q, K, V, [0, 2], [70], [2], dtype, float(np.float32(scale)))
 
 
 def test_attention_statuses_and_what_it_leaves():

@@ -132,7 +132,7 @@ def _attention(**kw):
     (dict(d=32), 2), (dict(page=24), 2), (dict(num=0), 2), (dict(num=1 << 31), 2),
     (dict(ldt=0), 2), (dict(ldt=(1 << 26) + 1), 2), (dict(ldq=511), 2), (dict(ldo=511), 2),
     (dict(maxc=0), 2), (dict(maxc=(1 << 30) + 1), 2), (dict(scale=0.0), 2),
-    (dict(scale=-1.0), 2), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2),
+    (dict(scale=-1.0), 2), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2), (dict(scale=2.1e38), 2),
     (dict(window=-1), 2), (dict(sinks=-1), 2), (dict(pages=F + 4), 2),
     (dict(maxc=100000, ws=None), 1), (dict(maxc=100000, ws=F + 4), 1),
     (dict(maxc=100000, wsb=64), 4)])
