@@ -531,14 +531,12 @@ def test_pages_past_32_bit_offsets():
     cache = binding.KVCache(pages=pool, page_table=_i([[num - 1, num - 2]]), seq_lens=_i([300]),
                             ref_counts=torch.zeros(num, dtype=torch.int32, device=DEV),
                             page_size=page, kv_heads=kv, head_dim=d)
-    rng = np.random.default_rng(0)
     x = torch.randn(300, 3 * kv, d, device=DEV).to(torch.bfloat16)
     q, _, k, v = binding.kv_append(cache, x[:, :kv], x[:, kv:2 * kv], x[:, 2 * kv:], _i([0, 300]),
                                    _i([0]), want_values=True)
     out, st = binding.kv_attention(cache, q[-2:], _i([0, 2]), _i([298]), max_k=1, max_context=300)
     assert st.cpu().tolist() == [0]
     check_attention(out, q[-2:], [_f64(k)], [_f64(v)], [0, 2], [298], [2], "bf16", d ** -0.5)
-    assert rng is not None
 
 
 # -------------------------------------------------------------------- pages
@@ -620,6 +618,20 @@ def test_page_calls_in_random_order(seqs, width, num, page):
                 w.fork(pairs)
         else:
             w.compact()
+    w.compact()
+
+
+@pytest.mark.parametrize("num", [9000, 65535, 65536, 65537])
+def test_prompts_that_take_thousands_of_pages(num):
+    """Admissions next to single steps, with shared tails to copy, up to a full pool."""
+    width = num // 20
+    w = World(40, width, num, 16, layers=1, seed=num)
+    w.reserve([5] * 10 + [0] * 30)
+    w.fork([(i, 10 + i, None) for i in range(10)])
+    w.reserve([16 * (width - 1)] * 7 + [1] * 13 + [0] * 20)      # both holders copy
+    w.release([0, 16 * width // 2] + [0] * 38)
+    w.reserve([0] * 20 + [16 * width - 3] * 20)                  # the pool ends among these
+    w.reserve([0] * 8 + [1] * 12 + [0] * 20)
     w.compact()
 
 
