@@ -149,7 +149,6 @@ struct Attn {
   // fp32's 24): products with the exact bf16 K and V then lose nothing
   static constexpr int NT = sizeof(T) == 4 ? 3 : 1;
 
-  bf16x8 q[MT][STEPS][NT];
   f32x4 o[MT][FR];
   f32x4 l[MT];            // sums of the weights: a row of ones among the products (4 equal)
   // running max m of the raw scores: m, m scale log2 e (0 before the first visible
@@ -174,22 +173,45 @@ struct Attn {
     return (int)(((float)r + 0.5f) * a.inv_group);
   }
 
-  // The query rows' operands: requested first, taken over once they are there.
+  // The query rows' operands lie in LDS, [row tile][step][term][lane], for all waves of
+  // the workgroup: in registers they would take the place of a tile on its way.
+  static constexpr int Q_BYTES = MT * STEPS * NT * 64 * 16;
+  // A wave's share of them: requested first, written once they are there.
+  template <int WAVES>
   struct Raw {
-    T x[MT][STEPS][8];
-  };
-  static __device__ __forceinline__ void ask(const AttnArgs& a, Raw& raw, const Share& w, int h) {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    static constexpr int N = (MT * STEPS + WAVES - 1) / WAVES;
+    T x[N][8];
+    __device__ __forceinline__ void ask(const AttnArgs& a, const Share& w, int h, int wave) {
+      const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = min((w.rb * MT + mt) * 16 + n, w.R - 1);
-      const int j = row_of(a, r), hq = h * a.group + r - j * a.group;
-      const T* src = (const T*)a.q + (int64_t)(w.row0 + j) * a.ld_q + (uint32_t)(hq * D + g * (D / 4));
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) __builtin_memcpy(raw.x[mt][s], src + 8 * s, sizeof(raw.x[mt][s]));
+      for (int i = 0; i < N; ++i) {
+        const int at = min(wave + i * WAVES, MT * STEPS - 1), mt = at / STEPS, s = at % STEPS;
+        const int r = min((w.rb * MT + mt) * 16 + n, w.R - 1);
+        const int j = row_of(a, r), hq = h * a.group + r - j * a.group;
+        __builtin_memcpy(x[i], (const T*)a.q + (int64_t)(w.row0 + j) * a.ld_q +
+                                   (uint32_t)(hq * D + g * (D / 4) + 8 * s), sizeof(x[i]));
+      }
     }
-  }
-  __device__ __forceinline__ void init(const Raw& raw) {
+    __device__ __forceinline__ void put(bf16x8* q, int wave) const {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int at = wave + i * WAVES;
+        if (MT * STEPS % WAVES != 0 && at >= MT * STEPS) continue;
+        bf16x8 y[NT];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          __bf16 t[NT];
+          if constexpr (NT == 1) t[0] = x[i][k];
+          else split(to_f32<T>(x[i][k]), t);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) y[u][k] = t[u];
+        }
+#pragma unroll
+        for (int u = 0; u < NT; ++u) q[(at * NT + u) * 64 + (threadIdx.x & 63)] = y[u];
+      }
+    }
+  };
+  __device__ __forceinline__ void init() {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       m[mt] = over[mt] = -INFINITY;
@@ -197,16 +219,6 @@ struct Attn {
       l[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int f = 0; f < FR; ++f) o[mt][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          __bf16 t[NT];
-          if constexpr (NT == 1) t[0] = raw.x[mt][s][i];
-          else split(to_f32<T>(raw.x[mt][s][i]), t);
-#pragma unroll
-          for (int k = 0; k < NT; ++k) q[mt][s][k][i] = t[k];
-        }
     }
   }
 
@@ -262,8 +274,10 @@ struct Attn {
   // One tile for the first M row tiles.  masked: some row does not see some token.
   template <int M>
   __device__ __forceinline__ void step(const AttnArgs& a, Tile<D>& t, bool masked, int base,
-                                       const Share& w) {
+                                       const Share& w, const bf16x8* q) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    int ql = lane;
+    asm volatile("" : "+v"(ql));              // (or the reads move out of the loop, into registers)
     auto sees = [&](int tok, int pos) {
       return tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
     };
@@ -301,11 +315,18 @@ struct Attn {
     // scores: s[half][mt], lane: row n, tokens base + 16*half + 4g + r
     f32x4 s[2][M];
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
+    for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
       for (int mt = 0; mt < M; ++mt) s[hf][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
+    for (int st = 0; st < STEPS; ++st) {
+      bf16x8 qt[M][NT];
+#pragma unroll
+      for (int mt = 0; mt < M; ++mt)
+#pragma unroll
+        for (int k = 0; k < NT; ++k) qt[mt][k] = q[((mt * STEPS + st) * NT + k) * 64 + ql];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
         const float sc = ksc[hf][st / 4];
         const uint32_t x = t.k[hf][st];
         u32x4 kb;
@@ -318,7 +339,7 @@ struct Attn {
         for (int mt = 0; mt < M; ++mt)
 #pragma unroll
           for (int k = NT - 1; k >= 0; --k)
-            s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, q[mt][st][k], s[hf][mt], 0, 0, 0);
+            s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, qt[mt][k], s[hf][mt], 0, 0, 0);
       }
     }
     if (masked) {
@@ -457,7 +478,8 @@ struct Attn {
   // id: lane i holds the pages of tile tbegin + i (its two halves).
   template <int M, int WAVES, int DEPTH>
   __device__ __forceinline__ void run(const AttnArgs& a, const Share& w, Tile<D> (&t)[DEPTH],
-                                      const int (&id)[2], const Lane& at, int wave) {
+                                      const int (&id)[2], const Lane& at, int wave,
+                                      const bf16x8* q) {
     const int last = w.tend - 1;
     for (int i = w.tbegin + wave; i < w.tend; i += DEPTH * WAVES) {
 #pragma unroll
@@ -467,7 +489,7 @@ struct Attn {
           const bool masked =
               base + TILE - 1 > w.ctx ||
               (a.window > 0 && base <= w.ctx + w.rows - 1 - a.window && base + TILE > a.sinks);
-          step<M>(a, t[k], masked, base, w);
+          step<M>(a, t[k], masked, base, w, q);
         }
         fetch(a, w, t[k], id, at, min(i + (k + DEPTH) * WAVES, last));
       }
@@ -594,7 +616,11 @@ template <int D, int MT, int DEPTH, int WAVES, typename T>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
   using A = Attn<D, MT, T>;
   constexpr int FR = A::FR;
-  __shared__ float part_o[WAVES][MT * FR * 4][64];
+  // the query operands, and once all waves are done their results for a row tile
+  constexpr int O_BYTES = WAVES * FR * 4 * 64 * 4;
+  __shared__ __align__(16) uint8_t smem[O_BYTES > A::Q_BYTES ? O_BYTES : A::Q_BYTES];
+  bf16x8* const q_lds = (bf16x8*)smem;
+  float (*const part_o)[FR * 4][64] = (float (*)[FR * 4][64])smem;
   __shared__ float part_m[WAVES][MT][16], part_l[WAVES][MT][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int items = a.batch * a.kv_heads * a.row_blocks * a.chunks;
@@ -658,12 +684,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
   const int R = w.R;
 
   A x;
-  typename A::Raw raw;
+  x.init();
   bool bad = st != SV_ROW_OK;
-  if (bad) {
-    A::ask(a, raw, w, h);
-    x.init(raw);
-  } else {
+  if (!bad) {
     const int32_t* tab = a.table + (int64_t)b * a.ld_table;
     // lane i: the pages of the chunk's tile i (its first and second 16 tokens)
     int id[2];
@@ -677,7 +700,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
       bad |= need && !in_pool;
       if (!in_pool) id[hf] = 0;
     }
-    A::ask(a, raw, w, h);
+    typename A::template Raw<WAVES> raw;
+    raw.ask(a, w, h, wave);
     bad = __any(bad);
     const typename A::Lane at = A::lane_offsets(a.page);
     // DEPTH tiles are on their way at any time: a buffer is filled again as soon
@@ -688,32 +712,27 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k)
       A::fetch(a, w, t[k], id, at, min(w.tbegin + wave + k * WAVES, w.tend - 1));
-    x.init(raw);
+    raw.put(q_lds, wave);
+    __syncthreads();
     // row tiles that hold rows: a short request does not pay for a long one's
     const int tiles = (min(R - rb * MT * 16, MT * 16) + 15) / 16;
-    if (MT == 1 || tiles == 1) x.template run<1, WAVES>(a, w, t, id, at, wave);
-    else if (MT == 2 || tiles == 2) x.template run<(MT < 2 ? 1 : 2), WAVES>(a, w, t, id, at, wave);
-    else if (tiles == 3) x.template run<(MT < 3 ? 1 : 3), WAVES>(a, w, t, id, at, wave);
-    else x.template run<MT, WAVES>(a, w, t, id, at, wave);
+    if (MT == 1 || tiles == 1) x.template run<1, WAVES>(a, w, t, id, at, wave, q_lds);
+    else if (MT == 2 || tiles == 2) x.template run<(MT < 2 ? 1 : 2), WAVES>(a, w, t, id, at, wave, q_lds);
+    else if (tiles == 3) x.template run<(MT < 3 ? 1 : 3), WAVES>(a, w, t, id, at, wave, q_lds);
+    else x.template run<MT, WAVES>(a, w, t, id, at, wave, q_lds);
   }
   if (__any(x.poison != 0)) x.apply_poison();
 
-  // join the waves: each takes its share of every row's dims (those that are entry r
-  // of the accumulators, r = wave + WAVES i)
+  // join the waves, a row tile at a time: each takes its share of every row's dims
+  // (those that are entry r of the accumulators, r = wave + WAVES i)
   const int n = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int mt = 0; mt < MT; ++mt)
     if (g == 0) {
       part_m[wave][mt][n] = x.m[mt];
       // a page id out of range: the request's rows are NaN
       part_l[wave][mt][n] = bad ? __builtin_nanf("") : x.l[mt][0];
     }
-#pragma unroll
-    for (int f = 0; f < FR; ++f)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) part_o[wave][(mt * FR + f) * 4 + r][lane] = x.o[mt][f][r];
-  }
-  __syncthreads();
 
   const bool whole = st != SV_ROW_OK || w.sp.tiles <= a.chunk_tiles;
   // this item's place among the partials
@@ -722,6 +741,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
   float* stat = a.part + (int64_t)items * (MT * 16) * D + item * (MT * 16) * 2;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
+    __syncthreads();                          // (every wave is done with what lay here)
+#pragma unroll
+    for (int f = 0; f < FR; ++f)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part_o[wave][f * 4 + r][lane] = x.o[mt][f][r];
+    __syncthreads();
     const int r = (rb * MT + mt) * 16 + n;
     float m = part_m[0][mt][n];
 #pragma unroll
@@ -745,7 +770,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
         y[f] = 0.f;
 #pragma unroll
         for (int k = 0; k < WAVES; ++k)
-          y[f] = __builtin_fmaf(part_o[k][(mt * FR + f) * 4 + e][lane], part_w[k], y[f]);
+          y[f] = __builtin_fmaf(part_o[k][f * 4 + e][lane], part_w[k], y[f]);
       }
       if (r >= R) continue;
       if (whole) {
@@ -900,12 +925,6 @@ struct Plan {
 static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, int d,
                     int max_context, int window, int sinks, Plan& p) {
   const int64_t R = (int64_t)(max_k + 1) * (heads / kv_heads);
-  // what fits the registers without spills: more rows per workgroup at D=128 or 256
-  // spilled, and the spilling code gave wrong rows; fp32 rows are three terms
-  const int most = dtype == SV_F32 ? 1 : 256 / d;
-  p.mt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
-  if (p.mt > most) p.mt = most;
-  p.row_blocks = (int)((R + p.mt * 16 - 1) / (p.mt * 16));
   // tiles a request can have: two borders more than its tokens fill
   int64_t tokens = max_context;
   if (window > 0) {
@@ -913,15 +932,28 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
     if (seen < tokens) tokens = seen;
   }
   const int64_t tiles = (tokens + TILE - 1) / TILE;
-  const int64_t wide = (int64_t)batch * kv_heads * p.row_blocks;
-  // chunks of 64 tiles (a lane of a wave each), halved down to 256 tokens while
-  // there is less than a workgroup per compute unit.  (One user over 32,000
-  // positions: 18.5 us with 256 workgroups, 21.5 with 512, 26 with 1,024.)
-  int64_t ct = 64;
-  while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 256) ct /= 2;
-  p.chunk_tiles = (int)ct;
-  p.chunks = (int)((tiles + ct - 1) / ct);
-  const int64_t items = wide * p.chunks;
+  // what fits the registers without spills: with 16 MT = 8192/D more of the kernels
+  // spilled, and the spilling code gave wrong rows
+  const int most = 256 / d;
+  p.mt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+  if (p.mt > most) p.mt = most;
+  int64_t items;
+  for (;; p.mt = 1) {
+    p.row_blocks = (int)((R + p.mt * 16 - 1) / (p.mt * 16));
+    const int64_t wide = (int64_t)batch * kv_heads * p.row_blocks;
+    // chunks of 64 tiles (a lane of a wave each), halved down to 256 tokens while
+    // there is less than a workgroup per compute unit.  (One user over 32,000
+    // positions: 18.5 us with 256 workgroups, 21.5 with 512, 26 with 1,024.)
+    int64_t ct = 64;
+    while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 256) ct /= 2;
+    p.chunk_tiles = (int)ct;
+    p.chunks = (int)((tiles + ct - 1) / ct);
+    items = wide * p.chunks;
+    // fp32 rows cost a wave three times the products: where workgroups are few, its
+    // time is that of the longest wave, and 16 rows each are better (R=24: 32 requests
+    // over 1 to 2,000 positions 16.0 us, with 32 rows 22; 64 over 2,000 73 and 60)
+    if (p.mt == 1 || dtype != SV_F32 || items >= 512) break;
+  }
   if (items * (p.mt * 16) >= (1ll << 31) - 4096) return false;
   p.part_bytes = p.chunks > 1 ? (size_t)items * (p.mt * 16) * (d + 2) * sizeof(float) : 0;
   p.plan = items > 1024;
@@ -932,7 +964,7 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
   // over 1 to 2,000 positions 16.1 us, with four 18.0; 8 over 2,000 19.5 both ways).
   // bf16 only loses by the longer join (4 over 500: 13.4 us against 12.0), and at
   // D=256 the waves have no registers left to overlap (29.0 us against 28.1)
-  if (items < 512 && dtype == SV_F32 && d < 256) p.waves = 8;
+  if (items < 512 && dtype == SV_F32 && d < 256) p.waves = 8;    // (p.mt is 1)
   p.bytes = p.part_bytes + (p.plan ? (size_t)(items + 1) * sizeof(Item) : 0);
   return true;
 }
@@ -958,7 +990,7 @@ static int launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
   } else if (p.waves == 4) {
     hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 4, T>), dim3(grid), dim3(256), 0, s, a);
   } else {
-    if constexpr (sizeof(T) == 4 && D < 256)
+    if constexpr (sizeof(T) == 4 && D < 256 && MT == 1)
       hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 8, T>), dim3(grid), dim3(512), 0, s, a);
   }
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
@@ -1055,7 +1087,10 @@ int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_
   } else {
     SVK_CASE(64, 1, 2, float);
     SVK_CASE(128, 1, 2, float);
-    SVK_CASE(256, 1, 1, float);
+    SVK_CASE(256, 1, 2, float);
+    SVK_CASE(128, 2, 2, float);
+    SVK_CASE(64, 2, 2, float);
+    SVK_CASE(64, 4, 1, float);
   }
 #undef SVK_CASE
   return SV_ERR_SHAPE;

@@ -349,6 +349,24 @@ def test_attention_of_many_short_items(dtype, d, heads):
     check_many(dtype, d, heads, 2, rows, ctx, 100, 20, 3, range(3, 520, 7))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads,batch,max_context", [(16, 300, 100), (8, 300, 100), (16, 520, 100),
+                                                     (8, 520, 100), (16, 40, 20000),
+                                                     (8, 40, 20000)])
+def test_attention_of_many_items_with_rows_of_every_tiling(dtype, d, heads, batch, max_context):
+    """Up to 32 and 64 rows per KV head where items are many: with and without a plan,
+    two and four waves per workgroup, whole and split."""
+    rng = np.random.default_rng(batch + heads)
+    rows = [int(x) for x in rng.integers(1, 9, batch)]
+    rows[:4] = [8, 1, 7, 3]
+    ctx = [int(x) for x in rng.integers(0, 90, batch)]
+    if max_context > 100:
+        ctx[1], ctx[7], ctx[39] = 2047, 4100, 2500
+    check_many(dtype, d, heads, 2, rows, ctx, max_context, 0, 0,
+               range(0, 8) if max_context > 100 else range(0, batch, 29))
+
+
 def check_many(dtype, d, heads, kv, rows, ctx, max_context, window, sinks, some):
     cache, K, V = make_attention(d, 16, kv, [max(r, 1) for r in rows], ctx, 1)
     cu = _cu(rows)
