@@ -523,14 +523,17 @@ struct Item {
 
 // The items of a call that has room for more than the device runs at once: the
 // full chunks of all requests, then the chunks 0, which hold what is left over of
-// full ones.  So the shortest start last, and workgroups without an item come
-// after all others (a batch of ragged contexts has a third of the items that its
-// sizes allow).  (Starting every compute unit with a full chunk
-// beside a chunk 0, so that they do not end together, changed nothing.)  One
-// workgroup of 1,024, a thread per request, then per item.
+// full ones, by falling work (tiles and row tiles).  So the shortest start last, and
+// workgroups without an item come after all others (a batch of ragged contexts has a
+// third of the items that its sizes allow).  One workgroup of 1,024, a thread per
+// request, then per item.
 __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
-  __shared__ int wred[3][16], sfull[MAX_BATCH + 1], srest[MAX_BATCH + 1], seach[MAX_BATCH];
+  constexpr int LEVELS = 64;
+  __shared__ int wred[2][16], sfull[MAX_BATCH], seach[MAX_BATCH];
   __shared__ int srow0[MAX_BATCH], srows[MAX_BATCH], sctx[MAX_BATCH];
+  // chunks 0 by level of work, most first: how many requests (upper half) and items
+  __shared__ unsigned long long level[LEVELS + 1];
+  __shared__ int order[MAX_BATCH], srest[MAX_BATCH];
   const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
   const int G = a.heads / a.kv_heads;
   int c0 = 0, c1 = 0, ctx = 0, broken = a.batch;
@@ -540,6 +543,7 @@ __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
     ctx = a.ctx[b];
     if (c0 < 0 || c1 < c0 || c1 > a.total_rows) broken = b;
   }
+  if (b < LEVELS) level[b] = 0;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) broken = min(broken, __shfl_xor(broken, d));
   if (lane == 0) wred[0][wave] = broken;
@@ -547,58 +551,72 @@ __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
 #pragma unroll
   for (int w = 0; w < 16; ++w) broken = min(broken, wred[0][w]);
   const int rows = c1 - c0;
-  int full = 0, rest = 0;
+  const bool fits = ctx >= 0 && (int64_t)ctx + rows <= a.max_context;
+  int full = 0, rest = 0, at_level = LEVELS - 1;
   if (b < broken && rows >= 1 && rows <= a.max_k + 1) {
     rest = a.kv_heads * ((rows * G + a.block_rows - 1) / a.block_rows);
-    if (ctx >= 0 && (int64_t)ctx + rows <= a.max_context)
-      full = (span_of(ctx, rows, a.window, a.sinks).tiles - 1) / a.chunk_tiles * rest;
+    if (fits) {
+      const int tiles = span_of(ctx, rows, a.window, a.sinks).tiles;
+      full = (tiles - 1) / a.chunk_tiles * rest;
+      // a tile costs about as much as two row tiles' products with it
+      const int mt = (min(rows * G, a.block_rows) + 15) / 16, most = a.chunk_tiles * (2 + a.block_rows / 16);
+      const int work = ((tiles - 1) % a.chunk_tiles + 1) * (2 + mt);
+      at_level = LEVELS - 1 - work * (LEVELS - 1) / most;
+    }
   }
-  int f = full, r = rest;
+  // (places within a level come as they come: which workgroup computes an item
+  // changes nothing in its result)
+  const unsigned long long mine = b < a.batch ? atomicAdd(&level[at_level], 1ull << 32 | (unsigned)rest) : 0;
+  int f = full;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int yf = __shfl_up(f, d), yr = __shfl_up(r, d);
-    if (lane >= d) {
-      f += yf;
-      r += yr;
-    }
+    const int y = __shfl_up(f, d);
+    if (lane >= d) f += y;
   }
-  if (lane == 63) {
-    wred[1][wave] = f;
-    wred[2][wave] = r;
-  }
+  if (lane == 63) wred[1][wave] = f;
   __syncthreads();
-  int all_full = 0, all_rest = 0;
-  for (int w = 0; w < 16; ++w) {
-    if (w == wave) {
-      f += all_full;
-      r += all_rest;
+  if (wave == 0) {
+    unsigned long long x = level[lane], sum = x;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const unsigned long long y = __shfl_up(sum, d);
+      if (lane >= d) sum += y;
     }
+    level[lane] = sum - x;
+    if (lane == 63) level[LEVELS] = sum;
+  }
+  int all_full = 0;
+  for (int w = 0; w < 16; ++w) {
+    if (w == wave) f += all_full;
     all_full += wred[1][w];
-    all_rest += wred[2][w];
   }
   sfull[b] = f - full;
-  srest[b] = r - rest;
   seach[b] = rest;
   srow0[b] = c0;
   srows[b] = rows;
-  sctx[b] = ctx >= 0 && (int64_t)ctx + rows <= a.max_context ? ctx : -1;
-  if (b == 0) {
-    sfull[MAX_BATCH] = all_full;
-    srest[MAX_BATCH] = all_rest;
-    a.plan[0].b = all_full + all_rest;
-  }
+  sctx[b] = fits ? ctx : -1;
   __syncthreads();
-  for (int i = b; i < all_full + all_rest; i += 1024) {
+  const int all = all_full + (int)(unsigned)level[LEVELS];
+  if (b < a.batch) {
+    const unsigned long long place = level[at_level] + mine;
+    order[place >> 32] = b;
+    srest[place >> 32] = (int)(unsigned)place;
+  }
+  if (b == 0) a.plan[0].b = all;
+  __syncthreads();
+  for (int i = b; i < all; i += 1024) {
     const bool rem = i >= all_full;
     const int* start = rem ? srest : sfull;
     const int at = rem ? i - all_full : i;
-    int lo = 0, hi = a.batch;                 // the request whose range holds it
+    int lo = 0, hi = a.batch;                 // the range that holds it
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (start[mid] <= at) lo = mid;
       else hi = mid;
     }
-    const int in = at - start[lo], each = seach[lo], local = in % each, blocks = each / a.kv_heads;
+    const int in = at - start[lo];
+    if (rem) lo = order[lo];
+    const int each = seach[lo], local = in % each, blocks = each / a.kv_heads;
     Item it;
     it.b = lo;
     it.row0 = srow0[lo];
