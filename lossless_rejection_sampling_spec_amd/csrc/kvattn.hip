@@ -975,9 +975,15 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
   if (items * (p.mt * 16) >= (1ll << 31) - 4096) return false;
   p.part_bytes = p.chunks > 1 ? (size_t)items * (p.mt * 16) * (d + 2) * sizeof(float) : 0;
   p.plan = items > 1024;
-  // two waves per workgroup where items are many and short (B=512 over 1 to 2,000
-  // positions 97 us, with four 108; all at 2,000, the longest unsplit, 145 and 142)
-  p.waves = p.plan && p.chunks == 1 ? 2 : 4;
+  // two waves per workgroup (more items at once, each twice as long) where items are
+  // many, and whole or rich in products: 512 requests over 1 to 2,000 positions 64 us,
+  // with four 81; 256 over 1 to 4,000 (R=28) 67.5 and 76.5; 128 over 1 to 8,000 with
+  // R=56 81.5 and 92; but 64 over 8,000 with R=4 128 and 122, D=256 (16 rows at a
+  // time) 83 and 80.  fp32 waves take longer for an item and need more of them: 512
+  // over 1 to 2,000 79.5 and 97, 256 with R=48 69 and 58
+  p.waves = 4;
+  if (p.plan && (dtype == SV_F32 ? p.chunks == 1 && items >= 4096 : p.chunks == 1 || p.mt > 1))
+    p.waves = 2;
   // eight for fp32, whose waves are the slowest, where workgroups are few (32 requests
   // over 1 to 2,000 positions 16.1 us, with four 18.0; 8 over 2,000 19.5 both ways).
   // bf16 only loses by the longer join (4 over 500: 13.4 us against 12.0), and at

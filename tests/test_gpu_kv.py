@@ -352,8 +352,8 @@ def test_attention_of_many_short_items(dtype, d, heads):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("heads,batch,max_context", [(16, 300, 100), (8, 300, 100), (16, 520, 100),
-                                                     (8, 520, 100), (16, 40, 20000),
-                                                     (8, 40, 20000)])
+                                                     (8, 520, 100), (16, 60, 20000),
+                                                     (8, 60, 20000)])
 def test_attention_of_many_items_with_rows_of_every_tiling(dtype, d, heads, batch, max_context):
     """Up to 32 and 64 rows per KV head where items are many: with and without a plan,
     two and four waves per workgroup, whole and split."""
@@ -365,6 +365,18 @@ def test_attention_of_many_items_with_rows_of_every_tiling(dtype, d, heads, batc
         ctx[1], ctx[7], ctx[39] = 2047, 4100, 2500
     check_many(dtype, d, heads, 2, rows, ctx, max_context, 0, 0,
                range(0, 8) if max_context > 100 else range(0, batch, 29))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", [4, 16, 32])
+def test_attention_of_a_full_batch_in_fp32(d, heads):
+    """1,024 requests over 4 KV heads: as many items as a call of fp32 rows takes two
+    waves per workgroup for; 8, 32 and 64 rows each."""
+    rng = np.random.default_rng(heads)
+    rows = [int(x) for x in rng.integers(0, 9, 1024)]
+    ctx = [int(x) for x in rng.integers(0, 60, 1024)]
+    rows[1], rows[37] = 8, 0
+    check_many("f32", d, heads, 4, rows, ctx, 68, 0, 0, range(0, 1024, 111))
 
 
 def check_many(dtype, d, heads, kv, rows, ctx, max_context, window, sinks, some):
