@@ -380,7 +380,24 @@ def test_attention_of_a_full_batch_in_fp32(d, heads):
 
 
 def check_many(dtype, d, heads, kv, rows, ctx, max_context, window, sinks, some):
-    cache, K, V = make_attention(d, 16, kv, [max(r, 1) for r in rows], ctx, 1)
+    """Pages of random codes; the requests `some` are compared."""
+    page, rng, some = 16, np.random.default_rng(1), set(some)
+    n = [c + max(r, 1) for c, r in zip(ctx, rows)]
+    need = [-(-x // page) for x in n]
+    pages = rng.integers(0, 256, (1, sum(need) + 2, kv, page * (d + d // 16)), np.uint8)
+    pages[..., page * d:] = rng.integers(122, 128, pages[..., page * d:].shape, np.uint8)
+    ids, table = rng.permutation(sum(need)), np.full((len(rows), max(need)), -1)
+    ks, vs = U.places(page, d)[2:]
+    K, V = [None] * len(rows), [None] * len(rows)
+    for b, first in enumerate(np.cumsum([0] + need[:-1])):
+        mine = table[b, :need[b]] = ids[first:first + need[b]]
+        for at in (ks, vs):                      # stale bytes behind the last position
+            pages[0, mine[-1]][:, at[n[b] - (need[b] - 1) * page:]] = 255
+        if b in some:
+            units = [[U.read_unit(pages[0, p, h], page, d) for h in range(kv)] for p in mine]
+            K[b], V[b] = (np.concatenate([np.stack([u[i] for u in p], 1) for p in units])[:n[b]]
+                          for i in (0, 1))
+    cache = _cache(pages, table, n, np.zeros(pages.shape[1]), page, kv, d)
     cu = _cu(rows)
     q = torch.randn(int(cu[-1]), heads, d, device=DEV).to(DTYPES[dtype])
     out, st = binding.kv_attention(cache, q, _i(cu), _i(ctx), max_k=7, max_context=max_context,
@@ -388,7 +405,7 @@ def check_many(dtype, d, heads, kv, rows, ctx, max_context, window, sinks, some)
     assert st.cpu().tolist() == [0 if r else 3 for r in rows]
     assert not torch.isnan(out).any()
     check_attention(out, q, K, V, cu, ctx, rows, dtype, d ** -0.5, window, sinks,
-                    skip=set(range(len(rows))) - set(some))
+                    skip=set(range(len(rows))) - some)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
