@@ -17,14 +17,15 @@
 // without LDS or shuffles.  K and V come as e2m1 codes and are widened to bf16 by the
 // hardware conversion, which applies the power-of-two block scale (exact).
 //
-// What bounds it: HBM reads of the cache (D*17/16 bytes per token and KV head) and
-// the vector instructions that widen it (half a conversion and, for V, half a byte
-// permutation per value of a tile and row block, besides the softmax) share the
-// time.  64 requests over 1 to 8,000 positions (k=6, 32 heads over 8 KV heads of
-// D=128): 94 us, of these plan 5, this kernel 78 (301 MB, 3.9 TB/s), join 7; with the
-// loads alone 81 in all.  One user over 32,000 positions, k=0: 18 us, of these join
-// 5; 64 requests over 4,000 with 64 heads (R=56, two row blocks that both read and
-// widen the cache): 133 us, 440 TFLOP/s.
+// What bounds it: the vector instructions that widen the cache (half a conversion
+// and, for V, half a byte permutation per value of a tile and row block) and make the
+// softmax, and HBM reads (D*17/16 bytes per token and KV head), which do not overlap
+// fully at two waves per SIMD.  64 requests over 512 to 16,384 positions (k=6, 32
+// heads over 8 KV heads of D=128, 301 MB): 80 us, of these plan 5, this kernel 69
+// (4.4 TB/s, vector units busy 54 % and matrix units 28 % of the time), join 7.  One
+// user over 32,000 positions, k=0: 18.5 us, of these join 4.4; 64 requests over 4,000
+// with 64 heads (R=56, two row blocks that both read and widen the cache): 130 us,
+// 450 TFLOP/s.
 
 #include "kv_common.h"
 
@@ -1021,7 +1022,7 @@ static int launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
   if (p.chunks > 1) {
     const int wide = a.batch * a.kv_heads * p.row_blocks;
     // a workgroup per row where few rows have many chunks (one user over 32,000
-    // positions: 18.1 us a call, with the other form 21.8), else per 16 rows (8
+    // positions: 18.5 us a call, with the other form 22), else per 16 rows (8
     // requests over 2,000: 16.5 us, a workgroup per row 20.8)
     if (p.chunks > 8 && wide * MT * 16 <= 2048)
       hipLaunchKernelGGL((k_attn_join<D, MT, T>), dim3(wide * (MT * 16)), dim3(256), 0, s, a);
