@@ -416,7 +416,8 @@ size_t spec_kv_attention_workspace_bytes(int dtype, int batch, int max_k, int he
  * What a row does not see never reaches it, NaN included.  scale q.k log2 e, and
  * sums of weights (up to 2^8 each before the division) times V, have to stay in
  * fp32's range: past it a row is NaN or infinite.
- *   q, out         [total_rows][heads][head_dim] of dtype, rows ld_q / ld_out apart
+ *   q, out         [total_rows][heads][head_dim] of dtype, rows ld_q / ld_out apart;
+ *                  out may be q itself with the same ld
  *   max_k          at most 63; requests with more drafts are SV_ROW_BAD_K
  *   max_context    bound of context_lens[b] + rows; requests past it are
  *                  SV_ROW_BAD_PARAM, like context_lens[b] < 0

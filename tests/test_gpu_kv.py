@@ -507,6 +507,26 @@ def test_attention_scales_from_the_smallest_to_the_largest(dtype, scale, shift):
     check_attention(out, q, K, V, [0, 2], [70], [2], dtype, float(np.float32(scale)))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("max_context", [1200, 20000])
+def test_attention_writes_over_its_queries(dtype, d, max_context):
+    """Several row blocks, whole and split, planned and not: out = q gives the same bits."""
+    rng = np.random.default_rng(d)
+    batch = 4 if max_context == 1200 else 40
+    rows = [int(x) for x in rng.integers(1, 9, batch)]
+    ctx = [int(x) for x in rng.integers(0, 1100, batch)]
+    cache, _, _ = make_attention(d, 64, 1, rows, ctx, 7)
+    q = torch.randn(sum(rows), 20, d, device=DEV).to(DTYPES[dtype])
+    kw = dict(max_k=7, max_context=max_context)
+    out, _ = binding.kv_attention(cache, q, _i(_cu(rows)), _i(ctx), **kw)
+    for _ in range(3):
+        x = q.clone()
+        same, st = binding.kv_attention(cache, x, _i(_cu(rows)), _i(ctx), out=x, **kw)
+        assert same is x and st.cpu().tolist() == [0] * batch
+        assert torch.equal(x, out)
+
+
 def test_attention_statuses_and_what_it_leaves():
     d, page = 64, 16
     rows, ctx = [2, 2, 2, 3, 2, 2], [20, 30, 40, 30, 30, 30]
