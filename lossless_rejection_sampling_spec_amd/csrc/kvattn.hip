@@ -735,7 +735,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
     __syncthreads();
     // row tiles that hold rows: a short request does not pay for a long one's
     const int tiles = (min(R - rb * MT * 16, MT * 16) + 15) / 16;
-    if (MT == 1 || tiles == 1) x.template run<1, WAVES>(a, w, t, id, at, wave, q_lds);
+    // (not where the copies of the loop would not fit the registers)
+    if (MT * FR >= 32) x.template run<MT, WAVES>(a, w, t, id, at, wave, q_lds);
+    else if (MT == 1 || tiles == 1) x.template run<1, WAVES>(a, w, t, id, at, wave, q_lds);
     else if (MT == 2 || tiles == 2) x.template run<(MT < 2 ? 1 : 2), WAVES>(a, w, t, id, at, wave, q_lds);
     else if (tiles == 3) x.template run<(MT < 3 ? 1 : 3), WAVES>(a, w, t, id, at, wave, q_lds);
     else x.template run<MT, WAVES>(a, w, t, id, at, wave, q_lds);
@@ -951,9 +953,12 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
     if (seen < tokens) tokens = seen;
   }
   const int64_t tiles = (tokens + TILE - 1) / TILE;
-  // what fits the registers without spills: with 16 MT = 8192/D more of the kernels
-  // spilled, and the spilling code gave wrong rows
-  const int most = 256 / d;
+  // what fits the registers without spills: kernels of more rows spilled, and the
+  // spilling code gave wrong rows.  (64 requests over 2,000 positions, R=28, D=256: 65
+  // us with 32 rows per workgroup, 93 with 16.  64 rows at D=128, K widened for each
+  // row tile again to fit: R=56, 64 over 4,000 116 us, with 32 rows 130; but 128 over 1
+  // to 8,000 99 and 82, 8 over 4,000 30 and 27.)
+  const int most = dtype == SV_BF16 && d == 256 ? 2 : 256 / d;
   p.mt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   if (p.mt > most) p.mt = most;
   int64_t items;
@@ -979,12 +984,12 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
   // two waves per workgroup (more items at once, each twice as long) where items are
   // many, and whole or rich in products: 512 requests over 1 to 2,000 positions 64 us,
   // with four 81; 256 over 1 to 4,000 (R=28) 67.5 and 76.5; 128 over 1 to 8,000 with
-  // R=56 81.5 and 92; but 64 over 8,000 with R=4 128 and 122, D=256 (16 rows at a
-  // time) 83 and 80.  fp32 waves take longer for an item and need more of them: 512
-  // over 1 to 2,000 79.5 and 97, 256 with R=48 69 and 58
-  p.waves = 4;
-  if (p.plan && (dtype == SV_F32 ? p.chunks == 1 && items >= 4096 : p.chunks == 1 || p.mt > 1))
-    p.waves = 2;
+  // R=56 81.5 and 92; but 64 over 8,000 with R=4 128 and 122, 64 over 1 to 8,000 at
+  // D=256 (one tile on its way per wave) 80 and 61.  fp32 waves take longer for an item
+  // and need more of them: 512 over 1 to 2,000 79.5 and 97, 256 with R=48 69 and 58
+  const bool two = dtype == SV_F32 ? p.chunks == 1 && items >= 4096
+                                   : p.chunks == 1 || (p.mt > 1 && d < 256);
+  p.waves = p.plan && two ? 2 : 4;
   // eight for fp32, whose waves are the slowest, where workgroups are few (32 requests
   // over 1 to 2,000 positions 16.1 us, with four 18.0; 8 over 2,000 19.5 both ways).
   // bf16 only loses by the longer join (4 over 500: 13.4 us against 12.0), and at
@@ -1108,6 +1113,7 @@ int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_
     SVK_CASE(64, 4, 2, __bf16);
     SVK_CASE(128, 1, 3, __bf16);
     SVK_CASE(128, 2, 2, __bf16);
+    SVK_CASE(256, 2, 1, __bf16);
     SVK_CASE(256, 1, 2, __bf16);
   } else {
     SVK_CASE(64, 1, 2, float);
