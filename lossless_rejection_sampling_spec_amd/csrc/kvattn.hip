@@ -368,7 +368,9 @@ struct Attn {
         for (int k = 0; k < FR; ++k) o[mt][k] *= f;
         m[mt] = nm;
         mc[mt] = nm == -INFINITY ? 0.f : nm * w.c;
-        over[mt] = nm + RAISE / w.c;
+        // (finite for the smallest scales too: a row that has seen nothing stays at -inf,
+        // so that its first visible score raises it)
+        over[mt] = nm + __builtin_fminf(RAISE / w.c, 3.4e38f);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {

@@ -1,0 +1,50 @@
+"""GPU tests of the cache calls at the ends of what they accept: scales and scores at
+the limits, many chunks, sizes at which a launch or a workspace could not hold."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import test_gpu_kv as T  # noqa: E402
+from lossless_rejection_sampling_spec_amd import binding  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = T.DEV
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    binding.lib()
+    yield
+
+
+def repeated(cache, times):
+    """The cache's first request `times` times over the same pages."""
+    table = cache.page_table[:1].expand(times, -1).contiguous()
+    return binding.KVCache(pages=cache.pages, page_table=table,
+                           seq_lens=cache.seq_lens[:1].expand(times).contiguous(),
+                           ref_counts=cache.ref_counts, page_size=cache.page_size,
+                           kv_heads=cache.kv_heads, head_dim=cache.head_dim)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,heads", [(64, 4), (128, 4), (256, 2)])
+@pytest.mark.parametrize("scale", [1e-38, 3e-39, 1e-44, 1e-30])
+@pytest.mark.parametrize("batch,window", [(1, 200), (256, 700)])
+def test_the_smallest_scales_with_a_window(dtype, d, heads, scale, batch, window):
+    """Rows that see nothing of a wave's first tile, but of its later ones: the window of
+    row 0 starts at the last position of a tile, those of the others behind it.  The
+    result is the mean of the visible V."""
+    rows = 6
+    ctx = 639 + window - 1                             # row 0's first position: 639, 31 mod 32
+    cache, K, V = T.make_attention(d, 16, 1, [rows], [ctx], d)
+    q = torch.randn(rows, heads, d, device=DEV).to(T.DTYPES[dtype])
+    cu = [rows * b for b in range(batch + 1)]
+    out, st = binding.kv_attention(repeated(cache, batch), q.repeat(batch, 1, 1), T._i(cu),
+                                   T._i([ctx] * batch), max_k=5, max_context=ctx + rows, scale=scale,
+                                   window=window)
+    assert st.cpu().tolist() == [0] * batch
+    T.check_attention(out, q, K, V, [0, rows], [ctx], [rows], dtype, float(np.float32(scale)), window)
+    assert (out.view(batch, -1) == out.view(batch, -1)[0]).all()
