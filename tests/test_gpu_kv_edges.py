@@ -48,3 +48,42 @@ def test_the_smallest_scales_with_a_window(dtype, d, heads, scale, batch, window
     assert st.cpu().tolist() == [0] * batch
     T.check_attention(out, q, K, V, [0, rows], [ctx], [rows], dtype, float(np.float32(scale)), window)
     assert (out.view(batch, -1) == out.view(batch, -1)[0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,heads", [(64, 1), (128, 20), (256, 2)])
+@pytest.mark.parametrize("power", [10, 25, 31, 40, 90])
+@pytest.mark.parametrize("batch", [1, 300])
+def test_scores_far_beyond_the_exponents_of_fp32(dtype, d, heads, power, batch):
+    """Queries of a single power of two: every score is exact, the largest ones are
+    equal, and few of the others count beside them.  The result is the mean of V over the
+    largest, and from 2^30 on that or NaN for the whole row."""
+    rows, ctx = 3, 900
+    cache, K, V = T.make_attention(d, 16, 1, [rows], [ctx], power)
+    x = torch.zeros(rows, heads, d)
+    for j in range(rows):
+        for h in range(heads):
+            x[j, h, (7 * j + 11 * h) % d] = (-1) ** h * 2.0 ** power
+    q = x.to(T.DTYPES[dtype]).to(DEV)
+    cu = [rows * b for b in range(batch + 1)]
+    out, st = binding.kv_attention(repeated(cache, batch), q.repeat(batch, 1, 1), T._i(cu),
+                                   T._i([ctx] * batch), max_k=2, max_context=ctx + rows, scale=1.0)
+    assert st.cpu().tolist() == [0] * batch
+    o = T._f64(out)
+    for j in range(rows):
+        for h in range(heads):
+            s = (-1) ** h * K[0][:ctx + j + 1, 0, (7 * j + 11 * h) % d] * 2.0 ** power
+            w = np.exp(s - s.max())
+            want = w @ V[0][:ctx + j + 1, 0] / w.sum()
+            mass = w @ np.abs(V[0][:ctx + j + 1, 0]) / w.sum()
+            # the scores are exact: a step of s - m times log2 e, of exp2, of each sum
+            # and of the result, and half a bf16 step of each weight of bf16 rows
+            gap = np.minimum(s.max() - s, 200.0)
+            rel = (T.HALF["bf16"] if dtype == "bf16" else 0) + 2.0 ** -20 + 2 * ctx * 2.0 ** -24
+            tol = (mass * rel + (w * gap * 4 * 2.0 ** -24) @ np.abs(V[0][:ctx + j + 1, 0]) / w.sum()
+                   + T.HALF[dtype] * np.abs(want))
+            if np.abs(s).max() * 1.4427 >= 2.0 ** 30 and np.isnan(o[j, h]).all():
+                assert np.isnan(o[-rows + j, h]).all()
+                continue
+            for b in {0, batch - 1}:
+                assert np.all(np.abs(o[b * rows + j, h] - want) <= tol), (j, h, b)
