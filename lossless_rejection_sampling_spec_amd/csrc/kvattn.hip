@@ -961,8 +961,12 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
     if (seen < tokens) tokens = seen;
   }
   const int64_t tiles = (tokens + TILE - 1) / TILE;
-  // what fits the registers without spills: kernels of more rows spilled, and the
-  // spilling code gave wrong rows.  (64 requests over 2,000 positions, R=28, D=256: 65
+  // what fits the vector registers; tests/test_kernel_registers.py holds every instance
+  // to it.  The compiler (clang 22.0.0git, roc-7.2.0) made a wrong kernel of one that
+  // did not fit: 32 rows at D=256 with two tiles on their way spilled 113 registers, the
+  // four words of row tile 1's first query operand among them, two to scratch and two to
+  // accumulation registers, of which only one was read back before the matrix
+  // instructions, so that rows 16 to 31 were wrong.  (64 requests over 2,000 positions, R=28, D=256: 65
   // us with 32 rows per workgroup, 93 with 16.  64 rows at D=128, K widened for each
   // row tile again to fit: R=56, 64 over 4,000 116 us, with 32 rows 130; but 128 over 1
   // to 8,000 99 and 82, 8 over 4,000 30 and 27.)
