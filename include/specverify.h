@@ -356,8 +356,9 @@ int spec_verify_sampled_noalloc(const void* target_logits, int target_dtype, int
  *   total_rows, and every later one, is SV_ROW_BAD_K.
  * Calls that change the same tables, counts or pages are ordered by the
  *   caller (one stream).  Batches hold at most 1,024 requests, pools at most
- *   2^24 pages.  Return values as elsewhere (SV_ERR_NULL also for a workspace
- *   that is needed and NULL or not 16-byte aligned).
+ *   2^24 pages.  Return values as elsewhere.  A workspace that is needed and NULL
+ *   is SV_ERR_NULL; one that is not 16-byte aligned is SV_ERR_NULL in
+ *   spec_kv_attention and SV_ERR_SHAPE in spec_kv_reserve and spec_kv_compact.
  */
 
 /* Bytes of a page of one layer (0 on invalid sizes). */
