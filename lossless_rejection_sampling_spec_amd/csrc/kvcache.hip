@@ -434,6 +434,7 @@ struct PageArgs {
   int32_t* dst;           // [batch] the page for a copy (small pools)
   int32_t* first;         // [batch + 1] rank of a request's first new page among the free ones
   int32_t* copy;          // [batch] page to copy into the request's first new page, or -1
+  int copy_layers;        // workgroups that share a small pool's copies of one request
 };
 
 __device__ __forceinline__ int pages_of(int64_t n, int page_log2) {
@@ -646,15 +647,19 @@ __device__ __forceinline__ void copy_tail(const PageArgs& a, int src, int dst, i
 }
 
 // The copies of all layers (first: they are the longest), then 1,024 pages per
-// workgroup to hand out.
+// workgroup to hand out.  A workgroup per request and layer up to 1,024 layers, so that
+// the grid stays under the 2^24 workgroups of 256 that a launch can have.
+constexpr int MAX_COPY_LAYERS = 1024;
 __global__ __launch_bounds__(256) void k_reserve_finish(PageArgs a) {
-  if ((int)blockIdx.x < a.batch * a.layers) {
+  if ((int)blockIdx.x < a.batch * a.copy_layers) {
     const int b = (int)blockIdx.x % a.batch, src = a.copy[b];
-    if (src >= 0) copy_tail(a, src, a.dst[b], (int)blockIdx.x / a.batch);
+    if (src < 0) return;
+    for (int layer = (int)blockIdx.x / a.batch; layer < a.layers; layer += a.copy_layers)
+      copy_tail(a, src, a.dst[b], layer);
     return;
   }
   __shared__ int first[MAX_BATCH + 1], ctx[MAX_BATCH], copy[MAX_BATCH];
-  const int w0 = ((int)blockIdx.x - a.batch * a.layers) * 16;
+  const int w0 = ((int)blockIdx.x - a.batch * a.copy_layers) * 16;
   if (a.rank[w0] >= a.first[a.batch]) return;
   for (int i = threadIdx.x; i <= a.batch; i += 256) first[i] = a.first[i];
   for (int i = threadIdx.x; i < a.batch; i += 256) {
@@ -1044,6 +1049,7 @@ int spec_kv_reserve(const int32_t* cu_seqlens, int batch, int page_size, int32_t
   a.page_bytes = page_bytes;
   a.layer_bytes = layer_bytes;
   a.layers = layers;
+  a.copy_layers = layers < MAX_COPY_LAYERS ? layers : MAX_COPY_LAYERS;
   a.ctx = context_lens;
   a.status = status;
   uint8_t* w = (uint8_t*)workspace;
@@ -1060,7 +1066,7 @@ int spec_kv_reserve(const int32_t* cu_seqlens, int batch, int page_size, int32_t
     const int groups = (a.num_pages + 1023) / 1024;
     hipLaunchKernelGGL(k_pool_bits, dim3(groups), dim3(256), 0, s, a.refs, a.num_pages, a.bits);
     hipLaunchKernelGGL(k_reserve_small, dim3(1), dim3(1024), 0, s, a);
-    hipLaunchKernelGGL(k_reserve_finish, dim3(batch * layers + groups), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_reserve_finish, dim3(batch * a.copy_layers + groups), dim3(256), 0, s, a);
   } else {
     hipLaunchKernelGGL(k_count, dim3(a.chunks), dim3(256), 0, s, a.refs, a.num_pages, a.used);
     hipLaunchKernelGGL(k_reserve_plan, dim3(1), dim3(1024), 0, s, a);

@@ -87,3 +87,27 @@ def test_scores_far_beyond_the_exponents_of_fp32(dtype, d, heads, power, batch):
                 continue
             for b in {0, batch - 1}:
                 assert np.all(np.abs(o[b * rows + j, h] - want) <= tol), (j, h, b)
+
+
+def test_reserve_of_a_full_batch_over_very_many_layers():
+    """1,024 requests and 20,000 layers: a workgroup for each request and layer would be
+    more than a launch can have.  The shared tail is copied in every layer."""
+    layers, page, batch = 20000, 16, 1024
+    cache = binding.KVCache.create(layers=layers, num_pages=6, page_size=page, kv_heads=1, head_dim=64,
+                                   requests=batch, max_context=64, device=DEV)
+    cache.pages.random_(0, 256)
+    rows = [0] * batch
+    rows[0] = 20
+    ctx, st = binding.kv_reserve(cache, T._i(T._cu(rows)))
+    assert st.cpu().tolist() == [0] + [3] * (batch - 1)
+    st = binding.kv_fork(cache, T._i([0]), T._i([batch - 1]))
+    assert st.cpu().tolist() == [0]
+    before = cache.pages.clone()
+    rows[0], rows[-1] = 0, 1
+    ctx, st = binding.kv_reserve(cache, T._i(T._cu(rows)))
+    assert st.cpu().tolist() == [3] * (batch - 1) + [0] and int(ctx[-1]) == 20
+    assert cache.page_table.cpu()[[0, -1], :2].tolist() == [[0, 1], [0, 2]]
+    assert cache.ref_counts.cpu().tolist() == [2, 1, 1, 0, 0, 0]
+    assert torch.equal(cache.pages[:, 2], before[:, 1])
+    for p in (0, 1, 3, 4, 5):
+        assert torch.equal(cache.pages[:, p], before[:, p])
