@@ -353,11 +353,14 @@ int spec_verify_sampled_noalloc(const void* target_logits, int target_dtype, int
  *   ceil(seq_len / P) mean nothing.  A request (slot) without rows in a call
  *   is SV_ROW_BAD_K there and left alone.
  * Offsets: the first request whose offsets are negative, go back or pass
- *   total_rows, and every later one, is SV_ROW_BAD_K.
+ *   total_rows (which spec_kv_reserve does not know), and every later one, is
+ *   SV_ROW_BAD_K.
  * Calls that change the same tables, counts or pages are ordered by the
  *   caller (one stream).  Batches hold at most 1,024 requests, pools at most
- *   2^24 pages.  Return values as elsewhere.  A workspace that is needed and NULL
- *   is SV_ERR_NULL; one that is not 16-byte aligned is SV_ERR_NULL in
+ *   2^24 pages, and a call with rows at least one (total_rows >= 1: a step in
+ *   which no request has rows makes no append and no attention).  Return values
+ *   as elsewhere.  A workspace that is needed and NULL is SV_ERR_NULL; one that
+ *   is not 16-byte aligned is SV_ERR_NULL in
  *   spec_kv_attention and SV_ERR_SHAPE in spec_kv_reserve and spec_kv_compact.
  */
 

@@ -415,6 +415,9 @@ class KVCache:
                 or t.shape[1] < 1 or t.stride(1) != 1 or t.stride(0) < t.shape[1]):
             raise ValueError("page_table must be an int32 device tensor [requests, pages], "
                              "unit stride along a row")
+        # (past these every call, or fork and compact, would refuse: spec_kv_* take no more)
+        if t.shape[0] > 1024 or p.shape[1] > 1 << 24 or p.shape[0] > 65535:
+            raise ValueError("a cache holds at most 1024 requests, 2^24 pages and 65535 layers")
         _check_vec(self.seq_lens, "seq_lens", torch.int32, t.shape[0])
         _check_vec(self.ref_counts, "ref_counts", torch.int32, p.shape[1])
         if self.seq_lens.device != p.device or self.ref_counts.device != p.device:
@@ -431,7 +434,8 @@ class KVCache:
     @classmethod
     def create(cls, *, layers: int, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
                requests: int, max_context: int, device) -> "KVCache":
-        """An empty cache: every page free, every request of length 0."""
+        """An empty cache: every page free, every request of length 0.
+        At most 1,024 requests."""
         n = kv_page_bytes(kv_heads, head_dim, page_size)
         if n == 0:
             raise ValueError("KVCache: head_dim is 64, 128 or 256, page_size 16, 32, 64, 128 or 256")

@@ -111,3 +111,26 @@ def test_reserve_of_a_full_batch_over_very_many_layers():
     assert torch.equal(cache.pages[:, 2], before[:, 1])
     for p in (0, 1, 3, 4, 5):
         assert torch.equal(cache.pages[:, p], before[:, p])
+
+
+def test_a_cache_of_more_requests_than_the_calls_take_is_refused():
+    def make(**kw):
+        return binding.KVCache.create(**{**dict(layers=1, num_pages=4, page_size=16, kv_heads=1,
+                                                head_dim=64, requests=2, max_context=16, device=DEV),
+                                         **kw})
+    cache = make(requests=1024)
+    assert binding.kv_compact(cache).cpu().tolist() == [0]
+    assert binding.kv_fork(cache, T._i([0]), T._i([1023])).cpu().tolist() == [0]
+    for kw in (dict(requests=1025), dict(layers=65536, num_pages=1)):
+        with pytest.raises(ValueError, match="at most 1024 requests"):
+            make(**kw)
+    # a step in which no request has rows: the page calls take it, the others are not made
+    cu = T._i([0, 0, 0])
+    ctx, st = binding.kv_reserve(cache, cu)
+    assert st.cpu().tolist() == [3, 3] and ctx.cpu().tolist() == [-1, -1]
+    assert binding.kv_release(cache, T._i([0, 0]), ctx).cpu().tolist() == [0, 0]
+    none = torch.empty(0, 1, 64, device=DEV)
+    with pytest.raises(ValueError):
+        binding.kv_append(cache, none, none, none, cu, ctx)
+    with pytest.raises(ValueError):
+        binding.kv_attention(cache, none, cu, ctx, max_k=0, max_context=16)
