@@ -134,3 +134,35 @@ def test_a_cache_of_more_requests_than_the_calls_take_is_refused():
         binding.kv_append(cache, none, none, none, cu, ctx)
     with pytest.raises(ValueError):
         binding.kv_attention(cache, none, cu, ctx, max_k=0, max_context=16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_append_gives_the_same_bytes_whatever_the_call(dtype, d):
+    """The rows of two requests in one call, in a call of each, and one by one."""
+    rows, ctx, heads, kv = [9, 14], [5, 20], 6, 2
+    x = torch.randn(sum(rows), heads + 2 * kv, d, device=DEV).to(T.DTYPES[dtype])
+    w = 1 + 0.1 * torch.randn(2, d, device=DEV)
+    cs = torch.from_numpy(T._rotation(64, d)).to(DEV)
+
+    def make():
+        cache = binding.KVCache.create(layers=1, num_pages=8, page_size=16, kv_heads=kv, head_dim=d,
+                                       requests=2, max_context=64, device=DEV)
+        cache.page_table.copy_(torch.arange(8, device=DEV).view(2, 4))
+        return cache
+
+    def append(cache, x, cu, ctx):
+        q, st = binding.kv_append(cache, x[:, :heads], x[:, heads:heads + kv], x[:, heads + kv:],
+                                  T._i(cu), T._i(ctx), q_weight=w[0], k_weight=w[1], cos_sin=cs)
+        assert all(s in (0, 3) for s in st.cpu().tolist())
+        return q
+
+    whole = make()
+    q = append(whole, x, [0, 9, 23], ctx)
+    apart = make()
+    q2 = torch.cat([append(apart, x[:9], [0, 9, 9], ctx), append(apart, x[9:], [0, 0, 14], ctx)])
+    single = make()
+    q3 = torch.cat([append(single, x[i:i + 1], [0, 1, 1] if i < 9 else [0, 0, 1],
+                           [5 + i, 0] if i < 9 else [0, 11 + i]) for i in range(23)])
+    for other, oq in ((apart, q2), (single, q3)):
+        assert torch.equal(whole.pages, other.pages) and torch.equal(q, oq)
