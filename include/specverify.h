@@ -405,7 +405,13 @@ int spec_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, con
                    void* q_out, int64_t ld_qout, void* k_values, void* v_values, int32_t* status,
                    void* stream);
 
-/* Bytes of workspace spec_kv_attention needs with these sizes (0 on invalid sizes). */
+/*
+ * Bytes of workspace spec_kv_attention needs with these sizes (0 on invalid sizes, and
+ * on those that would be 2^24 workgroups or more).  They follow the bound max_context,
+ * not what the requests hold, up to 512 MiB of partial results or 8 places per request,
+ * KV head and block of rows: k=6, 32 heads over 8 KV heads of D=128 bf16 and a bound of
+ * 131,072 positions take 512 MiB for 64 requests, 488 for 256, 1,042 for 1,024.
+ */
 size_t spec_kv_attention_workspace_bytes(int dtype, int batch, int max_k, int heads, int kv_heads,
                                          int head_dim, int max_context, int window, int sinks);
 

@@ -65,7 +65,7 @@ struct AttnArgs {
   int64_t ld_out;
   int32_t* status;
   float* part;          // chunk partials: [item][rows][D], then [item][rows][2] (max, sum)
-  int chunks, chunk_tiles, row_blocks, block_rows;
+  int chunks, chunk_tiles, row_blocks, block_rows;   // chunks of a request at most
   struct Item* plan;    // [1 + items], the first holds how many there are; or NULL
 };
 
@@ -84,6 +84,12 @@ __device__ __forceinline__ Span span_of(int ctx, int rows, int window, int sinks
   s.sink_tiles = min((sinks + TILE - 1) / TILE, s.tile0);
   s.tiles = s.sink_tiles + (s.n - 1) / TILE - s.tile0 + 1;
   return s;
+}
+
+// Tiles of a chunk of a request: the call's, or more where the request would have more
+// chunks than the call has places for.
+__device__ __forceinline__ int chunk_of(const AttnArgs& a, int tiles) {
+  return tiles <= a.chunks * a.chunk_tiles ? a.chunk_tiles : (tiles + a.chunks - 1) / a.chunks;
 }
 
 // A request's numbers and its SV_ROW_* by them alone (pages are checked where
@@ -488,9 +494,42 @@ struct Attn {
 
   // The wave's tiles: every WAVES-th of the share, for the first M row tiles.
   // id: lane i holds the pages of tile tbegin + i (its two halves).
+  static __device__ __forceinline__ int base_of(const Span& sp, int i) {
+    return (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.tile0) * TILE;
+  }
+  // Lane i: the pages of tile first + i (its two halves), 64 tiles of the share at a time.
+  struct Pages {
+    int id[2], first;
+    // (true if a page is missing or outside the pool; page 0 is read in its place)
+    __device__ __forceinline__ bool ask(const AttnArgs& a, const Share& w, const int32_t* tab, int from) {
+      const int lane = threadIdx.x & 63;
+      bool bad = false;
+      first = from;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int slot = (base_of(w.sp, from + lane) + 16 * hf) >> a.page_log2;
+        const bool need = from + lane < w.tend && page_needed(w.sp, slot, a.page_log2, a.sinks);
+        const bool have = need && slot < a.ld_table;
+        id[hf] = tab[have ? slot : 0];
+        const bool in_pool = have && (uint32_t)id[hf] < (uint64_t)a.num_pages;
+        bad |= need && !in_pool;
+        if (!in_pool) id[hf] = 0;
+      }
+      return __any(bad);
+    }
+  };
+  static __device__ __forceinline__ void fetch(const AttnArgs& a, const Share& w, Tile<D>& t,
+                                               const Pages& id, const Lane& at, int i) {
+    const uint32_t i0 = (uint32_t)__builtin_amdgcn_readlane(id.id[0], i - id.first);
+    const uint32_t i1 = (uint32_t)__builtin_amdgcn_readlane(id.id[1], i - id.first);
+    const int tb = base_of(w.sp, i) & (a.page - 1);
+    load(t, 0, w.pool + (uint64_t)i0 * w.page_bytes, a.unit, at, tb);
+    load(t, 1, w.pool + (uint64_t)i1 * w.page_bytes, a.unit, at, (tb + 16) & (a.page - 1));
+  }
+
   template <int M, int WAVES, int DEPTH>
   __device__ __forceinline__ void run(const AttnArgs& a, const Share& w, Tile<D> (&t)[DEPTH],
-                                      const int (&id)[2], const Lane& at, int wave,
+                                      Pages& id, const int32_t* tab, bool& bad, const Lane& at, int wave,
                                       const bf16x8* q) {
     const int last = w.tend - 1;
     for (int i = w.tbegin + wave; i < w.tend; i += DEPTH * WAVES) {
@@ -503,20 +542,11 @@ struct Attn {
               (a.window > 0 && base <= w.ctx + w.rows - 1 - a.window && base + TILE > a.sinks);
           step<M>(a, t[k], masked, base, w, q);
         }
-        fetch(a, w, t[k], id, at, min(i + (k + DEPTH) * WAVES, last));
+        const int ahead = min(i + (k + DEPTH) * WAVES, last);
+        if (ahead - id.first >= 64) bad |= id.ask(a, w, tab, ahead);   // (chunks of more than 64 tiles)
+        fetch(a, w, t[k], id, at, ahead);
       }
     }
-  }
-  static __device__ __forceinline__ int base_of(const Span& sp, int i) {
-    return (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.tile0) * TILE;
-  }
-  static __device__ __forceinline__ void fetch(const AttnArgs& a, const Share& w, Tile<D>& t,
-                                               const int (&id)[2], const Lane& at, int i) {
-    const uint32_t i0 = (uint32_t)__builtin_amdgcn_readlane(id[0], i - w.tbegin);
-    const uint32_t i1 = (uint32_t)__builtin_amdgcn_readlane(id[1], i - w.tbegin);
-    const int tb = base_of(w.sp, i) & (a.page - 1);
-    load(t, 0, w.pool + (uint64_t)i0 * w.page_bytes, a.unit, at, tb);
-    load(t, 1, w.pool + (uint64_t)i1 * w.page_bytes, a.unit, at, (tb + 16) & (a.page - 1));
   }
 };
 
@@ -569,10 +599,11 @@ __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
     rest = a.kv_heads * ((rows * G + a.block_rows - 1) / a.block_rows);
     if (fits) {
       const int tiles = span_of(ctx, rows, a.window, a.sinks).tiles;
-      full = (tiles - 1) / a.chunk_tiles * rest;
+      const int ct = chunk_of(a, tiles);
+      full = (tiles - 1) / ct * rest;
       // a tile costs about as much as two row tiles' products with it
       const int mt = (min(rows * G, a.block_rows) + 15) / 16, most = a.chunk_tiles * (2 + a.block_rows / 16);
-      const int work = ((tiles - 1) % a.chunk_tiles + 1) * (2 + mt);
+      const int work = min(min((tiles - 1) % ct + 1, a.chunk_tiles) * (2 + mt), most);
       at_level = LEVELS - 1 - work * (LEVELS - 1) / most;
     }
   }
@@ -698,9 +729,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
   }
   Share w;
   w.sp = span_of(ctx, rows, a.window, a.sinks);
-  const int over = (w.sp.tiles - 1) % a.chunk_tiles + 1;
-  w.tend = over + chunk * a.chunk_tiles;
-  w.tbegin = max(0, w.tend - a.chunk_tiles);
+  const int ct = chunk_of(a, w.sp.tiles);
+  w.tend = (w.sp.tiles - 1) % ct + 1 + chunk * ct;
+  w.tbegin = max(0, w.tend - ct);
   if (st == SV_ROW_OK ? w.tend > w.sp.tiles : chunk > 0) return;
   w.row0 = row0;
   w.ctx = ctx;
@@ -717,21 +748,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
   bool bad = st != SV_ROW_OK;
   if (!bad) {
     const int32_t* tab = a.table + (int64_t)b * a.ld_table;
-    // lane i: the pages of the chunk's tile i (its first and second 16 tokens)
-    int id[2];
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int slot = (A::base_of(w.sp, w.tbegin + lane) + 16 * hf) >> a.page_log2;
-      const bool need = w.tbegin + lane < w.tend && page_needed(w.sp, slot, a.page_log2, a.sinks);
-      const bool have = need && slot < a.ld_table;
-      id[hf] = tab[have ? slot : 0];
-      const bool in_pool = have && (uint32_t)id[hf] < (uint64_t)a.num_pages;
-      bad |= need && !in_pool;
-      if (!in_pool) id[hf] = 0;
-    }
+    typename A::Pages id;
+    bad = id.ask(a, w, tab, w.tbegin);
     typename A::template Raw<WAVES> raw;
     raw.ask(a, w, h, wave);
-    bad = __any(bad);
     const typename A::Lane at = A::lane_offsets(a.page);
     // DEPTH tiles are on their way at any time: a buffer is filled again as soon
     // as its tile is done.  Past the end the last tile is loaded once more: with a
@@ -746,11 +766,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
     // row tiles that hold rows: a short request does not pay for a long one's
     const int tiles = (min(R - rb * MT * 16, MT * 16) + 15) / 16;
     // (not where the copies of the loop would not fit the registers)
-    if (MT * FR >= 32) x.template run<MT, WAVES>(a, w, t, id, at, wave, q_lds);
-    else if (MT == 1 || tiles == 1) x.template run<1, WAVES>(a, w, t, id, at, wave, q_lds);
-    else if (MT == 2 || tiles == 2) x.template run<(MT < 2 ? 1 : 2), WAVES>(a, w, t, id, at, wave, q_lds);
-    else if (tiles == 3) x.template run<(MT < 3 ? 1 : 3), WAVES>(a, w, t, id, at, wave, q_lds);
-    else x.template run<MT, WAVES>(a, w, t, id, at, wave, q_lds);
+    if (MT * FR >= 32) x.template run<MT, WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
+    else if (MT == 1 || tiles == 1) x.template run<1, WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
+    else if (MT == 2 || tiles == 2) x.template run<(MT < 2 ? 1 : 2), WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
+    else if (tiles == 3) x.template run<(MT < 3 ? 1 : 3), WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
+    else x.template run<MT, WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
   }
   if (__any(x.poison != 0)) x.apply_poison();
 
@@ -765,7 +785,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
       part_l[wave][mt][n] = bad ? __builtin_nanf("") : x.l[mt][0];
     }
 
-  const bool whole = st != SV_ROW_OK || w.sp.tiles <= a.chunk_tiles;
+  const bool whole = st != SV_ROW_OK || w.sp.tiles <= ct;
   // this item's place among the partials
   const int64_t item = (((int64_t)chunk * a.batch + b) * a.kv_heads + h) * a.row_blocks + rb;
   float* part = a.part + item * (MT * 16) * D;
@@ -835,7 +855,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   int row0, rows, ctx;
   if (request_status(a, b, row0, rows, ctx) != SV_ROW_OK) return;
   const Span sp = span_of(ctx, rows, a.window, a.sinks);
-  const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+  const int ct = chunk_of(a, sp.tiles), n = (sp.tiles + ct - 1) / ct;
   const int r = rb * MT * 16 + local;
   if (n < 2 || r >= rows * a.group) return;
   const int64_t per_chunk = (int64_t)a.batch * a.kv_heads * a.row_blocks;
@@ -900,7 +920,7 @@ __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
   int row0, rows, ctx;
   if (request_status(a, b, row0, rows, ctx) != SV_ROW_OK) return;
   const Span sp = span_of(ctx, rows, a.window, a.sinks);
-  const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+  const int ct = chunk_of(a, sp.tiles), n = (sp.tiles + ct - 1) / ct;
   const int local = mt * 16 + (threadIdx.x >> 4), r = rb * MT * 16 + local;
   if (n < 2 || r >= rows * a.group) return;  // (whole groups of 16 lanes)
   const int64_t per_chunk = (int64_t)a.batch * a.kv_heads * a.row_blocks;
@@ -950,6 +970,13 @@ struct Plan {
   bool plan;
 };
 
+// What the partial results of a call may take: its bound on contexts is often far above
+// what the requests hold, and every place is a workgroup to start.  (256 requests over 200
+// to 2,000 positions, k=6, 32 heads over 8 KV heads of D=128, bound 131,072: 488 MiB and
+// 93 us, with a place for every chunk 2,084 MiB and 113; 1,024 requests 347 and 441.  One
+// request of 131,072 among the 256, in 15 chunks of 274 tiles: 164 us, in 64 157.)
+constexpr int64_t PLACES = 512ll << 20;
+
 // Rows per workgroup and the split over the context, by the call's sizes alone.
 static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, int d,
                     int max_context, int window, int sinks, Plan& p) {
@@ -983,14 +1010,19 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
     int64_t ct = 64;
     while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 256) ct /= 2;
     p.chunk_tiles = (int)ct;
-    p.chunks = (int)((tiles + ct - 1) / ct);
+    // a place for the partial results of every chunk that the sizes allow, up to 512 MiB
+    // or 8 chunks per request: those who would have more get longer ones
+    const int64_t places = PLACES / (wide * p.mt * 16 * (d + 2) * (int64_t)sizeof(float));
+    const int64_t chunks = (tiles + ct - 1) / ct, room = places < 8 ? 8 : places;
+    p.chunks = (int)(chunks < room ? chunks : room);
     items = wide * p.chunks;
     // fp32 rows cost a wave three times the products: where workgroups are few, its
     // time is that of the longest wave, and 16 rows each are better (R=24: 32 requests
     // over 1 to 2,000 positions 16.0 us, with 32 rows 22; 64 over 2,000 73 and 60)
     if (p.mt == 1 || dtype != SV_F32 || items >= 512) break;
   }
-  if (items * (p.mt * 16) >= (1ll << 31) - 4096) return false;
+  // (a launch has less than 2^32 threads)
+  if (items >= (1ll << 24) - MAX_BATCH) return false;
   p.part_bytes = p.chunks > 1 ? (size_t)items * (p.mt * 16) * (d + 2) * sizeof(float) : 0;
   p.plan = items > 1024;
   // two waves per workgroup (more items at once, each twice as long) where items are

@@ -6,6 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import kv_util as U  # noqa: E402
 import test_gpu_kv as T  # noqa: E402
 from lossless_rejection_sampling_spec_amd import binding  # noqa: E402
 
@@ -166,3 +167,53 @@ def test_append_gives_the_same_bytes_whatever_the_call(dtype, d):
                            [5 + i, 0] if i < 9 else [0, 11 + i]) for i in range(23)])
     for other, oq in ((apart, q2), (single, q3)):
         assert torch.equal(whole.pages, other.pages) and torch.equal(q, oq)
+
+
+def long_cache(d, page, kv, n, seed):
+    """One sequence of n positions of random codes: (cache, K, V)."""
+    rng, pages = np.random.default_rng(seed), -(-n // page)
+    units = rng.integers(0, 256, (1, pages, kv, page * (d + d // 16)), np.uint8)
+    units[..., page * d:] = rng.integers(122, 128, units[..., page * d:].shape, np.uint8)
+    ids = rng.permutation(pages)
+    K, V = (np.empty((pages * page, kv, d)) for _ in range(2))
+    for i, p in enumerate(ids):
+        for h in range(kv):
+            K[i * page:(i + 1) * page, h], V[i * page:(i + 1) * page, h] = U.read_unit(units[0, p, h], page, d)
+    return T._cache(units, ids.reshape(1, -1), [n], np.ones(pages), page, kv, d), K[:n], V[:n]
+
+
+@pytest.mark.parametrize("dtype,d,heads,kv,batch", [("bf16", 128, 32, 4, 1024), ("bf16", 64, 32, 4, 1024),
+                                                    ("bf16", 256, 16, 2, 1024), ("f32", 64, 16, 2, 1024),
+                                                    ("bf16", 128, 4, 4, 1024), ("f32", 128, 4, 4, 1024)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50000, 40)])
+def test_contexts_of_more_tiles_than_chunks_hold(dtype, d, heads, kv, batch, window, sinks):
+    """A batch so large that a request has few chunks: long ones take chunks of hundreds
+    of tiles, whose page ids are read 64 at a time.  One long request loses a page far
+    inside a chunk; a bound of 2^20 positions changes the chunks again."""
+    cache, K, V = long_cache(d, 64, kv, 70003, d)
+    cache = repeated(cache, batch)
+    rng = np.random.default_rng(heads)
+    rows = [int(x) for x in rng.integers(1, 4, batch)]
+    ctx = [int(x) for x in rng.integers(0, 500, batch)]
+    some = {0: 70000, 1: 16384, 2: 16383, 5: 16352, 77: 33000, 1000: 65535, batch - 1: 2048}
+    for b, c in some.items():
+        ctx[b], rows[b] = c, 2
+    rows[0] = 3
+    cache.page_table[77, 300] = 1 << 25
+    cu = T._cu(rows)
+    q = torch.randn(int(cu[-1]), heads, d, device=DEV).to(T.DTYPES[dtype])
+    want = [0] * batch
+    want[77] = 8
+    for bound in (70003, 1 << 20):
+        out, st = binding.kv_attention(cache, q, T._i(cu), T._i(ctx), max_k=6, max_context=bound,
+                                       window=window, sinks=sinks)
+        assert st.cpu().tolist() == want
+        o = T._f64(out)
+        assert np.isnan(o[cu[77]:cu[78]]).all()
+        for b in sorted(set(some) - {77}) + [3, 500]:
+            n = ctx[b] + rows[b]
+            for h in (0, kv - 1):                      # the last query head of a KV head
+                at = (h + 1) * (heads // kv) - 1
+                T.check_attention(out[cu[b]:cu[b + 1], at:at + 1], q[cu[b]:cu[b + 1], at:at + 1],
+                                  [K[:n, h:h + 1]], [V[:n, h:h + 1]], [0, rows[b]], [ctx[b]], [rows[b]],
+                                  dtype, d ** -0.5, window, sinks)
