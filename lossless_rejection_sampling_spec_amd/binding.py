@@ -411,10 +411,11 @@ class KVCache:
             raise ValueError(f"pages must be a 16-byte aligned uint8 device tensor "
                              f"[layers, num_pages, {n}]")
         t = self.page_table
+        # (rows further apart than they are long would lend the calls the entries between them:
+        # the stride is all they know of a row's length)
         if (t.dtype != torch.int32 or t.device != p.device or t.dim() != 2 or t.shape[0] < 1
-                or t.shape[1] < 1 or t.stride(1) != 1 or t.stride(0) < t.shape[1]):
-            raise ValueError("page_table must be an int32 device tensor [requests, pages], "
-                             "unit stride along a row")
+                or t.shape[1] < 1 or not t.is_contiguous()):
+            raise ValueError("page_table must be a contiguous int32 device tensor [requests, pages]")
         # (past these every call, or fork and compact, would refuse: spec_kv_* take no more)
         if t.shape[0] > 1024 or p.shape[1] > 1 << 24 or p.shape[0] > 65535:
             raise ValueError("a cache holds at most 1024 requests, 2^24 pages and 65535 layers")
@@ -429,7 +430,7 @@ class KVCache:
         object.__setattr__(self, "page_bytes", n)
         object.__setattr__(self, "layer_bytes", p.stride(0) if p.shape[0] > 1 else p.shape[1] * n)
         object.__setattr__(self, "requests", t.shape[0])
-        object.__setattr__(self, "ld_table", t.stride(0))
+        object.__setattr__(self, "ld_table", t.shape[1])
 
     @classmethod
     def create(cls, *, layers: int, num_pages: int, page_size: int, kv_heads: int, head_dim: int,

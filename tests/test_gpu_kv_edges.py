@@ -217,3 +217,27 @@ def test_contexts_of_more_tiles_than_chunks_hold(dtype, d, heads, kv, batch, win
                 T.check_attention(out[cu[b]:cu[b + 1], at:at + 1], q[cu[b]:cu[b + 1], at:at + 1],
                                   [K[:n, h:h + 1]], [V[:n, h:h + 1]], [0, rows[b]], [ctx[b]], [rows[b]],
                                   dtype, d ** -0.5, window, sinks)
+
+
+def test_a_page_table_whose_rows_are_part_of_longer_ones_is_refused():
+    """The calls would use the entries behind a row, which are not the cache's."""
+    wide = torch.full((2, 8), -1, dtype=torch.int32, device=DEV)
+    pages = torch.zeros(1, 12, binding.kv_page_bytes(1, 64, 16), dtype=torch.uint8, device=DEV)
+
+    def make(table):
+        return binding.KVCache(pages=pages, page_table=table, seq_lens=T._i([0] * len(table)),
+                               ref_counts=T._i([0] * 12), page_size=16, kv_heads=1, head_dim=64)
+
+    for table in (wide[:, :4], wide[:, ::2], wide.t()[:2], wide[:1].expand(2, -1)):
+        with pytest.raises(ValueError, match="page_table"):
+            make(table)
+    # a single row has no stride of its own
+    for table in (wide[:1], wide[:1, :4], wide[0].as_strided((1, 4), (0, 1))):
+        cache = make(table)
+        ctx, st = binding.kv_reserve(cache, T._i([0, 16 * table.shape[1] + 1]))
+        assert st.cpu().tolist() == [7]
+        ctx, st = binding.kv_reserve(cache, T._i([0, 16 * table.shape[1]]))
+        assert st.cpu().tolist() == [0]
+        assert table.cpu().tolist() == [list(range(table.shape[1]))]
+        assert wide.cpu()[0, table.shape[1]:].tolist() == [-1] * (8 - table.shape[1])
+        wide.fill_(-1)
