@@ -241,3 +241,30 @@ def test_a_page_table_whose_rows_are_part_of_longer_ones_is_refused():
         assert table.cpu().tolist() == [list(range(table.shape[1]))]
         assert wide.cpu()[0, table.shape[1]:].tolist() == [-1] * (8 - table.shape[1])
         wide.fill_(-1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("batch,heads,n", [(1, 3, 40007), (1, 1, 20000), (130, 2, 50001), (33, 5, 70000)])
+def test_contexts_of_many_chunks_are_joined(dtype, d, batch, heads, n):
+    """79 and 157 chunks of one user and 35 of a request in a small batch (a workgroup per
+    row joins them, 64 at a time), 25 of some requests of a larger one (16 threads per
+    row, 16 at a time)."""
+    cache, K, V = long_cache(d, 16, 1, n, heads)
+    cache = repeated(cache, batch)
+    rng = np.random.default_rng(d)
+    rows = [int(x) for x in rng.integers(1, 4, batch)]
+    ctx = [int(x) for x in rng.integers(0, 3000, batch)]
+    rows[0], ctx[0] = 3, n - 3
+    some = {0}
+    if batch > 1:
+        some |= {7, 20, batch - 1}
+        ctx[7], ctx[20] = 16 * 2048 + 5, 17 * 2048 - rows[20]
+    cu = T._cu(rows)
+    q = torch.randn(int(cu[-1]), heads, d, device=DEV).to(T.DTYPES[dtype])
+    out, st = binding.kv_attention(cache, q, T._i(cu), T._i(ctx), max_k=2, max_context=n)
+    assert st.cpu().tolist() == [0] * batch
+    for b in some:
+        m = ctx[b] + rows[b]
+        T.check_attention(out[cu[b]:cu[b + 1]], q[cu[b]:cu[b + 1]], [K[:m]], [V[:m]], [0, rows[b]], [ctx[b]],
+                          [rows[b]], dtype, d ** -0.5)
