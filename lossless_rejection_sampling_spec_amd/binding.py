@@ -379,6 +379,8 @@ def accounting(cu_seqlens: torch.Tensor, accepted: torch.Tensor, status: torch.T
 
 def kv_page_bytes(kv_heads: int, head_dim: int, page_size: int) -> int:
     """Bytes of one page of one layer (0 on invalid sizes)."""
+    if not (0 < kv_heads <= 1024 and 0 < head_dim <= 256 and 0 < page_size <= 256):
+        return 0                     # (ctypes would take the low 32 bits of a larger number)
     return int(lib().spec_kv_page_bytes(kv_heads, head_dim, page_size))
 
 
@@ -599,6 +601,10 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor,
         o_rows, o_heads, ld_out = _heads_of(out, "out", cache, q.dtype)
         if o_rows != rows or o_heads != heads:
             raise ValueError("out must match q's shape")
+    # (ctypes would take the low 32 bits of a larger number)
+    if not (0 <= max_k <= MAX_K and 1 <= max_context <= 1 << 30 and 0 <= window <= 1 << 30
+            and 0 <= sinks <= 1 << 30):
+        raise ValueError(f"max_k is at most {MAX_K}, max_context, window and sinks at most 2^30")
     status = context_lens.new_empty(batch)
     scale = cache.head_dim ** -0.5 if scale is None else scale
     L = lib()

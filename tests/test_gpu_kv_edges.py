@@ -268,3 +268,13 @@ def test_contexts_of_many_chunks_are_joined(dtype, d, batch, heads, n):
         m = ctx[b] + rows[b]
         T.check_attention(out[cu[b]:cu[b + 1]], q[cu[b]:cu[b + 1]], [K[:m]], [V[:m]], [0, rows[b]], [ctx[b]],
                           [rows[b]], dtype, d ** -0.5)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Their low 32 bits would be sizes that the call takes."""
+    cache, q, cu, ctx, kw = T._small()
+    binding.kv_attention(cache, q, cu, ctx, **kw)
+    for change in (dict(window=(1 << 32) + 16), dict(window=20, sinks=1 << 32), dict(max_k=(1 << 32) + 4),
+                   dict(max_context=(1 << 32) + 705), dict(max_context=(1 << 30) + 1)):
+        with pytest.raises(ValueError):
+            binding.kv_attention(cache, q, cu, ctx, **{**kw, **change})

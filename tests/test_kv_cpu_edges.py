@@ -44,3 +44,11 @@ def test_a_call_of_more_workgroups_than_a_launch_takes_is_refused():
     big = dict(batch=1024, max_k=63, heads=1024, kv=1024, d=256, ldq=1 << 18, ldo=1 << 18, rows=1024)
     assert _workspace(0, 1024, 63, 1024, 1024, 256, 1 << 20) == 0
     assert C._attention(dt=0, maxc=1 << 20, **big) == 2
+
+
+def test_page_bytes_of_sizes_past_32_bits():
+    assert C.binding.kv_page_bytes(2, 128, 16) == 2 * 16 * 136
+    for i in range(3):
+        sizes = [2, 128, 16]
+        sizes[i] += 1 << 32
+        assert C.binding.kv_page_bytes(*sizes) == 0
