@@ -28,7 +28,7 @@ _lib = None
 _lock = threading.Lock()
 _ws_cache: dict = {}
 _kv_ws_cache: dict = {}
-_kv_lock = threading.RLock()
+_kv_locks: dict = {}
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int
@@ -473,23 +473,29 @@ def _kv_workspace(device: torch.device, nbytes: int,
 
 class _on:
     """A call's launches: on the cache's device, and not between those of another
-    thread's call (a call is several launches that hand over in the workspace)."""
-    __slots__ = ("device", "guard")
+    thread's call on the same stream (a call is several launches that hand over in the
+    stream's workspace)."""
+    __slots__ = ("device", "guard", "lock")
 
     def __init__(self, device):
         self.device, self.guard = device, None
 
     def __enter__(self):
-        _kv_lock.acquire()
-        if torch.cuda.current_device() != self.device.index:
+        index = self.device.index
+        stream = torch._C._cuda_getCurrentRawStream(index)
+        self.lock = _kv_locks.get((index, stream))
+        if self.lock is None:
+            self.lock = _kv_locks.setdefault((index, stream), threading.RLock())
+        self.lock.acquire()
+        if torch.cuda.current_device() != index:
             self.guard = torch.cuda.device(self.device)
             self.guard.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return stream
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
-        _kv_lock.release()
+        self.lock.release()
 
 
 def _check_ints(t: torch.Tensor | None, name: str, device, n: int) -> None:

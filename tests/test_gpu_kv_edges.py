@@ -278,3 +278,31 @@ def test_sizes_past_32_bits_are_refused():
                    dict(max_context=(1 << 32) + 705), dict(max_context=(1 << 30) + 1)):
         with pytest.raises(ValueError):
             binding.kv_attention(cache, q, cu, ctx, **{**kw, **change})
+
+
+def test_a_call_does_not_wait_for_a_thread_on_another_stream():
+    """One thread in the middle of a call's launches; another's call on its own stream goes
+    through, one on the same stream waits."""
+    import threading
+    cache, q, cu, ctx, kw = T._small()
+    want, _ = binding.kv_attention(cache, q, cu, ctx, **kw)
+    torch.cuda.synchronize()
+    done = [threading.Event(), threading.Event()]
+    outs = []
+
+    def call(i, stream):
+        with torch.cuda.stream(stream):
+            outs.append(binding.kv_attention(cache, q, cu, ctx, **kw)[0])
+        done[i].set()
+
+    here = torch.cuda.current_stream()
+    threads = [threading.Thread(target=call, args=a) for a in ((0, torch.cuda.Stream()), (1, here))]
+    with binding._on(cache.device):
+        for t in threads:
+            t.start()
+        assert done[0].wait(30) and not done[1].is_set()
+    assert done[1].wait(30)
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(outs) == 2 and all(torch.equal(o, want) for o in outs)
