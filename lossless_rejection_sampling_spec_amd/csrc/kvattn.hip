@@ -160,7 +160,14 @@ struct Attn {
   static constexpr int FR = D / 16;              // output fragments of 16 dims
   static constexpr int KB = (D + 127) / 128;     // scale blocks of a lane's K dims
   // fp32 queries and weights are split into three bf16 terms (3 x 8 bits hold
-  // fp32's 24): products with the exact bf16 K and V then lose nothing
+  // fp32's 24): products with the exact bf16 K and V then lose nothing.  The weights of
+  // bf16 rows are rounded to one term, and the sum they are divided by is that of the
+  // rounded ones, so the roundings are independent errors of at most 2^-8 of each weight
+  // that average out over the tokens like the values do: 0.0023 of the result's norm from
+  // 64 bits, of which the result's own rounding to bf16 is 0.0017.  Two terms leave only
+  // that 0.0017, for 86 us instead of 75 in the verify batch, 72 instead of 59 in the
+  // windowed one and 63 instead of 54 at D=256; the caller who needs more bits than the
+  // result's has fp32 rows.
   static constexpr int NT = sizeof(T) == 4 ? 3 : 1;
 
   f32x4 o[MT][FR];
