@@ -366,7 +366,9 @@ struct Attn {
     if (masked) {
 #pragma unroll
       for (int mt = 0; mt < M; ++mt) {
-        const int pos = w.ctx + row_of(a, (w.rb * MT + mt) * 16 + n);
+        // (lanes past the last row repeat it, in what they see too: they take part in
+        // raising the tile's maxima)
+        const int pos = w.ctx + row_of(a, min((w.rb * MT + mt) * 16 + n, w.R - 1));
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (!sees(base + token(g, i), pos)) s[i >> 2][mt][i & 3] = -INFINITY;

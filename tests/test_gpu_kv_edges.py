@@ -306,3 +306,45 @@ def test_a_call_does_not_wait_for_a_thread_on_another_stream():
         t.join()
     torch.cuda.synchronize()
     assert len(outs) == 2 and all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("batch,heads,window", [(1, 3, 0), (24, 3, 0), (24, 3, 37), (300, 10, 0)])
+def test_what_lies_behind_the_last_position_changes_no_bit(dtype, d, batch, heads, window):
+    """Stale bytes behind a request's last position, and pages it does not hold, as scales
+    of NaN, as large values and as small ones: the same bits.  (Rows that fill up a tile of
+    16 must not see them either: they share the moments at which maxima are raised.)"""
+    rng = np.random.default_rng(d + batch)
+    rows = [int(x) for x in rng.integers(1, 6, batch)]
+    ctx = [int(x) for x in rng.integers(0, 400, batch)]
+    page, n = 16, [c + r for c, r in zip(ctx, rows)]
+    cache, K, V = T.make_attention(d, page, 1, [rows[0]] * 3, [700] * 3, batch)
+    table = cache.page_table[0]
+    pages = cache.pages.cpu().numpy().reshape(1, -1, 1, page * (d + d // 16))
+    ids = table.cpu().numpy()
+    cu = T._cu(rows)
+    q = torch.randn(int(cu[-1]), heads, d, device=DEV).to(T.DTYPES[dtype]) * 2
+    ks, vs = U.places(page, d)[2:]
+    outs = []
+    for fill in (255, 252, 140, 1):
+        out = []
+        for b in range(min(batch, 24)):            # a call of each request's own stale bytes
+            host = np.full_like(pages, fill)
+            held = -(-n[b] // page)
+            host[0, ids[:held]] = pages[0, ids[:held]]
+            for at in (ks, vs):
+                host[0, ids[held - 1]][:, at[n[b] - (held - 1) * page:]] = fill
+            c2 = T._cache(host, ids.reshape(1, -1), [n[b]], np.zeros(host.shape[1]), page, 1, d)
+            c2 = repeated(c2, batch)
+            only = [0] * (b + 1) + [rows[b]] * (batch - b)
+            o, st = binding.kv_attention(c2, q[cu[b]:cu[b + 1]], T._i(only),
+                                         T._i([ctx[b] if i == b else 0 for i in range(batch)]), max_k=4,
+                                         max_context=500, window=window)
+            assert int(st[b]) == 0
+            out.append(o)
+        outs.append(torch.cat(out))
+    for o in outs[1:]:
+        assert torch.equal(o.view(torch.uint8), outs[0].view(torch.uint8))
+    T.check_attention(outs[0], q, [K[0][:x] for x in n[:24]], [V[0][:x] for x in n[:24]], cu[:25], ctx[:24],
+                      rows[:24], dtype, d ** -0.5, window)
