@@ -40,7 +40,8 @@ constexpr float RAISE = 8.0f;
 // Weights are 2^(s c - mc), c = scale log2 e, with one rounding of the exponent; mc is
 // the maximum m times c, rounded.  Everything is counted from mc (raises and joins
 // too), so what mc is off by cancels in the division, but the largest weight is
-// 2^(m c - mc): half a step of mc, below 2^64 up to here.  Larger maxima make their row NaN.
+// 2^(m c - mc): half a step of mc, below 2^64 up to here.  mc is held within +-FAR: past
+// it weights become infinite, or all 0, and their row NaN.
 // (Weights 2^((s - m) c) would have no such end, at an instruction more per score: the
 // windowed batch of 256 requests 61.3 us, with this 59.5, the verify batch 77.5 and 76.4.)
 constexpr float FAR = 1073741824.0f;          // 2^30
@@ -172,8 +173,8 @@ struct Attn {
 
   f32x4 o[MT][FR];
   f32x4 l[MT];            // sums of the weights: a row of ones among the products (4 equal)
-  // running max m of the raw scores: m, mc = m scale log2 e, rounded (0 before the first
-  // visible score), and what a score has to pass to raise it
+  // running max m of the raw scores: m, mc = m scale log2 e, rounded (-FAR before the
+  // first visible score), and what a score has to pass to raise it
   float m[MT], mc[MT], over[MT];
   // rows that saw a block stored as NaN.  V: bit 4 mt + r, dims g*D/4 + r*D/16 ...;
   // K: bit 16 + mt, all dims
@@ -236,7 +237,7 @@ struct Attn {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       m[mt] = over[mt] = -INFINITY;
-      mc[mt] = 0.f;
+      mc[mt] = -FAR;
       l[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int f = 0; f < FR; ++f) o[mt][f] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -384,9 +385,8 @@ struct Attn {
       // (a first visible score raises -inf; a row that has seen nothing stays there)
       if (__any(mx > over[mt])) {
         const float nm = fmaxf(m[mt], row_max(mx));
-        const float at = nm * w.c;
-        const float nc = nm == -INFINITY ? 0.f : __builtin_fabsf(at) < FAR ? at : __builtin_nanf("");
-        const float f = m[mt] == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mc[mt] - nc);
+        const float nc = __builtin_amdgcn_fmed3f(nm * w.c, -FAR, FAR);
+        const float f = __builtin_amdgcn_exp2f(mc[mt] - nc);
         l[mt] *= f;
 #pragma unroll
         for (int k = 0; k < FR; ++k) o[mt][k] *= f;
@@ -789,7 +789,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
     if (g == 0) {
-      part_m[wave][mt][n] = x.m[mt] == -INFINITY ? -INFINITY : x.mc[mt];
+      part_m[wave][mt][n] = x.mc[mt];
       // a page id out of range: the request's rows are NaN
       part_l[wave][mt][n] = bad ? __builtin_nanf("") : x.l[mt][0];
     }
