@@ -536,7 +536,7 @@ struct Attn {
     load(t, 1, w.pool + (uint64_t)i1 * w.page_bytes, a.unit, at, (tb + 16) & (a.page - 1));
   }
 
-  template <int M, int WAVES, int DEPTH>
+  template <int M, int WAVES, bool LONG, int DEPTH>
   __device__ __forceinline__ void run(const AttnArgs& a, const Share& w, Tile<D> (&t)[DEPTH],
                                       Pages& id, const int32_t* tab, bool& bad, const Lane& at, int wave,
                                       const bf16x8* q) {
@@ -552,7 +552,8 @@ struct Attn {
           step<M>(a, t[k], masked, base, w, q);
         }
         const int ahead = min(i + (k + DEPTH) * WAVES, last);
-        if (ahead - id.first >= 64) bad |= id.ask(a, w, tab, ahead);   // (chunks of more than 64 tiles)
+        if constexpr (LONG)                   // (chunks of more than 64 tiles)
+          if (ahead - id.first >= 64) bad |= id.ask(a, w, tab, ahead);
         fetch(a, w, t[k], id, at, ahead);
       }
     }
@@ -682,7 +683,9 @@ __global__ __launch_bounds__(1024) void k_attn_plan(AttnArgs a) {
   }
 }
 
-template <int D, int MT, int DEPTH, int WAVES, typename T>
+// LONG: with chunks of more than 64 tiles.  (An instance of its own: the check at every
+// tile takes 1 % of the verify batch, 2 % of the windowed one.)
+template <int D, int MT, int DEPTH, int WAVES, bool LONG, typename T>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
   using A = Attn<D, MT, T>;
   constexpr int FR = A::FR;
@@ -738,7 +741,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
   }
   Share w;
   w.sp = span_of(ctx, rows, a.window, a.sinks);
-  const int ct = chunk_of(a, w.sp.tiles);
+  const int ct = LONG ? chunk_of(a, w.sp.tiles) : a.chunk_tiles;
   w.tend = (w.sp.tiles - 1) % ct + 1 + chunk * ct;
   w.tbegin = max(0, w.tend - ct);
   if (st == SV_ROW_OK ? w.tend > w.sp.tiles : chunk > 0) return;
@@ -775,11 +778,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn(AttnArgs a) {
     // row tiles that hold rows: a short request does not pay for a long one's
     const int tiles = (min(R - rb * MT * 16, MT * 16) + 15) / 16;
     // (not where the copies of the loop would not fit the registers)
-    if (MT * FR >= 32) x.template run<MT, WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
-    else if (MT == 1 || tiles == 1) x.template run<1, WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
-    else if (MT == 2 || tiles == 2) x.template run<(MT < 2 ? 1 : 2), WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
-    else if (tiles == 3) x.template run<(MT < 3 ? 1 : 3), WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
-    else x.template run<MT, WAVES>(a, w, t, id, tab, bad, at, wave, q_lds);
+    if (MT * FR >= 32) x.template run<MT, WAVES, LONG>(a, w, t, id, tab, bad, at, wave, q_lds);
+    else if (MT == 1 || tiles == 1) x.template run<1, WAVES, LONG>(a, w, t, id, tab, bad, at, wave, q_lds);
+    else if (MT == 2 || tiles == 2)
+      x.template run<(MT < 2 ? 1 : 2), WAVES, LONG>(a, w, t, id, tab, bad, at, wave, q_lds);
+    else if (tiles == 3)
+      x.template run<(MT < 3 ? 1 : 3), WAVES, LONG>(a, w, t, id, tab, bad, at, wave, q_lds);
+    else x.template run<MT, WAVES, LONG>(a, w, t, id, tab, bad, at, wave, q_lds);
   }
   if (__any(x.poison != 0)) x.apply_poison();
 
@@ -976,8 +981,18 @@ __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
 struct Plan {
   int mt, row_blocks, chunks, chunk_tiles, waves;
   size_t part_bytes, bytes;
-  bool plan;
+  bool plan, longer;    // longer: a request can have more tiles than full chunks hold
 };
+
+// Of planned calls: two waves per workgroup (more items at once, each twice as long)
+// where items are many, and whole or rich in products: 512 requests over 1 to 2,000
+// positions 64 us, with four 81; 256 over 1 to 4,000 (R=28) 67.5 and 76.5; 128 over 1 to
+// 8,000 with R=56 81.5 and 92; but 64 over 8,000 with R=4 128 and 122, 64 over 1 to 8,000
+// at D=256 (one tile on its way per wave) 80 and 61.  fp32 waves take longer for an item
+// and need more of them: 512 over 1 to 2,000 79.5 and 97, 256 with R=48 69 and 58.
+static constexpr bool two_waves(int dtype, int mt, int d, bool whole, int64_t items) {
+  return dtype == SV_F32 ? whole && items >= 4096 : whole || (mt > 1 && d < 256);
+}
 
 // What the partial results of a call may take: its bound on contexts is often far above
 // what the requests hold, and every place is a workgroup to start.  (256 requests over 200
@@ -1024,6 +1039,7 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
     const int64_t places = PLACES / (wide * p.mt * 16 * (d + 2) * (int64_t)sizeof(float));
     const int64_t chunks = (tiles + ct - 1) / ct, room = places < 8 ? 8 : places;
     p.chunks = (int)(chunks < room ? chunks : room);
+    p.longer = chunks > room;
     items = wide * p.chunks;
     // fp32 rows cost a wave three times the products: where workgroups are few, its
     // time is that of the longest wave, and 16 rows each are better (R=24: 32 requests
@@ -1034,15 +1050,7 @@ static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, in
   if (items >= (1ll << 24) - MAX_BATCH) return false;
   p.part_bytes = p.chunks > 1 ? (size_t)items * (p.mt * 16) * (d + 2) * sizeof(float) : 0;
   p.plan = items > 1024;
-  // two waves per workgroup (more items at once, each twice as long) where items are
-  // many, and whole or rich in products: 512 requests over 1 to 2,000 positions 64 us,
-  // with four 81; 256 over 1 to 4,000 (R=28) 67.5 and 76.5; 128 over 1 to 8,000 with
-  // R=56 81.5 and 92; but 64 over 8,000 with R=4 128 and 122, 64 over 1 to 8,000 at
-  // D=256 (one tile on its way per wave) 80 and 61.  fp32 waves take longer for an item
-  // and need more of them: 512 over 1 to 2,000 79.5 and 97, 256 with R=48 69 and 58
-  const bool two = dtype == SV_F32 ? p.chunks == 1 && items >= 4096
-                                   : p.chunks == 1 || (p.mt > 1 && d < 256);
-  p.waves = p.plan && two ? 2 : 4;
+  p.waves = p.plan && two_waves(dtype, p.mt, d, p.chunks == 1, items) ? 2 : 4;
   // eight for fp32, whose waves are the slowest, where workgroups are few (32 requests
   // over 1 to 2,000 positions 16.1 us, with four 18.0; 8 over 2,000 19.5 both ways).
   // bf16 only loses by the longer join (4 over 500: 13.4 us against 12.0), and at
@@ -1068,13 +1076,16 @@ static int launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
     if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   }
   const int grid = items + (a.batch + p.waves - 1) / p.waves;
-  if (p.waves == 2) {
-    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 2, T>), dim3(grid), dim3(128), 0, s, a);
+  if (p.longer) {                             // (planned, with several chunks: see plan_of)
+    constexpr int WAVES = two_waves(sizeof(T) == 4 ? SV_F32 : SV_BF16, MT, D, false, 0) ? 2 : 4;
+    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, WAVES, true, T>), dim3(grid), dim3(64 * WAVES), 0, s, a);
+  } else if (p.waves == 2) {
+    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 2, false, T>), dim3(grid), dim3(128), 0, s, a);
   } else if (p.waves == 4) {
-    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 4, T>), dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 4, false, T>), dim3(grid), dim3(256), 0, s, a);
   } else {
     if constexpr (sizeof(T) == 4 && D < 256 && MT == 1)
-      hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 8, T>), dim3(grid), dim3(512), 0, s, a);
+      hipLaunchKernelGGL((k_attn<D, MT, DEPTH, 8, false, T>), dim3(grid), dim3(512), 0, s, a);
   }
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   if (p.chunks > 1) {

@@ -28,7 +28,7 @@ def spills(remarks: str) -> dict:
     return {k: tuple(v) for k, v in found.items()}
 
 
-@pytest.mark.parametrize("source,kernels", [("kvattn.hip", {"k_attn": 28, "k_attn_join": 13,
+@pytest.mark.parametrize("source,kernels", [("kvattn.hip", {"k_attn": 41, "k_attn_join": 13,
                                                             "k_attn_join_rows": 13,
                                                             "k_attn_plan": 1}),
                                             ("kvcache.hip", {"k_append": 6})])
