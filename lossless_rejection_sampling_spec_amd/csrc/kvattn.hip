@@ -22,10 +22,10 @@
 // softmax, and HBM reads (D*17/16 bytes per token and KV head), which do not overlap
 // fully at two waves per SIMD.  64 requests over 512 to 16,384 positions (k=6, 32
 // heads over 8 KV heads of D=128, 301 MB): 80 us, of these plan 5, this kernel 69
-// (4.4 TB/s, vector units busy 54 % and matrix units 28 % of the time), join 7.  One
-// user over 32,000 positions, k=0: 18.5 us, of these join 4.4; 64 requests over 4,000
-// with 64 heads (R=56, two row blocks that both read and widen the cache): 130 us,
-// 450 TFLOP/s.
+// (4.4 TB/s, vector units busy 52 % and matrix units 27 % of the time), join 7.  One
+// user over 32,000 positions, k=0: 18 us, of these join 4.2; 64 requests over 4,000
+// with 64 heads (R=56, two row blocks that both read and widen the cache): 124 us,
+// 470 TFLOP/s.
 
 #include "kv_common.h"
 
