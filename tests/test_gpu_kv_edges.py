@@ -348,3 +348,45 @@ def test_what_lies_behind_the_last_position_changes_no_bit(dtype, d, batch, head
         assert torch.equal(o.view(torch.uint8), outs[0].view(torch.uint8))
     T.check_attention(outs[0], q, [K[0][:x] for x in n[:24]], [V[0][:x] for x in n[:24]], cu[:25], ctx[:24],
                       rows[:24], dtype, d ** -0.5, window)
+
+
+@pytest.mark.parametrize("num,pairs", [(64, 3), (70000, 3), (600, 150)])
+def test_forks_and_compactions_captured_in_a_graph(num, pairs):
+    """Fork, reserve, release and compact as one graph, replayed against eager calls on an
+    equal cache, with eager work in between."""
+    seqs = pairs + 2
+
+    def make():
+        cache = binding.KVCache.create(layers=2 if num < 1000 else 1, num_pages=num, page_size=16,
+                                       kv_heads=1, head_dim=64, requests=seqs, max_context=128, device=DEV)
+        cache.pages.copy_(torch.arange(cache.pages.numel(), device=DEV).view_as(cache.pages) % 251)
+        binding.kv_reserve(cache, T._i(T._cu([40, 21] + [0] * pairs)))
+        return cache
+
+    a, b = make(), make()
+    src, dst = T._i([i % 2 for i in range(pairs)]), T._i(range(2, seqs))
+    cu = T._i(T._cu([1, 0] + [3] * pairs))
+    give = T._i([1, 0] + [43 if i % 2 == 0 else 24 for i in range(pairs)])
+    lens = T._i([40 if i % 2 == 0 else 21 for i in range(pairs)])
+
+    def step(c):
+        f = binding.kv_fork(c, src, dst, lens)
+        ctx, r = binding.kv_reserve(c, cu)
+        return f, ctx, r, binding.kv_release(c, give), binding.kv_compact(c)
+
+    state = [t.clone() for t in (a.pages, a.page_table, a.seq_lens, a.ref_counts)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(a)
+    for t, k in zip((a.pages, a.page_table, a.seq_lens, a.ref_counts), state):
+        assert torch.equal(t, k)
+    for i in range(5):
+        g.replay()
+        want = step(b)
+        torch.cuda.synchronize()
+        assert [int(x) for x in got[0]] == [0] * pairs and int(got[4]) == int(want[4])
+        for u, v in zip(got, want):
+            assert torch.equal(u, v), i
+        for n in ("pages", "page_table", "seq_lens", "ref_counts"):
+            assert torch.equal(getattr(a, n), getattr(b, n)), (i, n)
+        binding.kv_compact(b)                      # (nothing left to move)
