@@ -21,6 +21,12 @@ def _gpu():
     yield
 
 
+@pytest.fixture(autouse=True)
+def _seed():
+    """Each test's values are its own, whichever tests run before it."""
+    torch.manual_seed(11)
+
+
 def repeated(cache, times):
     """The cache's first request `times` times over the same pages."""
     table = cache.page_table[:1].expand(times, -1).contiguous()
