@@ -544,7 +544,8 @@ def kv_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     cos_sin float32 [positions, rot_dim], cos first, or None; `out` may be q.
 
     Returns (q_out, status[B]), and with want_values (q_out, status, k_values,
-    v_values): the values the cache now stands for."""
+    v_values): the values the cache now stands for.  Rows that are not processed (of no
+    request, or without a position) stay as `out` holds them, undefined without `out`."""
     batch = _kv_batch(cache, cu_seqlens)
     code = _dtype_code(q)
     rows, heads, ld_q = _heads_of(q, "q", cache, q.dtype)
@@ -593,7 +594,11 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor,
                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """spec_kv_attention: attention of the k+1 verify rows of each request over
     the cache (k = 0: decode).  scale defaults to head_dim ** -0.5.  Returns
-    (out [rows, heads, D], status[B])."""
+    (out [rows, heads, D], status[B]).
+
+    Rows of no request, and of requests with more than max_k + 1 rows, stay as `out` holds
+    them (undefined without `out`).  Without `workspace` the scratch of the largest call
+    so far stays with the stream; spec_kv_attention_workspace_bytes says how large."""
     batch = _kv_batch(cache, cu_seqlens)
     code = _dtype_code(q)
     rows, heads, ld_q = _heads_of(q, "q", cache, q.dtype)
