@@ -425,7 +425,7 @@ size_t spec_kv_attention_workspace_bytes(int dtype, int batch, int max_k, int he
  * enter as three bf16 terms: exact from 2^-110 up), the result rounded once.
  * What a row does not see never reaches it, NaN included.  A row whose largest
  * |scale q.k log2 e| reaches 2^30 may be NaN.  q.k, and sums of weights (up to 2^9 each
- * before the division, 2^72 where those scores pass 2^24) times V, have to stay in
+ * before the division, 2^41 where those scores pass 2^24) times V, have to stay in
  * fp32's range: past it a row is NaN or infinite.
  *   q, out         [total_rows][heads][head_dim] of dtype, rows ld_q / ld_out apart;
  *                  out may be q itself with the same ld
