@@ -448,6 +448,42 @@ int spec_kv_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_
                       float scale, int window, int sinks, void* out, int64_t ld_out,
                       int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of workspace spec_kv_prompt_attention needs with these sizes (0 on invalid sizes,
+ * and on those that would be 2^24 workgroups or more).  Most of it is the requests' cache
+ * in bf16: 4 head_dim bytes per KV head and position, total_context positions (with a
+ * window: those that rows see, at most). */
+size_t spec_kv_prompt_workspace_bytes(int dtype, int batch, int total_rows, int heads,
+                                      int kv_heads, int head_dim, int max_context,
+                                      int64_t total_context, int window, int sinks);
+
+/*
+ * Attention of whole prompts over the cache: spec_kv_attention for any number of rows per
+ * request.  Row j of request b, at position p = context_lens[b] + j, sees the positions
+ * t <= p, and with window > 0 only t > p - window or t < sinks; its own and the earlier
+ * rows' K and V are in the cache (spec_kv_append), and so is what lies before them
+ * (context_lens[b] > 0: a prompt in parts, or after a prefix that spec_kv_fork shares).
+ * Formula, precision and what never reaches a row: as spec_kv_attention.
+ *   q, out         [total_rows][heads][head_dim] of dtype, rows ld_q / ld_out apart,
+ *                  not the same memory (SV_ERR_SHAPE if out == q); total_rows * heads < 2^31
+ *   max_context    bound of context_lens[b] + rows; requests past it are
+ *                  SV_ROW_BAD_PARAM, like context_lens[b] < 0
+ *   total_context  bound of the sum of context_lens[b] + rows over the requests, at most
+ *                  2^30; requests with which the sum passes it are SV_ROW_BAD_PARAM
+ *   scale, window, sinks, status: as spec_kv_attention
+ *   workspace      spec_kv_prompt_workspace_bytes(), any contents; calls that may run at
+ *                  once (two captured graphs among them) need their own
+ * Rows of BAD_PARAM and BAD_PAGE requests are NaN; rows of BAD_K requests (none here for
+ * too many rows) and of no request are left as they were.  Identical inputs give identical
+ * bits, and a request's rows depend on the call's sizes but not on the other requests.
+ */
+int spec_kv_prompt_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_seqlens,
+                             const int32_t* context_lens, int batch, int total_rows, int heads,
+                             int kv_heads, int head_dim, const void* pages, int64_t num_pages,
+                             int page_size, const int32_t* page_table, int64_t ld_table,
+                             int max_context, int64_t total_context, float scale, int window,
+                             int sinks, void* out, int64_t ld_out, int32_t* status,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Bytes of workspace spec_kv_reserve and spec_kv_compact need (0 on invalid sizes). */
 size_t spec_kv_pages_workspace_bytes(int seqs, int64_t num_pages);
 

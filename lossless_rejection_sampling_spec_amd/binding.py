@@ -89,6 +89,12 @@ def load_library(path: str) -> ctypes.CDLL:
     L.spec_kv_attention.argtypes = [
         _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i64,
         _i32, ctypes.c_float, _i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp]
+    L.spec_kv_prompt_workspace_bytes.restype = _sz
+    L.spec_kv_prompt_workspace_bytes.argtypes = [_i32] * 7 + [_i64, _i32, _i32]
+    L.spec_kv_prompt_attention.restype = _i32
+    L.spec_kv_prompt_attention.argtypes = [
+        _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i64, _i32,
+        _i64, ctypes.c_float, _i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp]
     L.spec_kv_pages_workspace_bytes.restype = _sz
     L.spec_kv_pages_workspace_bytes.argtypes = [_i32, _i64]
     L.spec_kv_reserve.restype = _i32
@@ -632,6 +638,56 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor,
             cache.page_table.data_ptr(), cache.ld_table, max_context, scale, window, sinks,
             out.data_ptr(), ld_out, status.data_ptr(), ws.data_ptr(),
             ws.numel() * ws.element_size(), stream))
+    return out, status
+
+
+def kv_prompt_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor,
+                        context_lens: torch.Tensor, *, max_context: int, total_context: int,
+                        layer: int = 0, scale: float | None = None, window: int = 0,
+                        sinks: int = 0, out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None):
+    """spec_kv_prompt_attention: attention of whole prompts over the cache, any number of
+    rows per request (append them first).  max_context bounds a request's context plus
+    rows, total_context their sum over the requests.  scale defaults to head_dim ** -0.5.
+    Returns (out [rows, heads, D], status[B]).
+
+    Rows of no request stay as `out` holds them (undefined without `out`).  Without
+    `workspace` the scratch of the largest call so far stays with the stream: the requests'
+    cache in bf16 for the most part (spec_kv_prompt_workspace_bytes)."""
+    batch = _kv_batch(cache, cu_seqlens)
+    code = _dtype_code(q)
+    rows, heads, ld_q = _heads_of(q, "q", cache, q.dtype)
+    _check_ints(context_lens, "context_lens", cache.device, batch)
+    if not 0 <= layer < cache.layers:
+        raise ValueError(f"layer {layer} of {cache.layers}")
+    if out is None:
+        out = _out_like(q)
+        ld_out = heads * cache.head_dim
+    else:
+        o_rows, o_heads, ld_out = _heads_of(out, "out", cache, q.dtype)
+        if o_rows != rows or o_heads != heads:
+            raise ValueError("out must match q's shape")
+        if out.data_ptr() == q.data_ptr():
+            raise ValueError("out must not be q's memory")
+    # (ctypes would take the low bits of a larger number)
+    if not (1 <= max_context <= 1 << 30 and 1 <= total_context <= 1 << 30 and rows < 1 << 31
+            and 0 <= window <= 1 << 30 and 0 <= sinks <= 1 << 30):
+        raise ValueError("max_context, total_context, window and sinks are at most 2^30")
+    status = context_lens.new_empty(batch)
+    scale = cache.head_dim ** -0.5 if scale is None else scale
+    L = lib()
+    need = L.spec_kv_prompt_workspace_bytes(code, batch, rows, heads, cache.kv_heads, cache.head_dim,
+                                            max_context, total_context, window, sinks)
+    if need == 0:
+        raise ValueError("invalid sizes for spec_kv_prompt_attention")
+    with _on(cache.device) as stream:
+        ws = _kv_workspace(cache.device, need, workspace)
+        _raise(L.spec_kv_prompt_attention(
+            q.data_ptr(), ld_q, code, cu_seqlens.data_ptr(), context_lens.data_ptr(), batch, rows,
+            heads, cache.kv_heads, cache.head_dim, cache.pages.data_ptr() + layer * cache.layer_bytes,
+            cache.num_pages, cache.page_size, cache.page_table.data_ptr(), cache.ld_table,
+            max_context, total_context, scale, window, sinks, out.data_ptr(), ld_out,
+            status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), stream))
     return out, status
 
 

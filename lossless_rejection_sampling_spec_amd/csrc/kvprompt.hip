@@ -1,0 +1,810 @@
+// kvprompt.hip -- spec_kv_prompt_attention: attention of whole prompts, any number
+// of rows per request, over the 4-bit paged cache (include/specverify.h states the
+// operator).
+//
+// For request b, row j (position c+j) and query head h over KV head h/G:
+//   out = sum_t exp(scale q.k_t - m) v_t / sum_t exp(scale q.k_t - m)
+// over the visible t, in one pass with a running maximum m and sum.
+//
+// Three launches: k_prompt_plan lists the work, k_prompt_widen turns the cache of the
+// call's requests into bf16 once, and k_prompt takes it from there (a fourth joins the
+// parts of rows whose context was split).
+//
+// Widening once, not per workgroup: a tile of 32 tokens is used by every block of rows
+// behind it, rows * G / 256 times.  The widened tile is laid out as the matrix
+// instructions' operands, [instruction][lane][8 values], so that its way through LDS is
+// straight copies and reads without bank conflicts.
+//
+// k_prompt: a workgroup of 4 waves takes one KV head and 128 MT of the request's rows * G
+// query rows (the G heads of a row side by side), a wave 32 MT of them.  Per tile it
+// computes S^T[token][row] = K Q^T, then O^T[dim][row] += V^T P^T with
+// v_mfma_f32_32x32x16_bf16.  With tokens as the rows of S^T a lane holds scores of ONE
+// query row, for 16 of the tile's tokens: statistics are per lane, and the weights are
+// the next product's operand as they are (V is laid out in the order of tokens in which
+// the accumulators hold them).
+
+#include "kv_common.h"
+
+namespace svk {
+namespace prompt {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int TILE = 32;                     // tokens
+constexpr float LOG2E = 1.44269504088896340736f;
+// the running maximum is raised when a score passes it by this much in powers of two
+// (weights stay below 2^8), and counted from its rounded product with the scale, held
+// within +-FAR; past it weights become infinite, or all 0, and their row NaN
+constexpr float RAISE = 8.0f;
+constexpr float FAR = 1073741824.0f;         // 2^30
+
+constexpr int tile_bytes(int d) { return TILE * d * 2 * 2; }    // K, then V, in bf16
+
+struct Block {                               // rows [rb * block_rows, ...) of request b's rows * G
+  int b, rb;
+};
+struct Item {                                // a block's share of the context
+  int block, chunk;
+};
+// What the plan writes; offsets in the workspace follow from the call's sizes.
+struct Head {
+  int items, blocks, tiles, odd;             // odd: some V block stored as NaN
+};
+
+struct Args {
+  const void* q;
+  int64_t ld_q;
+  const int32_t* cu;
+  const int32_t* ctx;
+  int batch, total_rows, heads, kv_heads, group;
+  const uint8_t* pages;
+  int64_t num_pages;
+  int page, page_log2, unit;
+  const int32_t* table;
+  int64_t ld_table;
+  int max_context;
+  int64_t total_context;
+  float scale;
+  int window, sinks;
+  void* out;
+  int64_t ld_out;
+  int32_t* status;
+  int block_rows, max_blocks, chunks, chunk_tiles;
+  int64_t max_tiles;
+  // workspace
+  Head* head;
+  int32_t* tile_off;                         // [batch + 1] first widened tile of a request
+  Block* blocks;
+  Item* items;
+  uint8_t* wide;                             // [kv_heads][max_tiles][tile_bytes]
+  uint8_t* odd;                              // [kv_heads][max_tiles][32]: a token's V blocks stored as NaN
+  float* part;
+};
+
+// Tiles that a request's rows see together: the first `early` of the sequence, then those
+// from `tile0` on.
+struct Span {
+  int n, first, early, tile0, tiles;
+};
+__device__ __forceinline__ Span span_of(int ctx, int rows, int window, int sinks) {
+  Span s;
+  s.n = ctx + rows;
+  s.first = window > 0 ? max(0, ctx - window + 1) : 0;
+  s.tile0 = s.first / TILE;
+  s.early = window > 0 ? min((sinks + TILE - 1) / TILE, s.tile0) : 0;
+  s.tiles = s.early + (s.n - 1) / TILE - s.tile0 + 1;
+  return s;
+}
+// The same of the rows first_row .. last_row alone.
+__device__ __forceinline__ Span block_span(int ctx, int first_row, int last_row, int window, int sinks) {
+  return span_of(ctx + first_row, last_row - first_row + 1, window, sinks);
+}
+
+// One workgroup of 1,024: a request per thread, then a block and chunk per thread.
+__global__ __launch_bounds__(1024) void k_prompt_plan(Args a) {
+  constexpr int LEVELS = 64;
+  __shared__ int red[16], sblock[MAX_BATCH + 1], sctx[MAX_BATCH], srows[MAX_BATCH];
+  __shared__ long long wide_sum[16];
+  __shared__ int level[LEVELS];
+  const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
+  int c0 = 0, c1 = 0, ctx = 0, broken = a.batch;
+  if (b < a.batch) {
+    c0 = a.cu[b];
+    c1 = a.cu[b + 1];
+    ctx = a.ctx[b];
+    if (c0 < 0 || c1 < c0 || c1 > a.total_rows) broken = b;
+  }
+  if (b < LEVELS) level[b] = 0;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) broken = min(broken, __shfl_xor(broken, d));
+  if (lane == 0) red[wave] = broken;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 16; ++w) broken = min(broken, red[w]);
+  const int rows = c1 - c0;
+  int st = b < broken && rows >= 1 ? SV_ROW_OK : SV_ROW_BAD_K;
+  if (st == SV_ROW_OK && (ctx < 0 || (int64_t)ctx + rows > a.max_context)) st = SV_ROW_BAD_PARAM;
+  // what the requests hold so far, against the call's bound
+  long long held = st == SV_ROW_OK ? (long long)ctx + rows : 0;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const long long y = __shfl_up(held, d);
+    if (lane >= d) held += y;
+  }
+  if (lane == 63) wide_sum[wave] = held;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) held += wide_sum[w];
+  if (st == SV_ROW_OK && held > a.total_context) st = SV_ROW_BAD_PARAM;
+
+  const int R = st == SV_ROW_BAD_K ? 0 : rows * a.group;
+  const int nb = (int)(((int64_t)R + a.block_rows - 1) / a.block_rows);
+  const int nt = st == SV_ROW_OK ? span_of(ctx, rows, a.window, a.sinks).tiles : 0;
+  int sb = nb, stl = nt;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(sb, d), z = __shfl_up(stl, d);
+    if (lane >= d) {
+      sb += y;
+      stl += z;
+    }
+  }
+  __syncthreads();
+  if (lane == 63) {
+    red[wave] = sb;
+    wide_sum[wave] = stl;
+  }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    sb += red[w];
+    stl += (int)wide_sum[w];
+  }
+  sblock[b] = sb - nb;
+  sctx[b] = st == SV_ROW_OK ? ctx : -1;
+  srows[b] = rows;
+  if (b < a.batch) {
+    a.status[b] = st;
+    a.tile_off[b] = stl - nt;
+  }
+  if (b == 1023) {
+    sblock[MAX_BATCH] = sb;
+    a.tile_off[a.batch] = stl;
+    a.head->blocks = sb;
+    a.head->tiles = stl;
+    a.head->odd = 0;
+  }
+  __syncthreads();
+  // items by falling work, so that the shortest end the call: count per level, then place
+  const int blocks = sblock[MAX_BATCH], all = blocks * a.chunks;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int i = b; i < all; i += 1024) {
+      const int blk = i / a.chunks, c = i - blk * a.chunks;
+      int lo = 0, hi = a.batch;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sblock[mid] <= blk) lo = mid;
+        else hi = mid;
+      }
+      const int rb = blk - sblock[lo];
+      if (pass == 0 && c == 0) a.blocks[blk] = Block{lo, rb};
+      int work = c == 0 ? 1 : 0;
+      if (sctx[lo] >= 0) {
+        const int64_t r0 = (int64_t)rb * a.block_rows, R0 = (int64_t)srows[lo] * a.group;
+        const int j0 = (int)(r0 / a.group);
+        const int j1 = (int)((min(r0 + a.block_rows, R0) - 1) / a.group);
+        const int tiles = block_span(sctx[lo], j0, j1, a.window, a.sinks).tiles;
+        work = max(work, min(tiles - c * a.chunk_tiles, a.chunk_tiles));
+      }
+      if (work <= 0) continue;
+      const int lv = LEVELS - 1 - (int)((int64_t)work * (LEVELS - 1) / a.chunk_tiles);
+      if (pass == 0) atomicAdd(&level[lv], 1);
+      // (places within a level come as they come: which workgroup computes an item changes
+      // nothing in its result)
+      else a.items[atomicAdd(&level[lv], 1)] = Item{blk, c};
+    }
+    __syncthreads();
+    if (pass == 0) {
+      if (wave == 0) {
+        const int x = level[lane];
+        int sum = x;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const int y = __shfl_up(sum, d);
+          if (lane >= d) sum += y;
+        }
+        level[lane] = sum - x;
+        if (lane == 63) a.head->items = sum;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <int BYTE>
+__device__ __forceinline__ uint32_t widen(uint32_t word, float scale) {
+  return __builtin_bit_cast(uint32_t,
+                            __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, BYTE));
+}
+
+// A tile of one KV head in bf16:
+//   K [D/16][64][8]     step s, lane (n, g): token n, dims 16 s + 8 g ..
+//   V [D/32][2][64][8]  dims' 32 i + n, tokens 16 u + 4 g + (0..3, 8..11)
+// Positions that no row sees become 0.  A V block stored as NaN becomes 0 as well, and is
+// noted, for it must not reach rows that do not see it (0 * NaN); a K block becomes NaN.
+template <int D>
+__global__ __launch_bounds__(256) void k_prompt_widen(Args a) {
+  const int lane = threadIdx.x & 63;
+  const int tile = blockIdx.x / a.kv_heads, h = blockIdx.x - tile * a.kv_heads;
+  if (tile >= a.tile_off[a.batch]) return;
+  int b = 0;                                  // the last request with tile_off <= tile
+  for (int i = lane; i < a.batch; i += 64) b += a.tile_off[i] <= tile;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) b += __shfl_xor(b, d);
+  b = __builtin_amdgcn_readfirstlane(b) - 1;
+  const int ctx = a.ctx[b], rows = a.cu[b + 1] - a.cu[b];
+  const Span sp = span_of(ctx, rows, a.window, a.sinks);
+  const int i = tile - a.tile_off[b];
+  const int base = (i < sp.early ? i : i - sp.early + sp.tile0) * TILE;
+  const int early = a.window > 0 ? min(a.sinks, sp.first) : 0;
+  auto seen = [&](int t) { return t < sp.n && (t >= sp.first || t < early); };
+  // its units: pages hold 16 tokens at least
+  const uint8_t* unit[2];
+  const int32_t* tab = a.table + (int64_t)b * a.ld_table;
+  bool bad = false;
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    const int t0 = base + 16 * hf, slot = t0 >> a.page_log2;
+    // whether some position of the half is seen
+    const bool need = t0 < sp.n && (t0 + 16 > sp.first || t0 < early);
+    uint32_t id = 0;
+    bool have = need && slot < a.ld_table;
+    if (have) {
+      id = (uint32_t)tab[slot];
+      have = id < (uint64_t)a.num_pages;
+    }
+    bad |= need && !have;
+    unit[hf] = have ? a.pages + ((int64_t)id * a.kv_heads + h) * a.unit : nullptr;
+  }
+  if (bad && threadIdx.x == 0) a.status[b] = SV_ROW_BAD_PAGE;
+  uint8_t* const dst = a.wide + ((int64_t)h * a.max_tiles + tile) * tile_bytes(D);
+  const int P = a.page;
+
+  for (int w = threadIdx.x; w < D / 16 * 64; w += 256) {
+    const int s = w >> 6, n = w & 31, g = w >> 5 & 1;
+    const int t = base + n, at = t & (P - 1);
+    const uint8_t* u = unit[n >> 4];
+    u32x4 y = {0, 0, 0, 0};
+    if (u && seen(t)) {
+      const uint32_t x = load_any<uint32_t>(u + at * (D / 2) + 8 * s + 4 * g);
+      const uint32_t e = u[off_ks(P, D) + (at >> 3) * (D / 4) + (s / 2) * 8 + (at & 7)];
+      const float sc = __builtin_bit_cast(float, e << 23);
+      y[0] = widen<0>(x, sc);
+      y[1] = widen<1>(x, sc);
+      y[2] = widen<2>(x, sc);
+      y[3] = widen<3>(x, sc);
+      if (e == 255) y = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+    }
+    *(u32x4*)(dst + w * 16) = y;
+  }
+  // V: a pair of dims (a byte of a token) for 8 tokens
+  for (int w = threadIdx.x; w < D / 2 * 4; w += 256) {
+    const int c = w % (D / 2), ug = w / (D / 2), u2 = ug >> 1, g = ug & 1;
+    const uint8_t* u = unit[u2];
+    const int n16 = 2 * c / (D / 16), byte = c % (D / 32);
+    uint32_t x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int t = base + 16 * u2 + 8 * (k >> 2) + 4 * g + (k & 3), at = t & (P - 1);
+      x[k] = 0;
+      if (u && seen(t)) {
+        const uint32_t v = u[off_v(P, D) + (at >> 3) * (4 * D) + n16 * (D / 4) + (at & 7) * (D / 32) + byte];
+        const uint32_t e = u[off_vs(P, D) + (at >> 3) * (D / 4) + (2 * c / 32) * 8 + (at & 7)];
+        if (e != 255) x[k] = widen<0>(v, __builtin_bit_cast(float, e << 23));
+      }
+    }
+    u32x4 lo, hi;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      lo[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], 0x05040100u);
+      hi[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], 0x07060302u);
+    }
+    u32x4* to = (u32x4*)(dst + TILE * D * 2) + ((c / 16 * 2 + u2) * 64 + 32 * g + 2 * c % 32);
+    to[0] = lo;
+    to[1] = hi;
+  }
+  if (threadIdx.x < 32) {
+    const int n = threadIdx.x, t = base + n, at = t & (P - 1);
+    const uint8_t* u = unit[n >> 4];
+    uint32_t m = 0;
+    if (u && seen(t))
+      for (int k = 0; k < D / 32; ++k)
+        m |= (uint32_t)(u[off_vs(P, D) + (at >> 3) * (D / 4) + k * 8 + (at & 7)] == 255) << k;
+    a.odd[((int64_t)h * a.max_tiles + tile) * TILE + n] = (uint8_t)m;
+    if (m) a.head->odd = 1;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x) { return (float)x; }
+
+template <int D, int OD, int MT, typename T>
+struct Prompt {
+  static constexpr int STEPS = D / 16, DT = OD / 32;
+  // fp32 queries and weights are split into three bf16 terms (3 x 8 bits hold fp32's 24)
+  static constexpr int NT = sizeof(T) == 4 ? 3 : 1;
+
+  // (of fp32 rows at D=256 the last term lies in LDS: all three do not fit the registers)
+  static constexpr int NR = NT == 3 && D == 256 ? 2 : NT;
+  static constexpr int Q_LDS = MT * STEPS * (NT - NR) * 64;    // 16-byte words of a wave
+
+  bf16x8 q[MT][STEPS][NR];
+  f32x16 o[MT][DT];
+  float l[MT], m[MT], mc[MT], over[MT];
+  int pos[MT];
+  uint32_t poison[MT];
+
+  static __device__ __forceinline__ void split(float x, __bf16* t) {
+    float r = x;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      t[i] = (__bf16)r;
+      r -= (float)t[i];
+    }
+  }
+  __device__ __forceinline__ void init(const Args& a, int row0, int ctx, int h, int64_t r0, int64_t R,
+                                       u32x4* q_lds) {
+    const int n = threadIdx.x & 31, g = threadIdx.x >> 5 & 1;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const uint32_t r = (uint32_t)min(r0 + mt * 32 + n, R - 1);
+      const uint32_t j = r / (uint32_t)a.group, hq = h * a.group + r - j * a.group;
+      pos[mt] = ctx + (int)j;
+      const T* src = (const T*)a.q + ((int64_t)row0 + j) * a.ld_q + (int64_t)hq * D + 8 * g;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        T x[8];
+        __builtin_memcpy(x, src + 16 * s, sizeof(x));
+        [[maybe_unused]] bf16x8 rest;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          __bf16 t[NT];
+          if constexpr (NT == 1) t[0] = x[k];
+          else split(to_f32<T>(x[k]), t);
+#pragma unroll
+          for (int u = 0; u < NR; ++u) q[mt][s][u][k] = t[u];
+          if constexpr (NR < NT) rest[k] = t[NT - 1];
+        }
+        if constexpr (NR < NT)
+          q_lds[(mt * STEPS + s) * 64 + (threadIdx.x & 63)] = __builtin_bit_cast(u32x4, rest);
+      }
+      l[mt] = 0.f;
+      m[mt] = over[mt] = -INFINITY;
+      mc[mt] = -FAR;
+      poison[mt] = 0;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[mt][dt][k] = 0.f;
+    }
+  }
+  __device__ __forceinline__ bool sees(const Args& a, int t, int mt) const {
+    const bool inside = (a.window == 0) | (t > pos[mt] - a.window) | (t < a.sinks);
+    return inside & (t <= pos[mt]);
+  }
+  // Token of accumulator entry r, relative to the tile.
+  static __device__ __forceinline__ int token(int g, int r) { return 8 * (r >> 2) + 4 * g + (r & 3); }
+
+  __device__ __forceinline__ void tile(const Args& a, const u32x4* lds, const u32x4* q_lds, int base, bool masked, float c) {
+    const int lane = threadIdx.x & 63, g = lane >> 5;
+    f32x16 s[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s[mt][k] = 0.f;
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) {
+      const bf16x8 kf = __builtin_bit_cast(bf16x8, lds[st * 64 + lane]);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        if constexpr (NR < NT)
+          s[mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              kf, __builtin_bit_cast(bf16x8, q_lds[(mt * STEPS + st) * 64 + lane]), s[mt], 0, 0, 0);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int u = NR - 1; u >= 0; --u)
+          s[mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[mt][st][u], s[mt], 0, 0, 0);
+      // (or all operands are read ahead and do not fit the registers)
+      if (D == 256 && st % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (masked) {
+      asm volatile("");                       // (a branch: most tiles need no mask)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[mt][r] = sees(a, base + token(g, r), mt) ? s[mt][r] : -INFINITY;
+    }
+    bf16x8 p[MT][2][NT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float mx = s[mt][0];
+#pragma unroll
+      for (int r = 1; r < 15; r += 2) mx = fmaxf(fmaxf(mx, s[mt][r]), s[mt][r + 1]);
+      mx = fmaxf(mx, s[mt][15]);
+      // (a first visible score raises -inf; a row that has seen nothing stays there)
+      if (__any(mx > over[mt])) {
+        mx = fmaxf(mx, __shfl_xor(mx, 32));   // the other half of the row's tokens
+        const float nm = fmaxf(m[mt], mx);
+        const float nc = __builtin_amdgcn_fmed3f(nm * c, -FAR, FAR);
+        const float f = __builtin_amdgcn_exp2f(mc[mt] - nc);
+        l[mt] *= f;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[mt][dt] *= f;
+        m[mt] = nm;
+        mc[mt] = nc;
+        over[mt] = nm + __builtin_fminf(RAISE / c, 3.4e38f);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][r], c, -mc[mt]));
+        __bf16 x[NT];
+        split(e, x);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) p[mt][r >> 3][u][r & 7] = x[u];
+        // (the sum is that of the rounded weights: their errors cancel in the division)
+        l[mt] += NT == 1 ? (float)x[0] : e;
+      }
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int u2 = 0; u2 < 2; ++u2) {
+        const bf16x8 vf = __builtin_bit_cast(bf16x8, lds[TILE * D * 2 / 16 + (dt * 2 + u2) * 64 + lane]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int u = NT - 1; u >= 0; --u)
+            o[mt][dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[mt][u2][u], o[mt][dt], 0, 0, 0);
+        if (D == 256) __builtin_amdgcn_sched_barrier(0);
+      }
+  }
+  // V blocks stored as NaN: rows that see the token are NaN in the block's dims.
+  __device__ __forceinline__ void note(const Args& a, const uint8_t* odd, int base) {
+#pragma nounroll
+    for (int t = 0; t < TILE; ++t) {
+      const uint32_t bits = odd[t];
+      if (!bits) continue;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (sees(a, base + t, mt)) poison[mt] |= bits;
+      }
+    }
+  }
+};
+
+template <int D, int OD, int MT, int WAVES, int PER_SIMD, typename T>
+__global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
+  using A = Prompt<D, OD, MT, T>;
+  constexpr int PARTS = D / OD;              // workgroups that share a block's dims
+  constexpr int STAGE = D == 256 ? 1 : 2;     // tiles on their way at a time
+  constexpr int K_WORDS = TILE * D * 2 / 16, V_WORDS = TILE * OD * 2 / 16, WORDS = K_WORDS + V_WORDS;
+  constexpr int LOADS = STAGE * WORDS / (64 * WAVES);
+  __shared__ u32x4 lds[2][STAGE * WORDS], q_lds[A::Q_LDS ? WAVES : 1][A::Q_LDS ? A::Q_LDS : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int of = blockIdx.x % PARTS, hit = blockIdx.x / PARTS, it = hit / a.kv_heads, h = hit - it * a.kv_heads;
+  if (it >= a.head->items) return;
+  const Item item = a.items[it];
+  const Block blk = a.blocks[item.block];
+  const int b = blk.b, row0 = a.cu[b], rows = a.cu[b + 1] - row0, ctx = a.ctx[b];
+  const int st = a.status[b];
+  const int64_t R = (int64_t)rows * a.group, r0 = (int64_t)blk.rb * a.block_rows;
+  const int64_t rw = r0 + wave * 32 * MT;     // the wave's first row
+  const int n = lane & 31, g = lane >> 5;
+  if (st != SV_ROW_OK) {                      // the request's rows are NaN
+    if (item.chunk > 0) return;
+    for (int mt = 0; mt < MT; ++mt) {
+      const int64_t r = rw + mt * 32 + n;
+      if (r >= R) continue;
+      const uint32_t j = (uint32_t)r / (uint32_t)a.group, hq = h * a.group + (uint32_t)r - j * a.group;
+      T* dst = (T*)a.out + ((int64_t)row0 + j) * a.ld_out + (int64_t)hq * D + of * OD + g * (OD / 2);
+      for (int i = 0; i < OD / 2; ++i) dst[i] = (T)__builtin_nanf("");
+    }
+    return;
+  }
+  const int j0 = (int)(r0 / a.group), j1 = (int)((min(r0 + a.block_rows, R) - 1) / a.group);
+  const Span all = span_of(ctx, rows, a.window, a.sinks);
+  const Span sp = block_span(ctx, j0, j1, a.window, a.sinks);
+  const int begin = item.chunk * a.chunk_tiles, end = min(sp.tiles, begin + a.chunk_tiles);
+  const bool whole = sp.tiles <= a.chunk_tiles;
+  const float c = a.scale * LOG2E;
+  const int64_t first = (int64_t)h * a.max_tiles + a.tile_off[b];
+  // tile i of the block, in tokens, and where its widened form lies
+  auto base_of = [&](int i) { return (i < sp.early ? i : i - sp.early + sp.tile0) * TILE; };
+  auto place = [&](int i) {
+    const int t = i < sp.early ? i : i - sp.early + sp.tile0;
+    return first + (t < all.early ? t : t - all.tile0 + all.early);
+  };
+  // positions of the wave's rows
+  const int w0 = ctx + (int)(min(rw, R - 1) / a.group);
+  const int w1 = ctx + (int)(min(rw + 32 * MT - 1, R - 1) / a.group);
+  const bool live = rw < R;
+  const bool odd = a.head->odd != 0;
+
+  // the next tiles go straight to LDS, 1 KiB per wave and instruction
+  auto ask = [&](int i, int buf) {
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) {
+      const int w = (k * WAVES + wave) * 64, t = w / WORDS;
+      const u32x4* src = (const u32x4*)(a.wide + place(min(i + t, end - 1)) * tile_bytes(D)) + (w - t * WORDS) +
+                         (w - t * WORDS < K_WORDS ? 0 : of * V_WORDS);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + lane),
+                                       (__attribute__((address_space(3))) void*)(lds[buf] + w), 16, 0, 0);
+    }
+  };
+  ask(begin, 0);
+  A x;
+  u32x4* const my_q = q_lds[A::Q_LDS ? wave : 0];
+  x.init(a, row0, ctx, h, rw, R, my_q);
+  __syncthreads();
+  int buf = 0;
+  for (int i = begin; i < end; i += STAGE) {
+    ask(min(i + STAGE, end - 1), buf ^ 1);
+#pragma unroll
+    for (int t = 0; t < STAGE; ++t) {
+      if (i + t >= end) break;
+      const int base = base_of(i + t);
+      if (!live || base > w1) continue;
+      const bool masked = base + TILE - 1 > w0 ||
+                          (a.window > 0 && base <= w1 - a.window && base + TILE > a.sinks);
+      x.tile(a, lds[buf] + t * WORDS, my_q, base, masked, c);
+      if (odd) x.note(a, a.odd + place(i + t) * TILE, base);
+    }
+    buf ^= 1;
+    __syncthreads();
+  }
+
+  const int64_t slot = (((int64_t)item.block * a.kv_heads + h) * a.chunks + item.chunk) * a.block_rows;
+  float* const part = a.part + slot * D;
+  float* const stat = a.part + (int64_t)a.max_blocks * a.kv_heads * a.chunks * a.block_rows * D + slot * 2;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const float sum = x.l[mt] + __shfl_xor(x.l[mt], 32);
+    const int64_t r = rw + mt * 32 + n;
+    if (r >= R) continue;
+    const uint32_t j = (uint32_t)r / (uint32_t)a.group, hq = h * a.group + (uint32_t)r - j * a.group;
+    const float inv = 1.f / sum;
+    T* dst = (T*)a.out + ((int64_t)row0 + j) * a.ld_out + (int64_t)hq * D;
+    const int local = (int)(r - r0);
+#pragma unroll
+    for (int dt = 0; dt < A::DT; ++dt) {
+      const bool nan = x.poison[mt] >> (of * A::DT + dt) & 1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = nan ? __builtin_nanf("") : x.o[mt][dt][4 * k + e];
+        const int dim = of * OD + 32 * dt + 8 * k + 4 * g;
+        if (whole) {
+          T z[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = (T)(y[e] * inv);
+          __builtin_memcpy(dst + dim, z, sizeof(z));
+        } else {
+          __builtin_memcpy(part + (int64_t)local * D + dim, y, sizeof(y));
+        }
+      }
+    }
+    if (!whole && g == 0 && of == 0) {
+      stat[local * 2] = x.mc[mt];
+      stat[local * 2 + 1] = sum;
+    }
+  }
+}
+
+// Joins the chunks of blocks that have several: 16 threads per row.
+template <int D, typename T>
+__global__ __launch_bounds__(256) void k_prompt_join(Args a) {
+  constexpr int E = D / 16;
+  const int per = a.block_rows / 16;
+  const int local = (int)(blockIdx.x % per) * 16 + (threadIdx.x >> 4), e0 = (threadIdx.x & 15) * E;
+  const int hb = blockIdx.x / per, h = hb % a.kv_heads, bl = hb / a.kv_heads;
+  if (bl >= a.head->blocks) return;
+  const Block blk = a.blocks[bl];
+  const int b = blk.b, row0 = a.cu[b], rows = a.cu[b + 1] - row0;
+  if (a.status[b] != SV_ROW_OK) return;
+  const int64_t R = (int64_t)rows * a.group, r0 = (int64_t)blk.rb * a.block_rows, r = r0 + local;
+  const int j0 = (int)(r0 / a.group), j1 = (int)((min(r0 + a.block_rows, R) - 1) / a.group);
+  const int tiles = block_span(a.ctx[b], j0, j1, a.window, a.sinks).tiles;
+  const int n = (tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+  if (n < 2 || r >= R) return;
+  const int64_t slot = ((int64_t)bl * a.kv_heads + h) * a.chunks * a.block_rows + local;
+  const float* part = a.part + slot * D + e0;
+  const float* stat = a.part + (int64_t)a.max_blocks * a.kv_heads * a.chunks * a.block_rows * D + slot * 2;
+  float m = -INFINITY;
+  for (int k = 0; k < n; ++k) m = fmaxf(m, stat[(int64_t)k * a.block_rows * 2]);
+  float acc[E] = {}, sum = 0.f;
+  for (int k = 0; k < n; ++k) {
+    const float mk = stat[(int64_t)k * a.block_rows * 2];
+    const float w = mk == m ? 1.f : __builtin_amdgcn_exp2f(mk - m);
+    sum += w * stat[(int64_t)k * a.block_rows * 2 + 1];
+    float y[E];
+    __builtin_memcpy(y, part + (int64_t)k * a.block_rows * D, sizeof(y));
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(y[e], w, acc[e]);
+  }
+  const uint32_t j = (uint32_t)r / (uint32_t)a.group, hq = h * a.group + (uint32_t)r - j * a.group;
+  T z[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) z[e] = (T)(acc[e] / sum);
+  __builtin_memcpy((T*)a.out + ((int64_t)row0 + j) * a.ld_out + (int64_t)hq * D + e0, z, sizeof(z));
+}
+
+// ---- host side
+
+struct Plan {
+  int block_rows, max_blocks, chunks, chunk_tiles;
+  int64_t max_tiles;
+  size_t tile_off, blocks, items, odd, wide, part, bytes;
+};
+
+static size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+static bool plan_of(int dtype, int batch, int total_rows, int heads, int kv_heads, int d,
+                    int max_context, int64_t total_context, int window, int sinks, Plan& p) {
+  const int64_t R = (int64_t)total_rows * (heads / kv_heads);
+  p.block_rows = d < 256 || dtype == SV_BF16 ? 256 : 128;
+  const int64_t blocks = (R + (int64_t)batch * (p.block_rows - 1)) / p.block_rows;
+  // tiles of all requests, and of one
+  int64_t tiles = total_context / TILE + batch, one = max_context / TILE + 1;
+  if (window > 0) {
+    const int64_t more = (int64_t)window / TILE + (sinks + TILE - 1) / TILE + 3;
+    const int64_t seen = total_rows / TILE + batch * more;
+    if (seen < tiles) tiles = seen;
+    const int64_t block_seen = p.block_rows / TILE + more;
+    if (block_seen < one) one = block_seen;
+  }
+  p.max_tiles = tiles;
+  int64_t chunks = 1;
+  const int64_t wide = blocks * kv_heads;
+  if (wide < 512) chunks = (512 + wide - 1) / wide;
+  int64_t ct = (one + chunks - 1) / chunks;
+  if (ct < 16) ct = 16;
+  chunks = (one + ct - 1) / ct;
+  p.chunks = (int)chunks;
+  p.chunk_tiles = (int)ct;
+  // (a launch has less than 2^32 threads)
+  if (wide * chunks * (p.block_rows / 16) * 2 >= (1ll << 24) || tiles * kv_heads >= (1ll << 24)) return false;
+  p.max_blocks = (int)blocks;
+  size_t at = round256(sizeof(Head));
+  p.tile_off = at;
+  at += round256(((size_t)batch + 1) * 4);
+  p.blocks = at;
+  at += round256((size_t)blocks * sizeof(Block));
+  p.items = at;
+  at += round256((size_t)(blocks * chunks) * sizeof(Item));
+  p.odd = at;
+  at += round256((size_t)(tiles * kv_heads) * TILE);
+  p.wide = at;
+  at += (size_t)(tiles * kv_heads) * tile_bytes(d);
+  p.part = at;
+  if (chunks > 1) at += (size_t)(wide * chunks * p.block_rows) * (d + 2) * sizeof(float);
+  p.bytes = at;
+  return true;
+}
+
+static bool sizes_ok(int dtype, int batch, int total_rows, int heads, int kv_heads, int d,
+                     int max_context, int64_t total_context, int window, int sinks) {
+  return (dtype == SV_F32 || dtype == SV_BF16) && batch >= 1 && batch <= MAX_BATCH &&
+         total_rows >= 1 && kv_heads >= 1 && heads >= kv_heads && heads % kv_heads == 0 &&
+         heads <= 1024 && dim_ok(d) && (int64_t)total_rows * heads < (1ll << 31) &&
+         max_context >= 1 && max_context <= (1 << 30) && total_context >= 1 &&
+         total_context <= (1ll << 30) && window >= 0 && window <= (1 << 30) && sinks >= 0 &&
+         sinks <= (1 << 30);
+}
+
+template <int D, int OD, int MT, int WAVES, int PER_SIMD, typename T>
+static int launch(const Args& a, const Plan& p, hipStream_t s) {
+  hipLaunchKernelGGL(k_prompt_plan, dim3(1), dim3(1024), 0, s, a);
+  if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
+  hipLaunchKernelGGL((k_prompt_widen<D>), dim3((uint32_t)(p.max_tiles * a.kv_heads)), dim3(256), 0, s, a);
+  if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
+  const uint32_t wide = (uint32_t)(p.max_blocks * a.kv_heads);
+  hipLaunchKernelGGL((k_prompt<D, OD, MT, WAVES, PER_SIMD, T>), dim3(wide * p.chunks * (D / OD)), dim3(64 * WAVES), 0, s, a);
+  if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
+  if (p.chunks > 1) {
+    hipLaunchKernelGGL((k_prompt_join<D, T>), dim3(wide * (a.block_rows / 16)), dim3(256), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
+  }
+  return SV_OK;
+}
+
+}  // namespace prompt
+}  // namespace svk
+
+using namespace svk;
+
+extern "C" {
+
+size_t spec_kv_prompt_workspace_bytes(int dtype, int batch, int total_rows, int heads, int kv_heads,
+                                      int head_dim, int max_context, int64_t total_context,
+                                      int window, int sinks) {
+  prompt::Plan p;
+  if (!prompt::sizes_ok(dtype, batch, total_rows, heads, kv_heads, head_dim, max_context, total_context,
+                        window, sinks) ||
+      !prompt::plan_of(dtype, batch, total_rows, heads, kv_heads, head_dim, max_context, total_context,
+                       window, sinks, p))
+    return 0;
+  return p.bytes;
+}
+
+int spec_kv_prompt_attention(const void* q, int64_t ld_q, int dtype, const int32_t* cu_seqlens,
+                             const int32_t* context_lens, int batch, int total_rows, int heads,
+                             int kv_heads, int head_dim, const void* pages, int64_t num_pages,
+                             int page_size, const int32_t* page_table, int64_t ld_table,
+                             int max_context, int64_t total_context, float scale, int window,
+                             int sinks, void* out, int64_t ld_out, int32_t* status, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!q || !cu_seqlens || !context_lens || !pages || !page_table || !out || !status)
+    return SV_ERR_NULL;
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  prompt::Plan p;
+  if (!prompt::sizes_ok(dtype, batch, total_rows, heads, kv_heads, head_dim, max_context, total_context,
+                        window, sinks) ||
+      !page_ok(page_size) || num_pages < 1 || num_pages > 0x7fffffff || ld_table < 1 ||
+      ld_table > (1 << 30) / page_size || ld_q < (int64_t)heads * head_dim ||
+      ld_out < (int64_t)heads * head_dim || !(scale > 0.f) || !(scale <= 2.0e38f) || !aligned16(pages) || out == q ||
+      !prompt::plan_of(dtype, batch, total_rows, heads, kv_heads, head_dim, max_context, total_context,
+                       window, sinks, p))
+    return SV_ERR_SHAPE;
+  if (!workspace || !aligned16(workspace)) return SV_ERR_NULL;
+  if (p.bytes > workspace_bytes) return SV_ERR_WORKSPACE;
+  prompt::Args a;
+  a.q = q;
+  a.ld_q = ld_q;
+  a.cu = cu_seqlens;
+  a.ctx = context_lens;
+  a.batch = batch;
+  a.total_rows = total_rows;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.group = heads / kv_heads;
+  a.pages = (const uint8_t*)pages;
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.page_log2 = __builtin_ctz((unsigned)page_size);
+  a.unit = (int)unit_bytes(page_size, head_dim);
+  a.table = page_table;
+  a.ld_table = ld_table;
+  a.max_context = max_context;
+  a.total_context = total_context;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.status = status;
+  a.block_rows = p.block_rows;
+  a.max_blocks = p.max_blocks;
+  a.chunks = p.chunks;
+  a.chunk_tiles = p.chunk_tiles;
+  a.max_tiles = p.max_tiles;
+  uint8_t* w = (uint8_t*)workspace;
+  a.head = (prompt::Head*)w;
+  a.tile_off = (int32_t*)(w + p.tile_off);
+  a.blocks = (prompt::Block*)(w + p.blocks);
+  a.items = (prompt::Item*)(w + p.items);
+  a.odd = w + p.odd;
+  a.wide = w + p.wide;
+  a.part = (float*)(w + p.part);
+  hipStream_t s = (hipStream_t)stream;
+  if (dtype == SV_BF16) {
+    if (head_dim == 64) return prompt::launch<64, 64, 1, 8, 2, __bf16>(a, p, s);
+    if (head_dim == 128) return prompt::launch<128, 128, 1, 8, 2, __bf16>(a, p, s);
+    return prompt::launch<256, 128, 1, 8, 2, __bf16>(a, p, s);
+  }
+  if (head_dim == 64) return prompt::launch<64, 64, 1, 8, 2, float>(a, p, s);
+  if (head_dim == 128) return prompt::launch<128, 128, 1, 8, 2, float>(a, p, s);
+  return prompt::launch<256, 128, 1, 4, 1, float>(a, p, s);
+}
+
+}  // extern "C"
