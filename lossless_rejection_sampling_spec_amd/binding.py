@@ -83,6 +83,11 @@ def load_library(path: str) -> ctypes.CDLL:
         _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _i32,
         _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp,
         _vp, _vp]
+    L.spec_kv_append_at.restype = _i32
+    L.spec_kv_append_at.argtypes = [
+        _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _i32,
+        _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp,
+        _vp, _vp, _vp]
     L.spec_kv_attention_workspace_bytes.restype = _sz
     L.spec_kv_attention_workspace_bytes.argtypes = [_i32] * 9
     L.spec_kv_attention.restype = _i32
@@ -95,6 +100,15 @@ def load_library(path: str) -> ctypes.CDLL:
     L.spec_kv_prompt_attention.argtypes = [
         _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i64, _i32,
         _i64, ctypes.c_float, _i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp]
+    L.spec_kv_weights_workspace_bytes.restype = _sz
+    L.spec_kv_weights_workspace_bytes.argtypes = [_i32] * 9
+    L.spec_kv_attention_weights.restype = _i32
+    L.spec_kv_attention_weights.argtypes = [
+        _vp, _i64, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp,
+        _i64, _i32, ctypes.c_float, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _sz, _vp]
+    L.spec_kv_evict.restype = _i32
+    L.spec_kv_evict.argtypes = [_vp, _i32, _i32, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _i64,
+                                _vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp]
     L.spec_kv_pages_workspace_bytes.restype = _sz
     L.spec_kv_pages_workspace_bytes.argtypes = [_i32, _i64]
     L.spec_kv_reserve.restype = _i32
@@ -541,13 +555,16 @@ def kv_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
               cu_seqlens: torch.Tensor, context_lens: torch.Tensor, *, layer: int = 0,
               q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
               eps: float = 1e-6, cos_sin: torch.Tensor | None = None, interleaved: bool = False,
-              out: torch.Tensor | None = None, want_values: bool = False):
+              out: torch.Tensor | None = None, want_values: bool = False,
+              position_offsets: torch.Tensor | None = None):
     """spec_kv_append: head norms, rotation and the 4-bit cache write of the
     call's rows in one pass.
 
     q [rows, heads, D], k and v [rows, kv_heads, D] (float32 or bfloat16, views
     of one fused projection are fine); q_weight, k_weight float32 [D] or None;
     cos_sin float32 [positions, rot_dim], cos first, or None; `out` may be q.
+    position_offsets (int32 [B], kv_evict's `evicted`): how far a request's positions are ahead
+    of its slots, for the angles.
 
     Returns (q_out, status[B]), and with want_values (q_out, status, k_values,
     v_values): the values the cache now stands for.  Rows that are not processed (of no
@@ -560,6 +577,7 @@ def kv_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if k_rows != rows or v_rows != rows or k_heads != cache.kv_heads or v_heads != cache.kv_heads:
         raise ValueError(f"k and v must be [{rows}, {cache.kv_heads}, {cache.head_dim}]")
     _check_ints(context_lens, "context_lens", cache.device, batch)
+    _check_ints(position_offsets, "position_offsets", cache.device, batch)
     rot = positions = 0
     for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight"), (cos_sin, "cos_sin")):
         if t is not None and (t.dtype != torch.float32 or t.device != cache.device
@@ -584,10 +602,10 @@ def kv_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     status = context_lens.new_empty(batch)
     k_values, v_values = (_out_like(k), _out_like(v)) if want_values else (None, None)
     with _on(cache.device) as stream:
-        _raise(lib().spec_kv_append(
+        _raise(lib().spec_kv_append_at(
             q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, code, _ptr(q_weight),
-            _ptr(k_weight), eps, _ptr(cos_sin), positions, rot, interleaved,
-            cu_seqlens.data_ptr(), context_lens.data_ptr(), batch, rows, heads, cache.kv_heads,
+            _ptr(k_weight), eps, _ptr(cos_sin), positions, rot, interleaved, cu_seqlens.data_ptr(),
+            context_lens.data_ptr(), _ptr(position_offsets), batch, rows, heads, cache.kv_heads,
             cache.head_dim, cache.pages.data_ptr() + layer * cache.layer_bytes, cache.num_pages,
             cache.page_size, cache.page_table.data_ptr(), cache.ld_table, out.data_ptr(), ld_out,
             _ptr(k_values), _ptr(v_values), status.data_ptr(), stream))
@@ -689,6 +707,91 @@ def kv_prompt_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tenso
             max_context, total_context, scale, window, sinks, out.data_ptr(), ld_out,
             status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), stream))
     return out, status
+
+
+def kv_attention_weights(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor,
+                         context_lens: torch.Tensor, *, max_k: int, max_context: int,
+                         weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         row_counts: torch.Tensor | None = None, layer: int = 0,
+                         scale: float | None = None, window: int = 0, sinks: int = 0,
+                         workspace: torch.Tensor | None = None):
+    """spec_kv_attention_weights: the attention weight that cached positions get from the rows
+    q (as kv_append turned them) of each request, summed over its first row_counts[b] rows
+    (None: all) and the query heads of each KV head, on top of `weights` (None: zeros).
+
+    weights, out  float32 [B, kv_heads, L], L >= max_context: one layer's.  `out` defaults to
+    `weights` itself, or to new memory.  Only positions below context_lens[b] + rows are written
+    (new memory is 0 behind them).  Returns (out, status[B])."""
+    batch = _kv_batch(cache, cu_seqlens)
+    code = _dtype_code(q)
+    rows, heads, ld_q = _heads_of(q, "q", cache, q.dtype)
+    _check_ints(context_lens, "context_lens", cache.device, batch)
+    _check_ints(row_counts, "row_counts", cache.device, batch)
+    if not 0 <= layer < cache.layers:
+        raise ValueError(f"layer {layer} of {cache.layers}")
+    # (ctypes would take the low 32 bits of a larger number)
+    if not (0 <= max_k <= MAX_K and 1 <= max_context <= 1 << 30 and 0 <= window <= 1 << 30
+            and 0 <= sinks <= 1 << 30):
+        raise ValueError(f"max_k is at most {MAX_K}, max_context, window and sinks at most 2^30")
+    scale = cache.head_dim ** -0.5 if scale is None else scale
+    L = lib()
+    need = L.spec_kv_weights_workspace_bytes(code, batch, max_k, heads, cache.kv_heads,
+                                             cache.head_dim, max_context, window, sinks)
+    if need == 0:
+        raise ValueError("invalid sizes for spec_kv_attention_weights")
+    if out is None:
+        out = weights if weights is not None else torch.zeros(
+            batch, cache.kv_heads, max_context, dtype=torch.float32, device=cache.device)
+    for t, name in ((weights, "weights"), (out, "out")):
+        if t is not None and (t.dtype != torch.float32 or t.device != cache.device
+                              or not t.is_contiguous() or t.dim() != 3 or t.shape[0] < batch
+                              or t.shape[1] != cache.kv_heads or t.shape[2] < max_context
+                              or t.shape[2] != out.shape[2]):
+            raise ValueError(f"{name} must be a contiguous float32 tensor [{batch}, {cache.kv_heads}, "
+                             f"at least {max_context}] on the cache's device")
+    status = context_lens.new_empty(batch)
+    with _on(cache.device) as stream:
+        ws = _kv_workspace(cache.device, need, workspace)
+        _raise(L.spec_kv_attention_weights(
+            q.data_ptr(), ld_q, code, cu_seqlens.data_ptr(), context_lens.data_ptr(),
+            _ptr(row_counts), batch, rows, max_k, heads, cache.kv_heads, cache.head_dim,
+            cache.pages.data_ptr() + layer * cache.layer_bytes, cache.num_pages, cache.page_size,
+            cache.page_table.data_ptr(), cache.ld_table, max_context, scale, window, sinks,
+            _ptr(weights), out.data_ptr(), out.shape[2], status.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size(), stream))
+    return out, status
+
+
+def kv_evict(cache: KVCache, weights: torch.Tensor, budgets: torch.Tensor, *, sinks: int = 0,
+             recent: int = 0, evicted: torch.Tensor | None = None):
+    """spec_kv_evict: requests longer than budgets[b] (int32 [B], 0: no budget) keep that many
+    positions: the first `sinks`, the last `recent`, and those of the largest weights between
+    them, per layer and KV head.  What stays moves to the front, pages behind it are free.
+
+    weights  float32 [layers, B, kv_heads, L], moved along; evicted int32 [B] or None, counted
+    up by the positions that left (kv_append's position_offsets).  Returns status[B]."""
+    batch = budgets.numel()
+    _check_ints(budgets, "budgets", cache.device, 1)
+    _check_ints(evicted, "evicted", cache.device, batch)
+    if batch > cache.requests:
+        raise ValueError(f"{batch} requests, but the page table has {cache.requests}")
+    if (weights.dtype != torch.float32 or weights.device != cache.device or weights.dim() != 4
+            or not weights.is_contiguous()
+            or weights.shape[:3] != (cache.layers, batch, cache.kv_heads)):
+        raise ValueError(f"weights must be a contiguous float32 tensor [{cache.layers}, {batch}, "
+                         f"{cache.kv_heads}, positions] on the cache's device")
+    # (ctypes would take the low 32 bits of a larger number)
+    if not (0 <= sinks <= 1 << 30 and 0 <= recent <= 1 << 30):
+        raise ValueError("sinks and recent are at most 2^30")
+    status = budgets.new_empty(batch)
+    with _on(cache.device) as stream:
+        _raise(lib().spec_kv_evict(
+            budgets.data_ptr(), batch, sinks, recent, weights.data_ptr(), weights.shape[3],
+            cache.kv_heads, cache.head_dim, cache.page_size, cache.seq_lens.data_ptr(),
+            cache.page_table.data_ptr(), cache.ld_table, cache.ref_counts.data_ptr(),
+            cache.num_pages, cache.pages.data_ptr(), cache.layers, cache.layer_bytes,
+            _ptr(evicted), status.data_ptr(), stream))
+    return status
 
 
 def _pages_workspace(cache: KVCache, seqs: int, workspace):

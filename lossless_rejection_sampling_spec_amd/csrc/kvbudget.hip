@@ -1,0 +1,943 @@
+// kvbudget.hip -- a cache held to a budget of positions (include/specverify.h states the
+// operators):
+//   spec_kv_attention_weights   the attention weight that cached positions get
+//   spec_kv_evict               positions of the least weight leave the cache
+//
+// No float atomics: every position's weight is summed by one workgroup in a fixed order, and
+// which positions stay follows from the weights and positions alone.
+
+#include "kv_common.h"
+
+namespace svk {
+namespace budget {
+
+// ------------------------------------------------------------------ weights
+//
+// W[b][h][t] = in[b][h][t] + sum over the counted rows j and the query heads of KV head h of
+//   exp(scale q.k_t - m) / sum_u exp(scale q.k_u - m)
+// The divisor needs every score of a row before the first weight, so the scores are made
+// twice: once for the rows' maxima and sums, once for the weights.  (Kept instead, they would
+// take R numbers per position, more than the position's codes from R = 16 on.)
+//
+// A workgroup of 4 waves takes a chunk of one KV head's context, all R = rows * G query rows
+// of it, 16 MT at a time; its waves take the tiles of 32 tokens in turn.  Scores are
+// S^T[token][row] = K Q^T with v_mfma_f32_16x16x32_bf16, K widened from its codes in
+// registers; a lane holds the scores of one row for 8 tokens.  Where a request is one chunk
+// (short contexts) both passes are one launch.
+
+constexpr int TILE = 32, SUB = 64;            // tokens of a tile; tiles whose pages a wave looks up at once
+constexpr int WAVES = 4;
+constexpr float LOG2E = 1.44269504088896340736f;
+// the rounded product of maximum and scale, from which exponents are counted, is held within
+// +-FAR: past it weights become infinite, or all 0, and their row adds nothing
+constexpr float FAR = 1073741824.0f;          // 2^30
+
+struct WeightArgs {
+  const void* q;
+  int64_t ld_q;
+  const int32_t *cu, *ctx, *counts;
+  int batch, total_rows, max_k, heads, kv_heads, group;
+  const uint8_t* pages;
+  int64_t num_pages;
+  int page, page_log2, unit;
+  const int32_t* table;
+  int64_t ld_table;
+  int max_context;
+  float scale;
+  int window, sinks;
+  const float* in;
+  float* out;
+  int64_t ld_w;
+  int32_t* status;
+  int chunks, chunk_tiles, max_rows;          // chunks of a request at most; R at most
+  float* stats;                               // [batch][kv_heads][chunks][max_rows][2]
+  int gap_blocks;                             // blocks per KV head that copy what no row sees
+};
+
+struct Request {
+  int row0, rows, count, ctx, status;
+};
+__device__ __forceinline__ Request request_of(const WeightArgs& a, int b) {
+  Request r;
+  const int c0 = a.cu[b], c1 = a.cu[b + 1], cx = a.ctx[b];
+  const int cnt = a.counts ? a.counts[b] : c1 - c0;
+  const int broken = first_broken(a.cu, a.batch, a.total_rows);
+  r.row0 = c0;
+  r.rows = c1 - c0;
+  r.count = cnt;
+  r.ctx = cx;
+  r.status = SV_ROW_OK;
+  if (b >= broken || r.rows < 1 || r.rows > a.max_k + 1) r.status = SV_ROW_BAD_K;
+  else if (cx < 0 || (int64_t)cx + r.rows > a.max_context || cnt < 0 || cnt > r.rows)
+    r.status = SV_ROW_BAD_PARAM;
+  return r;
+}
+
+// Tiles that the rows see: the first `early` of the sequence, then those from tile0 on.
+struct Span {
+  int n, first, early, tile0, tiles;
+};
+__device__ __forceinline__ Span span_of(const WeightArgs& a, const Request& r) {
+  Span s;
+  s.n = r.ctx + r.rows;
+  s.first = a.window > 0 ? max(0, r.ctx - a.window + 1) : 0;
+  s.tile0 = s.first / TILE;
+  s.early = a.window > 0 ? min((a.sinks + TILE - 1) / TILE, s.tile0) : 0;
+  s.tiles = s.early + (s.n - 1) / TILE - s.tile0 + 1;
+  return s;
+}
+__device__ __forceinline__ int base_of(const Span& s, int i) {
+  return (i < s.early ? i : i - s.early + s.tile0) * TILE;
+}
+// Whether some row sees a position of the 16 from t0 on.
+__device__ __forceinline__ bool half_needed(const WeightArgs& a, const Span& s, int t0) {
+  return t0 < s.n && (t0 + 16 > s.first || (a.window > 0 && t0 < a.sinks));
+}
+
+template <int BYTE>
+__device__ __forceinline__ uint32_t widen(uint32_t word, float scale) {
+  return __builtin_bit_cast(uint32_t,
+                            __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, BYTE));
+}
+
+template <int D>
+struct KTile {
+  uint32_t k[2][D / 32], ks[2][(D + 127) / 128];   // per half of 16 tokens: token n, D/4 dims
+};
+
+template <int D, int MT, typename T>
+struct Weights {
+  static constexpr int STEPS = D / 32, KB = (D + 127) / 128;
+  // fp32 queries are split into three bf16 terms (3 x 8 bits hold fp32's 24)
+  static constexpr int NT = sizeof(T) == 4 ? 3 : 1;
+  static constexpr int Q_WORDS = MT * STEPS * NT * 64;      // 16-byte words
+
+  // The rows' operands in LDS, [row tile][step][term][lane].
+  static __device__ __forceinline__ void put_q(const WeightArgs& a, bf16x8* q, const Request& rq,
+                                               int h, int r0, int R, int wave) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    for (int at = wave; at < MT * STEPS; at += WAVES) {
+      const int mt = at / STEPS, s = at % STEPS;
+      const int r = min(r0 + mt * 16 + n, R - 1);
+      const int j = r / a.group, hq = h * a.group + r - j * a.group;
+      T x[8];
+      __builtin_memcpy(x, (const T*)a.q + (int64_t)(rq.row0 + j) * a.ld_q + hq * D + g * (D / 4) + 8 * s,
+                       sizeof(x));
+      bf16x8 y[NT];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float rest = (float)x[k];
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          y[u][k] = (__bf16)rest;
+          rest -= (float)y[u][k];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < NT; ++u) q[(at * NT + u) * 64 + lane] = y[u];
+    }
+  }
+
+  // Pages of 64 tiles from `from` on: lane i holds those of tile from + i (its two halves).
+  struct Pages {
+    int id[2], first;
+    __device__ __forceinline__ bool ask(const WeightArgs& a, const Span& sp, const int32_t* tab,
+                                        int from, int end) {
+      const int i = from + (threadIdx.x & 63);
+      bool bad = false;
+      first = from;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int t0 = base_of(sp, min(i, end - 1)) + 16 * hf, slot = t0 >> a.page_log2;
+        const bool need = i < end && half_needed(a, sp, t0);
+        const bool have = need && slot < a.ld_table;
+        id[hf] = tab[have ? slot : 0];
+        const bool in_pool = have && (uint32_t)id[hf] < (uint64_t)a.num_pages;
+        bad |= need && !in_pool;
+        if (!in_pool) id[hf] = 0;
+      }
+      return __any(bad);
+    }
+  };
+  static __device__ __forceinline__ void fetch(const WeightArgs& a, KTile<D>& t, const uint8_t* pool,
+                                               const Pages& id, const Span& sp, int i) {
+    const uint32_t lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int base = base_of(sp, i);
+    const uint32_t at_k = n * (D / 2) + g * (D / 8);
+    const uint32_t at_s = off_ks(a.page, D) + (n >> 3) * (D / 4) + (g * (D / 4) / 32) * 8 + (n & 7);
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(id.id[hf], i - id.first);
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(pool + (uint64_t)page * ((uint32_t)a.unit * (uint32_t)a.kv_heads)), 0, a.unit, 0x00020000);
+      const int tb = (base + 16 * hf) & (a.page - 1);
+      if constexpr (D == 64) {
+        const u32x2 k = __builtin_amdgcn_raw_buffer_load_b64(r, at_k, tb * (D / 2), 0);
+        t.k[hf][0] = k[0];
+        t.k[hf][1] = k[1];
+      } else {
+#pragma unroll
+        for (int x = 0; x < D / 128; ++x) {
+          const u32x4 k = __builtin_amdgcn_raw_buffer_load_b128(r, at_k + 16 * x, tb * (D / 2), 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t.k[hf][4 * x + j] = k[j];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < KB; ++x)
+        t.ks[hf][x] = __builtin_amdgcn_raw_buffer_load_b8(r, at_s + 8 * x, tb * (D / 32), 0);
+    }
+  }
+
+  // Entry i of a lane's 8 tokens, relative to the tile.
+  static __device__ __forceinline__ int token(int g, int i) { return 16 * (i >> 2) + 4 * g + (i & 3); }
+
+  // A tile's scores, -inf where a row does not see the token.  Tokens of a block stored as
+  // NaN get `odd`: NaN for the sums, whose row then adds nothing, -inf for the weights.
+  static __device__ __forceinline__ void scores(const WeightArgs& a, const KTile<D>& t, const bf16x8* q,
+                                                f32x4 (&s)[2][MT], int base, bool masked,
+                                                const int (&pos)[MT], float odd) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    int ql = lane;
+    asm volatile("" : "+v"(ql));              // (or the reads move out of the loop, into registers)
+    float sc[2][KB];
+    bool nan = false;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int x = 0; x < KB; ++x) {
+        sc[hf][x] = __builtin_bit_cast(float, t.ks[hf][x] << 23);
+        nan |= t.ks[hf][x] == 255u;
+      }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[hf][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) {
+      bf16x8 qt[MT][NT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int u = 0; u < NT; ++u) qt[mt][u] = q[((mt * STEPS + st) * NT + u) * 64 + ql];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t x = t.k[hf][st];
+        const float f = sc[hf][st / 4];
+        u32x4 kb;
+        kb[0] = widen<0>(x, f);
+        kb[1] = widen<1>(x, f);
+        kb[2] = widen<2>(x, f);
+        kb[3] = widen<3>(x, f);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int u = NT - 1; u >= 0; --u)
+            s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kb), qt[mt][u],
+                                                                s[hf][mt], 0, 0, 0);
+      }
+    }
+    if (__any(nan)) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        bool o = false;
+#pragma unroll
+        for (int x = 0; x < KB; ++x) o |= t.ks[hf][x] == 255u;
+        uint64_t m = __ballot(o);             // bit 16 g + n: token n
+        m |= m >> 32;
+        m |= m >> 16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (m >> (4 * g + r) & 1)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) s[hf][mt][r] = odd;
+      }
+    }
+    if (masked) {
+      asm volatile("");                       // (a branch: most tiles need no mask)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int tok = base + token(g, i);
+          const bool inside = (a.window == 0) | (tok > pos[mt] - a.window) | (tok < a.sinks);
+          if (!(inside & (tok <= pos[mt]))) s[i >> 2][mt][i & 3] = -INFINITY;
+        }
+    }
+  }
+};
+
+// Sum over the 16 lanes of a row of lanes; every lane gets it.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum16(float x) {
+  x += dpp<0xb1>(x);                          // lane ^ 1
+  x += dpp<0x4e>(x);                          // lane ^ 2
+  x += dpp<0x141>(x);                         // the mirror of 8 lanes
+  return x + dpp<0x140>(x);                   // the mirror of 16
+}
+
+// PASS 1: statistics, 2: weights, 3: both (a request is one chunk).
+template <int D, int MT, int PASS, typename T>
+__global__ __launch_bounds__(64 * WAVES, 2) void k_weights(WeightArgs a) {
+  using A = Weights<D, MT, T>;
+  __shared__ bf16x8 q[A::Q_WORDS];
+  __shared__ float acc[PASS & 2 ? SUB * TILE : 1];
+  __shared__ float part_m[WAVES][MT][16], part_l[WAVES][MT][16];
+  __shared__ float row_m[MT * 16], row_inv[MT * 16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int status_blocks = PASS & 1 ? (a.batch + WAVES - 1) / WAVES : 0;
+  if ((int)blockIdx.x < status_blocks) {      // a request's status, a wave each
+    const int b = (int)blockIdx.x * WAVES + wave;
+    if (b >= a.batch) return;
+    const Request rq = request_of(a, b);
+    int st = rq.status;
+    if (st == SV_ROW_OK) {
+      const Span sp = span_of(a, rq);
+      const int32_t* tab = a.table + (int64_t)b * a.ld_table;
+      bool bad = false;
+      for (int s = lane; s <= (sp.n - 1) >> a.page_log2; s += 64) {
+        const int t0 = s << a.page_log2, t1 = t0 + a.page;
+        const bool need = t1 > sp.first || (a.window > 0 && t0 < a.sinks);
+        if (need) bad |= s >= a.ld_table || (uint32_t)tab[s] >= (uint64_t)a.num_pages;
+      }
+      if (__any(bad)) st = SV_ROW_BAD_PAGE;
+    }
+    if (lane == 0) a.status[b] = st;
+    return;
+  }
+  int it = (int)blockIdx.x - status_blocks;
+  const int items = a.batch * a.kv_heads * a.chunks;
+  if (it >= items) {                          // positions that no row sees keep what they have
+    it -= items;
+    const int part = it % a.gap_blocks, bh = it / a.gap_blocks, b = bh / a.kv_heads;
+    const Request rq = request_of(a, b);
+    if (rq.status != SV_ROW_OK || (PASS == 2 && a.status[b] != SV_ROW_OK)) return;
+    const Span sp = span_of(a, rq);
+    const int64_t row = (int64_t)bh * a.ld_w;
+    for (int i = part * 256 + threadIdx.x; i < sp.tile0 * TILE; i += a.gap_blocks * 256)
+      if (i >= sp.early * TILE) a.out[row + i] = a.in ? a.in[row + i] : 0.f;
+    return;
+  }
+  const int h = it % a.kv_heads;
+  it /= a.kv_heads;
+  const int b = it % a.batch, chunk = a.chunks - 1 - it / a.batch;
+  const Request rq = request_of(a, b);
+  if (rq.status != SV_ROW_OK || (PASS == 2 && a.status[b] != SV_ROW_OK)) return;
+  const Span sp = span_of(a, rq);
+  const int used = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+  const int begin = chunk * a.chunk_tiles, end = min(sp.tiles, begin + a.chunk_tiles);
+  if (begin >= end) return;
+  const int R = rq.count * a.group, blocks = (R + MT * 16 - 1) / (MT * 16);
+  const float c = a.scale * LOG2E;
+  const int32_t* tab = a.table + (int64_t)b * a.ld_table;
+  const uint8_t* pool = a.pages + (int64_t)h * a.unit;
+  float* const stats = a.stats + (((int64_t)b * a.kv_heads + h) * a.chunks) * a.max_rows * 2;
+  bool bad = false;
+  typename A::Pages id;
+  KTile<D> t[2];
+  int pos[MT];
+  int loaded = -1;                            // row block whose queries lie in LDS
+  auto queries = [&](int rb) {
+    if (loaded == rb) return;
+    __syncthreads();                          // (every wave is done with those before)
+    A::put_q(a, q, rq, h, rb * MT * 16, R, wave);
+    __syncthreads();
+    loaded = rb;
+  };
+  auto positions = [&](int rb) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) pos[mt] = rq.ctx + min(rb * MT * 16 + mt * 16 + n, R - 1) / a.group;
+  };
+  auto masked = [&](int base) {
+    return base + TILE - 1 > rq.ctx ||
+           (a.window > 0 && base <= rq.ctx + rq.rows - 1 - a.window && base + TILE > a.sinks);
+  };
+  // the wave's tiles of the 64 from `from` on; two are on their way at any time
+  auto each_tile = [&](int from, float odd, auto&& use) {
+    const int stop = min(from + SUB, end);
+    bad |= id.ask(a, sp, tab, from, stop);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) A::fetch(a, t[k], pool, id, sp, min(from + wave + k * WAVES, stop - 1));
+    for (int i = from + wave; i < stop; i += 2 * WAVES) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int at = i + k * WAVES;
+        if (at < stop) {
+          f32x4 s[2][MT];
+          const int base = base_of(sp, at);
+          A::scores(a, t[k], q, s, base, masked(base), pos, odd);
+          use(s, at - from);
+        }
+        A::fetch(a, t[k], pool, id, sp, min(at + 2 * WAVES, stop - 1));
+      }
+    }
+  };
+  auto statistics = [&](int rb) {
+    float m[MT], mc[MT], l[MT];
+    queries(rb);
+    positions(rb);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt] = -INFINITY;
+      mc[mt] = -FAR;
+      l[mt] = 0.f;
+    }
+    for (int from = begin; from < end; from += SUB)
+      each_tile(from, __builtin_nanf(""), [&](f32x4 (&s)[2][MT], int) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float mx = m[mt];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx = fmaxf(mx, s[i >> 2][mt][i & 3]);
+          if (__any(mx > m[mt])) {            // (per lane: its tokens of the row)
+            const float nc = __builtin_amdgcn_fmed3f(mx * c, -FAR, FAR);
+            l[mt] *= __builtin_amdgcn_exp2f(mc[mt] - nc);
+            m[mt] = mx;
+            mc[mt] = nc;
+          }
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc[mt]));
+          l[mt] += sum;
+        }
+      });
+    // join the row's four lanes, then the waves
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int d = 16; d < 64; d <<= 1) {
+        const float om = __shfl_xor(mc[mt], d), ol = __shfl_xor(l[mt], d);
+        const float nm = fmaxf(mc[mt], om);
+        l[mt] = l[mt] * (mc[mt] == nm ? 1.f : __builtin_amdgcn_exp2f(mc[mt] - nm)) +
+                ol * (om == nm ? 1.f : __builtin_amdgcn_exp2f(om - nm));
+        mc[mt] = nm;
+      }
+      if (g == 0) {
+        part_m[wave][mt][n] = mc[mt];
+        part_l[wave][mt][n] = l[mt];
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < MT * 16) {
+      const int mt = threadIdx.x >> 4, x = threadIdx.x & 15;
+      float nm = part_m[0][mt][x], sum = 0.f;
+#pragma unroll
+      for (int k = 1; k < WAVES; ++k) nm = fmaxf(nm, part_m[k][mt][x]);
+#pragma unroll
+      for (int k = 0; k < WAVES; ++k) {
+        const float om = part_m[k][mt][x];
+        sum += part_l[k][mt][x] * (om == nm ? 1.f : __builtin_amdgcn_exp2f(om - nm));
+      }
+      if constexpr (PASS == 3) {
+        row_m[threadIdx.x] = nm;
+        row_inv[threadIdx.x] = sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f;
+      }
+      const int r = rb * MT * 16 + threadIdx.x;
+      // (with several row blocks the second pass finds them in memory again)
+      if ((PASS == 1 || blocks > 1) && r < R) {
+        float* to = stats + ((int64_t)chunk * a.max_rows + r) * 2;
+        to[0] = nm;
+        to[1] = sum;
+      }
+    }
+    __syncthreads();
+  };
+  if constexpr (PASS & 1)
+    for (int rb = 0; rb < blocks; ++rb) statistics(rb);
+  if constexpr (PASS == 3) {                  // a page id out of range: the request is left alone
+    if (blocks == 0) bad |= id.ask(a, sp, tab, begin, min(begin + SUB, end));
+    if (threadIdx.x == 0) part_m[0][0][0] = 0.f;
+    __syncthreads();
+    if (bad && lane == 0) part_m[0][0][0] = 1.f;
+    __syncthreads();
+    if (part_m[0][0][0] != 0.f) return;
+    __threadfence_block();
+  }
+  if constexpr (PASS & 2) {
+    for (int from = begin; from < end; from += SUB) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < SUB * TILE; i += 64 * WAVES) acc[i] = 0.f;
+      __syncthreads();
+      for (int rb = 0; rb < blocks; ++rb) {
+        queries(rb);
+        positions(rb);
+        if (PASS == 2 || blocks > 1) {
+          __syncthreads();
+          if (threadIdx.x < MT * 16) {        // the rows' maxima and sums over all chunks
+            const int r = min(rb * MT * 16 + (int)threadIdx.x, R - 1);
+            float nm = -INFINITY, sum = 0.f;
+            for (int k = 0; k < used; ++k) nm = fmaxf(nm, stats[((int64_t)k * a.max_rows + r) * 2]);
+            for (int k = 0; k < used; ++k) {
+              const float om = stats[((int64_t)k * a.max_rows + r) * 2];
+              sum += stats[((int64_t)k * a.max_rows + r) * 2 + 1] *
+                     (om == nm ? 1.f : __builtin_amdgcn_exp2f(om - nm));
+            }
+            row_m[threadIdx.x] = nm;
+            row_inv[threadIdx.x] = sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f;
+          }
+          __syncthreads();
+        }
+        float mc[MT], inv[MT];
+        bool none = false;                    // rows that add nothing
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mc[mt] = row_m[mt * 16 + n];
+          // (lanes past the last row repeat it)
+          inv[mt] = rb * MT * 16 + mt * 16 + n < R ? row_inv[mt * 16 + n] : 0.f;
+          none |= row_inv[mt * 16 + n] == 0.f;
+        }
+        none = __any(none);
+        each_tile(from, -INFINITY, [&](f32x4 (&s)[2][MT], int at) {
+          if (none) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (inv[mt] == 0.f) s[i >> 2][mt][i & 3] = -INFINITY;
+          }
+          float w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            w[i] = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              w[i] = __builtin_fmaf(
+                  __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc[mt])), inv[mt], w[i]);
+            w[i] = sum16(w[i]);
+          }
+          if (n < 8) {                        // lane n of the row writes entry n
+            float y = w[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) y = n == i ? w[i] : y;
+            acc[at * TILE + A::token(g, n)] += y;
+          }
+        });
+      }
+      __syncthreads();
+      const int64_t row = ((int64_t)b * a.kv_heads + h) * a.ld_w;
+      for (int i = threadIdx.x; i < min(SUB, end - from) * TILE; i += 64 * WAVES) {
+        const int tok = base_of(sp, from + i / TILE) + i % TILE;
+        if (tok >= sp.n) continue;
+        const float before = a.in && tok < rq.ctx ? a.in[row + tok] : 0.f;
+        a.out[row + tok] = before + acc[i];
+      }
+    }
+  }
+}
+
+struct Plan {
+  int mt, chunks, chunk_tiles, max_rows;
+  size_t bytes;
+};
+
+static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, int d, int max_context,
+                    int window, int sinks, Plan& p) {
+  const int64_t R = (int64_t)(max_k + 1) * (heads / kv_heads);
+  p.mt = R <= 16 ? 1 : 2;
+  p.max_rows = (int)R;
+  int64_t tokens = max_context;
+  if (window > 0) {
+    const int64_t seen = (int64_t)window + max_k + 1 + sinks + 3 * TILE;
+    if (seen < tokens) tokens = seen;
+  }
+  const int64_t tiles = (tokens + TILE - 1) / TILE, wide = (int64_t)batch * kv_heads;
+  int64_t ct = SUB;
+  while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 512) ct /= 2;
+  // the statistics of a call take at most 256 MiB, or 8 chunks per request
+  while ((tiles + ct - 1) / ct > 8 && wide * ((tiles + ct - 1) / ct) * R * 8 > (256ll << 20)) ct *= 2;
+  p.chunks = (int)((tiles + ct - 1) / ct);
+  p.chunk_tiles = (int)ct;
+  if (wide * p.chunks >= (1ll << 23)) return false;
+  p.bytes = (size_t)(wide * p.chunks * R) * 2 * sizeof(float) + 16;
+  return true;
+}
+
+static bool sizes_ok(int dtype, int batch, int max_k, int heads, int kv_heads, int d, int max_context,
+                     int window, int sinks) {
+  return (dtype == SV_F32 || dtype == SV_BF16) && batch >= 1 && batch <= MAX_BATCH && max_k >= 0 &&
+         max_k <= 63 && kv_heads >= 1 && heads >= kv_heads && heads % kv_heads == 0 && heads <= 1024 &&
+         dim_ok(d) && max_context >= 1 && max_context <= (1 << 30) && window >= 0 &&
+         window <= (1 << 30) && sinks >= 0 && sinks <= (1 << 30);
+}
+
+template <int D, int MT, typename T>
+static int launch(WeightArgs a, const Plan& p, hipStream_t s) {
+  const int items = a.batch * a.kv_heads * p.chunks, statuses = (a.batch + WAVES - 1) / WAVES;
+  const int gaps = a.gap_blocks * a.batch * a.kv_heads;
+  if (p.chunks == 1) {
+    hipLaunchKernelGGL((k_weights<D, MT, 3, T>), dim3(statuses + items + gaps), dim3(64 * WAVES), 0, s, a);
+    return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
+  }
+  hipLaunchKernelGGL((k_weights<D, MT, 1, T>), dim3(statuses + items), dim3(64 * WAVES), 0, s, a);
+  if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
+  hipLaunchKernelGGL((k_weights<D, MT, 2, T>), dim3(items + gaps), dim3(64 * WAVES), 0, s, a);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
+}
+
+// -------------------------------------------------------------------- evict
+//
+// Per layer, request and KV head a workgroup finds the weight of the last position that
+// stays (a radix select over order-preserving keys), then moves what stays forward, in
+// order and in place: position p goes to slot i <= p, so that with positions taken in
+// order, and read before they are written, no write reaches what is still to be read.
+// A second launch sets tables, counts and lengths, once all of them are done.
+
+struct EvictArgs {
+  const int32_t* budgets;
+  int batch, sinks, recent;
+  float* weights;
+  int64_t ld_w;
+  int kv_heads, page, page_log2, unit;
+  int32_t* seq_lens;
+  int32_t* table;
+  int64_t ld_table;
+  int32_t* refs;
+  int64_t num_pages;
+  uint8_t* pages;
+  int64_t layer_bytes;
+  int32_t* evicted;
+  int32_t* status;
+};
+
+// Larger weights have larger keys, NaN the smallest; 0 and -0 are the same.
+__device__ __forceinline__ uint32_t key_of(float w) {
+  if (w != w) return 0;
+  const uint32_t u = __builtin_bit_cast(uint32_t, w + 0.f);
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+
+// A request's SV_ROW_*; n > m > 0 only where something is to be done.  All threads of the
+// workgroup take part.
+__device__ __forceinline__ int evict_status(const EvictArgs& a, int b, int& n, int& m) {
+  n = a.seq_lens[b];
+  m = a.budgets[b];
+  if (n < 0 || n > a.ld_w || ((int64_t)n + a.page - 1) >> a.page_log2 > a.ld_table) {
+    m = n = 0;
+    return SV_ROW_BAD_PARAM;
+  }
+  if (m <= 0 || n <= m) {
+    m = n = 0;
+    return SV_ROW_OK;
+  }
+  if ((int64_t)a.sinks + a.recent > m) {
+    m = n = 0;
+    return SV_ROW_BAD_PARAM;
+  }
+  const int32_t* tab = a.table + (int64_t)b * a.ld_table;
+  const int held = (n + a.page - 1) >> a.page_log2, kept = (m + a.page - 1) >> a.page_log2;
+  bool bad = false;                           // outside the pool, or written and not its own
+  for (int s = threadIdx.x; s < held; s += blockDim.x) {
+    const uint32_t id = (uint32_t)tab[s];
+    if (id >= (uint64_t)a.num_pages) bad = true;
+    else if (s < kept && a.refs[id] != 1) bad = true;
+  }
+  if (!__syncthreads_or(bad)) return SV_ROW_OK;
+  m = n = 0;
+  return SV_ROW_BAD_PAGE;
+}
+
+constexpr int THREADS = 1024;
+
+// A token's V codes of a 16th of the dims.
+template <int D> struct Piece { typedef uint32_t T; };
+template <> struct Piece<64> { typedef uint16_t T; };
+template <> struct Piece<256> { typedef u32x2 T; };
+
+template <int D>
+__global__ __launch_bounds__(THREADS) void k_evict(EvictArgs a) {
+  constexpr int BINS = 2048;
+  __shared__ int hist[BINS];
+  __shared__ int wsum[THREADS / 64], picked[2], wgt[THREADS / 64], weq[THREADS / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int h = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads % a.batch;
+  const int layer = blockIdx.x / a.kv_heads / a.batch;
+  int n, m;
+  const int st = evict_status(a, b, n, m);
+  if (layer == 0 && h == 0 && tid == 0) a.status[b] = st;
+  if (m == 0) return;
+  float* const w = a.weights + (int64_t)blockIdx.x * a.ld_w;
+  const int lo = a.sinks, hi = n - a.recent;  // positions that are chosen among
+  int need = m - a.sinks - a.recent;          // how many of them stay
+  uint32_t at = 0;                            // the key of the last that does
+  if (need > 0) {
+    int left = need;
+    uint32_t mask = 0;
+    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
+      const int bits = shift == 0 ? 10 : 11;
+      for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
+      __syncthreads();
+      for (int p = lo + tid; p < hi; p += THREADS) {
+        const uint32_t k = key_of(w[p]);
+        if ((k & mask) == at) atomicAdd(&hist[k >> shift & ((1 << bits) - 1)], 1);
+      }
+      __syncthreads();
+      // digits from the top: thread t takes the bins BINS-1-2t and BINS-2-2t
+      const int d1 = BINS - 1 - 2 * tid, c1 = hist[d1], c0 = hist[d1 - 1];
+      int sum = c1 + c0;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(sum, d);
+        if (lane >= d) sum += y;
+      }
+      if (lane == 63) wsum[wave] = sum;
+      __syncthreads();
+      for (int k = 0; k < wave; ++k) sum += wsum[k];
+      const int before = sum - c1 - c0;       // in larger digits
+      if (before < left && left <= before + c1) {
+        picked[0] = d1;
+        picked[1] = before;
+      } else if (before + c1 < left && left <= sum) {
+        picked[0] = d1 - 1;
+        picked[1] = before + c1;
+      }
+      __syncthreads();
+      at |= (uint32_t)picked[0] << shift;
+      mask |= ((1u << bits) - 1) << shift;
+      left -= picked[1];
+      __syncthreads();
+    }
+    need = left;                              // of those with just this key, the first so many
+  } else {
+    at = 0xffffffffu;                         // (no weight has this key)
+  }
+  const bool none = m - a.sinks - a.recent <= 0;
+
+  // move, 1,024 positions at a time
+  const int32_t* tab = a.table + (int64_t)b * a.ld_table;
+  uint8_t* const pool = a.pages + layer * a.layer_bytes;
+  const int64_t page_bytes = (int64_t)a.unit * a.kv_heads;
+  const int P = a.page;
+  int kept = 0, same = 0;                     // so far: kept, and with the last key
+  for (int p0 = 0; p0 < n; p0 += THREADS) {
+    const int p = p0 + tid;
+    const float x = p < n ? w[p] : 0.f;
+    const bool choice = p >= lo && p < hi && !none;
+    const uint32_t k = choice ? key_of(x) : 0;
+    const bool sure = p < n && (p < lo || p >= hi || (choice && k > at));
+    const bool tie = choice && k == at;
+    const uint64_t bs = __ballot(sure), bt = __ballot(tie);
+    if (lane == 0) {
+      wgt[wave] = __popcll(bs);
+      weq[wave] = __popcll(bt);
+    }
+    __syncthreads();
+    int before = kept, ties = same, all = kept, all_ties = same;
+    for (int v = 0; v < THREADS / 64; ++v) {
+      // (of the ties only the first `need` stay)
+      const int stay = wgt[v] + max(0, min(need - all_ties, weq[v]));
+      if (v < wave) {
+        before += stay;
+        ties += weq[v];
+      }
+      all += stay;
+      all_ties += weq[v];
+    }
+    const uint64_t below = (1ull << lane) - 1;
+    const int my_tie = ties + __popcll(bt & below);
+    const bool keep = sure || (tie && my_tie < need);
+    const int to = before + __popcll(bs & below) + max(0, min(need - ties, __popcll(bt & below)));
+    const bool move = keep && to != p;
+    kept = all;
+    same = all_ties;
+    // a position's codes and scales: K in one piece, V in 16
+    u32x4 kc[D / 32];
+    typename Piece<D>::T vc[16];
+    uint8_t ks[D / 32], vs[D / 32];
+    const int t0 = p & (P - 1), t1 = to & (P - 1);
+    if (move) {
+      const uint8_t* u = pool + (int64_t)tab[p >> a.page_log2] * page_bytes + (int64_t)h * a.unit;
+      const uint8_t* v = u + off_v(P, D) + (t0 >> 3) * (4 * D) + (t0 & 7) * (D / 32);
+      const uint8_t* e = u + off_ks(P, D) + (t0 >> 3) * (D / 4) + (t0 & 7);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) kc[i] = *(const u32x4*)(u + t0 * (D / 2) + 16 * i);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) vc[i] = *(const typename Piece<D>::T*)(v + i * (D / 4));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        ks[i] = e[i * 8];
+        vs[i] = e[P * (D / 32) + i * 8];
+      }
+    }
+    __syncthreads();                          // (all are read before one is written)
+    if (move) {
+      uint8_t* u = pool + (int64_t)tab[to >> a.page_log2] * page_bytes + (int64_t)h * a.unit;
+      uint8_t* v = u + off_v(P, D) + (t1 >> 3) * (4 * D) + (t1 & 7) * (D / 32);
+      uint8_t* e = u + off_ks(P, D) + (t1 >> 3) * (D / 4) + (t1 & 7);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) *(u32x4*)(u + t1 * (D / 2) + 16 * i) = kc[i];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) *(typename Piece<D>::T*)(v + i * (D / 4)) = vc[i];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        e[i * 8] = ks[i];
+        e[P * (D / 32) + i * 8] = vs[i];
+      }
+      w[to] = x;
+    }
+  }
+  __syncthreads();
+  for (int p = m + tid; p < n; p += THREADS) w[p] = 0.f;
+}
+
+// Tables, counts and lengths of the requests that k_evict cut: a workgroup each.
+__global__ __launch_bounds__(256) void k_evict_tables(EvictArgs a) {
+  const int b = blockIdx.x;
+  const int n = a.seq_lens[b], m = a.budgets[b];
+  if (a.status[b] != SV_ROW_OK || m <= 0 || n <= m) return;
+  int32_t* const tab = a.table + (int64_t)b * a.ld_table;
+  const int held = (n + a.page - 1) >> a.page_log2, kept = (m + a.page - 1) >> a.page_log2;
+  for (int s = kept + threadIdx.x; s < held; s += 256) {
+    atomicAdd(&a.refs[tab[s]], -1);
+    tab[s] = -1;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.seq_lens[b] = m;
+    if (a.evicted) a.evicted[b] += n - m;
+  }
+}
+
+}  // namespace budget
+}  // namespace svk
+
+using namespace svk;
+
+extern "C" {
+
+size_t spec_kv_weights_workspace_bytes(int dtype, int batch, int max_k, int heads, int kv_heads,
+                                       int head_dim, int max_context, int window, int sinks) {
+  budget::Plan p;
+  if (!budget::sizes_ok(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks) ||
+      !budget::plan_of(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks, p))
+    return 0;
+  return p.bytes;
+}
+
+int spec_kv_attention_weights(const void* q, int64_t ld_q, int dtype, const int32_t* cu_seqlens,
+                              const int32_t* context_lens, const int32_t* row_counts, int batch,
+                              int total_rows, int max_k, int heads, int kv_heads, int head_dim,
+                              const void* pages, int64_t num_pages, int page_size,
+                              const int32_t* page_table, int64_t ld_table, int max_context,
+                              float scale, int window, int sinks, const float* weights_in,
+                              float* weights_out, int64_t ld_weights, int32_t* status,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !cu_seqlens || !context_lens || !pages || !page_table || !weights_out || !status)
+    return SV_ERR_NULL;
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  budget::Plan p;
+  if (!budget::sizes_ok(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks) ||
+      total_rows < 1 || !page_ok(page_size) || num_pages < 1 || num_pages > 0x7fffffff ||
+      ld_table < 1 || ld_table > (1 << 30) / page_size || ld_q < (int64_t)heads * head_dim ||
+      ld_weights < max_context || !(scale > 0.f) || !(scale <= 2.0e38f) || !aligned16(pages) ||
+      !budget::plan_of(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks, p))
+    return SV_ERR_SHAPE;
+  if (!workspace || !aligned16(workspace)) return SV_ERR_NULL;
+  if (p.bytes > workspace_bytes) return SV_ERR_WORKSPACE;
+  budget::WeightArgs a;
+  a.q = q;
+  a.ld_q = ld_q;
+  a.cu = cu_seqlens;
+  a.ctx = context_lens;
+  a.counts = row_counts;
+  a.batch = batch;
+  a.total_rows = total_rows;
+  a.max_k = max_k;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.group = heads / kv_heads;
+  a.pages = (const uint8_t*)pages;
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.page_log2 = __builtin_ctz((unsigned)page_size);
+  a.unit = (int)unit_bytes(page_size, head_dim);
+  a.table = page_table;
+  a.ld_table = ld_table;
+  a.max_context = max_context;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.in = weights_in;
+  a.out = weights_out;
+  a.ld_w = ld_weights;
+  a.status = status;
+  a.chunks = p.chunks;
+  a.chunk_tiles = p.chunk_tiles;
+  a.max_rows = p.max_rows;
+  a.stats = (float*)workspace;
+  a.gap_blocks = 0;
+  if (window > 0 && weights_in != weights_out) {
+    const int64_t more = (max_context + 8191) / 8192, most = (1 << 22) / (batch * kv_heads);
+    a.gap_blocks = (int)(more < most ? more : most);
+    if (a.gap_blocks < 1) a.gap_blocks = 1;
+  }
+  hipStream_t s = (hipStream_t)stream;
+#define SVK_CASE(DD, TT)                                                       \
+  if (head_dim == DD)                                                          \
+  return p.mt == 1 ? budget::launch<DD, 1, TT>(a, p, s) : budget::launch<DD, 2, TT>(a, p, s)
+  if (dtype == SV_BF16) {
+    SVK_CASE(64, __bf16);
+    SVK_CASE(128, __bf16);
+    SVK_CASE(256, __bf16);
+  } else {
+    SVK_CASE(64, float);
+    SVK_CASE(128, float);
+    SVK_CASE(256, float);
+  }
+#undef SVK_CASE
+  return SV_ERR_SHAPE;
+}
+
+int spec_kv_evict(const int32_t* budgets, int batch, int sinks, int recent, float* weights,
+                  int64_t ld_weights, int kv_heads, int head_dim, int page_size, int32_t* seq_lens,
+                  int32_t* page_table, int64_t ld_table, int32_t* ref_counts, int64_t num_pages,
+                  void* pages, int layers, int64_t layer_bytes, int32_t* evicted, int32_t* status,
+                  void* stream) {
+  if (!budgets || !weights || !seq_lens || !page_table || !ref_counts || !pages || !status)
+    return SV_ERR_NULL;
+  if (batch < 1 || batch > MAX_BATCH || sinks < 0 || sinks > (1 << 30) || recent < 0 ||
+      recent > (1 << 30) || ld_weights < 1 || kv_heads < 1 || kv_heads > 1024 || !dim_ok(head_dim) ||
+      !page_ok(page_size) || ld_table < 1 || ld_table > (1 << 30) / page_size || num_pages < 1 ||
+      num_pages > (1 << 24) || !aligned16(pages) || layers < 1 || layers > 65535 ||
+      layer_bytes % 16 != 0 || (int64_t)layers * batch * kv_heads >= (1 << 22) ||
+      (layers > 1 && layer_bytes < num_pages * kv_heads * unit_bytes(page_size, head_dim)))
+    return SV_ERR_SHAPE;
+  budget::EvictArgs a;
+  a.budgets = budgets;
+  a.batch = batch;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.weights = weights;
+  a.ld_w = ld_weights;
+  a.kv_heads = kv_heads;
+  a.page = page_size;
+  a.page_log2 = __builtin_ctz((unsigned)page_size);
+  a.unit = (int)unit_bytes(page_size, head_dim);
+  a.seq_lens = seq_lens;
+  a.table = page_table;
+  a.ld_table = ld_table;
+  a.refs = ref_counts;
+  a.num_pages = num_pages;
+  a.pages = (uint8_t*)pages;
+  a.layer_bytes = layer_bytes;
+  a.evicted = evicted;
+  a.status = status;
+  hipStream_t s = (hipStream_t)stream;
+  const dim3 grid((uint32_t)(layers * batch * kv_heads));
+  if (head_dim == 64)
+    hipLaunchKernelGGL((budget::k_evict<64>), grid, dim3(budget::THREADS), 0, s, a);
+  else if (head_dim == 128)
+    hipLaunchKernelGGL((budget::k_evict<128>), grid, dim3(budget::THREADS), 0, s, a);
+  else
+    hipLaunchKernelGGL((budget::k_evict<256>), grid, dim3(budget::THREADS), 0, s, a);
+  if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
+  hipLaunchKernelGGL(budget::k_evict_tables, dim3(batch), dim3(256), 0, s, a);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
+}
+
+}  // extern "C"

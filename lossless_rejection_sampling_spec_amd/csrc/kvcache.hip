@@ -33,6 +33,7 @@ struct AppendArgs {
   const float* cos_sin;
   int max_position, rot, interleaved;
   const int32_t *cu, *ctx;
+  const int32_t* offsets;       // added to a request's positions in the angles' table, or NULL
   int batch, total_rows, heads, kv_heads;
   uint8_t* pages;
   int64_t num_pages;
@@ -139,9 +140,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : D == 256 ? 2 : 3) void k_
     if (b >= a.batch) return;
     int st = SV_ROW_BAD_K;
     if (b < broken && a.cu[b + 1] > a.cu[b]) {
-      const int rows = a.cu[b + 1] - a.cu[b], ctx = a.ctx[b];
+      const int rows = a.cu[b + 1] - a.cu[b], ctx = a.ctx[b], off = a.offsets ? a.offsets[b] : 0;
       st = SV_ROW_OK;
-      if (ctx < 0 || (int64_t)ctx + rows > a.max_position) st = SV_ROW_BAD_PARAM;
+      if (ctx < 0 || off < 0 || (int64_t)ctx + off + rows > a.max_position) st = SV_ROW_BAD_PARAM;
       else {
         bool bad = false;
         const int s1 = (ctx + rows - 1) >> a.page_log2;
@@ -192,14 +193,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : D == 256 ? 2 : 3) void k_
     const int b = lo, row0 = __builtin_amdgcn_readfirstlane(scu[b]);
     const int ctx = __builtin_amdgcn_readfirstlane(sctx[b]);
     const int64_t pos = (int64_t)ctx + (row - row0);
-    if (row < row0 || ctx < 0 || pos >= a.max_position) continue;
+    const int off = a.offsets ? a.offsets[b] : 0;
+    if (row < row0 || ctx < 0 || off < 0 || pos + off >= a.max_position) continue;
     // requested ahead of their use: the page and the angles
     const int64_t slot = pos >> a.page_log2;
     const uint32_t id = slot < a.ld_table ? (uint32_t)a.table[(int64_t)b * a.ld_table + slot]
                                           : 0xffffffffu;
     f32x4 co[2] = {}, si[2] = {};             // pairs of the lane's dims: 8, or 4 interleaved
     if (a.rot) {
-      const float* cs = a.cos_sin + pos * a.rot;
+      const float* cs = a.cos_sin + (pos + off) * a.rot;
       const int at = !in_rot ? 0 : a.interleaved ? 4 * c : 8 * c - (second ? half : 0);
       const int more = a.interleaved ? 0 : 4;
       co[0] = load_any<f32x4>(cs + at);
@@ -950,14 +952,14 @@ size_t spec_kv_page_bytes(int kv_heads, int head_dim, int page_size) {
   return (size_t)(kv_heads * unit_bytes(page_size, head_dim));
 }
 
-int spec_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
-                   int64_t ld_v, int dtype, const float* q_weight, const float* k_weight, float eps,
-                   const float* cos_sin, int max_position, int rot_dim, int interleaved,
-                   const int32_t* cu_seqlens, const int32_t* context_lens, int batch,
-                   int total_rows, int heads, int kv_heads, int head_dim, void* pages,
-                   int64_t num_pages, int page_size, const int32_t* page_table, int64_t ld_table,
-                   void* q_out, int64_t ld_qout, void* k_values, void* v_values, int32_t* status,
-                   void* stream) {
+int spec_kv_append_at(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                      int64_t ld_v, int dtype, const float* q_weight, const float* k_weight, float eps,
+                      const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                      const int32_t* cu_seqlens, const int32_t* context_lens,
+                      const int32_t* position_offsets, int batch, int total_rows, int heads, int kv_heads, int head_dim, void* pages,
+                      int64_t num_pages, int page_size, const int32_t* page_table, int64_t ld_table,
+                      void* q_out, int64_t ld_qout, void* k_values, void* v_values, int32_t* status,
+                      void* stream) {
   if (!q || !k || !v || !cu_seqlens || !context_lens || !pages || !page_table || !q_out || !status ||
       (rot_dim != 0 && !cos_sin) || (!k_values) != (!v_values))
     return SV_ERR_NULL;
@@ -986,6 +988,7 @@ int spec_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, con
   a.interleaved = interleaved;
   a.cu = cu_seqlens;
   a.ctx = context_lens;
+  a.offsets = position_offsets;
   a.batch = batch;
   a.total_rows = total_rows;
   a.heads = heads;
@@ -1010,6 +1013,21 @@ int spec_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, con
   return head_dim == 64    ? launch_append<64, float>(a, s)
          : head_dim == 128 ? launch_append<128, float>(a, s)
                            : launch_append<256, float>(a, s);
+}
+
+int spec_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                   int64_t ld_v, int dtype, const float* q_weight, const float* k_weight, float eps,
+                   const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                   const int32_t* cu_seqlens, const int32_t* context_lens, int batch,
+                   int total_rows, int heads, int kv_heads, int head_dim, void* pages,
+                   int64_t num_pages, int page_size, const int32_t* page_table, int64_t ld_table,
+                   void* q_out, int64_t ld_qout, void* k_values, void* v_values, int32_t* status,
+                   void* stream) {
+  return spec_kv_append_at(q, ld_q, k, ld_k, v, ld_v, dtype, q_weight, k_weight, eps, cos_sin,
+                           max_position, rot_dim, interleaved, cu_seqlens, context_lens, nullptr,
+                           batch, total_rows, heads, kv_heads, head_dim, pages, num_pages,
+                           page_size, page_table, ld_table, q_out, ld_qout, k_values, v_values,
+                           status, stream);
 }
 
 size_t spec_kv_pages_workspace_bytes(int seqs, int64_t num_pages) {
