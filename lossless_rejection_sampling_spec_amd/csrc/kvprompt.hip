@@ -326,21 +326,24 @@ __global__ __launch_bounds__(256) void k_prompt_widen(Args a) {
 template <typename T>
 __device__ __forceinline__ float to_f32(T x) { return (float)x; }
 
-template <int D, int OD, int MT, typename T>
+template <int D, int OD, typename T>
 struct Prompt {
   static constexpr int STEPS = D / 16, DT = OD / 32;
+  static constexpr int K_WORDS = TILE * D * 2 / 16, V_WORDS = TILE * OD * 2 / 16,
+                       WORDS = K_WORDS + V_WORDS;        // a tile in LDS, in 16 bytes
   // fp32 queries and weights are split into three bf16 terms (3 x 8 bits hold fp32's 24)
   static constexpr int NT = sizeof(T) == 4 ? 3 : 1;
-
   // (of fp32 rows at D=256 the last term lies in LDS: all three do not fit the registers)
   static constexpr int NR = NT == 3 && D == 256 ? 2 : NT;
-  static constexpr int Q_LDS = MT * STEPS * (NT - NR) * 64;    // 16-byte words of a wave
+  static constexpr int Q_LDS = STEPS * (NT - NR) * 64;    // 16-byte words of a wave
+  // tiles weighed at a time, as many as the registers hold
+  static constexpr int PAIR = NT == 1 && D == 128 ? 2 : 1;
 
-  bf16x8 q[MT][STEPS][NR];
-  f32x16 o[MT][DT];
-  float l[MT], m[MT], mc[MT], over[MT];
-  int pos[MT];
-  uint32_t poison[MT];
+  bf16x8 q[STEPS][NR];
+  f32x16 o[DT];
+  float l, m, mc, over;
+  int pos;
+  uint32_t poison;
 
   static __device__ __forceinline__ void split(float x, __bf16* t) {
     float r = x;
@@ -353,142 +356,147 @@ struct Prompt {
   __device__ __forceinline__ void init(const Args& a, int row0, int ctx, int h, int64_t r0, int64_t R,
                                        u32x4* q_lds) {
     const int n = threadIdx.x & 31, g = threadIdx.x >> 5 & 1;
+    const uint32_t r = (uint32_t)min(r0 + n, R - 1);
+    const uint32_t j = r / (uint32_t)a.group, hq = h * a.group + r - j * a.group;
+    pos = ctx + (int)j;
+    const T* src = (const T*)a.q + ((int64_t)row0 + j) * a.ld_q + (int64_t)hq * D + 8 * g;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const uint32_t r = (uint32_t)min(r0 + mt * 32 + n, R - 1);
-      const uint32_t j = r / (uint32_t)a.group, hq = h * a.group + r - j * a.group;
-      pos[mt] = ctx + (int)j;
-      const T* src = (const T*)a.q + ((int64_t)row0 + j) * a.ld_q + (int64_t)hq * D + 8 * g;
+    for (int st = 0; st < STEPS; ++st) {
+      T x[8];
+      __builtin_memcpy(x, src + 16 * st, sizeof(x));
+      [[maybe_unused]] bf16x8 rest;
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        T x[8];
-        __builtin_memcpy(x, src + 16 * s, sizeof(x));
-        [[maybe_unused]] bf16x8 rest;
+      for (int k = 0; k < 8; ++k) {
+        __bf16 t[NT];
+        if constexpr (NT == 1) t[0] = x[k];
+        else split(to_f32<T>(x[k]), t);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          __bf16 t[NT];
-          if constexpr (NT == 1) t[0] = x[k];
-          else split(to_f32<T>(x[k]), t);
-#pragma unroll
-          for (int u = 0; u < NR; ++u) q[mt][s][u][k] = t[u];
-          if constexpr (NR < NT) rest[k] = t[NT - 1];
-        }
-        if constexpr (NR < NT)
-          q_lds[(mt * STEPS + s) * 64 + (threadIdx.x & 63)] = __builtin_bit_cast(u32x4, rest);
+        for (int u = 0; u < NR; ++u) q[st][u][k] = t[u];
+        if constexpr (NR < NT) rest[k] = t[NT - 1];
       }
-      l[mt] = 0.f;
-      m[mt] = over[mt] = -INFINITY;
-      mc[mt] = -FAR;
-      poison[mt] = 0;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[mt][dt][k] = 0.f;
+      if constexpr (NR < NT) q_lds[st * 64 + (threadIdx.x & 63)] = __builtin_bit_cast(u32x4, rest);
     }
+    l = 0.f;
+    m = over = -INFINITY;
+    mc = -FAR;
+    poison = 0;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) o[dt][k] = 0.f;
   }
-  __device__ __forceinline__ bool sees(const Args& a, int t, int mt) const {
-    const bool inside = (a.window == 0) | (t > pos[mt] - a.window) | (t < a.sinks);
-    return inside & (t <= pos[mt]);
+  __device__ __forceinline__ bool sees(const Args& a, int t) const {
+    const bool inside = (a.window == 0) | (t > pos - a.window) | (t < a.sinks);
+    return inside & (t <= pos);
   }
   // Token of accumulator entry r, relative to the tile.
   static __device__ __forceinline__ int token(int g, int r) { return 8 * (r >> 2) + 4 * g + (r & 3); }
 
-  __device__ __forceinline__ void tile(const Args& a, const u32x4* lds, const u32x4* q_lds, int base, bool masked, float c) {
-    const int lane = threadIdx.x & 63, g = lane >> 5;
-    f32x16 s[MT];
+  __device__ __forceinline__ f32x16 scores(const u32x4* lds, const u32x4* q_lds) const {
+    const int lane = threadIdx.x & 63;
+    f32x16 y;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) s[mt][k] = 0.f;
+    for (int k = 0; k < 16; ++k) y[k] = 0.f;
 #pragma unroll
     for (int st = 0; st < STEPS; ++st) {
       const bf16x8 kf = __builtin_bit_cast(bf16x8, lds[st * 64 + lane]);
+      if constexpr (NR < NT)
+        y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            kf, __builtin_bit_cast(bf16x8, q_lds[st * 64 + lane]), y, 0, 0, 0);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        if constexpr (NR < NT)
-          s[mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              kf, __builtin_bit_cast(bf16x8, q_lds[(mt * STEPS + st) * 64 + lane]), s[mt], 0, 0, 0);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int u = NR - 1; u >= 0; --u)
-          s[mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[mt][st][u], s[mt], 0, 0, 0);
+      for (int u = NR - 1; u >= 0; --u)
+        y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[st][u], y, 0, 0, 0);
       // (or all operands are read ahead and do not fit the registers)
-      if (D == 256 && st % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      if ((D == 256 || NT == 3) && st % 4 == 3) __builtin_amdgcn_sched_barrier(0);
     }
+    return y;
+  }
+  // PAIR tiles at lds; their first tokens; masked: some row does not see some token.
+  __device__ __forceinline__ void step(const Args& a, const u32x4* lds, const u32x4* q_lds,
+                                       const int (&base)[PAIR], bool masked, float c) {
+    const int lane = threadIdx.x & 63, g = lane >> 5;
+    f32x16 s[PAIR];
+#pragma unroll
+    for (int t = 0; t < PAIR; ++t) s[t] = scores(lds + t * WORDS, q_lds);
+    // (the wave that has its scores goes before the one that makes them)
+    if (D < 256) __builtin_amdgcn_s_setprio(1);
     if (masked) {
       asm volatile("");                       // (a branch: most tiles need no mask)
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int t = 0; t < PAIR; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          s[mt][r] = sees(a, base + token(g, r), mt) ? s[mt][r] : -INFINITY;
+        for (int r = 0; r < 16; ++r) s[t][r] = sees(a, base[t] + token(g, r)) ? s[t][r] : -INFINITY;
     }
-    bf16x8 p[MT][2][NT];
+    float mx = fmaxf(s[0][0], s[0][1]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float mx = s[mt][0];
+    for (int r = 2; r < 16 * PAIR; r += 2)
+      mx = fmaxf(fmaxf(mx, s[r / 16][r % 16]), s[r / 16][r % 16 + 1]);
+    // (a first visible score raises -inf; a row that has seen nothing stays there)
+    if (__any(mx > over)) {
+      mx = fmaxf(mx, __shfl_xor(mx, 32));     // the other half of the row's tokens
+      const float nm = fmaxf(m, mx);
+      const float nc = __builtin_amdgcn_fmed3f(nm * c, -FAR, FAR);
+      const float f = __builtin_amdgcn_exp2f(mc - nc);
+      l *= f;
 #pragma unroll
-      for (int r = 1; r < 15; r += 2) mx = fmaxf(fmaxf(mx, s[mt][r]), s[mt][r + 1]);
-      mx = fmaxf(mx, s[mt][15]);
-      // (a first visible score raises -inf; a row that has seen nothing stays there)
-      if (__any(mx > over[mt])) {
-        mx = fmaxf(mx, __shfl_xor(mx, 32));   // the other half of the row's tokens
-        const float nm = fmaxf(m[mt], mx);
-        const float nc = __builtin_amdgcn_fmed3f(nm * c, -FAR, FAR);
-        const float f = __builtin_amdgcn_exp2f(mc[mt] - nc);
-        l[mt] *= f;
+      for (int dt = 0; dt < DT; ++dt) o[dt] *= f;
+      m = nm;
+      mc = nc;
+      over = nm + __builtin_fminf(RAISE / c, 3.4e38f);
+    }
+    bf16x8 p[PAIR][2][NT];
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[mt][dt] *= f;
-        m[mt] = nm;
-        mc[mt] = nc;
-        over[mt] = nm + __builtin_fminf(RAISE / c, 3.4e38f);
-      }
+    for (int t = 0; t < PAIR; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][r], c, -mc[mt]));
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], c, -mc));
         __bf16 x[NT];
         split(e, x);
 #pragma unroll
-        for (int u = 0; u < NT; ++u) p[mt][r >> 3][u][r & 7] = x[u];
-        // (the sum is that of the rounded weights: their errors cancel in the division)
-        l[mt] += NT == 1 ? (float)x[0] : e;
+        for (int u = 0; u < NT; ++u) p[t][r >> 3][u][r & 7] = x[u];
+        if constexpr (NT > 1) l += e;
       }
-    }
+    // (the sum of bf16 rows is that of the rounded weights: their errors cancel in the division)
+    if constexpr (NT == 1)
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
+      for (int t = 0; t < PAIR; ++t)
 #pragma unroll
-      for (int u2 = 0; u2 < 2; ++u2) {
-        const bf16x8 vf = __builtin_bit_cast(bf16x8, lds[TILE * D * 2 / 16 + (dt * 2 + u2) * 64 + lane]);
+        for (int r = 0; r < 16; r += 2) {
+          const bf16x2 two = {p[t][r >> 3][0][r & 7], p[t][r >> 3][0][(r & 7) + 1]};
+          l = __builtin_amdgcn_fdot2_f32_bf16(two, bf16x2{(__bf16)1.f, (__bf16)1.f}, l, false);
+        }
+    if (D < 256) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+    for (int t = 0; t < PAIR; ++t)
+#pragma unroll
+      for (int u2 = 0; u2 < 2; ++u2)
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          const bf16x8 vf =
+              __builtin_bit_cast(bf16x8, lds[t * WORDS + K_WORDS + (dt * 2 + u2) * 64 + lane]);
 #pragma unroll
           for (int u = NT - 1; u >= 0; --u)
-            o[mt][dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[mt][u2][u], o[mt][dt], 0, 0, 0);
-        if (D == 256) __builtin_amdgcn_sched_barrier(0);
-      }
+            o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[t][u2][u], o[dt], 0, 0, 0);
+          if (D == 256 || NT == 3) __builtin_amdgcn_sched_barrier(0);
+        }
   }
   // V blocks stored as NaN: rows that see the token are NaN in the block's dims.
   __device__ __forceinline__ void note(const Args& a, const uint8_t* odd, int base) {
 #pragma nounroll
     for (int t = 0; t < TILE; ++t) {
       const uint32_t bits = odd[t];
-      if (!bits) continue;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (sees(a, base + t, mt)) poison[mt] |= bits;
-      }
+      if (bits && sees(a, base + t)) poison |= bits;
     }
   }
 };
 
-template <int D, int OD, int MT, int WAVES, int PER_SIMD, typename T>
+template <int D, int OD, int WAVES, int PER_SIMD, typename T>
 __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
-  using A = Prompt<D, OD, MT, T>;
-  constexpr int PARTS = D / OD;              // workgroups that share a block's dims
-  constexpr int STAGE = D == 256 ? 1 : 2;     // tiles on their way at a time
-  constexpr int K_WORDS = TILE * D * 2 / 16, V_WORDS = TILE * OD * 2 / 16, WORDS = K_WORDS + V_WORDS;
-  constexpr int LOADS = STAGE * WORDS / (64 * WAVES);
+  using A = Prompt<D, OD, T>;
+  constexpr int PARTS = D / OD;               // workgroups that share a block's dims
+  // tiles in LDS between two barriers, twice (160 KiB per compute unit)
+  constexpr int STAGE = D == 256 ? 1 : WAVES / 2;
+  constexpr int WORDS = A::WORDS, LOADS = STAGE * WORDS / (64 * WAVES);
   __shared__ u32x4 lds[2][STAGE * WORDS], q_lds[A::Q_LDS ? WAVES : 1][A::Q_LDS ? A::Q_LDS : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int of = blockIdx.x % PARTS, hit = blockIdx.x / PARTS, it = hit / a.kv_heads, h = hit - it * a.kv_heads;
@@ -498,17 +506,16 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   const int b = blk.b, row0 = a.cu[b], rows = a.cu[b + 1] - row0, ctx = a.ctx[b];
   const int st = a.status[b];
   const int64_t R = (int64_t)rows * a.group, r0 = (int64_t)blk.rb * a.block_rows;
-  const int64_t rw = r0 + wave * 32 * MT;     // the wave's first row
+  const int64_t rw = r0 + wave * 32;          // the wave's first row
   const int n = lane & 31, g = lane >> 5;
+  auto row_out = [&](int64_t r) {
+    const uint32_t j = (uint32_t)r / (uint32_t)a.group, hq = h * a.group + (uint32_t)r - j * a.group;
+    return (T*)a.out + ((int64_t)row0 + j) * a.ld_out + (int64_t)hq * D + of * OD;
+  };
   if (st != SV_ROW_OK) {                      // the request's rows are NaN
-    if (item.chunk > 0) return;
-    for (int mt = 0; mt < MT; ++mt) {
-      const int64_t r = rw + mt * 32 + n;
-      if (r >= R) continue;
-      const uint32_t j = (uint32_t)r / (uint32_t)a.group, hq = h * a.group + (uint32_t)r - j * a.group;
-      T* dst = (T*)a.out + ((int64_t)row0 + j) * a.ld_out + (int64_t)hq * D + of * OD + g * (OD / 2);
-      for (int i = 0; i < OD / 2; ++i) dst[i] = (T)__builtin_nanf("");
-    }
+    if (item.chunk > 0 || rw + n >= R) return;
+    T* const dst = row_out(rw + n);
+    for (int i = 0; i < OD / 2; ++i) dst[g * (OD / 2) + i] = (T)__builtin_nanf("");
     return;
   }
   const int j0 = (int)(r0 / a.group), j1 = (int)((min(r0 + a.block_rows, R) - 1) / a.group);
@@ -526,18 +533,25 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   };
   // positions of the wave's rows
   const int w0 = ctx + (int)(min(rw, R - 1) / a.group);
-  const int w1 = ctx + (int)(min(rw + 32 * MT - 1, R - 1) / a.group);
+  const int w1 = ctx + (int)(min(rw + 31, R - 1) / a.group);
   const bool live = rw < R;
   const bool odd = a.head->odd != 0;
+  auto masked = [&](int base) {
+    return base + TILE - 1 > w0 || (a.window > 0 && base <= w1 - a.window && base + TILE > a.sinks);
+  };
 
   // the next tiles go straight to LDS, 1 KiB per wave and instruction
   auto ask = [&](int i, int buf) {
+    uint32_t mine = lane * 16;
+    asm volatile("" : "+v"(mine));            // (or its sum with the base is kept, and no scalar any more)
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) {
-      const int w = (k * WAVES + wave) * 64, t = w / WORDS;
-      const u32x4* src = (const u32x4*)(a.wide + place(min(i + t, end - 1)) * tile_bytes(D)) + (w - t * WORDS) +
-                         (w - t * WORDS < K_WORDS ? 0 : of * V_WORDS);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + lane),
+      const int w = (k * WAVES + wave) * 64, t = w / WORDS, x = w - t * WORDS;
+      // (scalar, so that a load's address costs no vector arithmetic)
+      const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((int)place(min(i + t, end - 1)));
+      const uint8_t* src = a.wide + ((int64_t)at * tile_bytes(D) +
+                                     (x + (x < A::K_WORDS ? 0 : of * A::V_WORDS)) * 16);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + mine),
                                        (__attribute__((address_space(3))) void*)(lds[buf] + w), 16, 0, 0);
     }
   };
@@ -548,56 +562,62 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   __syncthreads();
   int buf = 0;
   for (int i = begin; i < end; i += STAGE) {
-    ask(min(i + STAGE, end - 1), buf ^ 1);
+    if (i + STAGE < end) ask(i + STAGE, buf ^ 1);
 #pragma unroll
-    for (int t = 0; t < STAGE; ++t) {
-      if (i + t >= end) break;
-      const int base = base_of(i + t);
-      if (!live || base > w1) continue;
-      const bool masked = base + TILE - 1 > w0 ||
-                          (a.window > 0 && base <= w1 - a.window && base + TILE > a.sinks);
-      x.tile(a, lds[buf] + t * WORDS, my_q, base, masked, c);
-      if (odd) x.note(a, a.odd + place(i + t) * TILE, base);
+    for (int t = 0; t < STAGE; t += A::PAIR) {
+      int base[A::PAIR];
+      bool some = false, hide = false;
+#pragma unroll
+      for (int k = 0; k < A::PAIR; ++k) {
+        // (behind the last tile lies that tile once more: no row sees it there)
+        base[k] = i + t + k < end ? base_of(i + t + k) : 0x7fffff00;
+        some |= base[k] <= w1;
+        hide |= masked(base[k]);
+      }
+      if (live && some) {
+        x.step(a, lds[buf] + t * WORDS, my_q, base, hide, c);
+        if (odd)
+          for (int k = 0; k < A::PAIR; ++k)
+            if (i + t + k < end) x.note(a, a.odd + place(i + t + k) * TILE, base[k]);
+      }
     }
     buf ^= 1;
     __syncthreads();
   }
 
   const int64_t slot = (((int64_t)item.block * a.kv_heads + h) * a.chunks + item.chunk) * a.block_rows;
-  float* const part = a.part + slot * D;
+  float* const part = a.part + slot * D + of * OD;
   float* const stat = a.part + (int64_t)a.max_blocks * a.kv_heads * a.chunks * a.block_rows * D + slot * 2;
+  const float sum = x.l + __shfl_xor(x.l, 32);
+  int ln = lane & 31;
+  asm volatile("" : "+v"(ln));                // (or where the row lies takes registers in the loop)
+  const int64_t r = rw + ln;
+  if (r >= R) return;
+  T* const dst = row_out(r);
+  const float inv = 1.f / sum;
+  const int local = (int)(r - r0);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const float sum = x.l[mt] + __shfl_xor(x.l[mt], 32);
-    const int64_t r = rw + mt * 32 + n;
-    if (r >= R) continue;
-    const uint32_t j = (uint32_t)r / (uint32_t)a.group, hq = h * a.group + (uint32_t)r - j * a.group;
-    const float inv = 1.f / sum;
-    T* dst = (T*)a.out + ((int64_t)row0 + j) * a.ld_out + (int64_t)hq * D;
-    const int local = (int)(r - r0);
+  for (int dt = 0; dt < A::DT; ++dt) {
+    const bool nan = x.poison >> (of * A::DT + dt) & 1;
 #pragma unroll
-    for (int dt = 0; dt < A::DT; ++dt) {
-      const bool nan = x.poison[mt] >> (of * A::DT + dt) & 1;
+    for (int k = 0; k < 4; ++k) {
+      float y[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float y[4];
+      for (int e = 0; e < 4; ++e) y[e] = nan ? __builtin_nanf("") : x.o[dt][4 * k + e];
+      const int dim = 32 * dt + 8 * k + 4 * g;
+      if (whole) {
+        T z[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = nan ? __builtin_nanf("") : x.o[mt][dt][4 * k + e];
-        const int dim = of * OD + 32 * dt + 8 * k + 4 * g;
-        if (whole) {
-          T z[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[e] = (T)(y[e] * inv);
-          __builtin_memcpy(dst + dim, z, sizeof(z));
-        } else {
-          __builtin_memcpy(part + (int64_t)local * D + dim, y, sizeof(y));
-        }
+        for (int e = 0; e < 4; ++e) z[e] = (T)(y[e] * inv);
+        __builtin_memcpy(dst + dim, z, sizeof(z));
+      } else {
+        __builtin_memcpy(part + (int64_t)local * D + dim, y, sizeof(y));
       }
     }
-    if (!whole && g == 0 && of == 0) {
-      stat[local * 2] = x.mc[mt];
-      stat[local * 2 + 1] = sum;
-    }
+  }
+  if (!whole && g == 0 && of == 0) {
+    stat[local * 2] = x.mc;
+    stat[local * 2 + 1] = sum;
   }
 }
 
@@ -642,7 +662,7 @@ __global__ __launch_bounds__(256) void k_prompt_join(Args a) {
 // ---- host side
 
 struct Plan {
-  int block_rows, max_blocks, chunks, chunk_tiles;
+  int waves, block_rows, max_blocks, chunks, chunk_tiles;
   int64_t max_tiles;
   size_t tile_off, blocks, items, odd, wide, part, bytes;
 };
@@ -652,8 +672,19 @@ static size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 static bool plan_of(int dtype, int batch, int total_rows, int heads, int kv_heads, int d,
                     int max_context, int64_t total_context, int window, int sinks, Plan& p) {
   const int64_t R = (int64_t)total_rows * (heads / kv_heads);
-  p.block_rows = d < 256 || dtype == SV_BF16 ? 256 : 128;
-  const int64_t blocks = (R + (int64_t)batch * (p.block_rows - 1)) / p.block_rows;
+  // Four waves per workgroup, two workgroups per compute unit, so that one's start and end
+  // run beside the other's products; or eight for bf16 calls of many workgroups, which share
+  // a tile's way to LDS.  (One prompt of 15,991 rows, 2,000 blocks of 256 rows over all KV
+  // heads: 1,838 us, with four waves 1,940; four of 1,500 to 4,000 rows, 1,176 blocks: 304
+  // and 307; two of 150 to 600 after 8,000 to 30,000 positions: 306 and 265; eight fp32 ones
+  // with a window: 205 and 175.)
+  p.waves = 8;
+  int64_t blocks = 0;
+  for (;; p.waves = 4) {
+    p.block_rows = 32 * p.waves;
+    blocks = (R + (int64_t)batch * (p.block_rows - 1)) / p.block_rows;
+    if (p.waves == 4 || (dtype == SV_BF16 && R * kv_heads >= 1024 * 256)) break;
+  }
   // tiles of all requests, and of one
   int64_t tiles = total_context / TILE + batch, one = max_context / TILE + 1;
   if (window > 0) {
@@ -702,14 +733,21 @@ static bool sizes_ok(int dtype, int batch, int total_rows, int heads, int kv_hea
          sinks <= (1 << 30);
 }
 
-template <int D, int OD, int MT, int WAVES, int PER_SIMD, typename T>
+template <int D, int OD, typename T>
 static int launch(const Args& a, const Plan& p, hipStream_t s) {
+  constexpr int PER_SIMD = sizeof(T) == 4 && D == 256 ? 1 : 2;
   hipLaunchKernelGGL(k_prompt_plan, dim3(1), dim3(1024), 0, s, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   hipLaunchKernelGGL((k_prompt_widen<D>), dim3((uint32_t)(p.max_tiles * a.kv_heads)), dim3(256), 0, s, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   const uint32_t wide = (uint32_t)(p.max_blocks * a.kv_heads);
-  hipLaunchKernelGGL((k_prompt<D, OD, MT, WAVES, PER_SIMD, T>), dim3(wide * p.chunks * (D / OD)), dim3(64 * WAVES), 0, s, a);
+  const dim3 grid(wide * p.chunks * (D / OD));
+  if (p.waves == 4) {
+    hipLaunchKernelGGL((k_prompt<D, OD, 4, PER_SIMD, T>), grid, dim3(256), 0, s, a);
+  } else {
+    if constexpr (sizeof(T) == 2)
+      hipLaunchKernelGGL((k_prompt<D, OD, 8, PER_SIMD, T>), grid, dim3(512), 0, s, a);
+  }
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   if (p.chunks > 1) {
     hipLaunchKernelGGL((k_prompt_join<D, T>), dim3(wide * (a.block_rows / 16)), dim3(256), 0, s, a);
@@ -798,13 +836,13 @@ int spec_kv_prompt_attention(const void* q, int64_t ld_q, int dtype, const int32
   a.part = (float*)(w + p.part);
   hipStream_t s = (hipStream_t)stream;
   if (dtype == SV_BF16) {
-    if (head_dim == 64) return prompt::launch<64, 64, 1, 8, 2, __bf16>(a, p, s);
-    if (head_dim == 128) return prompt::launch<128, 128, 1, 8, 2, __bf16>(a, p, s);
-    return prompt::launch<256, 128, 1, 8, 2, __bf16>(a, p, s);
+    if (head_dim == 64) return prompt::launch<64, 64, __bf16>(a, p, s);
+    if (head_dim == 128) return prompt::launch<128, 128, __bf16>(a, p, s);
+    return prompt::launch<256, 128, __bf16>(a, p, s);
   }
-  if (head_dim == 64) return prompt::launch<64, 64, 1, 8, 2, float>(a, p, s);
-  if (head_dim == 128) return prompt::launch<128, 128, 1, 8, 2, float>(a, p, s);
-  return prompt::launch<256, 128, 1, 4, 1, float>(a, p, s);
+  if (head_dim == 64) return prompt::launch<64, 64, float>(a, p, s);
+  if (head_dim == 128) return prompt::launch<128, 128, float>(a, p, s);
+  return prompt::launch<256, 128, float>(a, p, s);
 }
 
 }  // extern "C"
