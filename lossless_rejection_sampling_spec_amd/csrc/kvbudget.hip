@@ -19,14 +19,18 @@ namespace budget {
 // twice: once for the rows' maxima and sums, once for the weights.  (Kept instead, they would
 // take R numbers per position, more than the position's codes from R = 16 on.)
 //
-// A workgroup of 4 waves takes a chunk of one KV head's context, all R = rows * G query rows
-// of it, 16 MT at a time; its waves take the tiles of 32 tokens in turn.  Scores are
-// S^T[token][row] = K Q^T with v_mfma_f32_16x16x32_bf16, K widened from its codes in
-// registers; a lane holds the scores of one row for 8 tokens.  Where a request is one chunk
-// (short contexts) both passes are one launch.
+// A workgroup of 4 waves takes a chunk of one KV head's context and all R = rows * G query
+// rows of it, whose operands lie in LDS; its waves take the tiles of 32 tokens in turn.
+// Scores are S^T[token][row] = K Q^T with v_mfma_f32_16x16x32_bf16, K widened from its codes
+// in registers; a lane holds the scores of one row for 8 tokens.  The sums go over the tiles
+// for each 16 MT rows (statistics in registers), the weights over the rows for each tile
+// (summed over the lanes once).  Where a request is
+// one chunk (short contexts) both passes are one launch.
 
 constexpr int TILE = 32, SUB = 64;            // tokens of a tile; tiles whose pages a wave looks up at once
-constexpr int WAVES = 4;
+// Waves of a workgroup: eight where it does both passes (64 requests over 100 to 1,000 positions
+// 22.5 us, four 23.7, sixteen 31, two launches 30).
+constexpr int waves_of(bool both) { return both ? 8 : 4; }
 constexpr float LOG2E = 1.44269504088896340736f;
 // the rounded product of maximum and scale, from which exponents are counted, is held within
 // +-FAR: past it weights become infinite, or all 0, and their row adds nothing
@@ -37,6 +41,7 @@ struct WeightArgs {
   int64_t ld_q;
   const int32_t *cu, *ctx, *counts;
   int batch, total_rows, max_k, heads, kv_heads, group;
+  float inv_group;
   const uint8_t* pages;
   int64_t num_pages;
   int page, page_log2, unit;
@@ -50,6 +55,7 @@ struct WeightArgs {
   int64_t ld_w;
   int32_t* status;
   int chunks, chunk_tiles, max_rows;          // chunks of a request at most; R at most
+  int group_rows;                             // rows whose queries lie in LDS at once
   float* stats;                               // [batch][kv_heads][chunks][max_rows][2]
   int gap_blocks;                             // blocks per KV head that copy what no row sees
 };
@@ -89,6 +95,17 @@ __device__ __forceinline__ Span span_of(const WeightArgs& a, const Request& r) {
 __device__ __forceinline__ int base_of(const Span& s, int i) {
   return (i < s.early ? i : i - s.early + s.tile0) * TILE;
 }
+// Whether a page that the rows need is missing; all lanes of a wave take part.
+__device__ __forceinline__ bool pages_missing(const WeightArgs& a, const Span& sp, int b) {
+  const int32_t* tab = a.table + (int64_t)b * a.ld_table;
+  bool bad = false;
+  for (int s = threadIdx.x & 63; s <= (sp.n - 1) >> a.page_log2; s += 64) {
+    const int t0 = s << a.page_log2, t1 = t0 + a.page;
+    if (t1 > sp.first || (a.window > 0 && t0 < a.sinks))
+      bad |= s >= a.ld_table || (uint32_t)tab[s] >= (uint64_t)a.num_pages;
+  }
+  return __any(bad);
+}
 // Whether some row sees a position of the 16 from t0 on.
 __device__ __forceinline__ bool half_needed(const WeightArgs& a, const Span& s, int t0) {
   return t0 < s.n && (t0 + 16 > s.first || (a.window > 0 && t0 < a.sinks));
@@ -110,13 +127,14 @@ struct Weights {
   static constexpr int STEPS = D / 32, KB = (D + 127) / 128;
   // fp32 queries are split into three bf16 terms (3 x 8 bits hold fp32's 24)
   static constexpr int NT = sizeof(T) == 4 ? 3 : 1;
-  static constexpr int Q_WORDS = MT * STEPS * NT * 64;      // 16-byte words
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int Q_WORDS = MT * STEPS * NT * 64;      // 16-byte words of 16 MT rows
 
-  // The rows' operands in LDS, [row tile][step][term][lane].
+  // The operands of rows r0 .. r0 + 16 tiles - 1 in LDS, [row tile][step][term][lane].
   static __device__ __forceinline__ void put_q(const WeightArgs& a, bf16x8* q, const Request& rq,
-                                               int h, int r0, int R, int wave) {
+                                               int h, int r0, int tiles, int R, int wave, int waves) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    for (int at = wave; at < MT * STEPS; at += WAVES) {
+    for (int at = wave; at < tiles * STEPS; at += waves) {
       const int mt = at / STEPS, s = at % STEPS;
       const int r = min(r0 + mt * 16 + n, R - 1);
       const int j = r / a.group, hq = h * a.group + r - j * a.group;
@@ -192,8 +210,9 @@ struct Weights {
   // Entry i of a lane's 8 tokens, relative to the tile.
   static __device__ __forceinline__ int token(int g, int i) { return 16 * (i >> 2) + 4 * g + (i & 3); }
 
-  // A tile's scores, -inf where a row does not see the token.  Tokens of a block stored as
-  // NaN get `odd`: NaN for the sums, whose row then adds nothing, -inf for the weights.
+  // A tile's scores with 16 MT rows, -inf where a row does not see the token.  Tokens of a
+  // block stored as NaN get `odd`: NaN for the sums, whose row then adds nothing, -inf for the
+  // weights.
   static __device__ __forceinline__ void scores(const WeightArgs& a, const KTile<D>& t, const bf16x8* q,
                                                 f32x4 (&s)[2][MT], int base, bool masked,
                                                 const int (&pos)[MT], float odd) {
@@ -201,13 +220,13 @@ struct Weights {
     int ql = lane;
     asm volatile("" : "+v"(ql));              // (or the reads move out of the loop, into registers)
     float sc[2][KB];
-    bool nan = false;
+    uint32_t top = 0;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
       for (int x = 0; x < KB; ++x) {
         sc[hf][x] = __builtin_bit_cast(float, t.ks[hf][x] << 23);
-        nan |= t.ks[hf][x] == 255u;
+        top = max(top, t.ks[hf][x]);
       }
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
@@ -215,29 +234,28 @@ struct Weights {
       for (int mt = 0; mt < MT; ++mt) s[hf][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int st = 0; st < STEPS; ++st) {
-      bf16x8 qt[MT][NT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int u = 0; u < NT; ++u) qt[mt][u] = q[((mt * STEPS + st) * NT + u) * 64 + ql];
+      u32x4 k[2];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const uint32_t x = t.k[hf][st];
         const float f = sc[hf][st / 4];
-        u32x4 kb;
-        kb[0] = widen<0>(x, f);
-        kb[1] = widen<1>(x, f);
-        kb[2] = widen<2>(x, f);
-        kb[3] = widen<3>(x, f);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int u = NT - 1; u >= 0; --u)
-            s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kb), qt[mt][u],
-                                                                s[hf][mt], 0, 0, 0);
+        k[hf][0] = widen<0>(x, f);
+        k[hf][1] = widen<1>(x, f);
+        k[hf][2] = widen<2>(x, f);
+        k[hf][3] = widen<3>(x, f);
       }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int u = NT - 1; u >= 0; --u) {
+          const bf16x8 y = q[((mt * STEPS + st) * NT + u) * 64 + ql];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[hf]), y,
+                                                                s[hf][mt], 0, 0, 0);
+        }
     }
-    if (__any(nan)) {
+    if (__any(top == 255u)) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         bool o = false;
@@ -280,14 +298,29 @@ __device__ __forceinline__ float sum16(float x) {
   return x + dpp<0x140>(x);                   // the mirror of 16
 }
 
-// PASS 1: statistics, 2: weights, 3: both (a request is one chunk).
-template <int D, int MT, int PASS, typename T>
-__global__ __launch_bounds__(64 * WAVES, 2) void k_weights(WeightArgs a) {
+// Adds a part of a row's sum, counted from om, to one counted from m.
+__device__ __forceinline__ void join(float& m, float& sum, float om, float osum) {
+  const float nm = fmaxf(m, om);
+  sum = sum * (m == nm ? 1.f : __builtin_amdgcn_exp2f(m - nm)) +
+        osum * (om == nm ? 1.f : __builtin_amdgcn_exp2f(om - nm));
+  m = nm;
+}
+
+// PASS 1: statistics, 2: weights, 3: both (a request is one chunk).  ONE: a request has at
+// most 16 MT rows.
+template <int D, int MT, bool ONE, int PASS, typename T>
+__global__ __launch_bounds__(64 * waves_of(PASS == 3), PASS != 3 || D == 256 || MT == 4 ? 2 : 4) void k_weights(WeightArgs a) {
   using A = Weights<D, MT, T>;
-  __shared__ bf16x8 q[A::Q_WORDS];
-  __shared__ float acc[PASS & 2 ? SUB * TILE : 1];
-  __shared__ float part_m[WAVES][MT][16], part_l[WAVES][MT][16];
-  __shared__ float row_m[MT * 16], row_inv[MT * 16];
+  constexpr int WAVES = waves_of(PASS == 3);
+  constexpr int ROWS = A::ROWS, DEPTH = 2;    // tiles on their way
+  // the queries of a.group_rows rows, then their waves' statistics or their maxima and
+  // reciprocal sums
+  extern __shared__ __align__(16) uint8_t smem[];
+  bf16x8* const q = (bf16x8*)smem;
+  f32x2* const part = (f32x2*)(smem + (size_t)a.group_rows * D * 2 * A::NT);   // [wave][row]
+  f32x2* const fin = part + (PASS & 1 ? WAVES * a.group_rows : 0);             // [row]
+  __shared__ int any_bad;
+  __shared__ float acc[PASS & 2 ? (PASS == 3 ? 4 * WAVES : SUB) * TILE : 1];      // weights of a chunk
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int status_blocks = PASS & 1 ? (a.batch + WAVES - 1) / WAVES : 0;
@@ -296,17 +329,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_weights(WeightArgs a) {
     if (b >= a.batch) return;
     const Request rq = request_of(a, b);
     int st = rq.status;
-    if (st == SV_ROW_OK) {
-      const Span sp = span_of(a, rq);
-      const int32_t* tab = a.table + (int64_t)b * a.ld_table;
-      bool bad = false;
-      for (int s = lane; s <= (sp.n - 1) >> a.page_log2; s += 64) {
-        const int t0 = s << a.page_log2, t1 = t0 + a.page;
-        const bool need = t1 > sp.first || (a.window > 0 && t0 < a.sinks);
-        if (need) bad |= s >= a.ld_table || (uint32_t)tab[s] >= (uint64_t)a.num_pages;
-      }
-      if (__any(bad)) st = SV_ROW_BAD_PAGE;
-    }
+    if (st == SV_ROW_OK && pages_missing(a, span_of(a, rq), b)) st = SV_ROW_BAD_PAGE;
     if (lane == 0) a.status[b] = st;
     return;
   }
@@ -314,12 +337,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_weights(WeightArgs a) {
   const int items = a.batch * a.kv_heads * a.chunks;
   if (it >= items) {                          // positions that no row sees keep what they have
     it -= items;
-    const int part = it % a.gap_blocks, bh = it / a.gap_blocks, b = bh / a.kv_heads;
+    const int share = it % a.gap_blocks, bh = it / a.gap_blocks, b = bh / a.kv_heads;
     const Request rq = request_of(a, b);
-    if (rq.status != SV_ROW_OK || (PASS == 2 && a.status[b] != SV_ROW_OK)) return;
+    if (rq.status != SV_ROW_OK) return;
     const Span sp = span_of(a, rq);
+    if (PASS == 2 ? a.status[b] != SV_ROW_OK : pages_missing(a, sp, b)) return;
     const int64_t row = (int64_t)bh * a.ld_w;
-    for (int i = part * 256 + threadIdx.x; i < sp.tile0 * TILE; i += a.gap_blocks * 256)
+    for (int i = share * 64 * WAVES + threadIdx.x; i < sp.tile0 * TILE; i += a.gap_blocks * 64 * WAVES)
       if (i >= sp.early * TILE) a.out[row + i] = a.in ? a.in[row + i] : 0.f;
     return;
   }
@@ -332,225 +356,230 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_weights(WeightArgs a) {
   const int used = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
   const int begin = chunk * a.chunk_tiles, end = min(sp.tiles, begin + a.chunk_tiles);
   if (begin >= end) return;
-  const int R = rq.count * a.group, blocks = (R + MT * 16 - 1) / (MT * 16);
+  const int R = rq.count * a.group;
   const float c = a.scale * LOG2E;
-  const int32_t* tab = a.table + (int64_t)b * a.ld_table;
   const uint8_t* pool = a.pages + (int64_t)h * a.unit;
-  float* const stats = a.stats + (((int64_t)b * a.kv_heads + h) * a.chunks) * a.max_rows * 2;
-  bool bad = false;
+  f32x2* const stats = (f32x2*)a.stats + ((int64_t)b * a.kv_heads + h) * a.chunks * a.max_rows;
   typename A::Pages id;
-  KTile<D> t[2];
+  const bool bad = id.ask(a, sp, a.table + (int64_t)b * a.ld_table, begin, end);
+  const int mine = (end - begin - wave + WAVES - 1) / WAVES;  // the wave's tiles
+  KTile<D> t[DEPTH];
   int pos[MT];
-  int loaded = -1;                            // row block whose queries lie in LDS
-  auto queries = [&](int rb) {
-    if (loaded == rb) return;
-    __syncthreads();                          // (every wave is done with those before)
-    A::put_q(a, q, rq, h, rb * MT * 16, R, wave);
-    __syncthreads();
-    loaded = rb;
-  };
-  auto positions = [&](int rb) {
+  auto positions = [&](int r0) {              // (fp32 divides these right: rows are below 2^16)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) pos[mt] = rq.ctx + min(rb * MT * 16 + mt * 16 + n, R - 1) / a.group;
+    for (int mt = 0; mt < MT; ++mt)
+      pos[mt] = rq.ctx + (int)(((float)min(r0 + mt * 16 + n, R - 1) + 0.5f) * a.inv_group);
   };
   auto masked = [&](int base) {
     return base + TILE - 1 > rq.ctx ||
            (a.window > 0 && base <= rq.ctx + rq.rows - 1 - a.window && base + TILE > a.sinks);
   };
-  // the wave's tiles of the 64 from `from` on; two are on their way at any time
-  auto each_tile = [&](int from, float odd, auto&& use) {
-    const int stop = min(from + SUB, end);
-    bad |= id.ask(a, sp, tab, from, stop);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) A::fetch(a, t[k], pool, id, sp, min(from + wave + k * WAVES, stop - 1));
-    for (int i = from + wave; i < stop; i += 2 * WAVES) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int at = i + k * WAVES;
-        if (at < stop) {
-          f32x4 s[2][MT];
-          const int base = base_of(sp, at);
-          A::scores(a, t[k], q, s, base, masked(base), pos, odd);
-          use(s, at - from);
-        }
-        A::fetch(a, t[k], pool, id, sp, min(at + 2 * WAVES, stop - 1));
-      }
-    }
+  // use(k-th tile of the wave, its codes) for all of them; DEPTH are on their way at any time,
+  // behind the last ones the first again, for the next round.
+  int ahead = 0;
+  bool primed = false;
+  auto ask = [&](KTile<D>& to) {
+    A::fetch(a, to, pool, id, sp, begin + wave + ahead * WAVES);
+    ahead = ahead + 1 < mine ? ahead + 1 : 0;
   };
-  auto statistics = [&](int rb) {
-    float m[MT], mc[MT], l[MT];
-    queries(rb);
-    positions(rb);
+  auto each_tile = [&](auto&& use) {
+    if (mine <= 0) return;
+    if (!primed) {
+      ahead = 0;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m[mt] = -INFINITY;
-      mc[mt] = -FAR;
-      l[mt] = 0.f;
+      for (int k = 0; k < DEPTH; ++k) ask(t[k]);
     }
-    for (int from = begin; from < end; from += SUB)
-      each_tile(from, __builtin_nanf(""), [&](f32x4 (&s)[2][MT], int) {
+    for (int i = 0; i < mine; i += DEPTH) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          float mx = m[mt];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mx = fmaxf(mx, s[i >> 2][mt][i & 3]);
-          if (__any(mx > m[mt])) {            // (per lane: its tokens of the row)
-            const float nc = __builtin_amdgcn_fmed3f(mx * c, -FAR, FAR);
-            l[mt] *= __builtin_amdgcn_exp2f(mc[mt] - nc);
-            m[mt] = mx;
-            mc[mt] = nc;
-          }
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc[mt]));
-          l[mt] += sum;
-        }
-      });
-    // join the row's four lanes, then the waves
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int d = 16; d < 64; d <<= 1) {
-        const float om = __shfl_xor(mc[mt], d), ol = __shfl_xor(l[mt], d);
-        const float nm = fmaxf(mc[mt], om);
-        l[mt] = l[mt] * (mc[mt] == nm ? 1.f : __builtin_amdgcn_exp2f(mc[mt] - nm)) +
-                ol * (om == nm ? 1.f : __builtin_amdgcn_exp2f(om - nm));
-        mc[mt] = nm;
-      }
-      if (g == 0) {
-        part_m[wave][mt][n] = mc[mt];
-        part_l[wave][mt][n] = l[mt];
+      for (int k = 0; k < DEPTH; ++k) {
+        if (i + k < mine) use(i + k, t[k]);
+        ask(t[k]);
       }
     }
-    __syncthreads();
-    if (threadIdx.x < MT * 16) {
-      const int mt = threadIdx.x >> 4, x = threadIdx.x & 15;
-      float nm = part_m[0][mt][x], sum = 0.f;
-#pragma unroll
-      for (int k = 1; k < WAVES; ++k) nm = fmaxf(nm, part_m[k][mt][x]);
-#pragma unroll
-      for (int k = 0; k < WAVES; ++k) {
-        const float om = part_m[k][mt][x];
-        sum += part_l[k][mt][x] * (om == nm ? 1.f : __builtin_amdgcn_exp2f(om - nm));
-      }
-      if constexpr (PASS == 3) {
-        row_m[threadIdx.x] = nm;
-        row_inv[threadIdx.x] = sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f;
-      }
-      const int r = rb * MT * 16 + threadIdx.x;
-      // (with several row blocks the second pass finds them in memory again)
-      if ((PASS == 1 || blocks > 1) && r < R) {
-        float* to = stats + ((int64_t)chunk * a.max_rows + r) * 2;
-        to[0] = nm;
-        to[1] = sum;
-      }
-    }
-    __syncthreads();
+    primed = mine % DEPTH == 0;               // (else the next round starts in another buffer)
   };
-  if constexpr (PASS & 1)
-    for (int rb = 0; rb < blocks; ++rb) statistics(rb);
-  if constexpr (PASS == 3) {                  // a page id out of range: the request is left alone
-    if (blocks == 0) bad |= id.ask(a, sp, tab, begin, min(begin + SUB, end));
-    if (threadIdx.x == 0) part_m[0][0][0] = 0.f;
-    __syncthreads();
-    if (bad && lane == 0) part_m[0][0][0] = 1.f;
-    __syncthreads();
-    if (part_m[0][0][0] != 0.f) return;
-    __threadfence_block();
-  }
-  if constexpr (PASS & 2) {
-    for (int from = begin; from < end; from += SUB) {
+
+#pragma unroll
+  for (int pass = 1; pass <= 2; ++pass) {
+    if (!(PASS & pass)) continue;
+    if (PASS == 3 && pass == 2) {             // a page id out of range: the request is left alone
+      if (threadIdx.x == 0) any_bad = 0;
       __syncthreads();
-      for (int i = threadIdx.x; i < SUB * TILE; i += 64 * WAVES) acc[i] = 0.f;
+      if (bad && lane == 0) any_bad = 1;
       __syncthreads();
-      for (int rb = 0; rb < blocks; ++rb) {
-        queries(rb);
-        positions(rb);
-        if (PASS == 2 || blocks > 1) {
-          __syncthreads();
-          if (threadIdx.x < MT * 16) {        // the rows' maxima and sums over all chunks
-            const int r = min(rb * MT * 16 + (int)threadIdx.x, R - 1);
-            float nm = -INFINITY, sum = 0.f;
-            for (int k = 0; k < used; ++k) nm = fmaxf(nm, stats[((int64_t)k * a.max_rows + r) * 2]);
-            for (int k = 0; k < used; ++k) {
-              const float om = stats[((int64_t)k * a.max_rows + r) * 2];
-              sum += stats[((int64_t)k * a.max_rows + r) * 2 + 1] *
-                     (om == nm ? 1.f : __builtin_amdgcn_exp2f(om - nm));
+      if (any_bad) return;
+    }
+    for (int g0 = 0; g0 < max(R, 1); g0 += a.group_rows) {
+      const int rows = min(a.group_rows, R - g0), blocks = (rows + ROWS - 1) / ROWS;
+      if (!(PASS == 3 && pass == 2 && R <= a.group_rows)) {
+        __syncthreads();                      // (every wave is done with the rows before)
+        A::put_q(a, q, rq, h, g0, blocks * MT, R, wave, WAVES);
+        if (pass == 2)                        // the rows' maxima and sums over all chunks
+          for (int i = threadIdx.x >> 3; i < (rows + 7) / 8 * 8; i += 8 * WAVES) {     // 8 lanes each
+            float nm = -FAR, sum = 0.f;
+            const f32x2* from = stats + g0 + min(i, rows - 1);
+            for (int k = lane & 7; k < used; k += 32) {
+              f32x2 y[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) y[u] = from[(int64_t)min(k + 8 * u, used - 1) * a.max_rows];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (k + 8 * u < used) join(nm, sum, y[u][0], y[u][1]);
             }
-            row_m[threadIdx.x] = nm;
-            row_inv[threadIdx.x] = sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f;
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) join(nm, sum, __shfl_xor(nm, d), __shfl_xor(sum, d));
+            if ((lane & 7) == 0 && i < rows)
+              fin[i] = f32x2{nm, sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f};
           }
-          __syncthreads();
-        }
-        float mc[MT], inv[MT];
-        bool none = false;                    // rows that add nothing
+        __syncthreads();
+      }
+      if (pass == 1) {
+        if (mine <= 0)                        // (a wave without tiles leaves what counts nothing)
+          for (int i = lane; i < rows; i += 64) part[wave * a.group_rows + i] = f32x2{-FAR, 0.f};
+        for (int rb = 0; rb < blocks; ++rb) {
+          if (mine <= 0) break;
+          float m[MT], mc[MT], l[MT];
+          positions(g0 + rb * ROWS);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mc[mt] = row_m[mt * 16 + n];
-          // (lanes past the last row repeat it)
-          inv[mt] = rb * MT * 16 + mt * 16 + n < R ? row_inv[mt * 16 + n] : 0.f;
-          none |= row_inv[mt * 16 + n] == 0.f;
-        }
-        none = __any(none);
-        each_tile(from, -INFINITY, [&](f32x4 (&s)[2][MT], int at) {
-          if (none) {
+          for (int mt = 0; mt < MT; ++mt) {
+            m[mt] = -INFINITY;
+            mc[mt] = -FAR;
+            l[mt] = 0.f;
+          }
+          each_tile([&](int k, const KTile<D>& kt) {
+            f32x4 s[2][MT];
+            const int base = base_of(sp, begin + wave + k * WAVES);
+            A::scores(a, kt, ONE ? q : q + rb * A::Q_WORDS, s, base, masked(base), pos, __builtin_nanf(""));
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt) {
+              float mx = m[mt];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) mx = fmaxf(mx, s[i >> 2][mt][i & 3]);
+              if (__any(mx > m[mt])) {        // (per lane: its tokens of the row)
+                const float nc = __builtin_amdgcn_fmed3f(mx * c, -FAR, FAR);
+                l[mt] *= __builtin_amdgcn_exp2f(mc[mt] - nc);
+                m[mt] = mx;
+                mc[mt] = nc;
+              }
+              float sum = 0.f;
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (inv[mt] == 0.f) s[i >> 2][mt][i & 3] = -INFINITY;
-          }
-          float w[8];
+                sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc[mt]));
+              l[mt] += sum;
+            }
+          });
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            w[i] = 0.f;
+          for (int mt = 0; mt < MT; ++mt) {   // join the row's four lanes
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              w[i] = __builtin_fmaf(
-                  __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc[mt])), inv[mt], w[i]);
-            w[i] = sum16(w[i]);
+            for (int d = 16; d < 64; d <<= 1) join(mc[mt], l[mt], __shfl_xor(mc[mt], d), __shfl_xor(l[mt], d));
+            if (g == 0) part[wave * a.group_rows + rb * ROWS + mt * 16 + n] = f32x2{mc[mt], l[mt]};
           }
-          if (n < 8) {                        // lane n of the row writes entry n
-            float y = w[0];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows; i += 64 * WAVES) {    // then the waves
+          float nm = -FAR, sum = 0.f;
 #pragma unroll
-            for (int i = 1; i < 8; ++i) y = n == i ? w[i] : y;
-            acc[at * TILE + A::token(g, n)] += y;
+          for (int k = 0; k < WAVES; ++k) {
+            const f32x2 y = part[k * a.group_rows + i];
+            join(nm, sum, y[0], y[1]);
           }
+          if (PASS == 3 && R <= a.group_rows)
+            fin[i] = f32x2{nm, sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f};
+          else
+            stats[(int64_t)chunk * a.max_rows + g0 + i] = f32x2{nm, sum};
+        }
+        if constexpr (PASS == 3) __syncthreads();
+      } else {
+        float mc[MT], inv[MT];
+        bool none = false;                    // some rows add nothing
+        auto state = [&](int rb) {
+          none = false;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int r = rb * ROWS + mt * 16 + n;
+            const f32x2 y = fin[max(min(r, rows - 1), 0)];
+            mc[mt] = y[0];
+            inv[mt] = r < rows ? y[1] : 0.f;  // (lanes past the last row repeat it)
+            none |= r < rows && y[1] == 0.f;
+          }
+          none = __any(none);
+          positions(g0 + rb * ROWS);
+        };
+        if (ONE) state(0);
+        each_tile([&](int k, const KTile<D>& kt) {
+          const int at = wave + k * WAVES, base = base_of(sp, begin + at);
+          const bool hide = masked(base);
+          float w[8] = {};
+          for (int rb = 0; rb < blocks; ++rb) {
+            if (!ONE) state(rb);
+            f32x4 s[2][MT];
+            A::scores(a, kt, ONE ? q : q + rb * A::Q_WORDS, s, base, hide, pos, -INFINITY);
+            if (none) {
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (inv[mt] == 0.f) s[i >> 2][mt][i & 3] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                w[i] = __builtin_fmaf(
+                    __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc[mt])), inv[mt], w[i]);
+            if (ONE) break;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = sum16(w[i]);
+          float y = w[0];                     // lane n of the row writes entry n
+#pragma unroll
+          for (int i = 1; i < 8; ++i) y = n == i ? w[i] : y;
+          if (n < 8) acc[at * TILE + A::token(g, n)] = y;
         });
-      }
-      __syncthreads();
-      const int64_t row = ((int64_t)b * a.kv_heads + h) * a.ld_w;
-      for (int i = threadIdx.x; i < min(SUB, end - from) * TILE; i += 64 * WAVES) {
-        const int tok = base_of(sp, from + i / TILE) + i % TILE;
-        if (tok >= sp.n) continue;
-        const float before = a.in && tok < rq.ctx ? a.in[row + tok] : 0.f;
-        a.out[row + tok] = before + acc[i];
+        __syncthreads();
+        const int64_t row = ((int64_t)b * a.kv_heads + h) * a.ld_w;
+        for (int i = threadIdx.x; i < (end - begin) * TILE; i += 64 * WAVES) {
+          const int tok = base_of(sp, begin + i / TILE) + i % TILE;
+          if (tok >= sp.n) continue;
+          const float* before = g0 ? a.out : tok < rq.ctx ? a.in : nullptr;
+          a.out[row + tok] = (before ? before[row + tok] : 0.f) + acc[i];
+        }
       }
     }
   }
 }
 
 struct Plan {
-  int mt, chunks, chunk_tiles, max_rows;
+  int mt, chunks, chunk_tiles, max_rows, group_rows;
+  bool one;
   size_t bytes;
 };
 
 static bool plan_of(int dtype, int batch, int max_k, int heads, int kv_heads, int d, int max_context,
                     int window, int sinks, Plan& p) {
   const int64_t R = (int64_t)(max_k + 1) * (heads / kv_heads);
-  p.mt = R <= 16 ? 1 : 2;
+  const int nt = dtype == SV_F32 ? 3 : 1;
+  p.mt = R <= 16 ? 1 : R <= 32 || (nt == 3 && d == 256) ? 2 : 4;
+  p.one = R <= 32;
   p.max_rows = (int)R;
+  // queries and statistics of a group of rows take at most 55 KiB of LDS, the weights of 64
+  // tiles 8; the groups are even
+  const int rows = 16 * p.mt, row_bytes = d * 2 * nt + (waves_of(true) + 1) * 8;
+  const int64_t most = (65536 - 9216) / row_bytes / rows * rows, groups = (R + most - 1) / most;
+  p.group_rows = (int)(((R + groups - 1) / groups + rows - 1) / rows * rows);
   int64_t tokens = max_context;
   if (window > 0) {
     const int64_t seen = (int64_t)window + max_k + 1 + sinks + 3 * TILE;
     if (seen < tokens) tokens = seen;
   }
   const int64_t tiles = (tokens + TILE - 1) / TILE, wide = (int64_t)batch * kv_heads;
+  // one launch where every request has at most four tiles per wave, else chunks of 64 tiles
+  // (whose pages a wave looks up at once), halved down to 256 tokens while there are less than
+  // two workgroups per compute unit
   int64_t ct = SUB;
-  while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 512) ct /= 2;
-  // the statistics of a call take at most 256 MiB, or 8 chunks per request
-  while ((tiles + ct - 1) / ct > 8 && wide * ((tiles + ct - 1) / ct) * R * 8 > (256ll << 20)) ct *= 2;
+  if (tiles <= 4 * waves_of(true)) ct = 4 * waves_of(true);
+  else
+    while (ct > 8 && wide * ((tiles + ct - 1) / ct) < 512) ct /= 2;
   p.chunks = (int)((tiles + ct - 1) / ct);
   p.chunk_tiles = (int)ct;
   if (wide * p.chunks >= (1ll << 23)) return false;
@@ -566,17 +595,20 @@ static bool sizes_ok(int dtype, int batch, int max_k, int heads, int kv_heads, i
          window <= (1 << 30) && sinks >= 0 && sinks <= (1 << 30);
 }
 
-template <int D, int MT, typename T>
-static int launch(WeightArgs a, const Plan& p, hipStream_t s) {
-  const int items = a.batch * a.kv_heads * p.chunks, statuses = (a.batch + WAVES - 1) / WAVES;
-  const int gaps = a.gap_blocks * a.batch * a.kv_heads;
+template <int D, int MT, bool ONE, typename T>
+static int launch(const WeightArgs& a, const Plan& p, hipStream_t s) {
+  const int items = a.batch * a.kv_heads * p.chunks, gaps = a.gap_blocks * a.batch * a.kv_heads;
+  const int waves = waves_of(p.chunks == 1), statuses = (a.batch + waves - 1) / waves;
+  const size_t queries = (size_t)p.group_rows * D * 2 * Weights<D, MT, T>::NT, stat = p.group_rows * 8;
   if (p.chunks == 1) {
-    hipLaunchKernelGGL((k_weights<D, MT, 3, T>), dim3(statuses + items + gaps), dim3(64 * WAVES), 0, s, a);
+    hipLaunchKernelGGL((k_weights<D, MT, ONE, 3, T>), dim3(statuses + items + gaps), dim3(64 * waves),
+                       queries + (waves + 1) * stat, s, a);
     return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
   }
-  hipLaunchKernelGGL((k_weights<D, MT, 1, T>), dim3(statuses + items), dim3(64 * WAVES), 0, s, a);
+  hipLaunchKernelGGL((k_weights<D, MT, ONE, 1, T>), dim3(statuses + items), dim3(64 * waves),
+                     queries + waves * stat, s, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
-  hipLaunchKernelGGL((k_weights<D, MT, 2, T>), dim3(items + gaps), dim3(64 * WAVES), 0, s, a);
+  hipLaunchKernelGGL((k_weights<D, MT, ONE, 2, T>), dim3(items + gaps), dim3(64 * waves), queries + stat, s, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
 }
 
@@ -851,6 +883,7 @@ int spec_kv_attention_weights(const void* q, int64_t ld_q, int dtype, const int3
   a.heads = heads;
   a.kv_heads = kv_heads;
   a.group = heads / kv_heads;
+  a.inv_group = 1.f / (float)a.group;
   a.pages = (const uint8_t*)pages;
   a.num_pages = num_pages;
   a.page = page_size;
@@ -869,6 +902,7 @@ int spec_kv_attention_weights(const void* q, int64_t ld_q, int dtype, const int3
   a.chunks = p.chunks;
   a.chunk_tiles = p.chunk_tiles;
   a.max_rows = p.max_rows;
+  a.group_rows = p.group_rows;
   a.stats = (float*)workspace;
   a.gap_blocks = 0;
   if (window > 0 && weights_in != weights_out) {
@@ -877,18 +911,27 @@ int spec_kv_attention_weights(const void* q, int64_t ld_q, int dtype, const int3
     if (a.gap_blocks < 1) a.gap_blocks = 1;
   }
   hipStream_t s = (hipStream_t)stream;
-#define SVK_CASE(DD, TT)                                                       \
-  if (head_dim == DD)                                                          \
-  return p.mt == 1 ? budget::launch<DD, 1, TT>(a, p, s) : budget::launch<DD, 2, TT>(a, p, s)
+#define SVK_CASE(DD, MM, OO, TT) \
+  if (head_dim == DD && p.mt == MM && p.one == OO) return budget::launch<DD, MM, OO, TT>(a, p, s)
+#define SVK_CASES(DD, TT)          \
+  SVK_CASE(DD, 1, true, TT);       \
+  SVK_CASE(DD, 2, true, TT)
   if (dtype == SV_BF16) {
-    SVK_CASE(64, __bf16);
-    SVK_CASE(128, __bf16);
-    SVK_CASE(256, __bf16);
+    SVK_CASES(64, __bf16);
+    SVK_CASES(128, __bf16);
+    SVK_CASES(256, __bf16);
+    SVK_CASE(64, 4, false, __bf16);
+    SVK_CASE(128, 4, false, __bf16);
+    SVK_CASE(256, 4, false, __bf16);
   } else {
-    SVK_CASE(64, float);
-    SVK_CASE(128, float);
-    SVK_CASE(256, float);
+    SVK_CASES(64, float);
+    SVK_CASES(128, float);
+    SVK_CASES(256, float);
+    SVK_CASE(64, 4, false, float);
+    SVK_CASE(128, 4, false, float);
+    SVK_CASE(256, 2, false, float);
   }
+#undef SVK_CASES
 #undef SVK_CASE
   return SV_ERR_SHAPE;
 }
