@@ -615,10 +615,10 @@ static int launch(const WeightArgs& a, const Plan& p, hipStream_t s) {
 // -------------------------------------------------------------------- evict
 //
 // Per layer, request and KV head a workgroup finds the weight of the last position that
-// stays (a radix select over order-preserving keys), then moves what stays forward, in
-// order and in place: position p goes to slot i <= p, so that with positions taken in
-// order, and read before they are written, no write reaches what is still to be read.
-// A second launch sets tables, counts and lengths, once all of them are done.
+// stays (a radix select over order-preserving keys), lists what stays, and moves it forward
+// in order and in place, a slot per thread: slot i gets a position p >= i, so that where a
+// step's positions are all read before its slots are written, no write reaches what a later
+// step reads.  A second launch sets tables, counts and lengths, once all of them are done.
 
 struct EvictArgs {
   const int32_t* budgets;
@@ -674,18 +674,54 @@ __device__ __forceinline__ int evict_status(const EvictArgs& a, int b, int& n, i
   return SV_ROW_BAD_PAGE;
 }
 
-constexpr int THREADS = 1024;
-
 // A token's V codes of a 16th of the dims.
 template <int D> struct Piece { typedef uint32_t T; };
 template <> struct Piece<64> { typedef uint16_t T; };
 template <> struct Piece<256> { typedef u32x2 T; };
 
+// A position's codes and scales: K in one piece, V in 16.
 template <int D>
-__global__ __launch_bounds__(THREADS) void k_evict(EvictArgs a) {
-  constexpr int BINS = 2048;
+struct Token {
+  u32x4 k[D / 32];
+  typename Piece<D>::T v[16];
+  uint8_t ks[D / 32], vs[D / 32];
+  __device__ __forceinline__ void load(const uint8_t* u, int t, int P) {
+    const uint8_t* pv = u + off_v(P, D) + (t >> 3) * (4 * D) + (t & 7) * (D / 32);
+    const uint8_t* e = u + off_ks(P, D) + (t >> 3) * (D / 4) + (t & 7);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) k[i] = *(const u32x4*)(u + t * (D / 2) + 16 * i);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = *(const typename Piece<D>::T*)(pv + i * (D / 4));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      ks[i] = e[i * 8];
+      vs[i] = e[P * (D / 32) + i * 8];
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* u, int t, int P) const {
+    uint8_t* pv = u + off_v(P, D) + (t >> 3) * (4 * D) + (t & 7) * (D / 32);
+    uint8_t* e = u + off_ks(P, D) + (t >> 3) * (D / 4) + (t & 7);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) *(u32x4*)(u + t * (D / 2) + 16 * i) = k[i];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) *(typename Piece<D>::T*)(pv + i * (D / 4)) = v[i];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      e[i * 8] = ks[i];
+      e[P * (D / 32) + i * 8] = vs[i];
+    }
+  }
+};
+
+// THREADS threads; the weights of KEEP * THREADS positions stay in registers, those past them
+// are read again at every use.
+template <int D, int THREADS, int KEEP>
+__global__ __launch_bounds__(THREADS, THREADS == 256 && D < 256 ? 5 : 1) void k_evict(EvictArgs a) {
+  constexpr int BINS = 2048, WAVES = THREADS / 64, PER = BINS / THREADS;
+  constexpr int LIST = 4 * THREADS < 4096 ? 2048 : 4096;      // positions that stay, listed at a time
   __shared__ int hist[BINS];
-  __shared__ int wsum[THREADS / 64], picked[2], wgt[THREADS / 64], weq[THREADS / 64];
+  __shared__ int wsum[WAVES], picked[2], wgt[WAVES], weq[WAVES];
+  __shared__ int list[LIST];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int h = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads % a.batch;
   const int layer = blockIdx.x / a.kv_heads / a.batch;
@@ -695,122 +731,141 @@ __global__ __launch_bounds__(THREADS) void k_evict(EvictArgs a) {
   if (m == 0) return;
   float* const w = a.weights + (int64_t)blockIdx.x * a.ld_w;
   const int lo = a.sinks, hi = n - a.recent;  // positions that are chosen among
-  int need = m - a.sinks - a.recent;          // how many of them stay
-  uint32_t at = 0;                            // the key of the last that does
-  if (need > 0) {
-    int left = need;
+  const int room = m - a.sinks - a.recent;    // how many of them stay
+  // a wave has a stretch of the positions, in steps of 64
+  const int steps = (n + THREADS - 1) / THREADS, from = wave * steps * 64;
+  // (0 for positions that are not chosen among, and for NaN)
+  auto key_at = [&](int i) {
+    const int p = from + i * 64 + lane;
+    return p >= lo && p < hi ? key_of(w[p]) : 0u;
+  };
+  uint32_t key[KEEP];
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) key[i] = i < steps ? key_at(i) : 0u;
+  // the steps whose position is chosen among, and those whose position stays anyway
+  uint32_t among = 0, always = 0;
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int p = from + i * 64 + lane;
+    among |= (uint32_t)(i < steps && p >= lo && p < hi) << i;
+    always |= (uint32_t)(i < steps && p < n && (p < lo || p >= hi)) << i;
+  }
+  auto is_among = [&](int i) {
+    const int p = from + i * 64 + lane;
+    return i < KEEP ? (bool)(among >> i & 1) : p >= lo && p < hi;
+  };
+  // each(f): f(step, key) for the wave's positions, in order
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+      if (i < steps) f(i, key[i]);
+    for (int i = KEEP; i < steps; ++i) f(i, key_at(i));
+  };
+
+  uint32_t last = 0xffffffffu;                // the key of the last that stays (no weight has this one)
+  int ties = 0;                               // of those with just this key, the first so many stay
+  if (room > 0) {
+    ties = room;
+    last = 0;
     uint32_t mask = 0;
     for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
       const int bits = shift == 0 ? 10 : 11;
       for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
       __syncthreads();
-      for (int p = lo + tid; p < hi; p += THREADS) {
-        const uint32_t k = key_of(w[p]);
-        if ((k & mask) == at) atomicAdd(&hist[k >> shift & ((1 << bits) - 1)], 1);
-      }
+      each([&](int i, uint32_t k) {
+        if (is_among(i) && (k & mask) == last) atomicAdd(&hist[k >> shift & ((1 << bits) - 1)], 1);
+      });
       __syncthreads();
-      // digits from the top: thread t takes the bins BINS-1-2t and BINS-2-2t
-      const int d1 = BINS - 1 - 2 * tid, c1 = hist[d1], c0 = hist[d1 - 1];
-      int sum = c1 + c0;
+      // digits from the top: thread t takes the PER bins below BINS - PER t
+      int c[PER], sum = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        c[i] = hist[BINS - 1 - (tid * PER + i)];
+        sum += c[i];
+      }
+      int upto = sum;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(sum, d);
-        if (lane >= d) sum += y;
+        const int y = __shfl_up(upto, d);
+        if (lane >= d) upto += y;
       }
-      if (lane == 63) wsum[wave] = sum;
+      if (lane == 63) wsum[wave] = upto;
       __syncthreads();
-      for (int k = 0; k < wave; ++k) sum += wsum[k];
-      const int before = sum - c1 - c0;       // in larger digits
-      if (before < left && left <= before + c1) {
-        picked[0] = d1;
-        picked[1] = before;
-      } else if (before + c1 < left && left <= sum) {
-        picked[0] = d1 - 1;
-        picked[1] = before + c1;
+      for (int k = 0; k < wave; ++k) upto += wsum[k];
+      int before = upto - sum;                // in larger digits
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (before < ties && ties <= before + c[i]) {
+          picked[0] = BINS - 1 - (tid * PER + i);
+          picked[1] = before;
+        }
+        before += c[i];
       }
       __syncthreads();
-      at |= (uint32_t)picked[0] << shift;
+      last |= (uint32_t)picked[0] << shift;
       mask |= ((1u << bits) - 1) << shift;
-      left -= picked[1];
-      __syncthreads();
+      ties -= picked[1];
     }
-    need = left;                              // of those with just this key, the first so many
-  } else {
-    at = 0xffffffffu;                         // (no weight has this key)
   }
-  const bool none = m - a.sinks - a.recent <= 0;
+  // what stays whatever the ties, and the ties
+  auto sure_of = [&](int i, uint32_t k) {
+    const int p = from + i * 64 + lane;
+    const bool stays = i < KEEP ? (bool)(always >> i & 1) : p < n && (p < lo || p >= hi);
+    return stays || (is_among(i) && k > last);
+  };
+  auto tie_of = [&](int i, uint32_t k) {
+    return room > 0 && is_among(i) && k == last;
+  };
+  int gt = 0, eq = 0;
+  each([&](int i, uint32_t k) {
+    gt += __popcll(__ballot(sure_of(i, k)));
+    eq += __popcll(__ballot(tie_of(i, k)));
+  });
+  if (lane == 0) {
+    wgt[wave] = gt;
+    weq[wave] = eq;
+  }
+  __syncthreads();
+  int slot0 = 0, tie0 = 0;                    // of the waves before
+  for (int v = 0; v < wave; ++v) {
+    slot0 += wgt[v] + max(0, min(ties - tie0, weq[v]));
+    tie0 += weq[v];
+  }
 
-  // move, 1,024 positions at a time
+  // move: slot i gets position list[i], LIST slots at a time
   const int32_t* tab = a.table + (int64_t)b * a.ld_table;
-  uint8_t* const pool = a.pages + layer * a.layer_bytes;
+  uint8_t* const pool = a.pages + layer * a.layer_bytes + (int64_t)h * a.unit;
   const int64_t page_bytes = (int64_t)a.unit * a.kv_heads;
   const int P = a.page;
-  int kept = 0, same = 0;                     // so far: kept, and with the last key
-  for (int p0 = 0; p0 < n; p0 += THREADS) {
-    const int p = p0 + tid;
-    const float x = p < n ? w[p] : 0.f;
-    const bool choice = p >= lo && p < hi && !none;
-    const uint32_t k = choice ? key_of(x) : 0;
-    const bool sure = p < n && (p < lo || p >= hi || (choice && k > at));
-    const bool tie = choice && k == at;
-    const uint64_t bs = __ballot(sure), bt = __ballot(tie);
-    if (lane == 0) {
-      wgt[wave] = __popcll(bs);
-      weq[wave] = __popcll(bt);
-    }
+  for (int s0 = 0; s0 < m; s0 += LIST) {
+    const int s1 = min(m, s0 + LIST);
+    __syncthreads();                          // (the list before is used up)
+    int slot = slot0, tied = tie0;
+    each([&](int i, uint32_t k) {
+      const uint64_t bs = __ballot(sure_of(i, k)), bt = __ballot(tie_of(i, k));
+      const uint64_t below = (1ull << lane) - 1;
+      const int my_ties = min(max(ties - tied, 0), (int)__popcll(bt & below));
+      const bool keep = (bs >> lane & 1) || ((bt >> lane & 1) && tied + (int)__popcll(bt & below) < ties);
+      const int to = slot + __popcll(bs & below) + my_ties;
+      if (keep && to >= s0 && to < s1) list[to - s0] = from + i * 64 + lane;
+      slot += __popcll(bs) + min(max(ties - tied, 0), (int)__popcll(bt));
+      tied += __popcll(bt);
+    });
     __syncthreads();
-    int before = kept, ties = same, all = kept, all_ties = same;
-    for (int v = 0; v < THREADS / 64; ++v) {
-      // (of the ties only the first `need` stay)
-      const int stay = wgt[v] + max(0, min(need - all_ties, weq[v]));
-      if (v < wave) {
-        before += stay;
-        ties += weq[v];
+    for (int i0 = s0; i0 < s1; i0 += THREADS) {
+      const int to = i0 + tid, p = to < s1 ? list[to - s0] : to;
+      const bool move = p != to;
+      Token<D> y;
+      float x;
+      if (move) {
+        x = w[p];
+        y.load(pool + tab[p >> a.page_log2] * page_bytes, p & (P - 1), P);
       }
-      all += stay;
-      all_ties += weq[v];
-    }
-    const uint64_t below = (1ull << lane) - 1;
-    const int my_tie = ties + __popcll(bt & below);
-    const bool keep = sure || (tie && my_tie < need);
-    const int to = before + __popcll(bs & below) + max(0, min(need - ties, __popcll(bt & below)));
-    const bool move = keep && to != p;
-    kept = all;
-    same = all_ties;
-    // a position's codes and scales: K in one piece, V in 16
-    u32x4 kc[D / 32];
-    typename Piece<D>::T vc[16];
-    uint8_t ks[D / 32], vs[D / 32];
-    const int t0 = p & (P - 1), t1 = to & (P - 1);
-    if (move) {
-      const uint8_t* u = pool + (int64_t)tab[p >> a.page_log2] * page_bytes + (int64_t)h * a.unit;
-      const uint8_t* v = u + off_v(P, D) + (t0 >> 3) * (4 * D) + (t0 & 7) * (D / 32);
-      const uint8_t* e = u + off_ks(P, D) + (t0 >> 3) * (D / 4) + (t0 & 7);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) kc[i] = *(const u32x4*)(u + t0 * (D / 2) + 16 * i);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) vc[i] = *(const typename Piece<D>::T*)(v + i * (D / 4));
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        ks[i] = e[i * 8];
-        vs[i] = e[P * (D / 32) + i * 8];
+      __syncthreads();                        // (all are read before one is written)
+      if (move) {
+        w[to] = x;
+        y.store(pool + tab[to >> a.page_log2] * page_bytes, to & (P - 1), P);
       }
-    }
-    __syncthreads();                          // (all are read before one is written)
-    if (move) {
-      uint8_t* u = pool + (int64_t)tab[to >> a.page_log2] * page_bytes + (int64_t)h * a.unit;
-      uint8_t* v = u + off_v(P, D) + (t1 >> 3) * (4 * D) + (t1 & 7) * (D / 32);
-      uint8_t* e = u + off_ks(P, D) + (t1 >> 3) * (D / 4) + (t1 & 7);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) *(u32x4*)(u + t1 * (D / 2) + 16 * i) = kc[i];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) *(typename Piece<D>::T*)(v + i * (D / 4)) = vc[i];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        e[i * 8] = ks[i];
-        e[P * (D / 32) + i * 8] = vs[i];
-      }
-      w[to] = x;
     }
   }
   __syncthreads();
@@ -972,12 +1027,17 @@ int spec_kv_evict(const int32_t* budgets, int batch, int sinks, int recent, floa
   a.status = status;
   hipStream_t s = (hipStream_t)stream;
   const dim3 grid((uint32_t)(layers * batch * kv_heads));
-  if (head_dim == 64)
-    hipLaunchKernelGGL((budget::k_evict<64>), grid, dim3(budget::THREADS), 0, s, a);
-  else if (head_dim == 128)
-    hipLaunchKernelGGL((budget::k_evict<128>), grid, dim3(budget::THREADS), 0, s, a);
-  else
-    hipLaunchKernelGGL((budget::k_evict<256>), grid, dim3(budget::THREADS), 0, s, a);
+  // small workgroups where they are many, large ones where each has long rows to itself
+  const bool many = grid.x >= 1024;
+#define SVK_CASE(DD)                                                                              \
+  if (head_dim == DD) {                                                                           \
+    if (many) hipLaunchKernelGGL((budget::k_evict<DD, 256, 16>), grid, dim3(256), 0, s, a);       \
+    else hipLaunchKernelGGL((budget::k_evict<DD, 1024, DD == 256 ? 16 : 32>), grid, dim3(1024), 0, s, a);          \
+  }
+  SVK_CASE(64)
+  SVK_CASE(128)
+  SVK_CASE(256)
+#undef SVK_CASE
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   hipLaunchKernelGGL(budget::k_evict_tables, dim3(batch), dim3(256), 0, s, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
