@@ -1,0 +1,152 @@
+"""Prompt attention, attention weights, eviction and appends at offsets on the CPU: every
+refusal of the C entry points (each call fails validation on the host, so no GPU is touched),
+the workspace sizes, the reference of an eviction, and that no kernel of theirs spills."""
+
+import subprocess
+
+import numpy as np
+import pytest
+
+import kv_budget_util as E
+from lossless_rejection_sampling_spec_amd import binding, build
+from test_kernel_registers import spills
+
+F = 0x1000        # a 16-byte aligned non-NULL pointer value that validation never reads
+BIG = 1 << 40     # more workspace than any call here needs
+
+
+def _prompt(**kw):
+    a = dict(q=F, ldq=512, dt=1, cu=F, ctx=F, batch=2, rows=6, heads=4, kv=2, d=128, pages=F, num=10,
+             page=16, table=F, ldt=4, maxc=64, total=128, scale=0.1, window=0, sinks=0, out=2 * F,
+             ldo=512, st=F, ws=F, wsb=BIG, stream=None)
+    a.update(kw)
+    return binding.lib().spec_kv_prompt_attention(*a.values())
+
+
+def _weights(**kw):
+    a = dict(q=F, ldq=512, dt=1, cu=F, ctx=F, counts=None, batch=2, rows=6, max_k=5, heads=4, kv=2,
+             d=128, pages=F, num=10, page=16, table=F, ldt=4, maxc=64, scale=0.1, window=0, sinks=0,
+             win=None, wout=F, ldw=64, st=F, ws=F, wsb=BIG, stream=None)
+    a.update(kw)
+    return binding.lib().spec_kv_attention_weights(*a.values())
+
+
+def _evict(**kw):
+    a = dict(budgets=F, batch=2, sinks=0, recent=0, weights=F, ldw=64, kv=2, d=128, page=16, lens=F,
+             table=F, ldt=4, refs=F, num=10, pages=F, layers=1, layer_bytes=1 << 20, evicted=None, st=F,
+             stream=None)
+    a.update(kw)
+    return binding.lib().spec_kv_evict(*a.values())
+
+
+COMMON = [(dict(q=None), 1), (dict(cu=None), 1), (dict(ctx=None), 1), (dict(pages=None), 1),
+          (dict(table=None), 1), (dict(st=None), 1), (dict(ws=None), 1), (dict(ws=F + 8), 1),
+          (dict(dt=2), 3), (dict(batch=0), 2), (dict(batch=1025), 2), (dict(rows=0), 2),
+          (dict(heads=3), 2), (dict(heads=1), 2), (dict(kv=0), 2), (dict(heads=1026), 2), (dict(d=96), 2),
+          (dict(page=8), 2), (dict(page=48), 2), (dict(num=0), 2), (dict(ldt=0), 2),
+          (dict(ldt=(1 << 26) + 1), 2), (dict(ldq=511), 2), (dict(maxc=0), 2), (dict(maxc=(1 << 30) + 1), 2),
+          (dict(scale=0.0), 2), (dict(scale=-1.0), 2), (dict(scale=float("nan")), 2),
+          (dict(scale=float("inf")), 2), (dict(window=-1), 2), (dict(sinks=-1), 2), (dict(pages=F + 4), 2),
+          (dict(wsb=0), 4)]
+
+
+@pytest.mark.parametrize("kw,rc", COMMON + [
+    (dict(out=None), 1), (dict(out=F), 2), (dict(ldo=511), 2), (dict(total=0), 2),
+    (dict(total=(1 << 30) + 1), 2), (dict(rows=1 << 29), 2), (dict(total=1 << 30, maxc=1 << 30), 2)])
+def test_prompt_refusals(kw, rc):
+    assert _prompt(**kw) == rc
+
+
+@pytest.mark.parametrize("kw,rc", COMMON + [
+    (dict(wout=None), 1), (dict(max_k=-1), 2), (dict(max_k=64), 2), (dict(ldw=63), 2),
+    (dict(batch=1024, heads=1024, kv=1024, ldq=1024 * 128, maxc=1 << 14, ldw=1 << 14), 2)])
+def test_weights_refusals(kw, rc):
+    assert _weights(**kw) == rc
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(budgets=None), 1), (dict(weights=None), 1), (dict(lens=None), 1), (dict(table=None), 1),
+    (dict(refs=None), 1), (dict(pages=None), 1), (dict(st=None), 1), (dict(batch=0), 2),
+    (dict(batch=1025), 2), (dict(sinks=-1), 2), (dict(recent=-1), 2), (dict(ldw=0), 2), (dict(kv=0), 2),
+    (dict(d=32), 2), (dict(page=24), 2), (dict(ldt=0), 2), (dict(num=0), 2), (dict(num=(1 << 24) + 1), 2),
+    (dict(pages=F + 8), 2), (dict(layers=0), 2), (dict(layers=65536), 2), (dict(layer_bytes=24), 2),
+    (dict(layers=2, layer_bytes=16), 2), (dict(layers=2048, batch=1024), 2)])
+def test_evict_refusals(kw, rc):
+    assert _evict(**kw) == rc
+
+
+def test_append_at_refuses_what_append_does():
+    L = binding.lib()
+
+    def call(**kw):
+        a = dict(q=F, ldq=512, k=F, ldk=256, v=F, ldv=256, dt=1, qw=None, kw=None, eps=1e-6, cs=None,
+                 maxp=0, rot=0, inter=0, cu=F, ctx=F, offs=None, batch=2, rows=6, heads=4, kv=2, d=128,
+                 pages=F, num=10, page=16, table=F, ldt=4, qo=F, ldo=512, kv_=None, vv_=None, st=F,
+                 stream=None)
+        a.update(kw)
+        return L.spec_kv_append_at(*a.values())
+    for kw, rc in ((dict(q=None), 1), (dict(rot=64), 1), (dict(kv_=F), 1), (dict(dt=2), 3), (dict(d=96), 2),
+                   (dict(rows=0), 2), (dict(rot=64, cs=F, maxp=0), 2), (dict(offs=F, heads=3), 2)):
+        assert call(**kw) == rc
+
+
+def test_workspace_sizes():
+    L = binding.lib()
+    prompt = dict(dt=1, batch=4, rows=1000, heads=32, kv=8, d=128, maxc=4000, total=9000, window=0, sinks=0)
+
+    def size(**kw):
+        return L.spec_kv_prompt_workspace_bytes(*{**prompt, **kw}.values())
+    # the requests' cache in bf16 (a tile more per request), and less than 64 MiB besides
+    wide = 4 * 128 * 8 * (9000 + 4 * 32)
+    assert wide - 4 * 128 * 8 * 32 * 4 <= size() <= wide + (64 << 20)
+    assert size(total=18000) > size() > size(window=64)
+    for kw in (dict(dt=2), dict(batch=0), dict(batch=1025), dict(rows=0), dict(heads=30), dict(d=96),
+               dict(maxc=0), dict(total=0), dict(total=(1 << 30) + 1), dict(window=-1), dict(sinks=-1),
+               dict(rows=1 << 30)):
+        assert size(**kw) == 0
+    weights = dict(dt=1, batch=4, max_k=6, heads=32, kv=8, d=128, maxc=4000, window=0, sinks=0)
+
+    def wsize(**kw):
+        return L.spec_kv_weights_workspace_bytes(*{**weights, **kw}.values())
+    assert 0 < wsize(maxc=100) < wsize() < wsize(max_k=63)
+    for kw in (dict(dt=2), dict(batch=0), dict(max_k=-1), dict(max_k=64), dict(heads=30), dict(d=32),
+               dict(maxc=0), dict(window=-1), dict(sinks=-1)):
+        assert wsize(**kw) == 0
+
+
+def test_reference_of_what_stays():
+    """Against sorting by hand; protected ends, ties, NaN and -0."""
+    w = np.array([0.0, 5, -0.0, 3, 3, np.nan, 9, 3, 1, 0], np.float32)
+    assert E.kept(w, 10, 4, 0, 0) == [1, 3, 4, 6]
+    assert E.kept(w, 10, 5, 1, 1) == [0, 1, 3, 6, 9]
+    assert E.kept(w, 10, 4, 2, 2) == [0, 1, 8, 9]
+    assert E.kept(w, 10, 9, 0, 0) == [0, 1, 2, 3, 4, 6, 7, 8, 9]       # NaN goes first
+    assert E.kept(np.zeros(6, np.float32), 6, 3, 0, 1) == [0, 1, 5]
+    w = np.array([-1, -np.inf, np.nan, np.inf, -2], np.float32)
+    assert [E.kept(w, 5, m, 0, 0) for m in (1, 2, 3, 4)] == [[3], [0, 3], [0, 3, 4], [0, 1, 3, 4]]
+
+
+def test_reference_weights_sum_to_the_counted_rows():
+    rng = np.random.default_rng(0)
+    k = rng.standard_normal((20, 2, 64))
+    q = rng.standard_normal((4, 6, 64))
+    w, tol = E.weights(q, k, 16, 3, 0.1, 0, 0)
+    assert np.allclose(w.sum(-1), 9) and w.shape == (2, 20) and not w[:, 19].any()
+    assert np.all(tol >= 0) and np.all(tol < 1e-4)
+
+
+@pytest.mark.parametrize("source,kernels", [
+    ("kvprompt.hip", {"8k_prompt": 9, "14k_prompt_widen": 3, "13k_prompt_join": 6, "13k_prompt_plan": 1}),
+    ("kvbudget.hip", {"9k_weights": 54, "7k_evict": 6, "14k_evict_tables": 1})])
+def test_no_kernel_spills(source, kernels, tmp_path):
+    flags = [f for f in build.HIPCC_FLAGS if f != "-shared"]
+    path = next(s for s in build.SRC if s.endswith(source))
+    done = subprocess.run([build.hipcc(), *flags, "-I", build.INC, "--cuda-device-only", "-c", path, "-o",
+                           str(tmp_path / "x.o"), "-Rpass-analysis=kernel-resource-usage"],
+                          capture_output=True, text=True)
+    assert done.returncode == 0, done.stderr[-2000:]
+    found = spills(done.stderr)
+    for kernel, count in kernels.items():
+        names = [n for n in found if f"{kernel}I" in n or f"{kernel}E" in n]
+        assert len(names) == count, (kernel, names)
+    assert not {n: v for n, v in found.items() if v != (0, 0)}
