@@ -6,9 +6,9 @@
 //   out = sum_t exp(scale q.k_t - m) v_t / sum_t exp(scale q.k_t - m)
 // over the visible t, in one pass with a running maximum m and sum.
 //
-// Three launches: k_prompt_plan lists the work, k_prompt_widen turns the cache of the
-// call's requests into bf16 once, and k_prompt takes it from there (a fourth joins the
-// parts of rows whose context was split).
+// Two launches: k_prompt_prepare lists the work and turns the cache of the call's requests
+// into bf16 once, and k_prompt takes it from there (a third joins the parts of rows whose
+// context was split).
 //
 // Widening once, not per workgroup: a tile of 32 tokens is used by every block of rows
 // behind it, rows * G / 256 times.  The widened tile is laid out as the matrix
@@ -40,15 +40,15 @@ constexpr float FAR = 1073741824.0f;         // 2^30
 
 constexpr int tile_bytes(int d) { return TILE * d * 2 * 2; }    // K, then V, in bf16
 
-struct Block {                               // rows [rb * block_rows, ...) of request b's rows * G
-  int b, rb;
+// A workgroup's work: rows [rb * block_rows, ...) of request b's rows * G over a chunk of their
+// context; with the request's numbers, so that one load tells a workgroup all (ctx < 0: its rows
+// are NaN).
+struct Item {
+  int b, rb, chunk, block, row0, rows, ctx, tile;
 };
-struct Item {                                // a block's share of the context
-  int block, chunk;
-};
-// What the plan writes; offsets in the workspace follow from the call's sizes.
+// What the plan writes.
 struct Head {
-  int items, blocks, tiles, odd;             // odd: some V block stored as NaN
+  int items, blocks;
 };
 
 struct Args {
@@ -73,11 +73,13 @@ struct Args {
   int64_t max_tiles;
   // workspace
   Head* head;
-  int32_t* tile_off;                         // [batch + 1] first widened tile of a request
-  Block* blocks;
-  Item* items;
+  Item* items;                               // by falling work
+  Item* blocks;                              // chunk 0 of every block, in order
   uint8_t* wide;                             // [kv_heads][max_tiles][tile_bytes]
-  uint8_t* odd;                              // [kv_heads][max_tiles][32]: a token's V blocks stored as NaN
+  // V blocks stored as NaN: [kv_heads][max_tiles] a tile's tokens that have some, and
+  // [kv_heads][max_tiles][32] which ones
+  uint32_t* odd;
+  uint8_t* odd_blocks;
   float* part;
 };
 
@@ -100,110 +102,170 @@ __device__ __forceinline__ Span block_span(int ctx, int first_row, int last_row,
   return span_of(ctx + first_row, last_row - first_row + 1, window, sinks);
 }
 
-// One workgroup of 1,024: a request per thread, then a block and chunk per thread.
-__global__ __launch_bounds__(1024) void k_prompt_plan(Args a) {
-  constexpr int LEVELS = 64;
-  __shared__ int red[16], sblock[MAX_BATCH + 1], sctx[MAX_BATCH], srows[MAX_BATCH];
-  __shared__ long long wide_sum[16];
-  __shared__ int level[LEVELS];
-  const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
-  int c0 = 0, c1 = 0, ctx = 0, broken = a.batch;
-  if (b < a.batch) {
-    c0 = a.cu[b];
-    c1 = a.cu[b + 1];
-    ctx = a.ctx[b];
-    if (c0 < 0 || c1 < c0 || c1 > a.total_rows) broken = b;
+// The requests of a call, in LDS: statuses by offsets and lengths alone, contexts (-1 where
+// a request has none), and running counts of row blocks and widened tiles.
+struct Requests {
+  int red[4][4], status[MAX_BATCH], row0[MAX_BATCH], rows[MAX_BATCH], ctx[MAX_BATCH];
+  int block[MAX_BATCH + 1], tile[MAX_BATCH + 1];
+  long long held[4];
+};
+// 256 threads, four requests in a row each.
+__device__ __forceinline__ void find_requests(const Args& a, Requests& q) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int c0[4], c1[4], cx[4], broken = a.batch;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = min(4 * tid + i, a.batch - 1);
+    c0[i] = a.cu[b];
+    c1[i] = a.cu[b + 1];
+    cx[i] = a.ctx[b];
   }
-  if (b < LEVELS) level[b] = 0;
+#pragma unroll
+  for (int i = 3; i >= 0; --i)
+    if (4 * tid + i < a.batch && (c0[i] < 0 || c1[i] < c0[i] || c1[i] > a.total_rows)) broken = 4 * tid + i;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) broken = min(broken, __shfl_xor(broken, d));
-  if (lane == 0) red[wave] = broken;
+  if (lane == 0) q.red[0][wave] = broken;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 16; ++w) broken = min(broken, red[w]);
-  const int rows = c1 - c0;
-  int st = b < broken && rows >= 1 ? SV_ROW_OK : SV_ROW_BAD_K;
-  if (st == SV_ROW_OK && (ctx < 0 || (int64_t)ctx + rows > a.max_context)) st = SV_ROW_BAD_PARAM;
-  // what the requests hold so far, against the call's bound
-  long long held = st == SV_ROW_OK ? (long long)ctx + rows : 0;
+  for (int w = 0; w < 4; ++w) broken = min(broken, q.red[0][w]);
+  int st[4];
+  long long held[4], sum = 0;                 // what the requests hold so far, against the call's bound
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const long long y = __shfl_up(held, d);
-    if (lane >= d) held += y;
+  for (int i = 0; i < 4; ++i) {
+    const int rows = c1[i] - c0[i];
+    st[i] = 4 * tid + i < broken && rows >= 1 ? SV_ROW_OK : SV_ROW_BAD_K;
+    if (st[i] == SV_ROW_OK && (cx[i] < 0 || (int64_t)cx[i] + rows > a.max_context)) st[i] = SV_ROW_BAD_PARAM;
+    if (st[i] == SV_ROW_OK) sum += (long long)cx[i] + rows;
+    held[i] = sum;
   }
-  if (lane == 63) wide_sum[wave] = held;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) held += wide_sum[w];
-  if (st == SV_ROW_OK && held > a.total_context) st = SV_ROW_BAD_PARAM;
-
-  const int R = st == SV_ROW_BAD_K ? 0 : rows * a.group;
-  const int nb = (int)(((int64_t)R + a.block_rows - 1) / a.block_rows);
-  const int nt = st == SV_ROW_OK ? span_of(ctx, rows, a.window, a.sinks).tiles : 0;
-  int sb = nb, stl = nt;
+  long long upto = sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(sb, d), z = __shfl_up(stl, d);
+    const long long y = __shfl_up(upto, d);
+    if (lane >= d) upto += y;
+  }
+  if (lane == 63) q.held[wave] = upto;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) upto += q.held[w];
+  int nb[4], nt[4], sb = 0, stl = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (st[i] == SV_ROW_OK && upto - sum + held[i] > a.total_context) st[i] = SV_ROW_BAD_PARAM;
+    const int rows = c1[i] - c0[i];
+    const int64_t R = st[i] == SV_ROW_BAD_K ? 0 : (int64_t)rows * a.group;
+    sb += nb[i] = (int)((R + a.block_rows - 1) / a.block_rows);
+    stl += nt[i] = st[i] == SV_ROW_OK ? span_of(cx[i], rows, a.window, a.sinks).tiles : 0;
+  }
+  int ub = sb, ut = stl;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(ub, d), z = __shfl_up(ut, d);
     if (lane >= d) {
-      sb += y;
-      stl += z;
+      ub += y;
+      ut += z;
     }
   }
-  __syncthreads();
   if (lane == 63) {
-    red[wave] = sb;
-    wide_sum[wave] = stl;
+    q.red[1][wave] = ub;
+    q.red[2][wave] = ut;
   }
   __syncthreads();
   for (int w = 0; w < wave; ++w) {
-    sb += red[w];
-    stl += (int)wide_sum[w];
+    ub += q.red[1][w];
+    ut += q.red[2][w];
   }
-  sblock[b] = sb - nb;
-  sctx[b] = st == SV_ROW_OK ? ctx : -1;
-  srows[b] = rows;
-  if (b < a.batch) {
-    a.status[b] = st;
-    a.tile_off[b] = stl - nt;
+  ub -= sb;
+  ut -= stl;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = 4 * tid + i;
+    q.status[b] = st[i];
+    q.row0[b] = c0[i];
+    q.rows[b] = c1[i] - c0[i];
+    q.ctx[b] = st[i] == SV_ROW_OK ? cx[i] : -1;
+    q.block[b] = ub;
+    q.tile[b] = ut;
+    ub += nb[i];
+    ut += nt[i];
   }
-  if (b == 1023) {
-    sblock[MAX_BATCH] = sb;
-    a.tile_off[a.batch] = stl;
-    a.head->blocks = sb;
-    a.head->tiles = stl;
-    a.head->odd = 0;
+  if (tid == 255) {
+    q.block[MAX_BATCH] = ub;
+    q.tile[MAX_BATCH] = ut;
   }
   __syncthreads();
-  // items by falling work, so that the shortest end the call: count per level, then place
-  const int blocks = sblock[MAX_BATCH], all = blocks * a.chunks;
+}
+// The last request whose count is at most x.
+__device__ __forceinline__ int request_at(const int* count, int batch, int x) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (count[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The 16 positions from t0 on: whether some row of the request sees one of them.
+__device__ __forceinline__ bool half_needed(const Args& a, const Span& sp, int t0) {
+  return t0 < sp.n && (t0 + 16 > sp.first || (a.window > 0 && t0 < min(a.sinks, sp.first)));
+}
+__device__ __forceinline__ int base_of(const Span& sp, int i) {
+  return (i < sp.early ? i : i - sp.early + sp.tile0) * TILE;
+}
+// Requests with a page missing where some row sees a position have no context either.
+__device__ __forceinline__ void check_pages(const Args& a, Requests& q) {
+  const int all = 2 * q.tile[MAX_BATCH];
+  for (int e = threadIdx.x; e < all; e += 256) {
+    const int b = request_at(q.tile, a.batch, e >> 1);
+    const Span sp = span_of(q.ctx[b], q.rows[b], a.window, a.sinks);
+    const int t0 = base_of(sp, (e >> 1) - q.tile[b]) + 16 * (e & 1), slot = t0 >> a.page_log2;
+    if (half_needed(a, sp, t0) &&
+        (slot >= a.ld_table ||
+         (uint32_t)a.table[(int64_t)b * a.ld_table + slot] >= (uint64_t)a.num_pages))
+      q.status[b] = SV_ROW_BAD_PAGE;
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.batch; b += 256)
+    if (q.status[b] == SV_ROW_BAD_PAGE) q.ctx[b] = -1;
+  __syncthreads();
+}
+
+// Items by falling work, so that the shortest end the call: counted per level, then placed.
+__device__ __forceinline__ void plan_items(const Args& a, const Requests& q, int* level) {
+  constexpr int LEVELS = 64;
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int b = tid; b < a.batch; b += 256) a.status[b] = q.status[b];
+  if (tid < LEVELS) level[tid] = 0;
+  __syncthreads();
+  const int blocks = q.block[MAX_BATCH], all = blocks * a.chunks;
   for (int pass = 0; pass < 2; ++pass) {
-    for (int i = b; i < all; i += 1024) {
+    for (int i = tid; i < all; i += 256) {
       const int blk = i / a.chunks, c = i - blk * a.chunks;
-      int lo = 0, hi = a.batch;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sblock[mid] <= blk) lo = mid;
-        else hi = mid;
-      }
-      const int rb = blk - sblock[lo];
-      if (pass == 0 && c == 0) a.blocks[blk] = Block{lo, rb};
+      const int b = request_at(q.block, a.batch, blk), rb = blk - q.block[b];
       int work = c == 0 ? 1 : 0;
-      if (sctx[lo] >= 0) {
-        const int64_t r0 = (int64_t)rb * a.block_rows, R0 = (int64_t)srows[lo] * a.group;
-        const int j0 = (int)(r0 / a.group);
-        const int j1 = (int)((min(r0 + a.block_rows, R0) - 1) / a.group);
-        const int tiles = block_span(sctx[lo], j0, j1, a.window, a.sinks).tiles;
+      if (q.ctx[b] >= 0) {
+        const uint32_t r0 = (uint32_t)rb * a.block_rows, R = (uint32_t)q.rows[b] * a.group;
+        const int j0 = (int)(r0 / (uint32_t)a.group);
+        const int j1 = (int)((min(r0 + a.block_rows, R) - 1) / (uint32_t)a.group);
+        const int tiles = block_span(q.ctx[b], j0, j1, a.window, a.sinks).tiles;
         work = max(work, min(tiles - c * a.chunk_tiles, a.chunk_tiles));
       }
       if (work <= 0) continue;
       const int lv = LEVELS - 1 - (int)((int64_t)work * (LEVELS - 1) / a.chunk_tiles);
-      if (pass == 0) atomicAdd(&level[lv], 1);
-      // (places within a level come as they come: which workgroup computes an item changes
-      // nothing in its result)
-      else a.items[atomicAdd(&level[lv], 1)] = Item{blk, c};
+      if (pass == 0) {
+        atomicAdd(&level[lv], 1);
+      } else {
+        const Item it = {b, rb, c, blk, q.row0[b], q.rows[b], q.ctx[b], q.tile[b]};
+        // (places within a level come as they come: which workgroup computes an item changes
+        // nothing in its result)
+        a.items[atomicAdd(&level[lv], 1)] = it;
+        if (c == 0) a.blocks[blk] = it;
+      }
     }
     __syncthreads();
     if (pass == 0) {
-      if (wave == 0) {
+      if (tid < 64) {
         const int x = level[lane];
         int sum = x;
 #pragma unroll
@@ -212,7 +274,10 @@ __global__ __launch_bounds__(1024) void k_prompt_plan(Args a) {
           if (lane >= d) sum += y;
         }
         level[lane] = sum - x;
-        if (lane == 63) a.head->items = sum;
+        if (lane == 63) {
+          a.head->items = sum;
+          a.head->blocks = blocks;
+        }
       }
       __syncthreads();
     }
@@ -225,56 +290,40 @@ __device__ __forceinline__ uint32_t widen(uint32_t word, float scale) {
                             __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, BYTE));
 }
 
-// A tile of one KV head in bf16:
+// A tile of one KV head in bf16, by a wave or a workgroup:
 //   K [D/16][64][8]     step s, lane (n, g): token n, dims 16 s + 8 g ..
 //   V [D/32][2][64][8]  dims' 32 i + n, tokens 16 u + 4 g + (0..3, 8..11)
 // Positions that no row sees become 0.  A V block stored as NaN becomes 0 as well, and is
 // noted, for it must not reach rows that do not see it (0 * NaN); a K block becomes NaN.
-template <int D>
-__global__ __launch_bounds__(256) void k_prompt_widen(Args a) {
-  const int lane = threadIdx.x & 63;
-  const int tile = blockIdx.x / a.kv_heads, h = blockIdx.x - tile * a.kv_heads;
-  if (tile >= a.tile_off[a.batch]) return;
-  int b = 0;                                  // the last request with tile_off <= tile
-  for (int i = lane; i < a.batch; i += 64) b += a.tile_off[i] <= tile;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) b += __shfl_xor(b, d);
-  b = __builtin_amdgcn_readfirstlane(b) - 1;
-  const int ctx = a.ctx[b], rows = a.cu[b + 1] - a.cu[b];
-  const Span sp = span_of(ctx, rows, a.window, a.sinks);
-  const int i = tile - a.tile_off[b];
-  const int base = (i < sp.early ? i : i - sp.early + sp.tile0) * TILE;
+template <int D, int THREADS>
+__device__ __forceinline__ void widen_tile(const Args& a, const Requests& q, int tile, int h) {
+  const int me = threadIdx.x & (THREADS - 1);
+  const int b = request_at(q.tile, a.batch, tile);
+  const Span sp = span_of(q.ctx[b], q.rows[b], a.window, a.sinks);
+  const int base = base_of(sp, tile - q.tile[b]);
   const int early = a.window > 0 ? min(a.sinks, sp.first) : 0;
   auto seen = [&](int t) { return t < sp.n && (t >= sp.first || t < early); };
   // its units: pages hold 16 tokens at least
   const uint8_t* unit[2];
   const int32_t* tab = a.table + (int64_t)b * a.ld_table;
-  bool bad = false;
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
     const int t0 = base + 16 * hf, slot = t0 >> a.page_log2;
-    // whether some position of the half is seen
-    const bool need = t0 < sp.n && (t0 + 16 > sp.first || t0 < early);
-    uint32_t id = 0;
-    bool have = need && slot < a.ld_table;
-    if (have) {
-      id = (uint32_t)tab[slot];
-      have = id < (uint64_t)a.num_pages;
-    }
-    bad |= need && !have;
-    unit[hf] = have ? a.pages + ((int64_t)id * a.kv_heads + h) * a.unit : nullptr;
+    const bool have = half_needed(a, sp, t0) && slot < a.ld_table;
+    const uint32_t id = have ? (uint32_t)tab[slot] : 0xffffffffu;
+    unit[hf] = id < (uint64_t)a.num_pages ? a.pages + ((int64_t)id * a.kv_heads + h) * a.unit : nullptr;
   }
-  if (bad && threadIdx.x == 0) a.status[b] = SV_ROW_BAD_PAGE;
   uint8_t* const dst = a.wide + ((int64_t)h * a.max_tiles + tile) * tile_bytes(D);
   const int P = a.page;
 
-  for (int w = threadIdx.x; w < D / 16 * 64; w += 256) {
-    const int s = w >> 6, n = w & 31, g = w >> 5 & 1;
+#pragma unroll
+  for (int w0 = 0; w0 < D / 16 * 64; w0 += THREADS) {
+    const int w = w0 + me, s = w >> 6, n = w & 31, g = w >> 5 & 1;
     const int t = base + n, at = t & (P - 1);
-    const uint8_t* u = unit[n >> 4];
+    const uint8_t* u = n < 16 ? unit[0] : unit[1];
     u32x4 y = {0, 0, 0, 0};
     if (u && seen(t)) {
-      const uint32_t x = load_any<uint32_t>(u + at * (D / 2) + 8 * s + 4 * g);
+      const uint32_t x = *(const uint32_t*)(u + at * (D / 2) + 8 * s + 4 * g);
       const uint32_t e = u[off_ks(P, D) + (at >> 3) * (D / 4) + (s / 2) * 8 + (at & 7)];
       const float sc = __builtin_bit_cast(float, e << 23);
       y[0] = widen<0>(x, sc);
@@ -285,20 +334,49 @@ __global__ __launch_bounds__(256) void k_prompt_widen(Args a) {
     }
     *(u32x4*)(dst + w * 16) = y;
   }
-  // V: a pair of dims (a byte of a token) for 8 tokens
-  for (int w = threadIdx.x; w < D / 2 * 4; w += 256) {
+  // V: a pair of dims (a byte of a token) for 8 tokens, 4 of which lie side by side
+  constexpr int B = D / 32;                   // bytes of a token in a 16th of the dims
+#pragma unroll
+  for (int w0 = 0; w0 < D / 2 * 4; w0 += THREADS) {
+    const int w = w0 + me;
+    if (D / 2 * 4 % THREADS != 0 && w >= D / 2 * 4) break;
     const int c = w % (D / 2), ug = w / (D / 2), u2 = ug >> 1, g = ug & 1;
-    const uint8_t* u = unit[u2];
-    const int n16 = 2 * c / (D / 16), byte = c % (D / 32);
+    const uint8_t* u = u2 ? unit[1] : unit[0];
+    const int n16 = 2 * c / (D / 16), byte = c % B;
     uint32_t x[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int t = base + 16 * u2 + 8 * (k >> 2) + 4 * g + (k & 3), at = t & (P - 1);
-      x[k] = 0;
-      if (u && seen(t)) {
-        const uint32_t v = u[off_v(P, D) + (at >> 3) * (4 * D) + n16 * (D / 4) + (at & 7) * (D / 32) + byte];
-        const uint32_t e = u[off_vs(P, D) + (at >> 3) * (D / 4) + (2 * c / 32) * 8 + (at & 7)];
-        if (e != 255) x[k] = widen<0>(v, __builtin_bit_cast(float, e << 23));
+    for (int k = 0; k < 8; ++k) x[k] = 0;
+    if (u) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int t0 = base + 16 * u2 + 8 * hf + 4 * g, at = t0 & (P - 1);
+        const uint8_t* v = u + off_v(P, D) + (at >> 3) * (4 * D) + n16 * (D / 4) + (at & 7) * B;
+        const uint32_t e4 = *(const uint32_t*)(u + off_vs(P, D) + (at >> 3) * (D / 4) + (2 * c / 32) * 8 + (at & 7));
+        uint32_t word[B];
+        if constexpr (B == 2) {
+          const u32x2 y = *(const u32x2*)v;
+          word[0] = y[0];
+          word[1] = y[1];
+        } else {
+#pragma unroll
+          for (int i = 0; i < B / 4; ++i) {
+            const u32x4 y = *(const u32x4*)(v + 16 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) word[4 * i + j] = y[j];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t e = e4 >> 8 * k & 255u;
+          uint32_t code;
+          if constexpr (B == 8) {
+            const uint32_t even = word[2 * k], more = word[2 * k + 1];
+            code = (byte < 4 ? even : more) >> 8 * (byte & 3);
+          }
+          else if constexpr (B == 4) code = word[k] >> 8 * byte;
+          else code = word[k / 2] >> 8 * (2 * (k & 1) + byte);
+          if (e != 255 && seen(t0 + k)) x[4 * hf + k] = widen<0>(code, __builtin_bit_cast(float, e << 23));
+        }
       }
     }
     u32x4 lo, hi;
@@ -311,15 +389,41 @@ __global__ __launch_bounds__(256) void k_prompt_widen(Args a) {
     to[0] = lo;
     to[1] = hi;
   }
-  if (threadIdx.x < 32) {
-    const int n = threadIdx.x, t = base + n, at = t & (P - 1);
-    const uint8_t* u = unit[n >> 4];
+  if (me < 32) {
+    const int n = me, t = base + n, at = t & (P - 1);
+    const uint8_t* u = n < 16 ? unit[0] : unit[1];
     uint32_t m = 0;
     if (u && seen(t))
+#pragma unroll
       for (int k = 0; k < D / 32; ++k)
         m |= (uint32_t)(u[off_vs(P, D) + (at >> 3) * (D / 4) + k * 8 + (at & 7)] == 255) << k;
-    a.odd[((int64_t)h * a.max_tiles + tile) * TILE + n] = (uint8_t)m;
-    if (m) a.head->odd = 1;
+    const int64_t at_tile = (int64_t)h * a.max_tiles + tile;
+    a.odd_blocks[at_tile * TILE + n] = (uint8_t)m;
+    const uint32_t any = (uint32_t)__ballot(m != 0);
+    if (n == 0) a.odd[at_tile] = any;
+  }
+}
+
+// Workgroup 0 lists the items, the others widen the tiles of the requests' KV heads.
+template <int D>
+__global__ __launch_bounds__(256) void k_prompt_prepare(Args a) {
+  __shared__ Requests q;
+  __shared__ int level[64];
+  find_requests(a, q);
+  if (blockIdx.x == 0) {
+    check_pages(a, q);
+    plan_items(a, q, level);
+    return;
+  }
+  // a tile of a KV head for each wave, or workgroup where there are few (64 prompts of 1 to 700
+  // rows, 18,000 positions: 13.6 us, a workgroup each 18.7; one of 40 rows: 10.2 and 7.2)
+  const int units = q.tile[MAX_BATCH] * a.kv_heads, first = (int)blockIdx.x - 1, step = (int)gridDim.x - 1;
+  if (units <= step) {
+    for (int u = first; u < units; u += step) widen_tile<D, 256>(a, q, u / a.kv_heads, u % a.kv_heads);
+  } else {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int u = 4 * first + wave; u < units; u += 4 * step)
+      widen_tile<D, 64>(a, q, u / a.kv_heads, u % a.kv_heads);
   }
 }
 
@@ -353,10 +457,10 @@ struct Prompt {
       r -= (float)t[i];
     }
   }
-  __device__ __forceinline__ void init(const Args& a, int row0, int ctx, int h, int64_t r0, int64_t R,
+  __device__ __forceinline__ void init(const Args& a, int row0, int ctx, int h, uint32_t r0, uint32_t R,
                                        u32x4* q_lds) {
     const int n = threadIdx.x & 31, g = threadIdx.x >> 5 & 1;
-    const uint32_t r = (uint32_t)min(r0 + n, R - 1);
+    const uint32_t r = min(r0 + n, R - 1);
     const uint32_t j = r / (uint32_t)a.group, hq = h * a.group + r - j * a.group;
     pos = ctx + (int)j;
     const T* src = (const T*)a.q + ((int64_t)row0 + j) * a.ld_q + (int64_t)hq * D + 8 * g;
@@ -481,11 +585,10 @@ struct Prompt {
         }
   }
   // V blocks stored as NaN: rows that see the token are NaN in the block's dims.
-  __device__ __forceinline__ void note(const Args& a, const uint8_t* odd, int base) {
-#pragma nounroll
-    for (int t = 0; t < TILE; ++t) {
-      const uint32_t bits = odd[t];
-      if (bits && sees(a, base + t)) poison |= bits;
+  __device__ __forceinline__ void note(const Args& a, int64_t place, int base) {
+    for (uint32_t m = a.odd[place]; m; m &= m - 1) {
+      const int t = __builtin_ctz(m);
+      if (sees(a, base + t)) poison |= a.odd_blocks[place * TILE + t];
     }
   }
 };
@@ -500,42 +603,40 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   __shared__ u32x4 lds[2][STAGE * WORDS], q_lds[A::Q_LDS ? WAVES : 1][A::Q_LDS ? A::Q_LDS : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int of = blockIdx.x % PARTS, hit = blockIdx.x / PARTS, it = hit / a.kv_heads, h = hit - it * a.kv_heads;
+  const Item item = a.items[it];              // (anything, past the last)
   if (it >= a.head->items) return;
-  const Item item = a.items[it];
-  const Block blk = a.blocks[item.block];
-  const int b = blk.b, row0 = a.cu[b], rows = a.cu[b + 1] - row0, ctx = a.ctx[b];
-  const int st = a.status[b];
-  const int64_t R = (int64_t)rows * a.group, r0 = (int64_t)blk.rb * a.block_rows;
-  const int64_t rw = r0 + wave * 32;          // the wave's first row
+  const int row0 = item.row0, rows = item.rows, ctx = item.ctx;
+  // (rows * heads of a call are less than 2^31)
+  const uint32_t R = (uint32_t)rows * a.group, r0 = (uint32_t)item.rb * a.block_rows;
+  const uint32_t rw = r0 + wave * 32;         // the wave's first row
   const int n = lane & 31, g = lane >> 5;
-  auto row_out = [&](int64_t r) {
-    const uint32_t j = (uint32_t)r / (uint32_t)a.group, hq = h * a.group + (uint32_t)r - j * a.group;
+  auto row_out = [&](uint32_t r) {
+    const uint32_t j = r / (uint32_t)a.group, hq = h * a.group + r - j * a.group;
     return (T*)a.out + ((int64_t)row0 + j) * a.ld_out + (int64_t)hq * D + of * OD;
   };
-  if (st != SV_ROW_OK) {                      // the request's rows are NaN
+  if (ctx < 0) {                              // the request's rows are NaN
     if (item.chunk > 0 || rw + n >= R) return;
     T* const dst = row_out(rw + n);
     for (int i = 0; i < OD / 2; ++i) dst[g * (OD / 2) + i] = (T)__builtin_nanf("");
     return;
   }
-  const int j0 = (int)(r0 / a.group), j1 = (int)((min(r0 + a.block_rows, R) - 1) / a.group);
+  const int j0 = (int)(r0 / (uint32_t)a.group);
+  const int j1 = (int)((min(r0 + a.block_rows, R) - 1) / (uint32_t)a.group);
   const Span all = span_of(ctx, rows, a.window, a.sinks);
   const Span sp = block_span(ctx, j0, j1, a.window, a.sinks);
   const int begin = item.chunk * a.chunk_tiles, end = min(sp.tiles, begin + a.chunk_tiles);
   const bool whole = sp.tiles <= a.chunk_tiles;
   const float c = a.scale * LOG2E;
-  const int64_t first = (int64_t)h * a.max_tiles + a.tile_off[b];
-  // tile i of the block, in tokens, and where its widened form lies
-  auto base_of = [&](int i) { return (i < sp.early ? i : i - sp.early + sp.tile0) * TILE; };
-  auto place = [&](int i) {
+  const int64_t first = (int64_t)h * a.max_tiles + item.tile;
+  // where tile i of the block lies in its widened form
+    auto place = [&](int i) {
     const int t = i < sp.early ? i : i - sp.early + sp.tile0;
     return first + (t < all.early ? t : t - all.tile0 + all.early);
   };
   // positions of the wave's rows
-  const int w0 = ctx + (int)(min(rw, R - 1) / a.group);
-  const int w1 = ctx + (int)(min(rw + 31, R - 1) / a.group);
+  const int w0 = ctx + (int)(min(rw, R - 1) / (uint32_t)a.group);
+  const int w1 = ctx + (int)(min(rw + 31, R - 1) / (uint32_t)a.group);
   const bool live = rw < R;
-  const bool odd = a.head->odd != 0;
   auto masked = [&](int base) {
     return base + TILE - 1 > w0 || (a.window > 0 && base <= w1 - a.window && base + TILE > a.sinks);
   };
@@ -559,6 +660,9 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   A x;
   u32x4* const my_q = q_lds[A::Q_LDS ? wave : 0];
   x.init(a, row0, ctx, h, rw, R, my_q);
+  uint32_t some_odd = 0;
+  for (int i = begin + (int)threadIdx.x; i < end; i += 64 * WAVES) some_odd |= a.odd[place(i)];
+  const bool odd = __syncthreads_or(some_odd != 0);
   __syncthreads();
   int buf = 0;
   for (int i = begin; i < end; i += STAGE) {
@@ -570,7 +674,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
 #pragma unroll
       for (int k = 0; k < A::PAIR; ++k) {
         // (behind the last tile lies that tile once more: no row sees it there)
-        base[k] = i + t + k < end ? base_of(i + t + k) : 0x7fffff00;
+        base[k] = i + t + k < end ? base_of(sp, i + t + k) : 0x7fffff00;
         some |= base[k] <= w1;
         hide |= masked(base[k]);
       }
@@ -578,7 +682,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
         x.step(a, lds[buf] + t * WORDS, my_q, base, hide, c);
         if (odd)
           for (int k = 0; k < A::PAIR; ++k)
-            if (i + t + k < end) x.note(a, a.odd + place(i + t + k) * TILE, base[k]);
+            if (i + t + k < end) x.note(a, place(i + t + k), base[k]);
       }
     }
     buf ^= 1;
@@ -591,7 +695,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   const float sum = x.l + __shfl_xor(x.l, 32);
   int ln = lane & 31;
   asm volatile("" : "+v"(ln));                // (or where the row lies takes registers in the loop)
-  const int64_t r = rw + ln;
+  const uint32_t r = rw + ln;
   if (r >= R) return;
   T* const dst = row_out(r);
   const float inv = 1.f / sum;
@@ -629,12 +733,13 @@ __global__ __launch_bounds__(256) void k_prompt_join(Args a) {
   const int local = (int)(blockIdx.x % per) * 16 + (threadIdx.x >> 4), e0 = (threadIdx.x & 15) * E;
   const int hb = blockIdx.x / per, h = hb % a.kv_heads, bl = hb / a.kv_heads;
   if (bl >= a.head->blocks) return;
-  const Block blk = a.blocks[bl];
-  const int b = blk.b, row0 = a.cu[b], rows = a.cu[b + 1] - row0;
-  if (a.status[b] != SV_ROW_OK) return;
-  const int64_t R = (int64_t)rows * a.group, r0 = (int64_t)blk.rb * a.block_rows, r = r0 + local;
-  const int j0 = (int)(r0 / a.group), j1 = (int)((min(r0 + a.block_rows, R) - 1) / a.group);
-  const int tiles = block_span(a.ctx[b], j0, j1, a.window, a.sinks).tiles;
+  const Item blk = a.blocks[bl];
+  if (blk.ctx < 0) return;
+  const int row0 = blk.row0, rows = blk.rows;
+  const uint32_t R = (uint32_t)rows * a.group, r0 = (uint32_t)blk.rb * a.block_rows, r = r0 + local;
+  const int j0 = (int)(r0 / (uint32_t)a.group);
+  const int j1 = (int)((min(r0 + a.block_rows, R) - 1) / (uint32_t)a.group);
+  const int tiles = block_span(blk.ctx, j0, j1, a.window, a.sinks).tiles;
   const int n = (tiles + a.chunk_tiles - 1) / a.chunk_tiles;
   if (n < 2 || r >= R) return;
   const int64_t slot = ((int64_t)bl * a.kv_heads + h) * a.chunks * a.block_rows + local;
@@ -652,7 +757,7 @@ __global__ __launch_bounds__(256) void k_prompt_join(Args a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(y[e], w, acc[e]);
   }
-  const uint32_t j = (uint32_t)r / (uint32_t)a.group, hq = h * a.group + (uint32_t)r - j * a.group;
+  const uint32_t j = r / (uint32_t)a.group, hq = h * a.group + r - j * a.group;
   T z[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) z[e] = (T)(acc[e] / sum);
@@ -664,7 +769,7 @@ __global__ __launch_bounds__(256) void k_prompt_join(Args a) {
 struct Plan {
   int waves, block_rows, max_blocks, chunks, chunk_tiles;
   int64_t max_tiles;
-  size_t tile_off, blocks, items, odd, wide, part, bytes;
+  size_t blocks, items, odd, odd_blocks, wide, part, bytes;
 };
 
 static size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -673,17 +778,19 @@ static bool plan_of(int dtype, int batch, int total_rows, int heads, int kv_head
                     int max_context, int64_t total_context, int window, int sinks, Plan& p) {
   const int64_t R = (int64_t)total_rows * (heads / kv_heads);
   // Four waves per workgroup, two workgroups per compute unit, so that one's start and end
-  // run beside the other's products; or eight for bf16 calls of many workgroups, which share
-  // a tile's way to LDS.  (One prompt of 15,991 rows, 2,000 blocks of 256 rows over all KV
-  // heads: 1,838 us, with four waves 1,940; four of 1,500 to 4,000 rows, 1,176 blocks: 304
-  // and 307; two of 150 to 600 after 8,000 to 30,000 positions: 306 and 265; eight fp32 ones
-  // with a window: 205 and 175.)
+  // run beside the other's products; or eight, which share a tile's way to LDS, for bf16 calls
+  // of many workgroups and long contexts.  (One prompt of 15,991 rows, 2,000 blocks of 256
+  // rows over all KV heads: 1,838 us, with four waves 1,940; four of 1,500 to 4,000 rows, 1,176
+  // blocks: 304 and 307; 64 of 1 to 700, 2,700 blocks at D=64: 86 and 83; two of 150 to 600
+  // after 8,000 to 30,000 positions: 306 and 265; eight fp32 ones with a window: 205 and 175.)
   p.waves = 8;
   int64_t blocks = 0;
   for (;; p.waves = 4) {
     p.block_rows = 32 * p.waves;
     blocks = (R + (int64_t)batch * (p.block_rows - 1)) / p.block_rows;
-    if (p.waves == 4 || (dtype == SV_BF16 && R * kv_heads >= 1024 * 256)) break;
+    if (p.waves == 4 ||
+        (dtype == SV_BF16 && R * kv_heads >= 1024 * 256 && total_context >= (int64_t)batch * 1024))
+      break;
   }
   // tiles of all requests, and of one
   int64_t tiles = total_context / TILE + batch, one = max_context / TILE + 1;
@@ -707,13 +814,13 @@ static bool plan_of(int dtype, int batch, int total_rows, int heads, int kv_head
   if (wide * chunks * (p.block_rows / 16) * 2 >= (1ll << 24) || tiles * kv_heads >= (1ll << 24)) return false;
   p.max_blocks = (int)blocks;
   size_t at = round256(sizeof(Head));
-  p.tile_off = at;
-  at += round256(((size_t)batch + 1) * 4);
   p.blocks = at;
-  at += round256((size_t)blocks * sizeof(Block));
+  at += round256((size_t)blocks * sizeof(Item));
   p.items = at;
   at += round256((size_t)(blocks * chunks) * sizeof(Item));
   p.odd = at;
+  at += round256((size_t)(tiles * kv_heads) * 4);
+  p.odd_blocks = at;
   at += round256((size_t)(tiles * kv_heads) * TILE);
   p.wide = at;
   at += (size_t)(tiles * kv_heads) * tile_bytes(d);
@@ -736,9 +843,8 @@ static bool sizes_ok(int dtype, int batch, int total_rows, int heads, int kv_hea
 template <int D, int OD, typename T>
 static int launch(const Args& a, const Plan& p, hipStream_t s) {
   constexpr int PER_SIMD = sizeof(T) == 4 && D == 256 ? 1 : 2;
-  hipLaunchKernelGGL(k_prompt_plan, dim3(1), dim3(1024), 0, s, a);
-  if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
-  hipLaunchKernelGGL((k_prompt_widen<D>), dim3((uint32_t)(p.max_tiles * a.kv_heads)), dim3(256), 0, s, a);
+  const int64_t units = p.max_tiles * a.kv_heads;
+  hipLaunchKernelGGL((k_prompt_prepare<D>), dim3(1 + (uint32_t)(units < 1024 ? units : 1024)), dim3(256), 0, s, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   const uint32_t wide = (uint32_t)(p.max_blocks * a.kv_heads);
   const dim3 grid(wide * p.chunks * (D / OD));
@@ -828,10 +934,10 @@ int spec_kv_prompt_attention(const void* q, int64_t ld_q, int dtype, const int32
   a.max_tiles = p.max_tiles;
   uint8_t* w = (uint8_t*)workspace;
   a.head = (prompt::Head*)w;
-  a.tile_off = (int32_t*)(w + p.tile_off);
-  a.blocks = (prompt::Block*)(w + p.blocks);
+  a.blocks = (prompt::Item*)(w + p.blocks);
   a.items = (prompt::Item*)(w + p.items);
-  a.odd = w + p.odd;
+  a.odd = (uint32_t*)(w + p.odd);
+  a.odd_blocks = w + p.odd_blocks;
   a.wide = w + p.wide;
   a.part = (float*)(w + p.part);
   hipStream_t s = (hipStream_t)stream;

@@ -136,7 +136,7 @@ def test_reference_weights_sum_to_the_counted_rows():
 
 
 @pytest.mark.parametrize("source,kernels", [
-    ("kvprompt.hip", {"8k_prompt": 9, "14k_prompt_widen": 3, "13k_prompt_join": 6, "13k_prompt_plan": 1}),
+    ("kvprompt.hip", {"8k_prompt": 9, "16k_prompt_prepare": 3, "13k_prompt_join": 6}),
     ("kvbudget.hip", {"9k_weights": 54, "7k_evict": 6, "14k_evict_tables": 1})])
 def test_no_kernel_spills(source, kernels, tmp_path):
     flags = [f for f in build.HIPCC_FLAGS if f != "-shared"]
