@@ -597,8 +597,9 @@ template <int D, int OD, int WAVES, int PER_SIMD, typename T>
 __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   using A = Prompt<D, OD, T>;
   constexpr int PARTS = D / OD;               // workgroups that share a block's dims
-  // tiles in LDS between two barriers, twice (160 KiB per compute unit)
-  constexpr int STAGE = D == 256 ? 1 : WAVES / 2;
+  // tiles in LDS between two barriers, twice (160 KiB per compute unit; the more, the better:
+  // four prompts of 1,500 to 4,000 rows at D=256 with two 1,096 us, with one 1,299)
+  constexpr int STAGE = D < 256 ? WAVES / 2 : sizeof(T) == 2 ? WAVES / 4 : 1;
   constexpr int WORDS = A::WORDS, LOADS = STAGE * WORDS / (64 * WAVES);
   __shared__ u32x4 lds[2][STAGE * WORDS], q_lds[A::Q_LDS ? WAVES : 1][A::Q_LDS ? A::Q_LDS : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
