@@ -837,20 +837,38 @@ __global__ __launch_bounds__(THREADS, THREADS == 256 && D < 256 ? 5 : 1) void k_
   uint8_t* const pool = a.pages + layer * a.layer_bytes + (int64_t)h * a.unit;
   const int64_t page_bytes = (int64_t)a.unit * a.kv_heads;
   const int P = a.page;
+  // A list ends within a wave's step as a rule: the wave goes on from there, with the step's
+  // ballots as they were.  Weights are never read again where the moves have changed them: in
+  // steps after slot s0 every position is s0 or more.
+  int slot = slot0, tied = tie0, next = 0;    // before the step that the wave goes on with
+  uint64_t bs = 0, bt = 0;
+  bool held = false;                          // its ballots are known
   for (int s0 = 0; s0 < m; s0 += LIST) {
     const int s1 = min(m, s0 + LIST);
     __syncthreads();                          // (the list before is used up)
-    int slot = slot0, tied = tie0;
-    each([&](int i, uint32_t k) {
-      const uint64_t bs = __ballot(sure_of(i, k)), bt = __ballot(tie_of(i, k));
+    auto put = [&](int i, auto&& key_of_step) {
+      if (i != next || slot >= s1) return;
+      if (!held) {
+        const uint32_t k = key_of_step(i);
+        bs = __ballot(sure_of(i, k));
+        bt = __ballot(tie_of(i, k));
+      }
       const uint64_t below = (1ull << lane) - 1;
       const int my_ties = min(max(ties - tied, 0), (int)__popcll(bt & below));
       const bool keep = (bs >> lane & 1) || ((bt >> lane & 1) && tied + (int)__popcll(bt & below) < ties);
       const int to = slot + __popcll(bs & below) + my_ties;
       if (keep && to >= s0 && to < s1) list[to - s0] = from + i * 64 + lane;
-      slot += __popcll(bs) + min(max(ties - tied, 0), (int)__popcll(bt));
+      const int after = slot + __popcll(bs) + min(max(ties - tied, 0), (int)__popcll(bt));
+      held = after > s1;
+      if (held) return;
+      slot = after;
       tied += __popcll(bt);
-    });
+      next = i + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+      if (i < steps) put(i, [&](int x) { return key[x]; });
+    for (int i = max(KEEP, next); i < steps && i == next && slot < s1; ++i) put(i, key_at);
     __syncthreads();
     for (int i0 = s0; i0 < s1; i0 += THREADS) {
       const int to = i0 + tid, p = to < s1 ? list[to - s0] : to;

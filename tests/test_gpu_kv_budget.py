@@ -290,6 +290,17 @@ def test_evict_of_many_workgroups_and_long_rows(d):
     run_evict(d, 16, 8, 1, lens, [3000 if b == 5 else 33 for b in range(130)], sinks=1, recent=1, seed=d)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict_of_few_from_long_rows(d, ties):
+    """Most positions stay, over several lists: what the first moves write lies where weights are
+    looked up again for the later ones."""
+    make = (lambda r, s: r.integers(0, 40, s)) if ties else None
+    run_evict(d, 64, 1, 1, [70000, 17], [67000, 16], sinks=3, recent=5, seed=d, make=make)
+    lens = [9000 if b == 5 else 40 + b % 20 for b in range(130)]
+    run_evict(d, 16, 8, 1, lens, [8500 if b == 5 else 33 for b in range(130)], seed=d, make=make)
+
+
 @pytest.mark.parametrize("name,make", [
     ("all equal", lambda r, s: np.ones(s)),
     ("zeros and minus zeros", lambda r, s: np.where(r.random(s) < 0.5, 0.0, -0.0)),
