@@ -327,11 +327,13 @@ int spec_verify_sampled_noalloc(const void* target_logits, int target_dtype, int
  * ---------------------------------------------------------------------------
  * The KV cache around a verify: paged, held in 4 bits
  * ---------------------------------------------------------------------------
- * A step of a serving loop is reserve -> (per layer: append, attention) ->
- * verify -> drain -> release: "The four high-risk coupling points" item 1 of
- * "Adding Speculative Decoding" (slots reserved for the k+1 rows, given back
- * after the drain), the chain mask of its "Verification and sampling" item 1,
- * and the page-wise free of the Rust page's "Production Pitfalls" item 2.
+ * A step of a serving loop is reserve -> (per layer: append, attention; of whole
+ * prompts: prompt_attention) -> verify -> drain -> release, and where requests
+ * are held to a budget of positions (per layer: attention_weights) -> evict: "The
+ * four high-risk coupling points" item 1 of "Adding Speculative Decoding" (slots
+ * reserved for the k+1 rows, given back after the drain), the chain mask of its
+ * "Verification and sampling" item 1, and the page-wise free of the Rust page's
+ * "Production Pitfalls" item 2.
  *
  * Values: blocks of 32 dims share a scale 2^(byte - 127); an element is a
  *   4-bit code, sign bit then {0, .5, 1, 1.5, 2, 3, 4, 6}.  A block's scale is
@@ -362,7 +364,8 @@ int spec_verify_sampled_noalloc(const void* target_logits, int target_dtype, int
  *   which no request has rows makes no append and no attention).  Return values
  *   as elsewhere.  A workspace that is needed and NULL is SV_ERR_NULL; one that
  *   is not 16-byte aligned is SV_ERR_NULL in
- *   spec_kv_attention and SV_ERR_SHAPE in spec_kv_reserve and spec_kv_compact.
+ *   the calls of attention and weights, SV_ERR_SHAPE in spec_kv_reserve and
+ *   spec_kv_compact.
  */
 
 /* Bytes of a page of one layer (0 on invalid sizes). */
@@ -522,8 +525,9 @@ size_t spec_kv_weights_workspace_bytes(int dtype, int batch, int max_k, int head
  *                  q_out)
  *   row_counts     int32 [batch], or NULL: all rows; outside [0, rows] is SV_ROW_BAD_PARAM
  *   weights_in     float [batch][kv_heads][ld_weights], or NULL: zeros
- *   weights_out    the same layout; weights_in itself, or memory apart from it.  Written for
- *                  t < n only; requests whose status is not SV_ROW_OK are left as they were
+ *   weights_out    the same layout; weights_in itself, or memory apart from it (SV_ERR_SHAPE
+ *                  where they overlap).  Written for t < n only; requests whose status is
+ *                  not SV_ROW_OK are left as they were
  *   ld_weights     at least max_context
  *   max_k, max_context, scale, window, sinks, status: as spec_kv_attention
  *   workspace      spec_kv_weights_workspace_bytes(), any contents; calls that may run at

@@ -944,6 +944,11 @@ int spec_kv_attention_weights(const void* q, int64_t ld_q, int dtype, const int3
       ld_weights < max_context || !(scale > 0.f) || !(scale <= 2.0e38f) || !aligned16(pages) ||
       !budget::plan_of(dtype, batch, max_k, heads, kv_heads, head_dim, max_context, window, sinks, p))
     return SV_ERR_SHAPE;
+  if (weights_in && weights_in != weights_out) {
+    const uintptr_t in = (uintptr_t)weights_in, out = (uintptr_t)weights_out;
+    const size_t bytes = (size_t)batch * kv_heads * ld_weights * sizeof(float);
+    if ((in < out ? out - in : in - out) < bytes) return SV_ERR_SHAPE;
+  }
   if (!workspace || !aligned16(workspace)) return SV_ERR_NULL;
   if (p.bytes > workspace_bytes) return SV_ERR_WORKSPACE;
   budget::WeightArgs a;

@@ -59,6 +59,7 @@ def test_prompt_refusals(kw, rc):
 
 @pytest.mark.parametrize("kw,rc", COMMON + [
     (dict(wout=None), 1), (dict(max_k=-1), 2), (dict(max_k=64), 2), (dict(ldw=63), 2),
+    (dict(win=F + 16), 2), (dict(wout=F + 16, win=F), 2), (dict(win=F + 2 * 2 * 64 * 4 - 16), 2),
     (dict(batch=1024, heads=1024, kv=1024, ldq=1024 * 128, maxc=1 << 14, ldw=1 << 14), 2)])
 def test_weights_refusals(kw, rc):
     assert _weights(**kw) == rc
