@@ -24,8 +24,15 @@ namespace budget {
 // Scores are S^T[token][row] = K Q^T with v_mfma_f32_16x16x32_bf16, K widened from its codes
 // in registers; a lane holds the scores of one row for 8 tokens.  The sums go over the tiles
 // for each 16 MT rows (statistics in registers), the weights over the rows for each tile
-// (summed over the lanes once).  Where a request is
-// one chunk (short contexts) both passes are one launch.
+// (summed over the lanes once).  Where a request is one chunk (short contexts) both passes
+// are one launch.  fp32 queries go in as three bf16 terms, exactly; nothing is rounded further.
+//
+// What bounds it: vector instructions (widening, exponentials), 62 % of the first pass's time
+// and 66 % of the second's, beside HBM at 3.8 and 3.0 TB/s: 51 + 70 us for 64 requests of 7
+// rows over 512 to 16,384 positions (32 heads over 8, D=128).  Four requests of 64 rows over
+// 1,500 to 4,000 positions, 26 + 32 us: 1.4 waves per SIMD whose reads of queries from LDS and
+// exponentials follow one another (smaller chunks give more waves, and more queries to
+// fetch: no faster; eight waves per workgroup 73 us against 58 for the call).
 
 constexpr int TILE = 32, SUB = 64;            // tokens of a tile; tiles whose pages a wave looks up at once
 // Waves of a workgroup: eight where it does both passes (64 requests over 100 to 1,000 positions
@@ -309,7 +316,8 @@ __device__ __forceinline__ void join(float& m, float& sum, float om, float osum)
 // PASS 1: statistics, 2: weights, 3: both (a request is one chunk).  ONE: a request has at
 // most 16 MT rows.
 template <int D, int MT, bool ONE, int PASS, typename T>
-__global__ __launch_bounds__(64 * waves_of(PASS == 3), PASS != 3 || D == 256 || MT == 4 ? 2 : 4) void k_weights(WeightArgs a) {
+__global__ __launch_bounds__(64 * waves_of(PASS == 3), PASS != 3 || D == 256 || MT == 4 ? 2 : 4)
+void k_weights(WeightArgs a) {
   using A = Weights<D, MT, T>;
   constexpr int WAVES = waves_of(PASS == 3);
   constexpr int ROWS = A::ROWS, DEPTH = 2;    // tiles on their way
@@ -449,7 +457,8 @@ __global__ __launch_bounds__(64 * waves_of(PASS == 3), PASS != 3 || D == 256 || 
           each_tile([&](int k, const KTile<D>& kt) {
             f32x4 s[2][MT];
             const int base = base_of(sp, begin + wave + k * WAVES);
-            A::scores(a, kt, ONE ? q : q + rb * A::Q_WORDS, s, base, masked(base), pos, __builtin_nanf(""));
+            A::scores(a, kt, ONE ? q : q + rb * A::Q_WORDS, s, base, masked(base), pos,
+                      __builtin_nanf(""));
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               float mx = m[mt];
@@ -471,7 +480,8 @@ __global__ __launch_bounds__(64 * waves_of(PASS == 3), PASS != 3 || D == 256 || 
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {   // join the row's four lanes
 #pragma unroll
-            for (int d = 16; d < 64; d <<= 1) join(mc[mt], l[mt], __shfl_xor(mc[mt], d), __shfl_xor(l[mt], d));
+            for (int d = 16; d < 64; d <<= 1)
+              join(mc[mt], l[mt], __shfl_xor(mc[mt], d), __shfl_xor(l[mt], d));
             if (g == 0) part[wave * a.group_rows + rb * ROWS + mt * 16 + n] = f32x2{mc[mt], l[mt]};
           }
         }
@@ -610,7 +620,8 @@ static int launch(const WeightArgs& a, const Plan& p, hipStream_t s) {
   hipLaunchKernelGGL((k_weights<D, MT, ONE, 1, T>), dim3(statuses + items), dim3(64 * waves),
                      queries + waves * stat, s, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
-  hipLaunchKernelGGL((k_weights<D, MT, ONE, 2, T>), dim3(items + gaps), dim3(64 * waves), queries + stat, s, a);
+  hipLaunchKernelGGL((k_weights<D, MT, ONE, 2, T>), dim3(items + gaps), dim3(64 * waves),
+                     queries + stat, s, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
 }
 
@@ -621,6 +632,12 @@ static int launch(const WeightArgs& a, const Plan& p, hipStream_t s) {
 // in order and in place, a slot per thread: slot i gets a position p >= i, so that where a
 // step's positions are all read before its slots are written, no write reaches what a later
 // step reads.  A second launch sets tables, counts and lengths, once all of them are done.
+//
+// What bounds it: the select (three passes over LDS counters, 22 us) and the list (10), then
+// the moves, near HBM's rate: a token's V codes lie in 16 pieces 32 bytes apart (the layout in
+// which attention reads them), so that lines of tokens that go are read too.  64 requests of
+// 900 to 4,096 positions cut to 1,024, 2 layers: 111 us, 238 MB read and 129 written.  One
+// workgroup per compute unit (256 of 32,768 positions): 133 us, 287 and 107 MB.
 
 struct EvictArgs {
   const int32_t* budgets;
@@ -1052,12 +1069,17 @@ int spec_kv_evict(const int32_t* budgets, int batch, int sinks, int recent, floa
   a.status = status;
   hipStream_t s = (hipStream_t)stream;
   const dim3 grid((uint32_t)(layers * batch * kv_heads));
-  // small workgroups where they are many, large ones where each has long rows to itself
-  const bool many = grid.x >= 1024;
+  // 256 threads where they hold whole rows in registers or the workgroups are many, 1,024 for
+  // long rows (us, with 256 and with 1,024: 512 rows of 900 to 4,096 positions 69 and 90, 8 of
+  // 4,000 38 and 42, 1,024 of 16,000 444 and 490; 512 of 16,000 275 and 257, 64 of 8,000 78 and
+  // 65, 256 of 8,000 to 32,768 242 and 143)
+  const bool small = grid.x >= 1024 || ld_weights <= 16 * 256;
 #define SVK_CASE(DD)                                                                              \
   if (head_dim == DD) {                                                                           \
-    if (many) hipLaunchKernelGGL((budget::k_evict<DD, 256, 16>), grid, dim3(256), 0, s, a);       \
-    else hipLaunchKernelGGL((budget::k_evict<DD, 1024, DD == 256 ? 16 : 32>), grid, dim3(1024), 0, s, a);          \
+    if (small) hipLaunchKernelGGL((budget::k_evict<DD, 256, 16>), grid, dim3(256), 0, s, a);      \
+    else                                                                                          \
+      hipLaunchKernelGGL((budget::k_evict<DD, 1024, DD == 256 ? 16 : 32>), grid, dim3(1024), 0,   \
+                         s, a);                                                                   \
   }
   SVK_CASE(64)
   SVK_CASE(128)

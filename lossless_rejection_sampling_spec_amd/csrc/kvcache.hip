@@ -956,10 +956,10 @@ int spec_kv_append_at(const void* q, int64_t ld_q, const void* k, int64_t ld_k, 
                       int64_t ld_v, int dtype, const float* q_weight, const float* k_weight, float eps,
                       const float* cos_sin, int max_position, int rot_dim, int interleaved,
                       const int32_t* cu_seqlens, const int32_t* context_lens,
-                      const int32_t* position_offsets, int batch, int total_rows, int heads, int kv_heads, int head_dim, void* pages,
-                      int64_t num_pages, int page_size, const int32_t* page_table, int64_t ld_table,
-                      void* q_out, int64_t ld_qout, void* k_values, void* v_values, int32_t* status,
-                      void* stream) {
+                      const int32_t* position_offsets, int batch, int total_rows, int heads,
+                      int kv_heads, int head_dim, void* pages, int64_t num_pages, int page_size,
+                      const int32_t* page_table, int64_t ld_table, void* q_out, int64_t ld_qout,
+                      void* k_values, void* v_values, int32_t* status, void* stream) {
   if (!q || !k || !v || !cu_seqlens || !context_lens || !pages || !page_table || !q_out || !status ||
       (rot_dim != 0 && !cos_sin) || (!k_values) != (!v_values))
     return SV_ERR_NULL;

@@ -13,15 +13,27 @@
 // Widening once, not per workgroup: a tile of 32 tokens is used by every block of rows
 // behind it, rows * G / 256 times.  The widened tile is laid out as the matrix
 // instructions' operands, [instruction][lane][8 values], so that its way through LDS is
-// straight copies and reads without bank conflicts.
+// straight copies and reads without bank conflicts.  It is bound by its writes: 29 us of the
+// 1,850 for one prompt of 15,991 rows, 23 of 285 for four of 1,500 to 4,000, 65 of 247 for
+// two of 150 to 600 after 8,000 to 30,000 positions.
 //
-// k_prompt: a workgroup of 4 waves takes one KV head and 128 MT of the request's rows * G
-// query rows (the G heads of a row side by side), a wave 32 MT of them.  Per tile it
-// computes S^T[token][row] = K Q^T, then O^T[dim][row] += V^T P^T with
-// v_mfma_f32_32x32x16_bf16.  With tokens as the rows of S^T a lane holds scores of ONE
-// query row, for 16 of the tile's tokens: statistics are per lane, and the weights are
-// the next product's operand as they are (V is laid out in the order of tokens in which
-// the accumulators hold them).
+// k_prompt: a workgroup of 4 or 8 waves takes one KV head and 32 of the request's rows * G
+// query rows for each wave (the G heads of a row side by side).  Per tile it computes
+// S^T[token][row] = K Q^T, then O^T[dim][row] += V^T P^T with v_mfma_f32_32x32x16_bf16.  With
+// tokens as the rows of S^T a lane holds scores of ONE query row, for 16 of the tile's tokens:
+// statistics are per lane, and the weights are the next product's operand as they are (V is
+// laid out in the order of tokens in which the accumulators hold them).
+//
+// Roundings: bf16 rows' weights are rounded to bf16 for the second product (and summed as
+// rounded), as the matrix instruction takes them; fp32 rows' queries and weights go in as
+// three bf16 terms, exactly.  Scores, statistics and sums are fp32.
+//
+// What bounds it: the waves' alternation of products and softmax, matrix instructions 51 % of
+// the time, vector ones 37 % (one prompt of 15,991 rows, 32 heads over 8 of D=128: 1.14
+// PFLOP/s, where a large bf16 matrix product reaches 1.20 to 1.27; four prompts of 1,500 to
+// 4,000 rows 0.84, their last workgroups ending alone).  Tried and slower: the next tile's
+// scores ahead of this one's softmax (2,307 us against 2,220 of the same kernel without, for
+// the first of these), a barrier per tile over a ring of buffers.
 
 #include "kv_common.h"
 
@@ -351,7 +363,8 @@ __device__ __forceinline__ void widen_tile(const Args& a, const Requests& q, int
       for (int hf = 0; hf < 2; ++hf) {
         const int t0 = base + 16 * u2 + 8 * hf + 4 * g, at = t0 & (P - 1);
         const uint8_t* v = u + off_v(P, D) + (at >> 3) * (4 * D) + n16 * (D / 4) + (at & 7) * B;
-        const uint32_t e4 = *(const uint32_t*)(u + off_vs(P, D) + (at >> 3) * (D / 4) + (2 * c / 32) * 8 + (at & 7));
+        const uint32_t e4 =
+            *(const uint32_t*)(u + off_vs(P, D) + (at >> 3) * (D / 4) + (2 * c / 32) * 8 + (at & 7));
         uint32_t word[B];
         if constexpr (B == 2) {
           const u32x2 y = *(const u32x2*)v;
@@ -603,7 +616,8 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   constexpr int WORDS = A::WORDS, LOADS = STAGE * WORDS / (64 * WAVES);
   __shared__ u32x4 lds[2][STAGE * WORDS], q_lds[A::Q_LDS ? WAVES : 1][A::Q_LDS ? A::Q_LDS : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int of = blockIdx.x % PARTS, hit = blockIdx.x / PARTS, it = hit / a.kv_heads, h = hit - it * a.kv_heads;
+  const int of = blockIdx.x % PARTS, hit = blockIdx.x / PARTS;
+  const int it = hit / a.kv_heads, h = hit - it * a.kv_heads;
   const Item item = a.items[it];              // (anything, past the last)
   if (it >= a.head->items) return;
   const int row0 = item.row0, rows = item.rows, ctx = item.ctx;
@@ -630,7 +644,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   const float c = a.scale * LOG2E;
   const int64_t first = (int64_t)h * a.max_tiles + item.tile;
   // where tile i of the block lies in its widened form
-    auto place = [&](int i) {
+  auto place = [&](int i) {
     const int t = i < sp.early ? i : i - sp.early + sp.tile0;
     return first + (t < all.early ? t : t - all.tile0 + all.early);
   };
@@ -845,7 +859,8 @@ template <int D, int OD, typename T>
 static int launch(const Args& a, const Plan& p, hipStream_t s) {
   constexpr int PER_SIMD = sizeof(T) == 4 && D == 256 ? 1 : 2;
   const int64_t units = p.max_tiles * a.kv_heads;
-  hipLaunchKernelGGL((k_prompt_prepare<D>), dim3(1 + (uint32_t)(units < 1024 ? units : 1024)), dim3(256), 0, s, a);
+  const dim3 prepare(1 + (uint32_t)(units < 1024 ? units : 1024));
+  hipLaunchKernelGGL((k_prompt_prepare<D>), prepare, dim3(256), 0, s, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_LAUNCH;
   const uint32_t wide = (uint32_t)(p.max_blocks * a.kv_heads);
   const dim3 grid(wide * p.chunks * (D / OD));
@@ -897,7 +912,8 @@ int spec_kv_prompt_attention(const void* q, int64_t ld_q, int dtype, const int32
                         window, sinks) ||
       !page_ok(page_size) || num_pages < 1 || num_pages > 0x7fffffff || ld_table < 1 ||
       ld_table > (1 << 30) / page_size || ld_q < (int64_t)heads * head_dim ||
-      ld_out < (int64_t)heads * head_dim || !(scale > 0.f) || !(scale <= 2.0e38f) || !aligned16(pages) || out == q ||
+      ld_out < (int64_t)heads * head_dim || !(scale > 0.f) || !(scale <= 2.0e38f) ||
+      !aligned16(pages) || out == q ||
       !prompt::plan_of(dtype, batch, total_rows, heads, kv_heads, head_dim, max_context, total_context,
                        window, sinks, p))
     return SV_ERR_SHAPE;
