@@ -28,7 +28,7 @@ namespace budget {
 // are one launch.  fp32 queries go in as three bf16 terms, exactly; nothing is rounded further.
 //
 // What bounds it: vector instructions (widening, exponentials), 62 % of the first pass's time
-// and 66 % of the second's, beside HBM at 3.8 and 3.0 TB/s: 51 + 70 us for 64 requests of 7
+// and 66 % of the second's, beside HBM at 3.9 and 3.1 TB/s: 51 + 70 us for 64 requests of 7
 // rows over 512 to 16,384 positions (32 heads over 8, D=128).  Four requests of 64 rows over
 // 1,500 to 4,000 positions, 26 + 32 us: 1.4 waves per SIMD whose reads of queries from LDS and
 // exponentials follow one another (smaller chunks give more waves, and more queries to
@@ -636,8 +636,8 @@ static int launch(const WeightArgs& a, const Plan& p, hipStream_t s) {
 // What bounds it: the select (three passes over LDS counters, 22 us) and the list (10), then
 // the moves, near HBM's rate: a token's V codes lie in 16 pieces 32 bytes apart (the layout in
 // which attention reads them), so that lines of tokens that go are read too.  64 requests of
-// 900 to 4,096 positions cut to 1,024, 2 layers: 111 us, 238 MB read and 129 written.  One
-// workgroup per compute unit (256 of 32,768 positions): 133 us, 287 and 107 MB.
+// 900 to 4,096 positions cut to 1,024, 2 layers: 111 us, 244 MB read and 132 written.  One
+// workgroup per compute unit (256 of 32,768 positions): 133 us, 294 and 109 MB.
 
 struct EvictArgs {
   const int32_t* budgets;
