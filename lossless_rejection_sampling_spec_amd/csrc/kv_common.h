@@ -16,7 +16,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "specverify.h"
+#include "specverify_cache.h"
 
 namespace svk {
 

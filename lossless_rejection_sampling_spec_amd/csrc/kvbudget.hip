@@ -1,5 +1,5 @@
-// kvbudget.hip -- a cache held to a budget of positions (include/specverify.h states the
-// operators):
+// kvbudget.hip -- a cache held to a budget of positions (include/specverify_cache.h states
+// the operators):
 //   spec_kv_attention_weights   the attention weight that cached positions get
 //   spec_kv_evict               positions of the least weight leave the cache
 //

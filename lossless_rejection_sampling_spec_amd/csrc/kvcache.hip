@@ -1,6 +1,8 @@
 // kvcache.hip -- the 4-bit paged KV cache around the verify
 // (include/specverify.h states each operator):
 //   spec_kv_append    head norms, rotation and quantisation of the call's rows
+//                     (spec_kv_append_at of specverify_cache.h: at slots that are not
+//                     positions)
 //   spec_kv_reserve   pages for the rows of a call, copy-on-write of shared tails
 //   spec_kv_release   positions given back after the drain
 //   spec_kv_fork      sequences that share another one's pages

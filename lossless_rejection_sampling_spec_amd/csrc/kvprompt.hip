@@ -1,6 +1,6 @@
 // kvprompt.hip -- spec_kv_prompt_attention: attention of whole prompts, any number
-// of rows per request, over the 4-bit paged cache (include/specverify.h states the
-// operator).
+// of rows per request, over the 4-bit paged cache (include/specverify_cache.h
+// states the operator).
 //
 // For request b, row j (position c+j) and query head h over KV head h/G:
 //   out = sum_t exp(scale q.k_t - m) v_t / sum_t exp(scale q.k_t - m)

@@ -91,6 +91,17 @@ def test_append_at_refuses_what_append_does():
         assert call(**kw) == rc
 
 
+def test_the_binding_has_the_headers_arity():
+    import os
+    import re
+    from test_abi import ROOT
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "specverify_cache.h")).read(), flags=re.S)
+    found = re.findall(r"\b(spec_kv_\w+)\s*\(([^;]*)\);", src, flags=re.S)
+    assert len(found) == 6
+    for name, args in found:
+        assert len(getattr(binding.lib(), name).argtypes) == len(args.split(",")), name
+
+
 def test_workspace_sizes():
     L = binding.lib()
     prompt = dict(dt=1, batch=4, rows=1000, heads=32, kv=8, d=128, maxc=4000, total=9000, window=0, sinks=0)
