@@ -21,22 +21,26 @@ namespace budget {
 //
 // A workgroup of 4 waves takes a chunk of one KV head's context and all R = rows * G query
 // rows of it, whose operands lie in LDS; its waves take the tiles of 32 tokens in turn.
-// Scores are S^T[token][row] = K Q^T with v_mfma_f32_16x16x32_bf16, K widened from its codes
-// in registers; a lane holds the scores of one row for 8 tokens.  The sums go over the tiles
-// for each 16 MT rows (statistics in registers), the weights over the rows for each tile
-// (summed over the lanes once).  Where a request is one chunk (short contexts) both passes
-// are one launch.  fp32 queries go in as three bf16 terms, exactly; nothing is rounded further.
+// Scores are made with v_mfma_f32_16x16x32_bf16, K widened from its codes in registers.  For
+// the sums as S^T[token][row] = K Q^T: a lane holds one row's scores for 8 tokens, and goes over
+// the tiles for each 16 MT rows with the row's statistics in registers.  For the weights as
+// S[row][token] = Q K^T: a lane holds two tokens' scores for 4 MT rows, and goes over the rows of
+// each tile with the tokens' weights in registers (with S^T there too, sums over 16 lanes
+// for each of 8 tokens, 64 requests of 7 rows over 512 to 16,384 positions took 123 us, so 113).
+// Where a request is one chunk (short contexts) both passes are one launch.  fp32 queries go in
+// as three bf16 terms, exactly; nothing is rounded further.
 //
-// What bounds it: vector instructions (widening, exponentials), 62 % of the first pass's time
-// and 66 % of the second's, beside HBM at 3.9 and 3.1 TB/s: 51 + 70 us for 64 requests of 7
+// What bounds it: vector instructions (widening, exponentials), 65 % of the first pass's time
+// and 59 % of the second's, beside HBM at 3.8 and 3.4 TB/s: 52 + 63 us for 64 requests of 7
 // rows over 512 to 16,384 positions (32 heads over 8, D=128).  Four requests of 64 rows over
-// 1,500 to 4,000 positions, 26 + 32 us: 1.4 waves per SIMD whose reads of queries from LDS and
+// 1,500 to 4,000 positions, 26 + 31 us: 1.4 waves per SIMD whose reads of queries from LDS and
 // exponentials follow one another (smaller chunks give more waves, and more queries to
 // fetch: no faster; eight waves per workgroup 73 us against 58 for the call).
 
 constexpr int TILE = 32, SUB = 64;            // tokens of a tile; tiles whose pages a wave looks up at once
 // Waves of a workgroup: eight where it does both passes (64 requests over 100 to 1,000 positions
-// 22.5 us, four 23.7, sixteen 31, two launches 30).
+// 21 us; before the weights went over rows in the lane 22.5, four waves 23.7, sixteen 31, two
+// launches 30).
 constexpr int waves_of(bool both) { return both ? 8 : 4; }
 constexpr float LOG2E = 1.44269504088896340736f;
 // the rounded product of maximum and scale, from which exponents are counted, is held within
@@ -214,16 +218,14 @@ struct Weights {
     }
   }
 
-  // Entry i of a lane's 8 tokens, relative to the tile.
-  static __device__ __forceinline__ int token(int g, int i) { return 16 * (i >> 2) + 4 * g + (i & 3); }
-
-  // A tile's scores with 16 MT rows, -inf where a row does not see the token.  Tokens of a
-  // block stored as NaN get `odd`: NaN for the sums, whose row then adds nothing, -inf for the
-  // weights.
+  // A tile's scores with 16 MT rows, -inf where a row (at pos_of(row tile, entry)) does not see
+  // the token.  For the sums entry i of s[hf][mt] is token 16 hf + 4 g + i with row 16 mt + n,
+  // and tokens of a block stored as NaN get NaN (their row then adds nothing); for the WEIGHTS
+  // it is token 16 hf + n with row 16 mt + 4 g + i, and such tokens get -inf.
+  template <bool WEIGHTS, typename Pos>
   static __device__ __forceinline__ void scores(const WeightArgs& a, const KTile<D>& t, const bf16x8* q,
-                                                f32x4 (&s)[2][MT], int base, bool masked,
-                                                const int (&pos)[MT], float odd) {
-    const int lane = threadIdx.x & 63, g = lane >> 4;
+                                                f32x4 (&s)[2][MT], int base, bool masked, Pos&& pos_of) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     int ql = lane;
     asm volatile("" : "+v"(ql));              // (or the reads move out of the loop, into registers)
     float sc[2][KB];
@@ -257,9 +259,11 @@ struct Weights {
         for (int u = NT - 1; u >= 0; --u) {
           const bf16x8 y = q[((mt * STEPS + st) * NT + u) * 64 + ql];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[hf]), y,
+          for (int hf = 0; hf < 2; ++hf) {
+            const bf16x8 x = __builtin_bit_cast(bf16x8, k[hf]);
+            s[hf][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(WEIGHTS ? y : x, WEIGHTS ? x : y,
                                                                 s[hf][mt], 0, 0, 0);
+          }
         }
     }
     if (__any(top == 255u)) {
@@ -273,9 +277,9 @@ struct Weights {
         m |= m >> 16;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (m >> (4 * g + r) & 1)
+          if (m >> (WEIGHTS ? n : 4 * g + r) & 1)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) s[hf][mt][r] = odd;
+            for (int mt = 0; mt < MT; ++mt) s[hf][mt][r] = WEIGHTS ? -INFINITY : __builtin_nanf("");
       }
     }
     if (masked) {
@@ -283,27 +287,18 @@ struct Weights {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int tok = base + token(g, i);
-          const bool inside = (a.window == 0) | (tok > pos[mt] - a.window) | (tok < a.sinks);
-          if (!(inside & (tok <= pos[mt]))) s[i >> 2][mt][i & 3] = -INFINITY;
+        for (int i = 0; i < 4; ++i) {
+          const int pos = pos_of(mt, i);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int tok = base + 16 * hf + (WEIGHTS ? n : 4 * g + i);
+            const bool inside = (a.window == 0) | (tok > pos - a.window) | (tok < a.sinks);
+            if (!(inside & (tok <= pos))) s[hf][mt][i] = -INFINITY;
+          }
         }
     }
   }
 };
-
-// Sum over the 16 lanes of a row of lanes; every lane gets it.
-template <int CTRL>
-__device__ __forceinline__ float dpp(float x) {
-  return __builtin_bit_cast(
-      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, false));
-}
-__device__ __forceinline__ float sum16(float x) {
-  x += dpp<0xb1>(x);                          // lane ^ 1
-  x += dpp<0x4e>(x);                          // lane ^ 2
-  x += dpp<0x141>(x);                         // the mirror of 8 lanes
-  return x + dpp<0x140>(x);                   // the mirror of 16
-}
 
 // Adds a part of a row's sum, counted from om, to one counted from m.
 __device__ __forceinline__ void join(float& m, float& sum, float om, float osum) {
@@ -372,12 +367,8 @@ void k_weights(WeightArgs a) {
   const bool bad = id.ask(a, sp, a.table + (int64_t)b * a.ld_table, begin, end);
   const int mine = (end - begin - wave + WAVES - 1) / WAVES;  // the wave's tiles
   KTile<D> t[DEPTH];
-  int pos[MT];
-  auto positions = [&](int r0) {              // (fp32 divides these right: rows are below 2^16)
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-      pos[mt] = rq.ctx + (int)(((float)min(r0 + mt * 16 + n, R - 1) + 0.5f) * a.inv_group);
-  };
+  // the position of row r (fp32 divides these right: rows are below 2^16)
+  auto position = [&](int r) { return rq.ctx + (int)(((float)min(r, R - 1) + 0.5f) * a.inv_group); };
   auto masked = [&](int base) {
     return base + TILE - 1 > rq.ctx ||
            (a.window > 0 && base <= rq.ctx + rq.rows - 1 - a.window && base + TILE > a.sinks);
@@ -423,7 +414,7 @@ void k_weights(WeightArgs a) {
         __syncthreads();                      // (every wave is done with the rows before)
         A::put_q(a, q, rq, h, g0, blocks * MT, R, wave, WAVES);
         if (pass == 2)                        // the rows' maxima and sums over all chunks
-          for (int i = threadIdx.x >> 3; i < (rows + 7) / 8 * 8; i += 8 * WAVES) {     // 8 lanes each
+          for (int i = threadIdx.x >> 3; i < blocks * ROWS; i += 8 * WAVES) {     // 8 lanes each
             float nm = -FAR, sum = 0.f;
             const f32x2* from = stats + g0 + min(i, rows - 1);
             for (int k = lane & 7; k < used; k += 32) {
@@ -436,8 +427,8 @@ void k_weights(WeightArgs a) {
             }
 #pragma unroll
             for (int d = 1; d < 8; d <<= 1) join(nm, sum, __shfl_xor(nm, d), __shfl_xor(sum, d));
-            if ((lane & 7) == 0 && i < rows)
-              fin[i] = f32x2{nm, sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f};
+            if ((lane & 7) == 0)              // (what is past the last row repeats it, and adds 0)
+              fin[i] = f32x2{nm, i < rows && sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f};
           }
         __syncthreads();
       }
@@ -447,9 +438,10 @@ void k_weights(WeightArgs a) {
         for (int rb = 0; rb < blocks; ++rb) {
           if (mine <= 0) break;
           float m[MT], mc[MT], l[MT];
-          positions(g0 + rb * ROWS);
+          int pos[MT];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
+            pos[mt] = position(g0 + rb * ROWS + mt * 16 + n);
             m[mt] = -INFINITY;
             mc[mt] = -FAR;
             l[mt] = 0.f;
@@ -457,8 +449,8 @@ void k_weights(WeightArgs a) {
           each_tile([&](int k, const KTile<D>& kt) {
             f32x4 s[2][MT];
             const int base = base_of(sp, begin + wave + k * WAVES);
-            A::scores(a, kt, ONE ? q : q + rb * A::Q_WORDS, s, base, masked(base), pos,
-                      __builtin_nanf(""));
+            A::template scores<false>(a, kt, ONE ? q : q + rb * A::Q_WORDS, s, base, masked(base),
+                                      [&](int mt, int) { return pos[mt]; });
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               float mx = m[mt];
@@ -486,65 +478,69 @@ void k_weights(WeightArgs a) {
           }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < rows; i += 64 * WAVES) {    // then the waves
+        for (int i = threadIdx.x; i < blocks * ROWS; i += 64 * WAVES) {    // then the waves
           float nm = -FAR, sum = 0.f;
 #pragma unroll
           for (int k = 0; k < WAVES; ++k) {
-            const f32x2 y = part[k * a.group_rows + i];
+            const f32x2 y = part[k * a.group_rows + min(i, rows - 1)];
             join(nm, sum, y[0], y[1]);
           }
           if (PASS == 3 && R <= a.group_rows)
-            fin[i] = f32x2{nm, sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f};
-          else
+            fin[i] = f32x2{nm, i < rows && sum > 0.f && sum < INFINITY ? 1.f / sum : 0.f};
+          else if (i < rows)
             stats[(int64_t)chunk * a.max_rows + g0 + i] = f32x2{nm, sum};
         }
         if constexpr (PASS == 3) __syncthreads();
       } else {
-        float mc[MT], inv[MT];
         bool none = false;                    // some rows add nothing
+        for (int i = lane; i < rows; i += 64) none |= fin[i][1] == 0.f;
+        none = __any(none);
+        f32x4 mc[MT], inv[MT];
         auto state = [&](int rb) {
-          none = false;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const int r = rb * ROWS + mt * 16 + n;
-            const f32x2 y = fin[max(min(r, rows - 1), 0)];
-            mc[mt] = y[0];
-            inv[mt] = r < rows ? y[1] : 0.f;  // (lanes past the last row repeat it)
-            none |= r < rows && y[1] == 0.f;
-          }
-          none = __any(none);
-          positions(g0 + rb * ROWS);
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const f32x4 y = *(const f32x4*)&fin[rb * ROWS + mt * 16 + 4 * g + i];
+              mc[mt][i] = y[0];
+              inv[mt][i] = y[1];
+              mc[mt][i + 1] = y[2];
+              inv[mt][i + 1] = y[3];
+            }
         };
         if (ONE) state(0);
         each_tile([&](int k, const KTile<D>& kt) {
           const int at = wave + k * WAVES, base = base_of(sp, begin + at);
           const bool hide = masked(base);
-          float w[8] = {};
+          float w[2] = {};                    // of tokens n and 16 + n, over the lane's rows
           for (int rb = 0; rb < blocks; ++rb) {
             if (!ONE) state(rb);
             f32x4 s[2][MT];
-            A::scores(a, kt, ONE ? q : q + rb * A::Q_WORDS, s, base, hide, pos, -INFINITY);
+            A::template scores<true>(
+                a, kt, ONE ? q : q + rb * A::Q_WORDS, s, base, hide,
+                [&](int mt, int i) { return position(g0 + rb * ROWS + mt * 16 + 4 * g + i); });
             if (none) {
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (inv[mt] == 0.f) s[i >> 2][mt][i & 3] = -INFINITY;
+                for (int i = 0; i < 4; ++i)
+                  if (inv[mt][i] == 0.f) s[0][mt][i] = s[1][mt][i] = -INFINITY;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                w[i] = __builtin_fmaf(
-                    __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][mt][i & 3], c, -mc[mt])), inv[mt], w[i]);
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                  w[hf] = __builtin_fmaf(
+                      __builtin_amdgcn_exp2f(__builtin_fmaf(s[hf][mt][i], c, -mc[mt][i])), inv[mt][i], w[hf]);
             if (ONE) break;
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = sum16(w[i]);
-          float y = w[0];                     // lane n of the row writes entry n
-#pragma unroll
-          for (int i = 1; i < 8; ++i) y = n == i ? w[i] : y;
-          if (n < 8) acc[at * TILE + A::token(g, n)] = y;
+          // over the lanes of a token: half of the tile each, then both lanes of a half
+          const bool upper = g & 2;
+          float y = (upper ? w[1] : w[0]) + __shfl_xor(upper ? w[0] : w[1], 32);
+          y += __shfl_xor(y, 16);
+          if (!(g & 1)) acc[at * TILE + 8 * g + n] = y;
         });
         __syncthreads();
         const int64_t row = ((int64_t)b * a.kv_heads + h) * a.ld_w;
