@@ -51,8 +51,9 @@ size_t spec_kv_prompt_workspace_bytes(int dtype, int batch, int total_rows, int 
  * rows' K and V are in the cache (spec_kv_append), and so is what lies before them
  * (context_lens[b] > 0: a prompt in parts, or after a prefix that spec_kv_fork shares).
  * Formula, precision and what never reaches a row: as spec_kv_attention.
- *   q, out         [total_rows][heads][head_dim] of dtype, rows ld_q / ld_out apart,
- *                  not the same memory (SV_ERR_SHAPE if out == q); total_rows * heads < 2^31
+ *   q, out         [total_rows][heads][head_dim] of dtype, rows ld_q / ld_out apart, without
+ *                  an element in common (SV_ERR_SHAPE; columns of one wider array are fine);
+ *                  total_rows * heads < 2^31
  *   max_context    bound of context_lens[b] + rows; requests past it are
  *                  SV_ROW_BAD_PARAM, like context_lens[b] < 0
  *   total_context  bound of the sum of context_lens[b] + rows over the requests, at most

@@ -669,7 +669,8 @@ def kv_prompt_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tenso
     rows, total_context their sum over the requests.  scale defaults to head_dim ** -0.5.
     Returns (out [rows, heads, D], status[B]).
 
-    Rows of no request stay as `out` holds them (undefined without `out`).  Without
+    Rows of no request stay as `out` holds them (undefined without `out`); `out` has no element
+    in common with q (columns of one wider tensor are fine).  Without
     `workspace` the scratch of the largest call so far stays with the stream: the requests'
     cache in bf16 for the most part (spec_kv_prompt_workspace_bytes)."""
     batch = _kv_batch(cache, cu_seqlens)
@@ -685,8 +686,6 @@ def kv_prompt_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tenso
         o_rows, o_heads, ld_out = _heads_of(out, "out", cache, q.dtype)
         if o_rows != rows or o_heads != heads:
             raise ValueError("out must match q's shape")
-        if out.data_ptr() == q.data_ptr():
-            raise ValueError("out must not be q's memory")
     # (ctypes would take the low bits of a larger number)
     if not (1 <= max_context <= 1 << 30 and 1 <= total_context <= 1 << 30 and rows < 1 << 31
             and 0 <= window <= 1 << 30 and 0 <= sinks <= 1 << 30):

@@ -36,6 +36,7 @@
 // the first of these), a barrier per tile over a ring of buffers.
 
 #include "kv_common.h"
+#include "row_ranges.h"
 
 namespace svk {
 namespace prompt {
@@ -913,12 +914,16 @@ int spec_kv_prompt_attention(const void* q, int64_t ld_q, int dtype, const int32
       !page_ok(page_size) || num_pages < 1 || num_pages > 0x7fffffff || ld_table < 1 ||
       ld_table > (1 << 30) / page_size || ld_q < (int64_t)heads * head_dim ||
       ld_out < (int64_t)heads * head_dim || !(scale > 0.f) || !(scale <= 2.0e38f) ||
-      !aligned16(pages) || out == q ||
+      !aligned16(pages) ||
       !prompt::plan_of(dtype, batch, total_rows, heads, kv_heads, head_dim, max_context, total_context,
                        window, sinks, p))
     return SV_ERR_SHAPE;
   if (!workspace || !aligned16(workspace)) return SV_ERR_NULL;
   if (p.bytes > workspace_bytes) return SV_ERR_WORKSPACE;
+  // (a row's queries are read by several workgroups, at no fixed time before its result is written)
+  const int64_t size = dtype == SV_F32 ? 4 : 2;
+  if (rows_overlap(q, ld_q * size, out, ld_out * size, total_rows, heads * (int64_t)head_dim * size))
+    return SV_ERR_SHAPE;
   prompt::Args a;
   a.q = q;
   a.ld_q = ld_q;

@@ -415,3 +415,24 @@ def test_the_binding_refuses_arguments_that_do_not_fit():
         with pytest.raises(ValueError):
             call(**over)
     call()
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_a_result_beside_its_queries(d):
+    """Columns of one wider tensor share no element: the rows of a call into other memory.  A
+    result that is shifted into the queries is refused, and nothing is written."""
+    cache, K, V = T.make_attention(d, 16, 2, [40, 130], [100, 7], 3)
+    both = torch.randn(171, 2 * 4 * d, device=DEV).to(torch.bfloat16)
+    q, out = both[:170, :4 * d].unflatten(1, (4, d)), both[:170, 4 * d:].unflatten(1, (4, d))
+    args = (T._i([0, 40, 170]), T._i([100, 7]))
+    kw = dict(max_context=150, total_context=400)
+    want, _ = binding.kv_prompt_attention(cache, q, *args, **kw)
+    held = both.clone()
+    for shifted in (both[:170, d:5 * d], both[1:, :4 * d], both[1:, 2 * d:6 * d], both.view(-1, 4 * d)[1:171]):
+        with pytest.raises(ValueError):
+            binding.kv_prompt_attention(cache, q, *args, out=shifted.unflatten(1, (4, d)), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(both, held)
+    got, st = binding.kv_prompt_attention(cache, q, *args, out=out, **kw)
+    assert st.cpu().tolist() == [0, 0] and got is out and torch.equal(out, want)
+    assert torch.equal(both[:, :4 * d], held[:, :4 * d])

@@ -2,6 +2,8 @@
 refusal of the C entry points (each call fails validation on the host, so no GPU is touched),
 the workspace sizes, the reference of an eviction, and that no kernel of theirs spills."""
 
+import ctypes
+import os
 import subprocess
 
 import numpy as np
@@ -55,6 +57,48 @@ COMMON = [(dict(q=None), 1), (dict(cu=None), 1), (dict(ctx=None), 1), (dict(page
     (dict(total=(1 << 30) + 1), 2), (dict(rows=1 << 29), 2), (dict(total=1 << 30, maxc=1 << 30), 2)])
 def test_prompt_refusals(kw, rc):
     assert _prompt(**kw) == rc
+
+
+# q: 6 rows of 1,024 bytes at Q
+Q = 1 << 20
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=Q + 1024), dict(out=Q - 1024), dict(out=Q + 256), dict(out=Q - 2), dict(out=Q + 5 * 1024 + 1022),
+    dict(out=Q + 1022, ldq=1024, ldo=1024),            # the last element of a row, rows 2,048 bytes apart
+    dict(out=Q + 5 * 2048 - 1022, ldq=1024, ldo=1024), dict(out=Q - 4 * 2048 + 1026, ldq=1024, ldo=1024),
+    dict(out=Q + 1024, ldq=1024, ldo=600),             # rows at other distances
+    dict(dt=0, out=Q + 6 * 1024), dict(dt=0, out=Q + 2044, ldq=1024, ldo=1024)])
+def test_prompt_refuses_a_result_that_overlaps_its_queries(kw):
+    assert _prompt(**{"q": Q, **kw}) == 2
+
+
+def test_overlap_of_strided_rows(tmp_path):
+    """The host's check of two strided arrays against every byte of them."""
+    source = tmp_path / "rows.cpp"
+    source.write_text('#include "row_ranges.h"\nextern "C" int meet(long long a, long long la, long long b, '
+                      'long long lb, long long rows, long long width) {\n  return svk::rows_overlap((void*)a, la, '
+                      '(void*)b, lb, rows, width); }\n')
+    lib = tmp_path / "rows.so"
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", os.path.join(build.PKG, "csrc"), str(source),
+                    "-o", str(lib)], check=True)
+    meet = ctypes.CDLL(str(lib)).meet
+    meet.argtypes = [ctypes.c_longlong] * 6
+    seen = set()
+    for rows in (1, 2, 5):
+        for width in (1, 3):
+            for la in range(width, 7):
+                mine = {i * la + x for i in range(rows) for x in range(width)}
+                for lb in range(width, 7):
+                    for gap in range(-32, 33):
+                        want = any(gap + j * lb + x in mine for j in range(rows) for x in range(width))
+                        seen.add(want)
+                        assert meet(1000, la, 1000 + gap, lb, rows, width) == want, (rows, width, la, lb, gap)
+    assert seen == {True, False}
+    # the largest sizes
+    assert meet(1 << 40, 1 << 40, (1 << 40) + 8192, 1 << 40, (1 << 31) - 1, 8192) == 0
+    assert meet(1 << 40, 1 << 40, (1 << 40) + 8191, 1 << 40, (1 << 31) - 1, 8192) == 1
+    assert meet(1 << 40, (1 << 62) - 1, 1 << 41, (1 << 62) - 2, 1 << 20, 8192) == 0
 
 
 @pytest.mark.parametrize("kw,rc", COMMON + [
