@@ -607,6 +607,10 @@ struct Prompt {
   }
 };
 
+// The wave's loads straight to LDS have arrived: before a barrier that hands them to the other
+// waves (the loads name no register that a later use would make the compiler wait for).
+__device__ __forceinline__ void direct_loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 template <int D, int OD, int WAVES, int PER_SIMD, typename T>
 __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   using A = Prompt<D, OD, T>;
@@ -679,6 +683,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
   uint32_t some_odd = 0;
   for (int i = begin + (int)threadIdx.x; i < end; i += 64 * WAVES) some_odd |= a.odd[place(i)];
   const bool odd = __syncthreads_or(some_odd != 0);
+  direct_loads_done();
   __syncthreads();
   int buf = 0;
   for (int i = begin; i < end; i += STAGE) {
@@ -702,6 +707,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void k_prompt(Args a) {
       }
     }
     buf ^= 1;
+    direct_loads_done();
     __syncthreads();
   }
 

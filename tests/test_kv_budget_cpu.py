@@ -206,3 +206,36 @@ def test_no_kernel_spills(source, kernels, tmp_path):
         names = [n for n in found if f"{kernel}I" in n or f"{kernel}E" in n]
         assert len(names) == count, (kernel, names)
     assert not {n: v for n, v in found.items() if v != (0, 0)}
+
+
+def test_direct_loads_to_lds_are_waited_for_before_they_are_shared(tmp_path):
+    """Every instance of k_prompt waits for its own loads to LDS, by an instruction of the source,
+    right before the barriers that hand the first and each next stage of tiles to the other
+    waves: not only where the compiler happens to put a wait."""
+    flags = [f for f in build.HIPCC_FLAGS if f != "-shared"]
+    path = next(s for s in build.SRC if s.endswith("kvprompt.hip"))
+    out = tmp_path / "x.s"
+    subprocess.run([build.hipcc(), *flags, "-I", build.INC, "--cuda-device-only", "-S", path, "-o", str(out)],
+                   check=True, capture_output=True)
+    kernels, name = {}, None
+    for line in out.read_text().splitlines():
+        text = line.strip()
+        if line.startswith("_ZN3svk6prompt8k_promptI"):
+            name = line.split(":")[0]
+            kernels[name] = []
+        elif line.startswith(".Lfunc_end"):
+            name = None
+        elif name and (text.startswith(";;#ASM") or text and text[0] not in ".;_" and not text.endswith(":")):
+            kernels[name].append(text.split()[0] if text.startswith(";;#ASM") else text)
+    assert len(kernels) == 9
+    for name, code in kernels.items():
+        waits = [i for i in range(1, len(code) - 1) if code[i].startswith("s_waitcnt vmcnt(0)")
+                 and code[i - 1] == ";;#ASMSTART" and code[i + 1] == ";;#ASMEND"]
+        assert len(waits) >= 2, name
+        for at in waits:
+            barrier = next(i for i in range(at, len(code)) if code[i].startswith("s_barrier"))
+            assert not any("load_lds" in x for x in code[at:barrier]), name
+        # a wait behind the first tiles' loads, and one behind the next ones'
+        loads = [i for i, x in enumerate(code) if "load_lds" in x]
+        between = [i for i in waits if any(l < i for l in loads) and any(l > i for l in loads)]
+        assert loads and between and waits[-1] > loads[-1], name
