@@ -37,9 +37,11 @@ int spec_kv_append_at(const void* q, int64_t ld_q, const void* k, int64_t ld_k, 
                       void* k_values, void* v_values, int32_t* status, void* stream);
 
 /* Bytes of workspace spec_kv_prompt_attention needs with these sizes (0 on invalid sizes,
- * and on those that would be 2^24 workgroups or more).  Most of it is the requests' cache
- * in bf16: 4 head_dim bytes per KV head and position, total_context positions (with a
- * window: those that rows see, at most). */
+ * and on those past two more limits: total_rows * heads, each KV head's rounded up to blocks of
+ * 128 or 256 with a block more per request, stays below 2^31, at head_dim 256 below 2^30; and
+ * (total_context / 32 + batch) * kv_heads, with a window the tiles of 32 positions that rows see
+ * at most, below 2^24).  Most of it is the requests' cache in bf16: 4 head_dim bytes per KV head
+ * and position, total_context positions (with a window: those that rows see, at most). */
 size_t spec_kv_prompt_workspace_bytes(int dtype, int batch, int total_rows, int heads,
                                       int kv_heads, int head_dim, int max_context,
                                       int64_t total_context, int window, int sinks);
@@ -53,7 +55,7 @@ size_t spec_kv_prompt_workspace_bytes(int dtype, int batch, int total_rows, int 
  * Formula, precision and what never reaches a row: as spec_kv_attention.
  *   q, out         [total_rows][heads][head_dim] of dtype, rows ld_q / ld_out apart, without
  *                  an element in common (SV_ERR_SHAPE; columns of one wider array are fine);
- *                  total_rows * heads < 2^31
+ *                  total_rows * heads < 2^31 (and spec_kv_prompt_workspace_bytes's limits)
  *   max_context    bound of context_lens[b] + rows; requests past it are
  *                  SV_ROW_BAD_PARAM, like context_lens[b] < 0
  *   total_context  bound of the sum of context_lens[b] + rows over the requests, at most

@@ -832,8 +832,10 @@ static bool plan_of(int dtype, int batch, int total_rows, int heads, int kv_head
   chunks = (one + ct - 1) / ct;
   p.chunks = (int)chunks;
   p.chunk_tiles = (int)ct;
-  // (a launch has less than 2^32 threads)
-  if (wide * chunks * (p.block_rows / 16) * 2 >= (1ll << 24) || tiles * kv_heads >= (1ll << 24)) return false;
+  // (a launch has less than 2^32 threads, two workgroups per block at D=256; the join is launched
+  // only where blocks are few)
+  if (wide * chunks * (d == 256 ? 2 : 1) * (64 * p.waves) >= (1ll << 32) || tiles * kv_heads >= (1ll << 24))
+    return false;
   p.max_blocks = (int)blocks;
   size_t at = round256(sizeof(Head));
   p.blocks = at;

@@ -436,3 +436,35 @@ def test_a_result_beside_its_queries(d):
     got, st = binding.kv_prompt_attention(cache, q, *args, out=out, **kw)
     assert st.cpu().tolist() == [0, 0] and got is out and torch.equal(out, want)
     assert torch.equal(both[:, :4 * d], held[:, :4 * d])
+
+
+def test_a_prompt_of_two_million_rows():
+    """2^27 query rows in one call (34 GB of queries and results), through a short window."""
+    rows, heads, kv, d, page, window = 1 << 21, 64, 8, 64, 256, 70
+    num = rows // page
+    # pages of 64 random ones' bytes
+    few, K, V = T.make_attention(d, page, kv, [64 * page], [0], 11)
+    order = few.page_table[0, :64].long()
+    pages = few.pages[:, order].repeat(1, num // 64, 1)
+    cache = binding.KVCache(pages=pages, page_table=torch.arange(num, dtype=torch.int32, device=DEV)[None],
+                            seq_lens=T._i([rows]), ref_counts=torch.ones(num, dtype=torch.int32, device=DEV),
+                            page_size=page, kv_heads=kv, head_dim=d)
+    q = torch.empty(rows, heads, d, dtype=torch.bfloat16, device=DEV)
+    q.view(64, -1).copy_(torch.randn(rows // 64, heads * d, device=DEV).view(1, -1))
+    out, st = binding.kv_prompt_attention(cache, q, T._i([0, rows]), T._i([0]), max_context=rows,
+                                          total_context=rows, window=window)
+    assert st.cpu().tolist() == [0]
+    rng = np.random.default_rng(3)
+    picks = [0, 69, 70, rows - 1, rows - 2] + [int(rng.integers(rows)) for _ in range(60)]
+    for j in picks:
+        h = int(rng.integers(heads))
+        t = np.arange(max(0, j - window + 1), j + 1) % (64 * page)
+        k, v = K[0][t, h // 8], V[0][t, h // 8]
+        want, mass, slip = U.attention_row(T._f64(q[j, h]), k, v, len(t) - 1, d ** -0.5, 0, 0)
+        tol = mass * (T.HALF["bf16"] + 4 * (d + 8) * 2.0 ** -24 * slip + (2 * window + 128) * 2.0 ** -24
+                      + 2.0 ** -20) + T.HALF["bf16"] * np.abs(want)
+        assert np.all(np.abs(T._f64(out[j, h]) - want) <= tol), (j, h)
+    # nothing is left out, and rows of equal queries over equal pages are equal
+    assert bool(torch.isfinite(out.view(64, -1)).all(1).all())
+    block = rows // 64
+    assert torch.equal(out[block + 100:block + 200], out[2 * block + 100:2 * block + 200])

@@ -170,6 +170,33 @@ def test_workspace_sizes():
         assert wsize(**kw) == 0
 
 
+def test_prompt_sizes_at_their_limits():
+    """Both sides of what one launch takes, and of the tiles' numbers; refusals and sizes agree."""
+    L = binding.lib()
+
+    def fits(**kw):
+        a = dict(dt=1, batch=1, rows=1 << 20, heads=128, kv=8, d=128, maxc=1 << 20, total=1 << 20, window=0,
+                 sinks=0)
+        a.update(kw)
+        size = L.spec_kv_prompt_workspace_bytes(*a.values())
+        rc = _prompt(**{"ldq": a["heads"] * a["d"], "ldo": a["heads"] * a["d"], "wsb": 0, **a})
+        assert rc == (4 if size else 2), kw                # no workspace, or sizes
+        return size > 0
+    assert fits() and fits(window=64) and fits(dt=0)
+    assert fits(d=256) and fits(rows=1 << 21, heads=64, d=64)
+    one = dict(heads=1, kv=1, maxc=4096, total=4096)
+    assert fits(**one, rows=(1 << 31) - 256) and not fits(**one, rows=(1 << 31) - 255)
+    assert fits(**one, d=256, rows=(1 << 30) - 256) and not fits(**one, d=256, rows=(1 << 30) - 255)
+    assert fits(**one, dt=0, rows=(1 << 31) - 128) and not fits(**one, dt=0, rows=(1 << 31) - 127)
+    # (many requests of short contexts: blocks of 128, one for each request besides)
+    assert fits(**one, batch=1024, rows=(1 << 31) - 1024 * 127 - 1)
+    assert not fits(**one, batch=1024, rows=(1 << 31) - 1024 * 127)
+    assert not fits(rows=1 << 24) and fits(rows=(1 << 24) - 1 - 64)
+    few = dict(rows=1000, heads=8)
+    assert fits(**few, total=(1 << 26) - 33) and not fits(**few, total=(1 << 26) - 32)
+    assert fits(**few, total=1 << 30, maxc=1 << 30, window=100)
+
+
 def test_reference_of_what_stays():
     """Against sorting by hand; protected ends, ties, NaN and -0."""
     w = np.array([0.0, 5, -0.0, 3, 3, np.nan, 9, 3, 1, 0], np.float32)
