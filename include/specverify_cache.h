@@ -4,8 +4,8 @@
  *
  * A request starts with reserve -> per layer (append, prompt_attention, and
  * attention_weights of the prompt's last rows) -> evict; where requests are held to a budget a
- * step is reserve -> per layer (append_at, attention, attention_weights of the rows that were
- * committed) -> verify -> drain -> release -> evict.
+ * step is reserve -> per layer (append_at, whose q_out is kept, attention) -> verify -> drain ->
+ * per layer attention_weights of the rows that were committed -> release -> evict.
  *
  * Pages, tables, offsets, statuses and return values are those of specverify.h.  A workspace
  * that is NULL or not 16-byte aligned is SV_ERR_NULL.
@@ -87,7 +87,9 @@ size_t spec_kv_weights_workspace_bytes(int dtype, int batch, int max_k, int head
  *                + sum over rows j < row_counts[b] and query heads of h of softmax_t(scale q.k)
  * the softmax over what the row sees, as in spec_kv_attention.  After a verify, row_counts =
  * accepted + 1 counts the rows that were committed; positions that were given back start from
- * 0 again when they are next written, for a call's own positions take nothing from `in`.
+ * 0 again when they are next written, for a call's own positions take nothing from `in`.  The
+ * call goes before spec_kv_release: the rows that do not count need their pages as well (a
+ * request whose release gave one back is SV_ROW_BAD_PAGE).
  * With the last 64 rows of a prompt and in = NULL it makes a new request's weights.  Scores
  * and sums in fp32, weights not rounded.  A row that sees a K block stored as NaN, or whose
  * scores leave fp32's range (see spec_kv_attention), adds nothing.

@@ -716,7 +716,9 @@ def kv_attention_weights(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tens
                          workspace: torch.Tensor | None = None):
     """spec_kv_attention_weights: the attention weight that cached positions get from the rows
     q (as kv_append turned them) of each request, summed over its first row_counts[b] rows
-    (None: all) and the query heads of each KV head, on top of `weights` (None: zeros).
+    (None: all) and the query heads of each KV head, on top of `weights` (None: zeros).  After a
+    verify and its drain, row_counts is accepted + 1, and the call goes before kv_release: all
+    rows need their pages, counted or not.
 
     weights, out  float32 [B, kv_heads, L], L >= max_context: one layer's.  `out` defaults to
     `weights` itself, or to new memory.  Only positions below context_lens[b] + rows are written

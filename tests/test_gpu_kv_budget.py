@@ -209,6 +209,32 @@ def test_weights_do_not_depend_on_the_other_requests():
     assert torch.equal(out[1], a[1])
 
 
+@pytest.mark.parametrize("ctx", [30, 1500])
+def test_weights_go_before_the_release(ctx):
+    """Rows that do not count need their pages too: after a release that gave one back the
+    request's weights stay as they were, before it they are added to."""
+    rows, kept = 6, 2                                      # 4 rows are given back, over a page's end
+    cache = binding.KVCache.create(layers=1, num_pages=120, page_size=16, kv_heads=1, head_dim=64,
+                                   requests=1, max_context=1600, device=DEV)
+    first = ctx // 16 * 16 + 14 - 3                        # the page ends after the first 3 + 2 positions
+    binding.kv_reserve(cache, T._i([0, first + 3]))
+    x = torch.randn(first + 3, 3, 64, device=DEV)
+    binding.kv_append(cache, x[:, :1], x[:, 1:2], x[:, 2:], T._i([0, first + 3]), T._i([0]))
+    cu = T._i([0, rows])
+    at, _ = binding.kv_reserve(cache, cu)
+    x = torch.randn(rows, 4, 64, device=DEV)
+    q, st = binding.kv_append(cache, x[:, :2], x[:, 2:3], x[:, 3:], cu, at)
+    before = torch.rand(1, 1, 1600, device=DEV)
+    kw = dict(max_k=5, max_context=first + 9, row_counts=T._i([kept]))
+    good, st = binding.kv_attention_weights(cache, q, cu, at, weights=before, out=before.clone(), **kw)
+    assert st.cpu().tolist() == [0]
+    assert abs(float((good[..., :first + 9] - before[..., :first + 9]).sum())
+               - 2 * kept + float(before[..., first + 3:first + 9].sum())) < 1e-3
+    binding.kv_release(cache, T._i([rows - kept]), at)
+    late, st = binding.kv_attention_weights(cache, q, cu, at, weights=before, out=before.clone(), **kw)
+    assert st.cpu().tolist() == [8] and torch.equal(late, before)
+
+
 # -------------------------------------------------------------------- evict
 
 def make_cache(lens, page, kv, d, layers, seed=0, spare=3, ld=None):
