@@ -770,7 +770,9 @@ def kv_evict(cache: KVCache, weights: torch.Tensor, budgets: torch.Tensor, *, si
     them, per layer and KV head.  What stays moves to the front, pages behind it are free.
 
     weights  float32 [layers, B, kv_heads, L], moved along; evicted int32 [B] or None, counted
-    up by the positions that left (kv_append's position_offsets).  Returns status[B]."""
+    up by the positions that left (kv_append's position_offsets).  No other call changes them:
+    set evicted[b] to 0 when slot b takes a new sequence, and after a kv_fork of an evicted
+    request copy evicted[src] and weights[:, src] to dst.  Returns status[B]."""
     batch = budgets.numel()
     _check_ints(budgets, "budgets", cache.device, 1)
     _check_ints(evicted, "evicted", cache.device, batch)

@@ -454,6 +454,71 @@ def test_append_at_offsets_statuses():
     assert (out == 7.0).all((1, 2)).cpu().tolist() == [False, True, True, True, False, False]
 
 
+def _rows(count, heads, kv, d, seed):
+    return torch.randn(count, heads + 2 * kv, d, generator=torch.Generator().manual_seed(seed)).to(DEV)
+
+
+def test_a_fork_and_a_reused_slot_after_an_eviction():
+    """An evicted request is forked, and its row, then reused: with `evicted` and weights copied
+    to the fork, and `evicted` back at 0 in the reused slot, new rows are turned by their own
+    positions and attend to what was kept; the reused slot's bytes are those of a new cache."""
+    heads, kv, d, page, n, budget, width = 4, 2, 64, 16, 90, 32, 160
+    cs = torch.from_numpy(T._rotation(300, d)).to(DEV)
+
+    def create():
+        return binding.KVCache.create(layers=1, num_pages=40, page_size=page, kv_heads=kv, head_dim=d,
+                                      requests=3, max_context=width, device=DEV)
+
+    def append(cache, x, cu, ctx, **kw):
+        q, st, k, v = binding.kv_append(cache, x[:, :heads], x[:, heads:heads + kv], x[:, heads + kv:], T._i(cu),
+                                        ctx, cos_sin=cs, want_values=True, **kw)
+        return q, k, v, st.cpu().tolist()
+    cache, plain = create(), create()
+    prompt, more, new = (_rows(c, heads, kv, d, s) for c, s in ((n, 1), (4, 2), (21, 3)))
+    evicted = torch.zeros(3, dtype=torch.int32, device=DEV)
+    weights = torch.zeros(1, 3, kv, width, device=DEV)
+    ctx, _ = binding.kv_reserve(cache, T._i([0, n, n, n]))
+    _, k0, v0, _ = append(cache, prompt, [0, n], ctx)
+    w = torch.rand(kv, n, generator=torch.Generator().manual_seed(4)).to(DEV)
+    weights[0, 0, :, :n] = w
+    assert binding.kv_evict(cache, weights, T._i([budget, 0, 0]), sinks=2, recent=4,
+                            evicted=evicted).cpu().tolist() == [0] * 3
+    assert evicted.cpu().tolist() == [n - budget, 0, 0]
+    # the fork: pages by kv_fork, the rest by the caller
+    assert binding.kv_fork(cache, T._i([0]), T._i([2])).cpu().tolist() == [0]
+    evicted[2], weights[:, 2] = evicted[0], weights[:, 0]
+    # the row that was forked takes a new sequence
+    assert binding.kv_release(cache, T._i([budget, 0, 0])).cpu().tolist() == [0] * 3
+    evicted[0] = 0
+    cu = [0, 21, 21, 25]
+    ctx, st = binding.kv_reserve(cache, T._i(cu))
+    assert ctx.cpu().tolist() == [0, -1, budget] and st.cpu().tolist() == [0, 3, 0]
+    q, k1, v1, st = append(cache, torch.cat((new, more)), cu, ctx, position_offsets=evicted)
+    assert st == [0, 3, 0]
+    # as rows of positions 0 .. 20 and 90 .. 93 in a cache that nothing left
+    plain.page_table.copy_(torch.arange(30, device=DEV).view(3, 10))
+    pq, pk, pv, st = append(plain, torch.cat((new, more)), cu, T._i([0, 0, n]))
+    assert st == [0, 3, 0]
+    assert torch.equal(q, pq) and torch.equal(k1, pk) and torch.equal(v1, pv)
+    kept = [E.kept(w[h].cpu().numpy(), n, budget, 2, 4) for h in range(kv)]
+    out, st = binding.kv_attention(cache, q, T._i(cu), ctx, max_k=20, max_context=width)
+    assert st.cpu().tolist() == [0, 3, 0]
+    K = [T._f64(k1[:21]), None] + [np.stack([np.concatenate((T._f64(k0[kept[h], h]), T._f64(k1[21:, h])))
+                                             for h in range(kv)], 1)]
+    V = [T._f64(v1[:21]), None] + [np.stack([np.concatenate((T._f64(v0[kept[h], h]), T._f64(v1[21:, h])))
+                                             for h in range(kv)], 1)]
+    T.check_attention(out, q, K, V, cu, [0, 0, budget], [21, 0, 4], "f32", d ** -0.5, skip=(1,))
+    # and the fork is cut by its own weights, now that its pages are its own
+    binding.kv_attention_weights(cache, q, T._i(cu), ctx, max_k=20, max_context=width, weights=weights[0])
+    before = weights[0, 2].cpu().numpy()
+    assert binding.kv_evict(cache, weights, T._i([0, 0, 20]), recent=4,
+                            evicted=evicted).cpu().tolist() == [0] * 3
+    assert evicted.cpu().tolist() == [0, 0, n - 20 + 4]
+    for h in range(kv):
+        now = E.kept(before[h], budget + 4, 20, 0, 4)
+        assert np.array_equal(weights[0, 2, h, :20].cpu().numpy(), before[h][now])
+
+
 # ------------------------------------------------- streams, graphs, the binding
 
 def _small(seed=0, ctx=(100, 1300)):
