@@ -106,6 +106,16 @@ def test_weights_with_window_and_sinks(dtype, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(1000, 0), (1500, 40), (1024, 1900)])
+def test_weights_in_two_launches_through_windows(dtype, d, window, sinks):
+    """Windows of several chunks that hide part of the context: positions that no row sees keep
+    what they have, or are 0."""
+    run_weights(dtype, d, 16, 4, 2, [3, 1, 5], [4500, 33, 1601], window=window, sinks=sinks, seed=2)
+    run_weights(dtype, d, 128, 8, 1, [9], [3300], window=window, sinks=sinks, seed=3, max_context=20000)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_weights_of_long_contexts(dtype):
     run_weights(dtype, 128, 16, 4, 1, [3, 1, 2], [3001, 700, 255], seed=2)
     run_weights(dtype, 64, 128, 2, 1, [1, 1], [5000, 10], seed=3, max_context=8192)

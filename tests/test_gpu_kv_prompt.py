@@ -98,6 +98,48 @@ def test_long_contexts_split_and_joined(dtype, d):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(1000, 0), (1500, 40), (700, 900), (2990, 4)])
+def test_split_contexts_through_windows(dtype, d, window, sinks):
+    """Windows of more than a chunk of 16 tiles: parts of a row's context that it does not see, or
+    sees only the first positions of, are joined."""
+    run_prompt(dtype, d, 16, 2, 1, [20, 1, 2], [3001, 700, 5], seed=2, window=window, sinks=sinks)
+    run_prompt(dtype, d, 128, 3, 1, [90], [2222], seed=3, max_context=9000, total=20000, window=window,
+               sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1000, 2)])
+def test_nan_blocks_in_split_contexts(dtype, d, window, sinks):
+    """NaN blocks of V in several chunks of a context, seen by all rows, some and none; then of K."""
+    rows, ctx, page = [40], [2000], 16
+    cache, K, V = T.make_attention(d, page, 1, rows, ctx, 4)
+    host = cache.pages.cpu().numpy().reshape(1, -1, 1, page * (d + d // 16))
+    table = cache.page_table.cpu().numpy()
+    _, _, ks, vs = U.places(page, d)
+    blocks = d // 32
+    q = torch.randn(40, 2, d, device=DEV).to(T.DTYPES[dtype])
+    args = dict(max_context=2040, total_context=2040, window=window, sinks=sinks)
+
+    def check():
+        cache.pages.copy_(torch.from_numpy(host.reshape(1, -1, host.shape[-1])))
+        out, st = binding.kv_prompt_attention(cache, q, T._i([0, 40]), T._i(ctx), **args)
+        assert st.cpu().tolist() == [0]
+        T.check_attention(out, q, K, V, [0, 40], ctx, rows, dtype, d ** -0.5, window, sinks)
+        nan = np.isnan(T._f64(out))
+        assert nan.any() and not nan.all()
+    for t, blk in ((1020, 0), (1500, blocks - 1), (2030, 2 % blocks)) if window else ((2030, blocks - 1),):
+        host[0, table[0, t // page], 0, vs[t % page, blk]] = 255
+        V[0][t, 0, 32 * blk:32 * blk + 32] = np.nan
+    check()
+    for t in (1010, 2035) if window else (2035,):          # rows up to 9, rows from 35 on
+        host[0, table[0, t // page], 0, ks[t % page, blocks - 1]] = 255
+        K[0][t, 0] = np.nan
+    check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_peaked_scores(dtype):
     """Large scores: the running maximum moves, most weights underflow."""
     run_prompt(dtype, 128, 16, 4, 2, [50, 3], [300, 0], loud=True, scale=1.0)
