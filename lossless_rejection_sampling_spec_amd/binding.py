@@ -743,7 +743,7 @@ def kv_attention_weights(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tens
     if out is None:
         out = weights if weights is not None else torch.zeros(
             batch, cache.kv_heads, max_context, dtype=torch.float32, device=cache.device)
-    for t, name in ((weights, "weights"), (out, "out")):
+    for t, name in ((out, "out"), (weights, "weights")):
         if t is not None and (t.dtype != torch.float32 or t.device != cache.device
                               or not t.is_contiguous() or t.dim() != 3 or t.shape[0] < batch
                               or t.shape[1] != cache.kv_heads or t.shape[2] < max_context

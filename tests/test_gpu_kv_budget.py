@@ -637,6 +637,16 @@ def test_the_binding_refuses_arguments_that_do_not_fit():
             binding.kv_evict(cache, *args, **kws)
 
 
+@pytest.mark.parametrize("shape", [(1400,), (2, 1400), (2, 2, 1400, 1)])
+def test_the_binding_refuses_results_of_another_rank(shape):
+    cache, q, cu, ctx, kw = _small()
+    w = torch.zeros(2, 2, 1400, device=DEV)
+    odd = torch.zeros(shape, device=DEV)
+    for over in (dict(weights=w, out=odd), dict(out=odd), dict(weights=odd), dict(weights=odd, out=w)):
+        with pytest.raises(ValueError):
+            binding.kv_attention_weights(cache, q, cu, ctx, **over, **kw)
+
+
 # ------------------------------------------------------------ the calls together
 
 @pytest.mark.parametrize("captured", [False, True])
