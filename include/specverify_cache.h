@@ -8,7 +8,8 @@
  * per layer attention_weights of the rows that were committed -> release -> evict.
  *
  * Pages, tables, offsets, statuses and return values are those of specverify.h.  A workspace
- * that is NULL or not 16-byte aligned is SV_ERR_NULL.
+ * that is NULL or not 16-byte aligned is SV_ERR_NULL.  Work is split by the bounds max_context and
+ * total_context, not by the lengths on the device: loose ones cost time, not accuracy.
  */
 #ifndef SPECVERIFY_CACHE_H
 #define SPECVERIFY_CACHE_H

@@ -30,12 +30,15 @@ namespace budget {
 // Where a request is one chunk (short contexts) both passes are one launch.  fp32 queries go in
 // as three bf16 terms, exactly; nothing is rounded further.
 //
-// What bounds it: vector instructions (widening, exponentials), 65 % of the first pass's time
-// and 59 % of the second's, beside HBM at 3.8 and 3.4 TB/s: 52 + 63 us for 64 requests of 7
-// rows over 512 to 16,384 positions (32 heads over 8, D=128).  Four requests of 64 rows over
-// 1,500 to 4,000 positions, 26 + 31 us: 1.4 waves per SIMD whose reads of queries from LDS and
-// exponentials follow one another (smaller chunks give more waves, and more queries to
-// fetch: no faster; eight waves per workgroup 73 us against 58 for the call).
+// What bounds it: vector instructions, 64 % of the first pass's time and 59 % of the second's,
+// beside HBM at 3.8 and 3.4 TB/s: 51 + 62 us for 64 requests of 7 rows over 512 to 16,384
+// positions (32 heads over 8, D=128).  They are widening, exponentials, and scalars kept in lanes
+// of vector registers for want of scalar ones (74 and 95 of them here, 181 to 335 with four
+// row tiles): ten to twenty reads of such lanes per tile, and 58 with 37 writes for a block of 64
+// rows that is masked.  Four requests of 64 rows over 1,500 to 4,000 positions, 26 + 31 us: 1.4
+// waves per SIMD whose reads of queries from LDS and exponentials follow one another (smaller
+// chunks give more waves, and more queries to fetch: no faster; eight waves per workgroup 73 us
+// against 58 for the call).
 
 constexpr int TILE = 32, SUB = 64;            // tokens of a tile; tiles whose pages a wave looks up at once
 // Waves of a workgroup: eight where it does both passes (64 requests over 100 to 1,000 positions

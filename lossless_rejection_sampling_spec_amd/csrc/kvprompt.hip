@@ -13,9 +13,11 @@
 // Widening once, not per workgroup: a tile of 32 tokens is used by every block of rows
 // behind it, rows * G / 256 times.  The widened tile is laid out as the matrix
 // instructions' operands, [instruction][lane][8 values], so that its way through LDS is
-// straight copies and reads without bank conflicts.  It is bound by its writes: 29 us of the
-// 1,850 for one prompt of 15,991 rows, 23 of 285 for four of 1,500 to 4,000, 65 of 247 for
-// two of 150 to 600 after 8,000 to 30,000 positions.
+// straight copies and reads without bank conflicts.  It takes 29 us of the 1,850 for one prompt
+// of 15,991 rows, 23 of 297 for four of 1,500 to 4,000, 65 of 251 for two of 150 to 600 after
+// 8,000 to 30,000 positions.  Latency bounds it: 45 MB read and 164 written in those 65 us are
+// 3.2 TB/s of the 5.1 that a copy reaches, with the vector units 18 % busy; a wave has two or
+// three tiles, each a chain of table, codes and stores with nothing else on its way.
 //
 // k_prompt: a workgroup of 4 or 8 waves takes one KV head and 32 of the request's rows * G
 // query rows for each wave (the G heads of a row side by side).  Per tile it computes
@@ -25,15 +27,21 @@
 // laid out in the order of tokens in which the accumulators hold them).
 //
 // Roundings: bf16 rows' weights are rounded to bf16 for the second product (and summed as
-// rounded), as the matrix instruction takes them; fp32 rows' queries and weights go in as
-// three bf16 terms, exactly.  Scores, statistics and sums are fp32.
+// rounded), as the matrix instruction takes them: results are 0.0017 to 0.0023 of their norm from
+// 64 bits.  Two bf16 terms per weight would leave the result's own rounding (0.0015 to 0.0017), for
+// 2,650 us instead of 1,850 for the prompt below and 86 instead of 79 for 64 short ones.  fp32
+// rows' queries and weights go in as three bf16 terms, exactly.  Scores, statistics and sums are
+// fp32.
 //
-// What bounds it: the waves' alternation of products and softmax, matrix instructions 51 % of
-// the time, vector ones 37 % (one prompt of 15,991 rows, 32 heads over 8 of D=128: 1.14
+// What bounds it: the waves' alternation of products and softmax, matrix instructions 52 % of
+// the time, vector ones 38 % (one prompt of 15,991 rows, 32 heads over 8 of D=128: 1.13
 // PFLOP/s, where a large bf16 matrix product reaches 1.20 to 1.27; four prompts of 1,500 to
-// 4,000 rows 0.84, their last workgroups ending alone).  Tried and slower: the next tile's
-// scores ahead of this one's softmax (2,307 us against 2,220 of the same kernel without, for
-// the first of these), a barrier per tile over a ring of buffers.
+// 4,000 rows 0.80, their last workgroups ending alone).  Within a wave nothing hides the loads of
+// the next stage: the compiler takes either half of the buffer for what they write, and has
+// them waited for before the stage's first product; other waves' products run meanwhile.  Tried
+// with that wait, and slower: the next tile's scores ahead of this one's softmax (2,307 us against
+// 2,220 of the same kernel without, for the first of these), a barrier per tile over a ring of
+// buffers.
 
 #include "kv_common.h"
 #include "row_ranges.h"
@@ -454,7 +462,9 @@ struct Prompt {
   // (of fp32 rows at D=256 the last term lies in LDS: all three do not fit the registers)
   static constexpr int NR = NT == 3 && D == 256 ? 2 : NT;
   static constexpr int Q_LDS = STEPS * (NT - NR) * 64;    // 16-byte words of a wave
-  // tiles weighed at a time, as many as the registers hold
+  // tiles weighed at a time: two where both fit the registers, but for D=64, whose short
+  // prompts lose more to the half pairs at their ends (64 of 1 to 700 rows 79 us, in pairs 87;
+  // four of 1,500 to 4,000 160 and 162)
   static constexpr int PAIR = NT == 1 && D == 128 ? 2 : 1;
 
   bf16x8 q[STEPS][NR];
@@ -801,10 +811,11 @@ static bool plan_of(int dtype, int batch, int total_rows, int heads, int kv_head
   const int64_t R = (int64_t)total_rows * (heads / kv_heads);
   // Four waves per workgroup, two workgroups per compute unit, so that one's start and end
   // run beside the other's products; or eight, which share a tile's way to LDS, for bf16 calls
-  // of many workgroups and long contexts.  (One prompt of 15,991 rows, 2,000 blocks of 256
-  // rows over all KV heads: 1,838 us, with four waves 1,940; four of 1,500 to 4,000 rows, 1,176
-  // blocks: 304 and 307; 64 of 1 to 700, 2,700 blocks at D=64: 86 and 83; two of 150 to 600
-  // after 8,000 to 30,000 positions: 306 and 265; eight fp32 ones with a window: 205 and 175.)
+  // of many workgroups and long contexts.  (us with eight waves and with four, by the call's rows
+  // of all KV heads over 256.  Eight: one prompt of 15,991 rows, 2,000: 1,850 and 1,945; four of
+  // 1,500 to 4,000, 1,150: 296 and 301 to 306.  Four: eight of 800 to 2,000 over 16 KV heads, 580:
+  // 108 and 102; two of 150 to 600 after 8,000 to 30,000 positions, 56: 287 and 251; 64 of 1 to
+  // 700, 2,150, short: equal; eight fp32 ones with a window: 203 and 172.)
   p.waves = 8;
   int64_t blocks = 0;
   for (;; p.waves = 4) {
