@@ -131,8 +131,8 @@ int spec_kv_attention_weights(const void* q, int64_t ld_q, int dtype, const int3
  * `evicted` or `weights`: the caller sets evicted[b] = 0 when slot b takes a new sequence (its
  * first weights then come from weights_in = NULL), and after spec_kv_fork of all of an evicted
  * request copies evicted[src] to evicted[dst], and the weights of src, in every layer, to dst.
- * status: SV_ROW_BAD_PARAM for sinks + recent > m, or a length that is negative or past
- * ld_weights or the table row; SV_ROW_BAD_PAGE for a page id outside the pool, or one of the
+ * status: SV_ROW_BAD_PARAM for sinks + recent > m where n > m, or, whatever the budget, a length
+ * that is negative or past ld_weights or the table row; SV_ROW_BAD_PAGE for a page id outside the pool, or one of the
  * ceil(m / page_size) pages that stay having a count other than 1 (evict before forking);
  * the request then stays as it is.
  *   budgets        int32 [batch]
